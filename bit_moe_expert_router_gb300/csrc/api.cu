@@ -56,11 +56,17 @@ int check_ws(const WsLayout& L, const void* ws, size_t bytes) {
 
 thread_local char g_last_error[256] = "";
 
-int cuda_status(cudaError_t e, const char* what) {
+}  // namespace
+
+int moe::cuda_status(cudaError_t e, const char* what) {
     if (e == cudaSuccess) return MOE_OK;
     snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
     return MOE_ERR_CUDA;
 }
+
+namespace {
+
+using moe::cuda_status;
 
 #define MOE_TRY(expr)                          \
     do {                                       \

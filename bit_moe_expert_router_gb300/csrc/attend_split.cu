@@ -1,0 +1,481 @@
+// Attention over the paged cache with the keys split over the warps of the
+// whole GPU, on mma.sync: the engine of decoding batches (a few rows against a
+// long cache).
+//
+// Per row: s_j = scale q . k_j over the positions j that the row sees; with a
+// running maximum m, l = sum_j 2^(s_j log2 e - m) and o = sum_j 2^(s_j log2 e - m) v_j
+// are kept in fp32 in one pass over the cache and rescaled when m grows; the
+// row is o / l.  Rows of one key/value head are taken together (token-major:
+// row = token * group + head of the group), 16 at a time, so the cache is read
+// once for a group's heads.
+//
+// Bound: HBM, the K and V bytes of the visible positions.  A CTA is 8 warps
+// (4 at D = 256) of their own pipelines: a warp takes 16 keys at a time, K and V by
+// 16-byte cp.async into its own ring (chunks XOR-swizzled by row so that
+// ldmatrix reads without bank conflicts), and keeps its own m, l, o; no
+// barrier inside a piece.  At a piece's end the warps' states are joined in
+// shared memory.  The pieces are equal shares of all (sequence, head, 16 keys)
+// units of the batch (the deal), so ragged lengths balance; pieces of one row tile go
+// to the workspace and a second kernel joins them in a fixed order.
+#include "attention_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kKeys = 16;  // keys of a unit: one warp's step
+
+template <int DH>
+struct SplitCfg {
+    static constexpr int kWarps = DH == 256 ? 4 : 8;
+    static constexpr int kStages = DH == 64 ? 6 : 3;
+    static constexpr int kCpr = DH / 8;                    // 16-byte chunks per row
+    static constexpr int kTile = kKeys * DH;               // elements of K (or V) in a stage
+    static constexpr int kQBytes = kSplitRows * DH * 2;
+    static constexpr int kWarpBytes = kStages * 2 * kTile * 2;
+    static constexpr int kSmem = kQBytes + kWarps * kWarpBytes + kWarps * kSplitRows * 8;
+    static constexpr bool kQRegs = DH <= 128;              // the queries' fragments stay in registers
+    static_assert(kWarpBytes >= kSplitRows * DH * 4, "a warp's ring holds its state at the join");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile whose rows are CPR chunks.
+template <int CPR>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return static_cast<uint32_t>(r * CPR + (c ^ (r & 7))) * 16;
+}
+
+// Where a warp's keys lie: the row offsets (elements) of a unit's 16 keys, one unit ahead of its
+// copies, so that the page ids are on their way while the unit before is computed.  ALIGNED: pages
+// of a multiple of 16 positions, a unit lies in one page; else each key is looked up by itself.
+template <bool ALIGNED>
+struct Rows {
+    int64_t k, v;  // ALIGNED: of the unit's first key (every lane); else of key lane % 16
+    bool ok;
+    int id, at;    // the next unit's page and the key's (or first key's) row in it
+    __device__ __forceinline__ void fetch(const KvArgs& a, int b, int unit, int end) {
+        const int key = unit * kKeys + (ALIGNED ? 0 : (threadIdx.x & 15));
+        const int p = key / a.page;
+        at = key - p * a.page;
+        id = unit < end ? page_id(a, b, p) : -1;
+    }
+    __device__ __forceinline__ void settle(const KvArgs& a, int h) {
+        ok = id >= 0;
+        const int64_t i = ok ? id : 0;
+        k = i * a.k_ps + static_cast<int64_t>(at) * a.k_rs + h * a.k_hs;
+        v = i * a.v_ps + static_cast<int64_t>(at) * a.v_rs + h * a.v_hs;
+    }
+};
+
+template <typename T, int DH, bool ALIGNED>
+__global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_kernel(const AttendArgs a) {
+    using C = SplitCfg<DH>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    T* sq = reinterpret_cast<T*>(smem);
+    unsigned char* rings = smem + C::kQBytes;
+    float2* ml = reinterpret_cast<float2*>(rings + C::kWarps * C::kWarpBytes);  // [warps][rows]
+    long long* prefix = reinterpret_cast<long long*>(reinterpret_cast<unsigned char*>(ml) + C::kWarps * kSplitRows * 8);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const KvArgs& kv = a.kv;
+    const T* kc = static_cast<const T*>(kv.k);
+    const T* vc = static_cast<const T*>(kv.v);
+    unsigned char* ring = rings + warp * C::kWarpBytes;
+    const int chunks = kv.d / 8;
+
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    // components past D are never copied: zero once (rows of the ring, and of the queries)
+    if (kv.d < DH) {
+        for (int i = threadIdx.x; i < (C::kQBytes + C::kWarps * C::kWarpBytes) / 16; i += blockDim.x)
+            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
+
+    Cursor c;
+    deal_begin<kSplitRows, kKeys>(a, prefix, 16, c);
+    if (a.split && threadIdx.x == 0) {
+        BoundaryRec r;
+        r.begin = c.u - c.off;
+        r.per = c.per;
+        r.n = c.n;
+        r.cut = c.u < c.end && c.off > 0;
+        r.b = c.b;
+        r.rt = c.rt;
+        r.h = c.h;
+        r.pad = 0;
+        a.recs[blockIdx.x] = r;
+    }
+    clear_stray_rows<T>(a);
+    const float sc = a.scale * kLog2e;
+    const long long u_begin = c.u;
+
+    while (c.u < c.end) {
+        const int taken = deal_take(a, c);
+        const int r0 = c.rt * kSplitRows;
+        const int rows = min(c.s.q_len * kv.group - r0, kSplitRows);
+        int lo, hi;
+        key_range(kv, a.window, c.s, r0, r0 + rows, lo, hi);
+        const int unit0 = c.first + c.off, unit1 = unit0 + taken;
+
+        // the queries of the tile
+        for (int i = threadIdx.x; i < kSplitRows * chunks; i += blockDim.x) {
+            const int r = i / chunks, x = i - r * chunks;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                const int tok = c.s.q0 + (r0 + r) / kv.group, head = c.h * kv.group + (r0 + r) % kv.group;
+                w = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + x * 8);
+            }
+            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sq) + chunk_at<C::kCpr>(r, x)) = w;
+        }
+        __syncthreads();
+        const int mat = lane >> 3, mrow = lane & 7;
+        uint32_t qf[C::kQRegs ? DH / 16 : 1][4];
+        const uint32_t q_addr = smem_u32(sq);
+        if constexpr (C::kQRegs) {
+#pragma unroll
+            for (int ks = 0; ks < DH / 16; ++ks) ldsm4(qf[ks], q_addr + chunk_at<C::kCpr>((mat & 1) * 8 + mrow, ks * 2 + (mat >> 1)));
+        }
+        // this thread's two rows: positions they see
+        int p_hi[2], p_lo[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = (lane >> 2) + 8 * x;
+            const int p = c.s.pos0 + (r0 + min(r, rows - 1)) / kv.group;
+            p_hi[x] = min(p, kv.cap - 1);
+            p_lo[x] = a.window > 0 ? p - a.window : -1;
+        }
+        const int all_hi = c.s.pos0 + r0 / kv.group;                                          // every row sees keys <= all_hi
+        const int all_lo = a.window > 0 ? c.s.pos0 + (r0 + rows - 1) / kv.group - a.window : -1;  // and > all_lo
+
+        float o[DH / 8][4];
+#pragma unroll
+        for (int n = 0; n < DH / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+
+        Rows<ALIGNED> rw;
+        rw.fetch(kv, c.b, unit0 + warp, unit1);
+        int fetch_unit = unit0 + warp;  // the unit whose ids rw holds
+        auto issue = [&](int stage) {
+            if (fetch_unit < unit1) {
+                rw.settle(kv, c.h);
+                unsigned char* sk = ring + stage * 2 * C::kTile * 2;
+                unsigned char* sv = sk + C::kTile * 2;
+                const int key0 = fetch_unit * kKeys;
+                const int x = lane % C::kCpr;
+                constexpr int kRowsPer = 32 / C::kCpr;
+#pragma unroll
+                for (int i = 0; i < kKeys / kRowsPer; ++i) {
+                    const int r = i * kRowsPer + lane / C::kCpr;
+                    int64_t ko, vo;
+                    bool ok;
+                    if constexpr (ALIGNED) {
+                        ko = rw.k + r * kv.k_rs;
+                        vo = rw.v + r * kv.v_rs;
+                        ok = rw.ok;
+                    } else {
+                        ko = __shfl_sync(~0u, rw.k, r);
+                        vo = __shfl_sync(~0u, rw.v, r);
+                        ok = __shfl_sync(~0u, rw.ok ? 1 : 0, r);
+                    }
+                    ok = ok && key0 + r < hi;
+                    if (x < chunks) {  // a key that no row sees is zeros: whatever the cache holds there stays out
+                        cp_async16(sk + chunk_at<C::kCpr>(r, x), kc + (ok ? ko + x * 8 : 0), ok ? 16 : 0);
+                        cp_async16(sv + chunk_at<C::kCpr>(r, x), vc + (ok ? vo + x * 8 : 0), ok ? 16 : 0);
+                    }
+                }
+                fetch_unit += C::kWarps;
+                rw.fetch(kv, c.b, fetch_unit, unit1);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int s = 0; s < C::kStages - 1; ++s) issue(s);
+        int stage = 0, fill = C::kStages - 1;
+        for (int u = unit0 + warp; u < unit1; u += C::kWarps) {
+            issue(fill);
+            fill = fill + 1 == C::kStages ? 0 : fill + 1;
+            cp_async_wait<C::kStages - 1>();
+            __syncwarp();
+            const uint32_t sk = smem_u32(ring + stage * 2 * C::kTile * 2), sv = sk + C::kTile * 2;
+            stage = stage + 1 == C::kStages ? 0 : stage + 1;
+            float s[2][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < DH / 16; ++ks) {
+                uint32_t kf[4];
+                ldsm4(kf, sk + chunk_at<C::kCpr>((mat >> 1) * 8 + mrow, ks * 2 + (mat & 1)));
+                if constexpr (C::kQRegs) {
+                    mma16816<T>(s[0], qf[ks], kf[0], kf[1]);
+                    mma16816<T>(s[1], qf[ks], kf[2], kf[3]);
+                } else {
+                    uint32_t qv[4];
+                    ldsm4(qv, q_addr + chunk_at<C::kCpr>((mat & 1) * 8 + mrow, ks * 2 + (mat >> 1)));
+                    mma16816<T>(s[0], qv, kf[0], kf[1]);
+                    mma16816<T>(s[1], qv, kf[2], kf[3]);
+                }
+            }
+            const int key0 = u * kKeys;
+            const bool masked = key0 + kKeys - 1 > min(all_hi, kv.cap - 1) || key0 <= all_lo;
+            float mx[2] = {kNegInf, kNegInf};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v = s[n][i] * sc;
+                    if (masked) {
+                        const int key = key0 + n * 8 + (lane & 3) * 2 + (i & 1);
+                        if (key > p_hi[i >> 1] || key <= p_lo[i >> 1]) v = kNegInf;
+                    }
+                    s[n][i] = v;
+                    mx[i >> 1] = fmaxf(mx[i >> 1], v);
+                }
+            bool grew = false;
+            float base[2], f[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                mx[x] = fmaxf(mx[x], __shfl_xor_sync(~0u, mx[x], 1));
+                mx[x] = fmaxf(mx[x], __shfl_xor_sync(~0u, mx[x], 2));
+                const float mn = fmaxf(m[x], mx[x]);
+                base[x] = mn == kNegInf ? 0.f : mn;
+                f[x] = exp2_fast(m[x] - base[x]);
+                grew |= mn != m[x];
+                m[x] = mn;
+            }
+            if (__any_sync(~0u, grew)) {
+#pragma unroll
+                for (int n = 0; n < DH / 8; ++n) {
+                    o[n][0] *= f[0];
+                    o[n][1] *= f[0];
+                    o[n][2] *= f[1];
+                    o[n][3] *= f[1];
+                }
+                l[0] *= f[0];
+                l[1] *= f[1];
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[n][i] = exp2_fast(s[n][i] - base[i >> 1]);
+                    l[i >> 1] += s[n][i];
+                }
+            // the weights as the second product's operand: rounded to the element type, their sum l is not
+            const uint32_t pf[4] = {Elem<T>::pack(s[0][0], s[0][1]), Elem<T>::pack(s[0][2], s[0][3]),
+                                    Elem<T>::pack(s[1][0], s[1][1]), Elem<T>::pack(s[1][2], s[1][3])};
+#pragma unroll
+            for (int j = 0; j < DH / 16; ++j) {
+                uint32_t vf[4];
+                ldsm4t(vf, sv + chunk_at<C::kCpr>((mat & 1) * 8 + mrow, j * 2 + (mat >> 1)));
+                mma16816<T>(o[2 * j], pf, vf[0], vf[1]);
+                mma16816<T>(o[2 * j + 1], pf, vf[2], vf[3]);
+            }
+            __syncwarp();  // the stage is read before its next copies
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+
+        // this warp's state into its ring
+        float* so = reinterpret_cast<float*>(ring);  // [rows][DH]
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            l[x] += __shfl_xor_sync(~0u, l[x], 1);
+            l[x] += __shfl_xor_sync(~0u, l[x], 2);
+            const int r = (lane >> 2) + 8 * x;
+            if (r < rows) {
+                if ((lane & 3) == 0) ml[warp * kSplitRows + r] = make_float2(m[x], l[x]);
+#pragma unroll
+                for (int n = 0; n < DH / 8; ++n)
+                    *reinterpret_cast<float2*>(so + r * DH + n * 8 + (lane & 3) * 2) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
+            }
+        }
+        __syncthreads();
+        const bool whole = taken == c.n;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (c.u == u_begin ? 0 : 1);
+        // the join of the warps: a warp per row
+        for (int r = warp; r < rows; r += C::kWarps) {
+            float mw = kNegInf, lw = 0.f;
+            if (lane < C::kWarps) {
+                const float2 v = ml[lane * kSplitRows + r];
+                mw = v.x;
+                lw = v.y;
+            }
+            float mm = mw;
+#pragma unroll
+            for (int x = C::kWarps / 2; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
+            mm = __shfl_sync(~0u, mm, 0);
+            const float fw = mw == kNegInf ? 0.f : exp2_fast(mw - mm);
+            float ll = lw * fw;
+#pragma unroll
+            for (int x = C::kWarps / 2; x; x >>= 1) ll += __shfl_xor_sync(~0u, ll, x);
+            ll = __shfl_sync(~0u, ll, 0);
+            float acc[DH / 32] = {};
+#pragma unroll
+            for (int w = 0; w < C::kWarps; ++w) {
+                const float fx = __shfl_sync(~0u, fw, w);
+                if (fx == 0.f) continue;
+                const float* p = reinterpret_cast<const float*>(rings + w * C::kWarpBytes) + r * DH + lane * 2;
+#pragma unroll
+                for (int x = 0; x < DH / 64; ++x) {
+                    const float2 v = *reinterpret_cast<const float2*>(p + x * 64);
+                    acc[2 * x] += v.x * fx;
+                    acc[2 * x + 1] += v.y * fx;
+                }
+            }
+            if (whole) {
+                const int tok = c.s.q0 + (r0 + r) / kv.group, head = c.h * kv.group + (r0 + r) % kv.group;
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                bool bad = ll != ll;
+#pragma unroll
+                for (int x = 0; x < DH / 32; ++x) bad |= acc[x] != acc[x];
+                if (__any_sync(~0u, bad)) {
+                    attend_row<T>(a, c.b, tok, head, c.s.pos0 + (r0 + r) / kv.group);
+                    continue;
+                }
+                T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + lane * 2;
+#pragma unroll
+                for (int x = 0; x < DH / 64; ++x)
+                    if (x * 64 + lane * 2 < kv.d)
+                        *reinterpret_cast<uint32_t*>(dst + x * 64) = Elem<T>::pack(acc[2 * x] * inv, acc[2 * x + 1] * inv);
+                if (lane == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
+            } else {
+                float* dst = a.part_o + (slot * kSplitRows + r) * DH + lane * 2;
+#pragma unroll
+                for (int x = 0; x < DH / 64; ++x) *reinterpret_cast<float2*>(dst + x * 64) = make_float2(acc[2 * x], acc[2 * x + 1]);
+                if (lane == 0) a.part_ml[slot * kSplitRows + r] = make_float2(mm, ll);
+            }
+        }
+        __syncthreads();
+        if (kv.d < DH) {  // the state overwrote the ring's zero columns
+            for (int i = threadIdx.x; i < C::kWarps * C::kWarpBytes / 16; i += blockDim.x)
+                reinterpret_cast<uint4*>(rings)[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+        }
+        deal_next<kSplitRows, kKeys>(a, c, taken);
+    }
+}
+
+// The join of the pieces of the tiles that CTA boundaries cut.  Block c stands for the boundary
+// before CTA c + 1; a tile cut by several boundaries has its rows dealt over their blocks.  Pieces are
+// added in the order of their CTAs, whatever order they were finished in.
+template <typename T, int ROWS, int DH>
+__global__ void __launch_bounds__(DH) attend_join_kernel(const AttendArgs a) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int cta = blockIdx.x + 1;
+    const BoundaryRec rec = a.recs[cta];
+    if (!rec.cut) return;
+    const KvArgs& kv = a.kv;
+    const int lane = threadIdx.x & 31;
+    const int c0 = static_cast<int>(rec.begin / rec.per), c1 = static_cast<int>((rec.begin + rec.n - 1) / rec.per);
+    const SeqInfo s = seq_info(kv, rec.b);
+    const int r0 = rec.rt * ROWS, rows = min(s.q_len * kv.group - r0, ROWS);
+    __shared__ int bad;
+    for (int r = cta - (c0 + 1); r < rows; r += c1 - c0) {
+        // every warp finds the tile's maximum and sum for itself
+        float mm = kNegInf;
+        for (int p = c0 + lane; p <= c1; p += 32) {
+            const int64_t slot = 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1);
+            mm = fmaxf(mm, a.part_ml[slot * ROWS + r].x);
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
+        const float base = mm == kNegInf ? 0.f : mm;
+        float ll = 0.f, acc = 0.f;
+        for (int p0 = c0; p0 <= c1; p0 += 32) {
+            float f = 0.f, lp = 0.f;
+            const int p = p0 + lane;
+            if (p <= c1) {
+                const int64_t slot = 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1);
+                const float2 v = a.part_ml[slot * ROWS + r];
+                f = exp2_fast(v.x - base);
+                lp = v.y * f;
+            }
+            const int n = min(32, c1 + 1 - p0);
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float fi = __shfl_sync(~0u, f, i);
+                ll += __shfl_sync(~0u, lp, i);
+                const int64_t slot = 2 * static_cast<int64_t>(p0 + i) + ((p0 + i) * rec.per >= rec.begin ? 0 : 1);
+                acc += a.part_o[(slot * ROWS + r) * DH + threadIdx.x] * fi;
+            }
+        }
+        const int tok = s.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
+        if (threadIdx.x == 0) bad = 0;
+        __syncthreads();
+        if (acc != acc || ll != ll) bad = 1;
+        __syncthreads();
+        if (bad) {
+            if (threadIdx.x < 32) attend_row<T>(a, rec.b, tok, head, s.pos0 + (r0 + r) / kv.group);
+        } else {
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            if (threadIdx.x < kv.d) {
+                const uint32_t w = Elem<T>::pack(acc * inv, 0.f);
+                reinterpret_cast<uint16_t*>(a.out)[tok * a.o_ts + head * a.o_hs + threadIdx.x] = static_cast<uint16_t>(w & 0xFFFF);
+            }
+            if (threadIdx.x == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int DH, bool ALIGNED>
+cudaError_t launch_t(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
+    using C = SplitCfg<DH>;
+    const int smem = C::kSmem + (a.kv.n_seqs + 1) * 8;
+    cudaError_t e = cudaFuncSetAttribute(attend_split_kernel<T, DH, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = a.split ? n_ctas : max(1, min(max_items, n_ctas * 8));
+    attend_split_kernel<T, DH, ALIGNED><<<grid, C::kWarps * 32, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !a.split || grid < 2) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid - 1);
+    cfg.blockDim = dim3(DH);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, kSplitRows, DH>, a);
+}
+
+template <typename T, int DH>
+cudaError_t launch_d(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
+    return a.kv.page % kKeys == 0 ? launch_t<T, DH, true>(a, n_ctas, max_items, st) : launch_t<T, DH, false>(a, n_ctas, max_items, st);
+}
+
+template <typename T>
+cudaError_t launch_e(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
+    switch (split_padded_dim(a.kv.d)) {
+        case 64: return launch_d<T, 64>(a, n_ctas, max_items, st);
+        case 128: return launch_d<T, 128>(a, n_ctas, max_items, st);
+        default: return launch_d<T, 256>(a, n_ctas, max_items, st);
+    }
+}
+
+}  // namespace
+
+int split_padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
+cudaError_t launch_attend_split(const AttendArgs& a, int dtype, int n_ctas, int max_items, cudaStream_t st) {
+    return dtype == 0 ? launch_e<__nv_bfloat16>(a, n_ctas, max_items, st) : launch_e<__half>(a, n_ctas, max_items, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,67 @@
+// Internal arguments and launchers of the attention operators (host side; the
+// C ABI in attention_api.cu validates everything before calling these).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// A paged cache and its ragged batch, as the kernels take it.
+struct KvArgs {
+    void* k;
+    void* v;
+    int64_t k_ps, k_rs, k_hs;  // page, row and head strides, elements
+    int64_t v_ps, v_rs, v_hs;
+    const int32_t* table;      // [n_seqs][width]
+    const int32_t* q_start;    // [n_seqs + 1]
+    const int32_t* kv_len;     // [n_seqs]
+    int n_tokens, n_seqs, hq, hkv, group, d, page, n_pages, width;
+    int cap;                   // positions a row of the table can hold
+};
+
+struct AppendArgs {
+    KvArgs kv;
+    const void *q, *k, *v;
+    void* q_out;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
+    const float* cos_sin;
+    const float* q_weight;
+    const float* k_weight;
+    const int32_t* positions;
+    int64_t table_rows;
+    int rot, interleaved;
+    float eps, weight_offset;
+};
+
+struct AttendArgs {
+    KvArgs kv;
+    const void* q;
+    void* out;
+    float* lse;                // [n_tokens][hq] or null
+    int64_t q_ts, q_hs, o_ts, o_hs;
+    float scale;
+    int window;                // 0: none
+    int split;                 // pieces of a row tile may go to several CTAs
+    struct BoundaryRec* recs;  // workspace: one per CTA
+    float* part_o;             // [2 * CTAs][tile rows][padded D]
+    float2* part_ml;           // [2 * CTAs][tile rows]: running maximum (base 2), sum
+};
+
+// A row tile of the batch cut by CTA c's first unit: written by CTA c, read by the join.
+struct BoundaryRec {
+    long long begin;   // the tile's first unit
+    long long per;     // units per CTA
+    int n;             // the tile's units
+    int cut;           // 1 if the tile began before CTA c
+    int b, rt, h, pad;
+};
+
+cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t st);
+
+// Attention on mma.sync with the keys split over the warps of the GPU.
+constexpr int kSplitRows = 16;
+int split_padded_dim(int d);
+cudaError_t launch_attend_split(const AttendArgs& a, int dtype, int n_ctas, int max_items, cudaStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,192 @@
+// C ABI of the attention operators: argument checks, workspace carving, engine
+// choice and launches.  Host code only.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <initializer_list>
+
+#include "attention.h"
+#include "kernels.h"
+#include "moe_w4a8.h"
+#include "moe_w4a8_attention.h"
+
+#define MOE_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+constexpr int64_t kMaxSeqs = 2048;
+constexpr int64_t kMaxHeads = 1024;
+constexpr int64_t kMaxHeadDim = 256;
+constexpr int64_t kI32 = (int64_t(1) << 31) - 1;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes and strides of a batch (no pointers).
+int check_sizes(const moe_kv_batch_t* b) {
+    if (!b) return MOE_ERR_INVALID_ARG;
+    for (int64_t v : {b->n_seqs, b->n_q_heads, b->n_kv_heads, b->head_dim, b->page_size, b->n_pages, b->table_width,
+                      b->max_q_len, b->max_kv_len})
+        if (v < 1) return MOE_ERR_INVALID_ARG;
+    if (b->n_q_heads % b->n_kv_heads != 0 || b->head_dim % 8 != 0 || (b->dtype != MOE_DTYPE_BF16 && b->dtype != MOE_DTYPE_FP16))
+        return MOE_ERR_INVALID_ARG;
+    for (int64_t v : {b->k_page_stride, b->k_row_stride, b->k_head_stride, b->v_page_stride, b->v_row_stride, b->v_head_stride})
+        if (v < 0 || v % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (b->head_dim > kMaxHeadDim || b->n_q_heads > kMaxHeads || b->n_seqs > kMaxSeqs || b->page_size > kI32 ||
+        b->n_pages > kI32 || b->table_width > kI32)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+int check_batch(const moe_kv_batch_t* b, int64_t n_tokens) {
+    if (int rc = check_sizes(b)) return rc;
+    if (n_tokens < 0) return MOE_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(b->k_cache), static_cast<const void*>(b->v_cache)})
+        if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+    for (const int32_t* p : {b->block_table, b->q_start, b->kv_len})
+        if (!p || !aligned4(p)) return MOE_ERR_INVALID_ARG;
+    if (n_tokens > kI32 / b->n_q_heads) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// One [T][heads][D] array.
+int check_rows(const void* p, int64_t token_stride, int64_t head_stride) {
+    return p && aligned16(p) && token_stride >= 0 && head_stride >= 0 && token_stride % 8 == 0 && head_stride % 8 == 0
+               ? MOE_OK
+               : MOE_ERR_INVALID_ARG;
+}
+
+moe::KvArgs kv_args(const moe_kv_batch_t* b, int64_t n_tokens) {
+    moe::KvArgs a{};
+    a.k = b->k_cache;
+    a.v = b->v_cache;
+    a.k_ps = b->k_page_stride;
+    a.k_rs = b->k_row_stride;
+    a.k_hs = b->k_head_stride;
+    a.v_ps = b->v_page_stride;
+    a.v_rs = b->v_row_stride;
+    a.v_hs = b->v_head_stride;
+    a.table = b->block_table;
+    a.q_start = b->q_start;
+    a.kv_len = b->kv_len;
+    a.n_tokens = static_cast<int>(n_tokens);
+    a.n_seqs = static_cast<int>(b->n_seqs);
+    a.hq = static_cast<int>(b->n_q_heads);
+    a.hkv = static_cast<int>(b->n_kv_heads);
+    a.group = a.hq / a.hkv;
+    a.d = static_cast<int>(b->head_dim);
+    a.page = static_cast<int>(b->page_size);
+    a.n_pages = static_cast<int>(b->n_pages);
+    a.width = static_cast<int>(b->table_width);
+    const __int128 cap = static_cast<__int128>(b->table_width) * b->page_size;
+    a.cap = static_cast<int>(cap < kI32 - 512 ? cap : kI32 - 512);  // a last tile's end stays in range
+    return a;
+}
+
+// Workspace of attend: boundary records, then the pieces' sums and accumulators.
+struct AttendLayout {
+    int n_ctas, rows, dim;
+    size_t recs, ml, o, total;
+};
+
+AttendLayout attend_layout(const moe_kv_batch_t* b) {
+    AttendLayout L{};
+    L.n_ctas = moe::num_sms();
+    L.rows = moe::kSplitRows;
+    L.dim = moe::split_padded_dim(static_cast<int>(b->head_dim));
+    size_t at = 0;
+    auto take = [&](size_t bytes) { size_t here = at; at = (at + bytes + 255) & ~size_t(255); return here; };
+    L.recs = take(sizeof(moe::BoundaryRec) * L.n_ctas);
+    L.ml = take(sizeof(float2) * 2 * L.n_ctas * L.rows);
+    L.o = take(sizeof(float) * 2 * L.n_ctas * L.rows * L.dim);
+    L.total = at;
+    return L;
+}
+
+// Up to this many positions a row tile stays with one CTA: the pieces' way through memory and the second
+// kernel cost more than the keys' streaming by one CTA.
+constexpr int64_t kWholeKeys = 768;
+
+}  // namespace
+
+MOE_API int moe_w4a8_kv_append(const moe_kv_batch_t* batch, const moe_head_prep_t* prep, int64_t n_tokens, const void* q,
+                               int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                               int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride, void* q_out,
+                               int64_t q_out_token_stride, int64_t q_out_head_stride, void* stream) {
+    if (int rc = check_batch(batch, n_tokens)) return rc;
+    if (!prep || prep->rot_dim < 0 || prep->rot_dim % 2 != 0 || prep->rot_dim > batch->head_dim || !(prep->eps >= 0.f) ||
+        !std::isfinite(prep->eps) || !std::isfinite(prep->weight_offset))
+        return MOE_ERR_INVALID_ARG;
+    if (prep->rot_dim > 0 && (!prep->cos_sin || !aligned4(prep->cos_sin) || prep->table_rows < 1)) return MOE_ERR_INVALID_ARG;
+    for (const float* w : {prep->q_weight, prep->k_weight})
+        if (w && !aligned16(w)) return MOE_ERR_INVALID_ARG;
+    if (prep->positions && !aligned4(prep->positions)) return MOE_ERR_INVALID_ARG;
+    if (n_tokens == 0) return MOE_OK;
+    for (int rc : {check_rows(q, q_token_stride, q_head_stride), check_rows(k, k_token_stride, k_head_stride),
+                   check_rows(v, v_token_stride, v_head_stride), check_rows(q_out, q_out_token_stride, q_out_head_stride)})
+        if (rc) return rc;
+    moe::AppendArgs a{};
+    a.kv = kv_args(batch, n_tokens);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.q_ts = q_token_stride;
+    a.q_hs = q_head_stride;
+    a.k_ts = k_token_stride;
+    a.k_hs = k_head_stride;
+    a.v_ts = v_token_stride;
+    a.v_hs = v_head_stride;
+    a.o_ts = q_out_token_stride;
+    a.o_hs = q_out_head_stride;
+    a.cos_sin = prep->cos_sin;
+    a.q_weight = prep->q_weight;
+    a.k_weight = prep->k_weight;
+    a.positions = prep->positions;
+    a.table_rows = prep->table_rows;
+    a.rot = static_cast<int>(prep->rot_dim);
+    a.interleaved = prep->interleaved != 0;
+    a.eps = prep->eps;
+    a.weight_offset = prep->weight_offset;
+    return moe::cuda_status(moe::launch_kv_append(a, static_cast<int>(batch->dtype), static_cast<cudaStream_t>(stream)), "kv_append");
+}
+
+MOE_API size_t moe_w4a8_paged_attention_workspace_size(const moe_kv_batch_t* batch) {
+    return check_sizes(batch) == MOE_OK ? attend_layout(batch).total : 0;
+}
+
+MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_tokens, const void* q, int64_t q_token_stride,
+                                     int64_t q_head_stride, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                                     float scale, int64_t window, void* workspace, size_t workspace_bytes, void* stream) {
+    if (int rc = check_batch(batch, n_tokens)) return rc;
+    if (!(scale > 0.f) || !std::isfinite(scale) || window < 0 || (lse && !aligned4(lse))) return MOE_ERR_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+    const AttendLayout L = attend_layout(batch);
+    if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (n_tokens == 0) return MOE_OK;
+    for (int rc : {check_rows(q, q_token_stride, q_head_stride), check_rows(out, out_token_stride, out_head_stride)})
+        if (rc) return rc;
+    moe::AttendArgs a{};
+    a.kv = kv_args(batch, n_tokens);
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.q_ts = q_token_stride;
+    a.q_hs = q_head_stride;
+    a.o_ts = out_token_stride;
+    a.o_hs = out_head_stride;
+    a.scale = scale;
+    a.window = static_cast<int>(std::min<int64_t>(window, kI32));
+    char* ws = static_cast<char*>(workspace);
+    a.recs = reinterpret_cast<moe::BoundaryRec*>(ws + L.recs);
+    a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+    a.part_o = reinterpret_cast<float*>(ws + L.o);
+    const int64_t tiles = (std::min(batch->max_q_len, n_tokens) * a.kv.group + moe::kSplitRows - 1) / moe::kSplitRows;
+    const int64_t items = std::min<int64_t>(batch->n_seqs * tiles * a.kv.hkv, int64_t(1) << 30);
+    const int64_t keys = std::min<int64_t>(std::min(batch->max_kv_len, window > 0 ? window + tiles * moe::kSplitRows : kI32), a.kv.cap);
+    a.split = keys > kWholeKeys;
+    return moe::cuda_status(moe::launch_attend_split(a, static_cast<int>(batch->dtype), L.n_ctas, static_cast<int>(items),
+                                                     static_cast<cudaStream_t>(stream)),
+                            "paged_attention");
+}

@@ -1,0 +1,292 @@
+// Device helpers shared by the attention kernels: element types, the ragged
+// batch, the deal of row tiles and key units over the grid, and the exact row.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attention.h"
+#include "common.cuh"
+
+namespace moe {
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+};
+template <>
+struct Elem<__half> {
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -INFINITY;
+
+// ---------------------------------------------------------------- the ragged batch
+struct SeqInfo {
+    int q0;     // first token
+    int q_len;
+    int pos0;   // position of the first token (may be negative)
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const KvArgs& a, int b) {
+    SeqInfo s;
+    const int e = min(max(__ldg(a.q_start + b + 1), 0), a.n_tokens);
+    s.q0 = min(max(__ldg(a.q_start + b), 0), a.n_tokens);
+    s.q_len = max(e - s.q0, 0);
+    s.pos0 = max(__ldg(a.kv_len + b), 0) - s.q_len;
+    return s;
+}
+
+// Page id of `idx` of sequence b, or -1 where there is none to read.
+__device__ __forceinline__ int page_id(const KvArgs& a, int b, int idx) {
+    if (idx >= a.width) return -1;
+    const int id = __ldg(a.table + static_cast<int64_t>(b) * a.width + idx);
+    return id >= 0 && id < a.n_pages ? id : -1;
+}
+
+// Keys [lo, hi) that rows [r0, r1) (row = token * group + head of the group) see, at least one of them.
+__device__ __forceinline__ void key_range(const KvArgs& a, int window, const SeqInfo& s, int r0, int r1, int& lo, int& hi) {
+    const int p0 = s.pos0 + r0 / a.group, p1 = s.pos0 + (r1 - 1) / a.group;
+    hi = min(p1, a.cap - 1) + 1;
+    lo = window > 0 ? max(p0 - window + 1, 0) : 0;
+    if (hi <= lo) lo = hi = 0;
+}
+
+// ---------------------------------------------------------------- the deal
+// The batch's work is a line of units: sequence by sequence, row tile by row tile (ROWS rows of one
+// sequence's token-major (token, head of the group) rows), key/value head by head, key unit by key
+// unit (KEYS consecutive positions).  CTA c takes units [c per, (c + 1) per), so the grid's shares
+// differ by one unit at most however ragged the batch is; a tile that a share's end cuts is finished
+// by the join.  A tile whose rows see nothing counts as one unit (its rows still have to be written).
+template <int ROWS, int KEYS>
+struct Deal {
+    static __device__ __forceinline__ int tiles(const KvArgs& a, const SeqInfo& s) {
+        return (s.q_len * a.group + ROWS - 1) / ROWS;
+    }
+    // First key unit and number of units of row tile rt.
+    static __device__ __forceinline__ int units(const AttendArgs& a, const SeqInfo& s, int rt, int& first) {
+        const int r1 = min((rt + 1) * ROWS, s.q_len * a.kv.group);
+        int lo, hi;
+        key_range(a.kv, a.window, s, rt * ROWS, r1, lo, hi);
+        first = lo / KEYS;
+        return max((hi + KEYS - 1) / KEYS - first, 1);
+    }
+};
+
+struct Cursor {
+    long long u, end;  // this CTA's next unit and its end
+    long long per;
+    int b, rt, h;      // the tile that unit `u` is in
+    int off;           // units of the tile before `u`
+    int first, n;      // the tile's first key unit and its number of units
+    SeqInfo s;
+};
+
+// Called by the whole block.  prefix: n_seqs + 1 shared words.  Sets `c` in every thread.
+template <int ROWS, int KEYS>
+__device__ void deal_begin(const AttendArgs& a, long long* prefix, long long min_per, Cursor& c) {
+    using D = Deal<ROWS, KEYS>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int B = a.kv.n_seqs;
+    for (int b = warp; b < B; b += warps) {
+        const SeqInfo s = seq_info(a.kv, b);
+        const int nt = D::tiles(a.kv, s);
+        long long sum = 0;
+        for (int rt = lane; rt < nt; rt += 32) {
+            int first;
+            sum += a.split ? D::units(a, s, rt, first) : 1;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) prefix[b + 1] = sum * a.kv.hkv;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long carry = 0;
+        if (lane == 0) prefix[0] = 0;
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            long long x = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b0 + lane < B) prefix[b0 + lane + 1] = x + carry;
+            carry += __shfl_sync(~0u, x, 31);
+        }
+    }
+    __syncthreads();
+    const long long total = prefix[B];
+    c.per = max((total + gridDim.x - 1) / gridDim.x, a.split ? min_per : 1LL);
+    c.u = min(static_cast<long long>(blockIdx.x) * c.per, total);
+    c.end = min(c.u + c.per, total);
+    c.b = c.rt = c.h = c.off = c.first = c.n = 0;
+    if (c.u >= c.end) return;
+    int lo = 0, hi = B - 1;  // the sequence that holds unit u: the last b with prefix[b] <= u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= c.u) lo = mid;
+        else hi = mid - 1;
+    }
+    c.b = lo;
+    c.s = seq_info(a.kv, lo);
+    const int nt = D::tiles(a.kv, c.s);
+    long long rel = c.u - prefix[lo];
+    for (int t0 = 0;; t0 += 32) {  // every warp walks the sequence's tiles, 32 at a time
+        int first = 0;
+        const int rt = t0 + lane;
+        const int n = rt < nt ? (a.split ? D::units(a, c.s, rt, first) : 1) : 0;
+        long long x = static_cast<long long>(n) * a.kv.hkv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
+        }
+        const unsigned past = __ballot_sync(~0u, x > rel);
+        if (past || t0 + 32 >= nt) {
+            const int l = past ? __ffs(past) - 1 : 31;
+            const long long before = __shfl_sync(~0u, x - static_cast<long long>(n) * a.kv.hkv, l);
+            const int nl = max(__shfl_sync(~0u, n, l), 1);
+            rel -= before;
+            c.rt = min(t0 + l, nt - 1);
+            c.h = static_cast<int>(rel / nl);
+            c.off = static_cast<int>(rel - static_cast<long long>(c.h) * nl);
+            break;
+        }
+        rel -= __shfl_sync(~0u, x, 31);
+    }
+    c.n = D::units(a, c.s, c.rt, c.first);
+}
+
+// Units of the current tile that are this CTA's.
+__device__ __forceinline__ int deal_take(const AttendArgs& a, const Cursor& c) {
+    return a.split ? static_cast<int>(min(static_cast<long long>(c.n - c.off), c.end - c.u)) : c.n;
+}
+
+// Past the current tile.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ void deal_next(const AttendArgs& a, Cursor& c, int taken) {
+    using D = Deal<ROWS, KEYS>;
+    c.u += a.split ? taken : 1;
+    c.off = 0;
+    if (c.u >= c.end) return;
+    if (++c.h < a.kv.hkv) return;
+    c.h = 0;
+    ++c.rt;
+    while (c.rt >= D::tiles(a.kv, c.s)) {  // ends at the sequence that holds unit u
+        c.s = seq_info(a.kv, ++c.b);
+        c.rt = 0;
+    }
+    c.n = D::units(a, c.s, c.rt, c.first);
+}
+
+// ---------------------------------------------------------------- the exact row
+// One (token, head) row over the positions it sees and no others, by one warp.  The tiled kernels
+// multiply the values of a masked position by a weight of zero, which is no zero where the value is
+// not finite; a row that ends with a NaN is therefore taken again here.  (A row whose NaN is its own
+// comes out the same.)
+template <typename T>
+__device__ __noinline__ void attend_row(const AttendArgs& a, int b, int token, int head, int pos) {
+    const int lane = threadIdx.x & 31;
+    const bool on = lane * 8 < a.kv.d;
+    const int hk = head / a.kv.group;
+    float q[8] = {}, o[8] = {};
+    if (on) {
+        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + token * a.q_ts + head * a.q_hs + lane * 8);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Elem<T>::unpack(ww[i]);
+            q[2 * i] = f.x;
+            q[2 * i + 1] = f.y;
+        }
+    }
+    const int hi = min(pos, a.kv.cap - 1) + 1;
+    const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const float c = a.scale * kLog2e;
+    float m = kNegInf, l = 0.f;
+    for (int j = lo; j < hi; ++j) {
+        const int id = page_id(a.kv, b, j / a.kv.page);
+        const int64_t row = j % a.kv.page;
+        uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
+        if (on && id >= 0) {
+            kw = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.k) + id * a.kv.k_ps + row * a.kv.k_rs + hk * a.kv.k_hs + lane * 8);
+            vw = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.v) + id * a.kv.v_ps + row * a.kv.v_rs + hk * a.kv.v_hs + lane * 8);
+        }
+        const uint32_t k4[4] = {kw.x, kw.y, kw.z, kw.w}, v4[4] = {vw.x, vw.y, vw.z, vw.w};
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Elem<T>::unpack(k4[i]);
+            s += q[2 * i] * f.x + q[2 * i + 1] * f.y;
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+        s *= c;
+        const float mn = fmaxf(m, s);  // a NaN score is not the maximum, but it reaches l below
+        const float base = mn == kNegInf ? 0.f : mn;
+        const float f = exp2f(m - base), p = exp2f(s - base);
+        m = mn;
+        l = l * f + p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 g = Elem<T>::unpack(v4[i]);
+            o[2 * i] = o[2 * i] * f + p * g.x;
+            o[2 * i + 1] = o[2 * i + 1] * f + p * g.y;
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (on) {
+        uint4 w;
+        w.x = Elem<T>::pack(o[0] * inv, o[1] * inv);
+        w.y = Elem<T>::pack(o[2] * inv, o[3] * inv);
+        w.z = Elem<T>::pack(o[4] * inv, o[5] * inv);
+        w.w = Elem<T>::pack(o[6] * inv, o[7] * inv);
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + lane * 8) = w;
+    }
+    if (lane == 0 && a.lse) a.lse[static_cast<int64_t>(token) * a.kv.hq + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+}
+
+// Rows of the tokens that belong to no sequence: zeros, and -inf.  Called by the whole grid.
+template <typename T>
+__device__ void clear_stray_rows(const AttendArgs& a) {
+    const int s0 = min(max(__ldg(a.kv.q_start), 0), a.kv.n_tokens);
+    const int s1 = min(max(__ldg(a.kv.q_start + a.kv.n_seqs), s0), a.kv.n_tokens);
+    const int stray = s0 + a.kv.n_tokens - s1;
+    if (stray == 0) return;
+    for (int i = blockIdx.x; i < stray; i += gridDim.x) {
+        const int t = i < s0 ? i : s1 + (i - s0);
+        const int chunks = a.kv.d / 8;
+        for (int x = threadIdx.x; x < a.kv.hq * chunks; x += blockDim.x)
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.o_ts + (x / chunks) * a.o_hs + (x % chunks) * 8) =
+                make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int x = threadIdx.x; x < a.kv.hq; x += blockDim.x) a.lse[static_cast<int64_t>(t) * a.kv.hq + x] = kNegInf;
+    }
+}
+
+}  // namespace moe

@@ -110,4 +110,7 @@ cudaError_t launch_requant_copy(const float* h, const uint32_t* amax, int64_t P,
 
 int num_sms();
 
+// MOE_OK, or MOE_ERR_CUDA with `what` and CUDA's message kept for moe_w4a8_last_error.
+int cuda_status(cudaError_t e, const char* what);
+
 }  // namespace moe
