@@ -17,6 +17,7 @@
 // shared memory.  The pieces are equal shares of all (sequence, head, 16 keys)
 // units of the batch (the deal), so ragged lengths balance; pieces of one row tile go
 // to the workspace and a second kernel joins them in a fixed order.
+#include "attend_join.cuh"
 #include "attention_common.cuh"
 
 namespace moe {
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
         __syncthreads();
     }
 
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
     Cursor c;
     deal_begin<kSplitRows, kKeys>(a, prefix, 16, c);
     if (a.split && threadIdx.x == 0) {
@@ -371,69 +373,6 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
     }
 }
 
-// The join of the pieces of the tiles that CTA boundaries cut.  Block c stands for the boundary
-// before CTA c + 1; a tile cut by several boundaries has its rows dealt over their blocks.  Pieces are
-// added in the order of their CTAs, whatever order they were finished in.
-template <typename T, int ROWS, int DH>
-__global__ void __launch_bounds__(DH) attend_join_kernel(const AttendArgs a) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int cta = blockIdx.x + 1;
-    const BoundaryRec rec = a.recs[cta];
-    if (!rec.cut) return;
-    const KvArgs& kv = a.kv;
-    const int lane = threadIdx.x & 31;
-    const int c0 = static_cast<int>(rec.begin / rec.per), c1 = static_cast<int>((rec.begin + rec.n - 1) / rec.per);
-    const SeqInfo s = seq_info(kv, rec.b);
-    const int r0 = rec.rt * ROWS, rows = min(s.q_len * kv.group - r0, ROWS);
-    __shared__ int bad;
-    for (int r = cta - (c0 + 1); r < rows; r += c1 - c0) {
-        // every warp finds the tile's maximum and sum for itself
-        float mm = kNegInf;
-        for (int p = c0 + lane; p <= c1; p += 32) {
-            const int64_t slot = 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1);
-            mm = fmaxf(mm, a.part_ml[slot * ROWS + r].x);
-        }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
-        const float base = mm == kNegInf ? 0.f : mm;
-        float ll = 0.f, acc = 0.f;
-        for (int p0 = c0; p0 <= c1; p0 += 32) {
-            float f = 0.f, lp = 0.f;
-            const int p = p0 + lane;
-            if (p <= c1) {
-                const int64_t slot = 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1);
-                const float2 v = a.part_ml[slot * ROWS + r];
-                f = exp2_fast(v.x - base);
-                lp = v.y * f;
-            }
-            const int n = min(32, c1 + 1 - p0);
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float fi = __shfl_sync(~0u, f, i);
-                ll += __shfl_sync(~0u, lp, i);
-                const int64_t slot = 2 * static_cast<int64_t>(p0 + i) + ((p0 + i) * rec.per >= rec.begin ? 0 : 1);
-                acc += a.part_o[(slot * ROWS + r) * DH + threadIdx.x] * fi;
-            }
-        }
-        const int tok = s.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
-        if (threadIdx.x == 0) bad = 0;
-        __syncthreads();
-        if (acc != acc || ll != ll) bad = 1;
-        __syncthreads();
-        if (bad) {
-            if (threadIdx.x < 32) attend_row<T>(a, rec.b, tok, head, s.pos0 + (r0 + r) / kv.group);
-        } else {
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            if (threadIdx.x < kv.d) {
-                const uint32_t w = Elem<T>::pack(acc * inv, 0.f);
-                reinterpret_cast<uint16_t*>(a.out)[tok * a.o_ts + head * a.o_hs + threadIdx.x] = static_cast<uint16_t>(w & 0xFFFF);
-            }
-            if (threadIdx.x == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
-        }
-        __syncthreads();
-    }
-}
-
 template <typename T, int DH, bool ALIGNED>
 cudaError_t launch_t(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
     using C = SplitCfg<DH>;
@@ -444,16 +383,7 @@ cudaError_t launch_t(const AttendArgs& a, int n_ctas, int max_items, cudaStream_
     attend_split_kernel<T, DH, ALIGNED><<<grid, C::kWarps * 32, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.split || grid < 2) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1);
-    cfg.blockDim = dim3(DH);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, kSplitRows, DH>, a);
+    return launch_attend_join<T, kSplitRows, DH, 8>(a, grid, st);
 }
 
 template <typename T, int DH>
@@ -463,7 +393,7 @@ cudaError_t launch_d(const AttendArgs& a, int n_ctas, int max_items, cudaStream_
 
 template <typename T>
 cudaError_t launch_e(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
-    switch (split_padded_dim(a.kv.d)) {
+    switch (padded_dim(a.kv.d)) {
         case 64: return launch_d<T, 64>(a, n_ctas, max_items, st);
         case 128: return launch_d<T, 128>(a, n_ctas, max_items, st);
         default: return launch_d<T, 256>(a, n_ctas, max_items, st);
@@ -471,8 +401,6 @@ cudaError_t launch_e(const AttendArgs& a, int n_ctas, int max_items, cudaStream_
 }
 
 }  // namespace
-
-int split_padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 cudaError_t launch_attend_split(const AttendArgs& a, int dtype, int n_ctas, int max_items, cudaStream_t st) {
     return dtype == 0 ? launch_e<__nv_bfloat16>(a, n_ctas, max_items, st) : launch_e<__half>(a, n_ctas, max_items, st);

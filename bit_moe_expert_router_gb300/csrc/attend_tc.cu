@@ -1,0 +1,615 @@
+// Attention over the paged cache on the fifth-generation tensor cores: the
+// engine of chunks and prompts (many rows against the same keys).
+//
+// The mathematics is attend_split.cu's: one pass over the keys with a running
+// reference m and sum l per row, s = scale q . k, p = 2^(s log2 e - m), o = sum p v,
+// the row is o / l.  Rows are (token, head of the group) pairs of one
+// key/value head, token-major, so a tile of 128 rows reads the cache once for
+// all heads of the group.
+//
+// Bound: the tensor pipe (4 D flops per pair and head) against the 2^x of the
+// special-function units and their surrounding instructions (one per pair and
+// head).  Per tile of 128 rows x 128 keys: S = Q K^T (operands in shared memory, 128 fp32
+// accumulator columns in tensor memory), a softmax warpgroup reads S (a thread
+// per row, so a row's maximum and sum need no exchange), writes P back over S as
+// packed 16-bit values, and O += P V takes P from tensor memory and V from shared
+// memory as an MN-major operand (rows of the cache are rows of K there, no transposition).
+//   D <= 128: two tiles of 128 rows per CTA share the keys' tiles; while one tile's
+//     softmax runs the tensor pipe does the other's products.
+//   D <= 256: one tile (O takes 256 of the 512 columns); S is double-buffered, so the
+//     tensor pipe does the next keys' S while the softmax of this one runs.
+// The reference m is raised, and O rescaled, only when a row's maximum has grown
+// by more than 2^8 over it: P stays below 2^8 (exact enough in 16 bits: the rounding is relative)
+// and almost every tile leaves O alone.
+//
+// K and V come by TMA straight from the pages (4-D map: component, row, head,
+// page; boxes of as many rows as divide both page and tile), into a ring of
+// slots; pages that are not there and rows past the last visible one read zeros, and
+// the rows of V behind it inside a box are cleared by hand, so whatever the cache holds there
+// stays out of the sums.  Work is dealt in equal shares of 128-key units; the pieces of a cut
+// tile go through the workspace and the join.
+//
+// Warps: 0 MMA issue (one thread) and the tensor-memory allocation, 1 the K and V
+// tiles, 2-3 nothing, then one warpgroup per row tile: Q into shared memory, softmax, output.
+// Every wait is bounded; a timeout sets the status word and every role leaves.
+#include <algorithm>
+
+#include "attend_join.cuh"
+#include "attention_common.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTcKeys = 128;  // keys of a unit
+
+template <int DH>
+struct TcCfg {
+    static constexpr int NQ = DH == 256 ? 1 : 2;        // row tiles per CTA
+    static constexpr int kRows = 128 * NQ;
+    static constexpr int kBlocks = DH / 64;             // 64-component column blocks
+    static constexpr int KS = DH == 256 ? 2 : 1;        // ring slots of a K or V tile
+    static constexpr int kKBlocks = kBlocks / KS;       // column blocks of a K slot (all 128 keys)
+    static constexpr int kVKeys = kTcKeys / KS;         // keys of a V slot (all column blocks)
+    static constexpr int kSlot = kTcKeys * DH * 2 / KS;
+    static constexpr int kSlots = DH == 256 ? 4 : DH == 128 ? 5 : 8;
+    static constexpr int kLook = NQ == 2 ? 1 : 2;       // K tiles ahead of V
+    static constexpr int kQTile = 128 * DH * 2;
+    static constexpr int kThreads = 128 + 128 * NQ;
+    static constexpr int kSCol = 0, kOCol = 256;        // two S (or P) buffers of 128 columns, then O
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffRing = kOffQ + NQ * kQTile;
+    static constexpr int kOffBars = kOffRing + kSlots * kSlot;
+    static constexpr int kBars = 2 * kSlots + 6 + 2 * NQ + 2;
+    static constexpr int kOffMisc = kOffBars + 8 * kBars;
+    static constexpr int kSmem = kOffMisc + 16 + 1024;
+    static_assert(kOCol + NQ * DH <= 512, "tensor-memory columns");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+template <typename T>
+struct MmaFmt;
+template <>
+struct MmaFmt<__nv_bfloat16> {
+    static constexpr uint32_t v = 1;
+};
+template <>
+struct MmaFmt<__half> {
+    static constexpr uint32_t v = 0;
+};
+
+// kind::f16 instruction descriptor: fp32 accumulator, A and B of one type, M = 128, N = n; b_mn: B is MN-major.
+template <typename T>
+__device__ constexpr uint32_t idesc16(int n, bool b_mn) {
+    return (1u << 4) | (MmaFmt<T>::v << 7) | (MmaFmt<T>::v << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
+    attend_tc_kernel(const AttendArgs a, int box_rows, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+    using C = TcCfg<DH>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
+    uint64_t* full = bars;                    // [slots] the slot's bytes have landed
+    uint64_t* empty = full + C::kSlots;       // [slots] MMA commit: the slot is read
+    uint64_t* s_full = empty + C::kSlots;     // [2] MMA commit: S is there
+    uint64_t* p_full = s_full + 2;            // [2] four softmax warps: P is there, S is read
+    uint64_t* q_full = p_full + 2;            // [NQ] the warpgroup's threads: Q is in shared memory
+    uint64_t* o_done = q_full + C::NQ;        // [2] MMA commit: P V is added (by P's buffer)
+    uint64_t* o_free = o_done + 2;            // [NQ] four softmax warps: the tile's O is read
+    uint64_t* tail = o_free + C::NQ;          // the bytes of a V slot that is cleared by hand
+    uint64_t* done = tail + 1;                // MMA commit: everything issued has finished
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const KvArgs& kv = a.kv;
+    const Ctl ctl{abort_flag, a.hdr};
+
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(o_done + i, 1);
+        }
+        for (int i = 0; i < C::NQ; ++i) {
+            mbar_init(q_full + i, 128);
+            mbar_init(o_free + i, 4);
+        }
+        mbar_init(tail, 1);
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        if (blockIdx.x == 0) a.hdr->status = kDevOk;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tmem_holder)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    Cursor c;
+    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, c);  // (scratch: the ring)
+    if (a.split && tid == 0) {
+        BoundaryRec r;
+        r.begin = c.u - c.off;
+        r.per = c.per;
+        r.n = c.n;
+        r.cut = c.u < c.end && c.off > 0;
+        r.b = c.b;
+        r.rt = c.rt;
+        r.h = c.h;
+        r.pad = 0;
+        a.recs[blockIdx.x] = r;
+    }
+    clear_stray_rows<T>(a);
+    tc_fence_before();
+    fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const uint32_t ring = smem_u32(smem + C::kOffRing);
+    const long long u_begin = c.u;
+    bool ok = true;
+
+    if (warp < 4) {
+        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------------ MMA issue
+            const uint32_t q0 = smem_u32(smem + C::kOffQ);
+            int use = 0;                      // ring slots taken so far
+            uint32_t tiles[2] = {0, 0};       // S buffers: uses so far
+            uint32_t items[2] = {0, 0};       // row tiles finished so far, by warpgroup
+            auto qk = [&](int w, int buf, int slot_use) {  // S[buf] = Q[w] K^T
+#pragma unroll
+                for (int k = 0; k < DH / 16; ++k) {
+                    const int blk = k / 4, s = (slot_use + blk / C::kKBlocks) % C::kSlots;
+                    mma_f16_ss(tmem + C::kSCol + 128 * buf, sdesc(q0 + w * C::kQTile + blk * 16384 + (k % 4) * 32),
+                               sdesc(ring + s * C::kSlot + (blk % C::kKBlocks) * 16384 + (k % 4) * 32), idesc16<T>(128, false), k > 0);
+                }
+                mma_commit(s_full + buf);
+            };
+            auto pv = [&](int w, int buf, int slot_use, bool first) {  // O[w] (+)= P[buf] V
+#pragma unroll
+                for (int k = 0; k < kTcKeys / 16; ++k) {
+                    const int s = (slot_use + k * 16 / C::kVKeys) % C::kSlots;
+                    mma_f16_ta(tmem + C::kOCol + DH * w, tmem + C::kSCol + 128 * buf + 8 * k,
+                               sdesc_mn(ring + s * C::kSlot + (k * 16 % C::kVKeys) * 128, C::kVKeys * 128), idesc16<T>(DH, true), !first || k > 0);
+                }
+                mma_commit(o_done + buf);
+            };
+            auto landed = [&](int slot_use) {
+                for (int i = 0; i < C::KS && ok; ++i) {
+                    const int u = slot_use + i;
+                    ok = wait_bar(full + u % C::kSlots, (u / C::kSlots) & 1, ctl);
+                }
+            };
+            auto release = [&](int slot_use) {
+                for (int i = 0; i < C::KS; ++i) mma_commit(empty + (slot_use + i) % C::kSlots);
+            };
+            while (ok && c.u < c.end) {
+                const int n = deal_take(a, c);
+                const int rows = min(c.s.q_len * kv.group - c.rt * C::kRows, C::kRows);
+                const int act = C::NQ == 2 && rows > 128 ? 2 : 1;
+                for (int w = 0; w < act && ok; ++w) ok = wait_bar(q_full + w, items[w] & 1, ctl);
+                if (!ok) break;
+                tc_fence_after();
+                if constexpr (C::NQ == 2) {
+                    // slots: K0, then V(j), K(j + 1)
+                    landed(use);
+                    if (!ok) break;
+                    for (int w = 0; w < act; ++w) qk(w, w, use);
+                    release(use);
+                    use += C::KS;
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int vs = use, ks = use + C::KS;
+                        landed(vs);
+                        if (j + 1 < n) landed(ks);
+                        for (int w = 0; w < act && ok; ++w) {
+                            ok = wait_bar(p_full + w, tiles[w] & 1, ctl);
+                            if (ok && j == 0) ok = wait_bar(o_free + w, (items[w] & 1) ^ 1, ctl);
+                            if (!ok) break;
+                            ++tiles[w];
+                            tc_fence_after();
+                            pv(w, w, vs, j == 0);
+                            if (w == act - 1) release(vs);
+                            if (j + 1 < n) qk(w, w, ks);
+                        }
+                        if (!ok) break;
+                        use += C::KS;
+                        if (j + 1 < n) {
+                            release(ks);
+                            use += C::KS;
+                        }
+                    }
+                } else {
+                    // slots: K0, K1, then V(j), K(j + 2); S buffers alternate over all tiles
+                    for (int j = 0; j < min(n, 2) && ok; ++j) {
+                        landed(use);
+                        if (!ok) break;
+                        qk(0, (tiles[0] + j) & 1, use);
+                        release(use);
+                        use += C::KS;
+                    }
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int buf = tiles[0] & 1;
+                        landed(use);
+                        if (ok) ok = wait_bar(p_full + buf, (tiles[0] >> 1) & 1, ctl);
+                        if (ok && j == 0) ok = wait_bar(o_free, (items[0] & 1) ^ 1, ctl);
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(0, buf, use, j == 0);
+                        release(use);
+                        use += C::KS;
+                        ++tiles[0];
+                        if (j + 2 < n) {
+                            landed(use);
+                            if (!ok) break;
+                            qk(0, buf, use);
+                            release(use);
+                            use += C::KS;
+                        }
+                    }
+                }
+                for (int w = 0; w < act; ++w) ++items[w];
+                deal_next<C::kRows, kTcKeys>(a, c, n);
+            }
+            mma_commit(done);
+            drain_bar(done, 0);
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ K and V tiles
+            int use = 0;
+            uint32_t tails = 0;
+            const int boxes = kTcKeys / box_rows;  // <= 16; lane i brings box i of a tile
+            int lo, hi;
+            auto where = [&](int unit, int& row, int& page) {  // this lane's box of tile `unit`
+                const int key = unit * kTcKeys + lane * box_rows;
+                page = kv.n_pages;  // outside the map: zeros
+                row = 0;
+                if (lane < boxes && key < hi) {
+                    const int p = key / kv.page, id = page_id(kv, c.b, p);
+                    row = key - p * kv.page;
+                    if (id >= 0) page = id;
+                }
+            };
+            auto claim = [&]() {
+                ok = __all_sync(~0u, wait_bar(empty + use % C::kSlots, ((use / C::kSlots) & 1) ^ 1, ctl));
+                return use % C::kSlots;
+            };
+            auto load_k = [&](int unit) {
+                int row, page;
+                where(unit, row, page);
+#pragma unroll
+                for (int i = 0; i < C::KS; ++i) {
+                    const int s = claim();
+                    if (!ok) return;
+                    if (lane == 0) mbar_expect_tx(full + s, C::kSlot);
+                    __syncwarp();
+                    if (lane < boxes)
+#pragma unroll
+                        for (int b = 0; b < C::kKBlocks; ++b)
+                            tma_tile4d(ring + s * C::kSlot + b * 16384 + lane * box_rows * 128, &kmap, (i * C::kKBlocks + b) * 64, row, c.h, page,
+                                       full + s);
+                    ++use;
+                }
+            };
+            auto load_v = [&](int unit) {
+                int row, page;
+                where(unit, row, page);
+#pragma unroll
+                for (int i = 0; i < C::KS; ++i) {
+                    const int s = claim();
+                    if (!ok) return;
+                    const int key0 = unit * kTcKeys + i * C::kVKeys;
+                    const int last = hi - key0;  // rows that some row of the tile sees
+                    const bool cut = last > 0 && last < C::kVKeys && last % box_rows != 0;
+                    uint64_t* bar = cut ? tail : full + s;
+                    if (lane == 0) mbar_expect_tx(bar, C::kSlot);
+                    __syncwarp();
+                    const int first = lane * box_rows - i * C::kVKeys;  // the box's first row in this slot
+                    if (lane < boxes && first >= 0 && first < C::kVKeys)
+#pragma unroll
+                        for (int b = 0; b < C::kBlocks; ++b)
+                            tma_tile4d(ring + s * C::kSlot + b * (C::kVKeys * 128) + first * 128, &vmap, b * 64, row, c.h, page, bar);
+                    if (cut) {  // the box's rows behind the last visible one
+                        ok = __all_sync(~0u, wait_bar(tail, tails & 1, ctl));
+                        if (!ok) return;
+                        ++tails;
+                        const int end = (last + box_rows - 1) / box_rows * box_rows;
+                        const int per = (end - last) * 8;
+                        for (int x = lane; x < per * C::kBlocks; x += 32) {
+                            const int b = x / per, y = x - b * per;
+                            *reinterpret_cast<uint4*>(smem + C::kOffRing + s * C::kSlot + b * (C::kVKeys * 128) + last * 128 + y * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_proxy();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full + s);
+                    }
+                    ++use;
+                }
+            };
+            while (ok && c.u < c.end) {
+                const int n = deal_take(a, c);
+                const int r0 = c.rt * C::kRows;
+                key_range(kv, a.window, c.s, r0, min(r0 + C::kRows, c.s.q_len * kv.group), lo, hi);
+                const int unit0 = c.first + c.off;
+                for (int j = 0; j < min(n, C::kLook) && ok; ++j) load_k(unit0 + j);
+                for (int j = 0; j < n && ok; ++j) {
+                    load_v(unit0 + j);
+                    if (ok && j + C::kLook < n) load_k(unit0 + j + C::kLook);
+                }
+                deal_next<C::kRows, kTcKeys>(a, c, n);
+            }
+            // every copy issued above lands before the CTA leaves (a cut slot's bytes are counted on
+            // `tail`, and have been waited for)
+            for (int u = max(use - C::kSlots, 0); u < use; ++u) drain_bar(full + u % C::kSlots, (u / C::kSlots) & 1);
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax, one row per thread
+        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+        const int w = (warp - 4) / 4;               // the warpgroup's row tile
+        const int row = (tid & 127);                // tile row = tensor-memory lane
+        const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t o_col = tmem + lane_base + C::kOCol + DH * w;
+        const float sc = a.scale * kLog2e;
+        uint8_t* sq = smem + C::kOffQ + w * C::kQTile;
+        uint32_t tiles = 0;                         // key tiles of this warpgroup so far
+        // Tile t's S, P and P V: which buffer, and which phase of its barriers.  (One tile per CTA: P V of two
+        // tiles can be under way when this warpgroup has stored the second P, so they need a barrier each.)
+        auto buf_of = [&](uint32_t t) { return C::NQ == 2 ? w : static_cast<int>(t & 1); };
+        auto phase_of = [&](uint32_t t) { return (C::NQ == 2 ? t : t >> 1) & 1; };
+        const int chunks = kv.d / 8;
+        while (ok && c.u < c.end) {
+            const int n = deal_take(a, c);
+            const int r0 = c.rt * C::kRows + 128 * w;
+            const int rows = min(c.s.q_len * kv.group - r0, 128);  // of this warpgroup
+            if (rows <= 0) {
+                deal_next<C::kRows, kTcKeys>(a, c, n);
+                continue;
+            }
+            // Q: chunk x of row r at its swizzled place; zeros past the rows and past D
+            for (int i = row; i < 128 * (DH / 8); i += 128) {
+                const int r = i / (DH / 8), x = i % (DH / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < rows && x < chunks) {
+                    const int tok = c.s.q0 + (r0 + r) / kv.group, head = c.h * kv.group + (r0 + r) % kv.group;
+                    v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + x * 8);
+                }
+                *reinterpret_cast<uint4*>(sq + (x / 8) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) << 4)) = v;
+            }
+            fence_async_proxy();
+            mbar_arrive(q_full + w);
+
+            const bool mine = row < rows;
+            const bool live = (row & ~31) < rows;   // some row of the warp is one
+            const int tok_i = (r0 + min(row, rows - 1)) / kv.group;
+            const int pos = c.s.pos0 + tok_i;
+            const int p_hi = min(pos, kv.cap - 1);
+            const int p_lo = a.window > 0 ? pos - a.window : -1;
+            float m = kNegInf;                       // the reference, in units of S
+            uint64_t l2 = pair(0.f, 0.f);
+            for (int j = 0; j < n; ++j, ++tiles) {
+                const int buf = buf_of(tiles);
+                ok = __all_sync(~0u, wait_bar(s_full + buf, phase_of(tiles), ctl));
+                if (!ok) break;
+                if (live) {
+                    tc_fence_after();
+                    uint32_t v[128];
+                    const uint32_t s_col = tmem + lane_base + C::kSCol + 128 * buf;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, v + 32 * i);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_tie32(v + 32 * i);
+                    const int key0 = (c.first + c.off + j) * kTcKeys;
+                    const int rel_hi = p_hi - key0, rel_lo = p_lo - key0;
+                    if (__any_sync(~0u, rel_hi < kTcKeys - 1 || rel_lo >= 0)) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i > rel_hi || i <= rel_lo) v[i] = __float_as_uint(kNegInf);
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(v[i]);
+#pragma unroll
+                    for (int i = 4; i < 128; i += 8) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mx[x] = fmaxf(mx[x], i + 4 + x < 128 ? fmaxf(__uint_as_float(v[i + x]), __uint_as_float(v[i + 4 + x])) : __uint_as_float(v[i + x]));
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    // (with m = -inf the difference is inf, or NaN if the row has seen nothing yet)
+                    const bool grew = (top - m) * sc > 8.f;
+                    if (j == 0) {
+                        m = top;
+                    } else if (__any_sync(~0u, grew)) {
+                        // O is rescaled between the products: the one before has to be there
+                        ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float f = grew ? (m == kNegInf ? 0.f : exp2_fast((m - top) * sc)) : 1.f;
+                        if (grew) m = top;
+                        const uint64_t f2 = pair(f, f);
+                        l2 = mul2(l2, f2);
+#pragma unroll 1
+                        for (int i = 0; i < DH; i += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(o_col + i, o);
+                            tmem_ld_wait();
+                            tmem_tie32(o);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tmem_st32(o_col + i, o);
+                        }
+                    }
+                    const float base = m == kNegInf ? 0.f : m * sc;
+                    const uint64_t sc2 = pair(sc, sc), nb2 = pair(-base, -base);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int e = 64 * h + 2 * i;
+                            const float2 x = unpair(fma2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nb2));
+                            const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
+                            l2 = add2(l2, pair(p0, p1));
+                            pk[i] = Elem<T>::pack(p0, p1);  // the product's operand: 16 bits; the sum l is of the fp32 values
+                        }
+                        tmem_st32(s_col + 32 * h, pk);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + buf);
+            }
+            if (!ok) break;
+            // ------------------------------------------------------------ the tile's output
+            ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
+            if (!ok) break;
+            tc_fence_after();
+            const bool whole = n == c.n;
+            const float2 lp = unpair(l2);
+            const float l = lp.x + lp.y;
+            const int tok = c.s.q0 + tok_i, head = c.h * kv.group + (r0 + min(row, rows - 1)) % kv.group;
+            bool bad = l != l;
+            if (live) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs;
+                const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (c.u == u_begin ? 0 : 1)) * C::kRows + 128 * w + row;
+                float* pdst = a.part_o + prow * DH;
+#pragma unroll 1
+                for (int i = 0; i < DH; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_col + i, o);
+                    tmem_ld_wait();
+                    tmem_tie32(o);
+                    if (!mine) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) bad |= __uint_as_float(o[x]) != __uint_as_float(o[x]);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 8)
+                            if (i + x < kv.d) {
+                                uint4 u;
+                                u.x = Elem<T>::pack(__uint_as_float(o[x]) * inv, __uint_as_float(o[x + 1]) * inv);
+                                u.y = Elem<T>::pack(__uint_as_float(o[x + 2]) * inv, __uint_as_float(o[x + 3]) * inv);
+                                u.z = Elem<T>::pack(__uint_as_float(o[x + 4]) * inv, __uint_as_float(o[x + 5]) * inv);
+                                u.w = Elem<T>::pack(__uint_as_float(o[x + 6]) * inv, __uint_as_float(o[x + 7]) * inv);
+                                *reinterpret_cast<uint4*>(dst + i + x) = u;
+                            }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) *reinterpret_cast<uint4*>(pdst + i + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    }
+                }
+                if (mine) {
+                    if (!whole) a.part_ml[prow] = make_float2(m == kNegInf ? kNegInf : m * sc, l);
+                    else if (a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = l == 0.f ? kNegInf : (m * sc + log2f(l)) * kLn2;
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free + w);
+            unsigned again = __ballot_sync(~0u, whole && mine && bad);
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                attend_row<T>(a, c.b, __shfl_sync(~0u, tok, src), __shfl_sync(~0u, head, src), __shfl_sync(~0u, pos, src));
+            }
+            deal_next<C::kRows, kTcKeys>(a, c, n);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512));
+    }
+}
+
+// The cache [pages][page_size][heads][D] as a 4-D map (component, row, head, page), boxes of 64 components x
+// `box` rows in 128-byte-swizzled rows.  Anything outside reads zeros: components past D, the page past the last.
+cudaError_t make_map(const KvArgs& kv, const void* base, int64_t ps, int64_t rs, int64_t hs, int dtype, int box, CUtensorMap* map) {
+    Encode encode = nullptr;
+    if (cudaError_t e = get_encode(&encode); e != cudaSuccess) return e;
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.d), static_cast<cuuint64_t>(kv.page), static_cast<cuuint64_t>(kv.hkv),
+                                static_cast<cuuint64_t>(kv.n_pages)};
+    auto bytes = [](int64_t s, int64_t n) { return static_cast<cuuint64_t>(n > 1 ? 2 * s : 16); };  // (a size of one has no stride)
+    const cuuint64_t strides[3] = {bytes(rs, kv.page), bytes(hs, kv.hkv), bytes(ps, kv.n_pages)};
+    const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1};
+    const CUresult r = encode(map, dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims,
+                              strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename T, int DH>
+cudaError_t launch_t(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st) {
+    using C = TcCfg<DH>;
+    const int box = std::min(tc_box_rows(a.kv.page), C::kVKeys);
+    CUtensorMap kmap, vmap;
+    if (cudaError_t e = make_map(a.kv, a.kv.k, a.kv.k_ps, a.kv.k_rs, a.kv.k_hs, dtype, box, &kmap); e != cudaSuccess) return e;
+    if (cudaError_t e = make_map(a.kv, a.kv.v, a.kv.v_ps, a.kv.v_rs, a.kv.v_hs, dtype, box, &vmap); e != cudaSuccess) return e;
+    cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attend_tc_kernel<T, DH><<<n_ctas, C::kThreads, C::kSmem, st>>>(a, box, kmap, vmap);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || n_ctas < 2) return e;
+    return launch_attend_join<T, C::kRows, DH, 1>(a, n_ctas, st);
+}
+
+template <typename T>
+cudaError_t launch_e(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st) {
+    switch (padded_dim(a.kv.d)) {
+        case 64: return launch_t<T, 64>(a, dtype, n_ctas, st);
+        case 128: return launch_t<T, 128>(a, dtype, n_ctas, st);
+        default: return launch_t<T, 256>(a, dtype, n_ctas, st);
+    }
+}
+
+}  // namespace
+
+int tc_box_rows(int page) { return std::min(page & -page, kTcKeys); }
+int tc_rows(int d) { return padded_dim(d) == 256 ? TcCfg<256>::kRows : TcCfg<128>::kRows; }
+
+cudaError_t launch_attend_tc(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st) {
+    return dtype == 0 ? launch_e<__nv_bfloat16>(a, dtype, n_ctas, st) : launch_e<__half>(a, dtype, n_ctas, st);
+}
+
+}  // namespace moe

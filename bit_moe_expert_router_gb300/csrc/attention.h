@@ -7,6 +7,8 @@
 
 namespace moe {
 
+struct Header;
+
 // A paged cache and its ragged batch, as the kernels take it.
 struct KvArgs {
     void* k;
@@ -43,6 +45,7 @@ struct AttendArgs {
     float scale;
     int window;                // 0: none
     int split;                 // pieces of a row tile may go to several CTAs
+    Header* hdr;               // workspace: the status word
     struct BoundaryRec* recs;  // workspace: one per CTA
     float* part_o;             // [2 * CTAs][tile rows][padded D]
     float2* part_ml;           // [2 * CTAs][tile rows]: running maximum (base 2), sum
@@ -59,9 +62,16 @@ struct BoundaryRec {
 
 cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t st);
 
+// Head sizes are padded to one of three.
+inline int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
 // Attention on mma.sync with the keys split over the warps of the GPU.
 constexpr int kSplitRows = 16;
-int split_padded_dim(int d);
 cudaError_t launch_attend_split(const AttendArgs& a, int dtype, int n_ctas, int max_items, cudaStream_t st);
+
+// Attention on tcgen05; pages of a multiple of 8 positions.
+int tc_box_rows(int page);  // rows of a page that one TMA box takes
+int tc_rows(int d);         // rows of a tile
+cudaError_t launch_attend_tc(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st);
 
 }  // namespace moe

@@ -84,24 +84,35 @@ moe::KvArgs kv_args(const moe_kv_batch_t* b, int64_t n_tokens) {
     return a;
 }
 
-// Workspace of attend: boundary records, then the pieces' sums and accumulators.
+// Workspace of attend: the status word, boundary records, then the pieces' sums and accumulators (laid out
+// for the engine with the larger row tiles; the other uses the front of each).
 struct AttendLayout {
-    int n_ctas, rows, dim;
-    size_t recs, ml, o, total;
+    int n_ctas;
+    size_t hdr, recs, ml, o, total;
 };
 
 AttendLayout attend_layout(const moe_kv_batch_t* b) {
     AttendLayout L{};
     L.n_ctas = moe::num_sms();
-    L.rows = moe::kSplitRows;
-    L.dim = moe::split_padded_dim(static_cast<int>(b->head_dim));
+    const int d = static_cast<int>(b->head_dim);
+    const size_t rows = 2 * static_cast<size_t>(L.n_ctas) * std::max(moe::kSplitRows, moe::tc_rows(d));
     size_t at = 0;
     auto take = [&](size_t bytes) { size_t here = at; at = (at + bytes + 255) & ~size_t(255); return here; };
+    L.hdr = take(sizeof(moe::Header));
     L.recs = take(sizeof(moe::BoundaryRec) * L.n_ctas);
-    L.ml = take(sizeof(float2) * 2 * L.n_ctas * L.rows);
-    L.o = take(sizeof(float) * 2 * L.n_ctas * L.rows * L.dim);
+    L.ml = take(sizeof(float2) * rows);
+    L.o = take(sizeof(float) * rows * moe::padded_dim(d));
     L.total = at;
     return L;
+}
+
+// The tcgen05 engine takes batches whose row tiles fill more than one tile of the split engine, from pages that
+// TMA boxes of whole 8-row groups divide.
+bool use_tc(const moe_kv_batch_t* b, int64_t rows) {
+    if (rows <= moe::kSplitRows || moe::tc_box_rows(static_cast<int>(b->page_size)) < 8) return false;
+    for (int64_t s : {b->k_page_stride, b->k_row_stride, b->k_head_stride, b->v_page_stride, b->v_row_stride, b->v_head_stride})
+        if (s == 0 || s >= int64_t(1) << 39) return false;  // what a tensor map can hold
+    return true;
 }
 
 // Up to this many positions a row tile stays with one CTA: the pieces' way through memory and the second
@@ -179,10 +190,17 @@ MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_toke
     a.scale = scale;
     a.window = static_cast<int>(std::min<int64_t>(window, kI32));
     char* ws = static_cast<char*>(workspace);
+    a.hdr = moe::ws_at<moe::Header>(workspace, L.hdr);
     a.recs = reinterpret_cast<moe::BoundaryRec*>(ws + L.recs);
     a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
     a.part_o = reinterpret_cast<float*>(ws + L.o);
-    const int64_t tiles = (std::min(batch->max_q_len, n_tokens) * a.kv.group + moe::kSplitRows - 1) / moe::kSplitRows;
+    const int64_t rows = std::min(batch->max_q_len, n_tokens) * a.kv.group;
+    if (use_tc(batch, rows)) {
+        a.split = 1;
+        return moe::cuda_status(moe::launch_attend_tc(a, static_cast<int>(batch->dtype), L.n_ctas, static_cast<cudaStream_t>(stream)),
+                                "paged_attention");
+    }
+    const int64_t tiles = (rows + moe::kSplitRows - 1) / moe::kSplitRows;
     const int64_t items = std::min<int64_t>(batch->n_seqs * tiles * a.kv.hkv, int64_t(1) << 30);
     const int64_t keys = std::min<int64_t>(std::min(batch->max_kv_len, window > 0 ? window + tiles * moe::kSplitRows : kI32), a.kv.cap);
     a.split = keys > kWholeKeys;
