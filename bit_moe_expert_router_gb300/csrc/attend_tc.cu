@@ -29,8 +29,8 @@
 // stays out of the sums.  Work is dealt in equal shares of 128-key units; the pieces of a cut
 // tile go through the workspace and the join.
 //
-// Warps: 0 MMA issue (one thread) and the tensor-memory allocation, 1 the K and V
-// tiles, 2-3 nothing, then one warpgroup per row tile: Q into shared memory, softmax, output.
+// Warps: 0 MMA issue (one lane) and the tensor-memory allocation, 1 the K and V
+// tiles, 2-3 Q, then one warpgroup per row tile: softmax and output.
 // Every wait is bounded; a timeout sets the status word and every role leaves.
 #include <algorithm>
 
@@ -60,7 +60,7 @@ struct TcCfg {
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = kOffQ + NQ * kQTile;
     static constexpr int kOffBars = kOffRing + kSlots * kSlot;
-    static constexpr int kBars = 2 * kSlots + 6 + 2 * NQ + 2;
+    static constexpr int kBars = 2 * kSlots + 6 + 3 * NQ + 2;
     static constexpr int kOffMisc = kOffBars + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 16 + 1024;
     static_assert(kOCol + NQ * DH <= 512, "tensor-memory columns");
@@ -124,8 +124,9 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     uint64_t* empty = full + C::kSlots;       // [slots] MMA commit: the slot is read
     uint64_t* s_full = empty + C::kSlots;     // [2] MMA commit: S is there
     uint64_t* p_full = s_full + 2;            // [2] four softmax warps: P is there, S is read
-    uint64_t* q_full = p_full + 2;            // [NQ] the warpgroup's threads: Q is in shared memory
-    uint64_t* o_done = q_full + C::NQ;        // [2] MMA commit: P V is added (by P's buffer)
+    uint64_t* q_full = p_full + 2;            // [NQ] the Q warps: Q is in shared memory
+    uint64_t* q_free = q_full + C::NQ;        // [NQ] MMA commit: the tile's last S is there
+    uint64_t* o_done = q_free + C::NQ;        // [2] MMA commit: P V is added (by P's buffer)
     uint64_t* o_free = o_done + 2;            // [NQ] four softmax warps: the tile's O is read
     uint64_t* tail = o_free + C::NQ;          // the bytes of a V slot that is cleared by hand
     uint64_t* done = tail + 1;                // MMA commit: everything issued has finished
@@ -147,7 +148,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             mbar_init(o_done + i, 1);
         }
         for (int i = 0; i < C::NQ; ++i) {
-            mbar_init(q_full + i, 128);
+            mbar_init(q_full + i, 2 / C::NQ);
+            mbar_init(q_free + i, 1);
             mbar_init(o_free + i, 4);
         }
         mbar_init(tail, 1);
@@ -186,107 +188,131 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 
     if (warp < 4) {
         if constexpr (C::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ------------------------------------------------------------ MMA issue
-            const uint32_t q0 = smem_u32(smem + C::kOffQ);
-            int use = 0;                      // ring slots taken so far
-            uint32_t tiles[2] = {0, 0};       // S buffers: uses so far
-            uint32_t items[2] = {0, 0};       // row tiles finished so far, by warpgroup
-            auto qk = [&](int w, int buf, int slot_use) {  // S[buf] = Q[w] K^T
+            const bool leader = elect_one();
+            const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(ring), vd = sdesc_mn(ring, C::kVKeys * 128);
+            int slot = 0;                     // the next ring slot of K or V,
+            uint32_t phase = 0;               // and the phase of its barrier
+            uint32_t tiles[2] = {0, 0};       // key tiles so far, by warpgroup
+            uint32_t items[2] = {0, 0};       // row tiles so far, by warpgroup
+            auto qk = [&](int w, int buf, int s) {  // S[buf] = Q[w] K^T, K in slots s ..
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < DH / 16; ++k) {
-                    const int blk = k / 4, s = (slot_use + blk / C::kKBlocks) % C::kSlots;
-                    mma_f16_ss(tmem + C::kSCol + 128 * buf, sdesc(q0 + w * C::kQTile + blk * 16384 + (k % 4) * 32),
-                               sdesc(ring + s * C::kSlot + (blk % C::kKBlocks) * 16384 + (k % 4) * 32), idesc16<T>(128, false), k > 0);
+                    for (int k = 0; k < DH / 16; ++k) {
+                        const int blk = k / 4;
+                        mma_f16_ss(tmem + C::kSCol + 128 * buf, qd + ((w * C::kQTile + blk * 16384 + (k % 4) * 32) >> 4),
+                                   kd + ((s * C::kSlot + blk / C::kKBlocks * C::kSlot + blk % C::kKBlocks * 16384 + (k % 4) * 32) >> 4),
+                                   idesc16<T>(128, false), k > 0);
+                    }
+                    mma_commit(s_full + buf);
                 }
-                mma_commit(s_full + buf);
+                __syncwarp();
             };
-            auto pv = [&](int w, int buf, int slot_use, bool first) {  // O[w] (+)= P[buf] V
+            auto pv = [&](int w, int buf, int s, bool first) {  // O[w] (+)= P[buf] V, V in slots s ..
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < kTcKeys / 16; ++k) {
-                    const int s = (slot_use + k * 16 / C::kVKeys) % C::kSlots;
-                    mma_f16_ta(tmem + C::kOCol + DH * w, tmem + C::kSCol + 128 * buf + 8 * k,
-                               sdesc_mn(ring + s * C::kSlot + (k * 16 % C::kVKeys) * 128, C::kVKeys * 128), idesc16<T>(DH, true), !first || k > 0);
+                    for (int k = 0; k < kTcKeys / 16; ++k)
+                        mma_f16_ta(tmem + C::kOCol + DH * w, tmem + C::kSCol + 128 * buf + 8 * k,
+                                   vd + ((s * C::kSlot + k * 16 / C::kVKeys * C::kSlot + k * 16 % C::kVKeys * 128) >> 4), idesc16<T>(DH, true),
+                                   !first || k > 0);
+                    mma_commit(o_done + buf);
                 }
-                mma_commit(o_done + buf);
+                __syncwarp();
             };
-            auto landed = [&](int slot_use) {
-                for (int i = 0; i < C::KS && ok; ++i) {
-                    const int u = slot_use + i;
-                    ok = wait_bar(full + u % C::kSlots, (u / C::kSlots) & 1, ctl);
-                }
+            auto landed = [&](int s, uint32_t ph) {
+#pragma unroll
+                for (int i = 0; i < C::KS; ++i) ok = ok && wait_bar(full + s + i, ph, ctl);
+                ok = __all_sync(~0u, ok);
             };
-            auto release = [&](int slot_use) {
-                for (int i = 0; i < C::KS; ++i) mma_commit(empty + (slot_use + i) % C::kSlots);
+            auto commit = [&](uint64_t* bar, int n) {
+                if (leader)
+                    for (int i = 0; i < n; ++i) mma_commit(bar + i);
+                __syncwarp();
+            };
+            auto wait = [&](uint64_t* bar, uint32_t ph) { ok = __all_sync(~0u, ok && wait_bar(bar, ph, ctl)); };
+            auto advance = [&]() {
+                slot += C::KS;
+                if (slot == C::kSlots) slot = 0, phase ^= 1;
             };
             while (ok && c.u < c.end) {
                 const int n = deal_take(a, c);
                 const int rows = min(c.s.q_len * kv.group - c.rt * C::kRows, C::kRows);
                 const int act = C::NQ == 2 && rows > 128 ? 2 : 1;
-                for (int w = 0; w < act && ok; ++w) ok = wait_bar(q_full + w, items[w] & 1, ctl);
-                if (!ok) break;
-                tc_fence_after();
                 if constexpr (C::NQ == 2) {
                     // slots: K0, then V(j), K(j + 1)
-                    landed(use);
+                    landed(slot, phase);
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (w >= act) break;
+                        wait(q_full + w, items[w] & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        qk(w, w, slot);
+                        if (n == 1) commit(q_free + w, 1);
+                    }
                     if (!ok) break;
-                    for (int w = 0; w < act; ++w) qk(w, w, use);
-                    release(use);
-                    use += C::KS;
+                    commit(empty + slot, 1);
+                    advance();
                     for (int j = 0; j < n && ok; ++j) {
-                        const int vs = use, ks = use + C::KS;
-                        landed(vs);
-                        if (j + 1 < n) landed(ks);
-                        for (int w = 0; w < act && ok; ++w) {
-                            ok = wait_bar(p_full + w, tiles[w] & 1, ctl);
-                            if (ok && j == 0) ok = wait_bar(o_free + w, (items[w] & 1) ^ 1, ctl);
+                        const int vs = slot;
+                        landed(slot, phase);
+                        advance();
+                        const bool more = j + 1 < n;
+                        const int ks = slot;
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            if (w >= act) break;
+                            wait(p_full + w, tiles[w] & 1);
+                            if (j == 0) wait(o_free + w, (items[w] & 1) ^ 1);
                             if (!ok) break;
                             ++tiles[w];
                             tc_fence_after();
                             pv(w, w, vs, j == 0);
-                            if (w == act - 1) release(vs);
-                            if (j + 1 < n) qk(w, w, ks);
+                            if (w == act - 1) commit(empty + vs, 1);
+                            if (more) {
+                                if (w == 0) landed(ks, phase);
+                                if (!ok) break;
+                                qk(w, w, ks);
+                                if (j + 2 == n) commit(q_free + w, 1);
+                            }
                         }
-                        if (!ok) break;
-                        use += C::KS;
-                        if (j + 1 < n) {
-                            release(ks);
-                            use += C::KS;
+                        if (ok && more) {
+                            commit(empty + ks, 1);
+                            advance();
                         }
                     }
                 } else {
                     // slots: K0, K1, then V(j), K(j + 2); S buffers alternate over all tiles
-                    for (int j = 0; j < min(n, 2) && ok; ++j) {
-                        landed(use);
-                        if (!ok) break;
-                        qk(0, (tiles[0] + j) & 1, use);
-                        release(use);
-                        use += C::KS;
-                    }
+                    wait(q_full, items[0] & 1);
+                    auto next_s = [&](int j) {
+                        landed(slot, phase);
+                        if (!ok) return;
+                        tc_fence_after();
+                        qk(0, (tiles[0] + j) & 1, slot);
+                        commit(empty + slot, C::KS);
+                        if (j + 1 == n) commit(q_free, 1);
+                        advance();
+                    };
+                    for (int j = 0; j < min(n, 2) && ok; ++j) next_s(j);
                     for (int j = 0; j < n && ok; ++j) {
-                        const int buf = tiles[0] & 1;
-                        landed(use);
-                        if (ok) ok = wait_bar(p_full + buf, (tiles[0] >> 1) & 1, ctl);
-                        if (ok && j == 0) ok = wait_bar(o_free, (items[0] & 1) ^ 1, ctl);
+                        const uint32_t t = tiles[0] + j;
+                        landed(slot, phase);
+                        wait(p_full + (t & 1), (t >> 1) & 1);
+                        if (j == 0) wait(o_free, (items[0] & 1) ^ 1);
                         if (!ok) break;
                         tc_fence_after();
-                        pv(0, buf, use, j == 0);
-                        release(use);
-                        use += C::KS;
-                        ++tiles[0];
-                        if (j + 2 < n) {
-                            landed(use);
-                            if (!ok) break;
-                            qk(0, buf, use);
-                            release(use);
-                            use += C::KS;
-                        }
+                        pv(0, t & 1, slot, j == 0);
+                        commit(empty + slot, C::KS);
+                        advance();
+                        if (j + 2 < n) next_s(j + 2);
                     }
+                    tiles[0] += n;
                 }
                 for (int w = 0; w < act; ++w) ++items[w];
                 deal_next<C::kRows, kTcKeys>(a, c, n);
             }
-            mma_commit(done);
+            commit(done, 1);
             drain_bar(done, 0);
         } else if (warp == 1) {
             // ------------------------------------------------------------ K and V tiles
@@ -376,6 +402,38 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             // every copy issued above lands before the CTA leaves (a cut slot's bytes are counted on
             // `tail`, and have been waited for)
             for (int u = max(use - C::kSlots, 0); u < use; ++u) drain_bar(full + u % C::kSlots, (u / C::kSlots) & 1);
+        } else {
+            // ------------------------------------------------------------ Q: warp 2 + w brings row tile w (one tile: half each)
+            const int w = C::NQ == 2 ? warp - 2 : 0;
+            uint8_t* sq = smem + C::kOffQ + w * C::kQTile;
+            uint32_t items = 0;
+            constexpr int kCpr = DH / 8, kPer = 32 / kCpr;  // chunks per row, rows per warp step
+            const int x = lane % kCpr;
+            while (ok && c.u < c.end) {
+                const int n = deal_take(a, c);
+                const int r0 = c.rt * C::kRows + 128 * w;
+                const int rows = min(c.s.q_len * kv.group - r0, 128);
+                if (rows > 0) {
+                    ok = __all_sync(~0u, wait_bar(q_free + w, (items & 1) ^ 1, ctl));
+                    if (!ok) break;
+                    ++items;
+#pragma unroll 8
+                    for (int i = 0; i < 128 / kPer / (2 / C::NQ); ++i) {
+                        const int r = (i + (C::NQ == 2 ? 0 : (warp - 2) * (64 / kPer))) * kPer + lane / kCpr;
+                        const bool in = r < rows && x * 8 < kv.d;
+                        const int rr = in ? r0 + r : r0;
+                        const int tok = c.s.q0 + rr / kv.group, head = c.h * kv.group + rr % kv.group;
+                        cp_async16(sq + (x / 8) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) << 4),
+                                   static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + (in ? x * 8 : 0), in ? 16 : 0);
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full + w);
+                }
+                deal_next<C::kRows, kTcKeys>(a, c, n);
+            }
         }
     } else {
         // ---------------------------------------------------------------- softmax, one row per thread
@@ -385,13 +443,11 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t o_col = tmem + lane_base + C::kOCol + DH * w;
         const float sc = a.scale * kLog2e;
-        uint8_t* sq = smem + C::kOffQ + w * C::kQTile;
         uint32_t tiles = 0;                         // key tiles of this warpgroup so far
         // Tile t's S, P and P V: which buffer, and which phase of its barriers.  (One tile per CTA: P V of two
         // tiles can be under way when this warpgroup has stored the second P, so they need a barrier each.)
         auto buf_of = [&](uint32_t t) { return C::NQ == 2 ? w : static_cast<int>(t & 1); };
         auto phase_of = [&](uint32_t t) { return (C::NQ == 2 ? t : t >> 1) & 1; };
-        const int chunks = kv.d / 8;
         while (ok && c.u < c.end) {
             const int n = deal_take(a, c);
             const int r0 = c.rt * C::kRows + 128 * w;
@@ -400,19 +456,6 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 deal_next<C::kRows, kTcKeys>(a, c, n);
                 continue;
             }
-            // Q: chunk x of row r at its swizzled place; zeros past the rows and past D
-            for (int i = row; i < 128 * (DH / 8); i += 128) {
-                const int r = i / (DH / 8), x = i % (DH / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows && x < chunks) {
-                    const int tok = c.s.q0 + (r0 + r) / kv.group, head = c.h * kv.group + (r0 + r) % kv.group;
-                    v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + x * 8);
-                }
-                *reinterpret_cast<uint4*>(sq + (x / 8) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) << 4)) = v;
-            }
-            fence_async_proxy();
-            mbar_arrive(q_full + w);
-
             const bool mine = row < rows;
             const bool live = (row & ~31) < rows;   // some row of the warp is one
             const int tok_i = (r0 + min(row, rows - 1)) / kv.group;

@@ -13,7 +13,6 @@
 namespace moe {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kSleepNs = 20000;  // longest sleep inside one barrier test
 
 __device__ __forceinline__ uint64_t global_ns() {
     uint64_t t;
@@ -27,17 +26,20 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
-// Barrier test; the thread may sleep in the instruction for up to `ns` nanoseconds (it is
-// woken when the phase completes): a waiting warp then takes no issue slots from the warps
-// doing the work.
-__device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, uint32_t ns) {
+__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+        : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
+}
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
@@ -50,11 +52,11 @@ struct Ctl {
 
 // Bounded wait for phase `parity` of `bar`; false if the CTA aborted or the
 // wait ran out (then the abort flag and the status word are set).
-static __device__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
-        if (mbar_wait_sleep(bar, parity, kSleepNs)) return true;
-        if ((it & 7) == 7) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63) == 63) {
             if (*c.abort) return false;
             const uint64_t t = global_ns();
             if (t0 == 0) {
@@ -71,7 +73,7 @@ static __device__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
 // The same wait for a thread that leaves: whether or not the CTA aborted, up to the same limit.
 static __device__ void drain_bar(uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = global_ns();
-    while (!mbar_wait_sleep(bar, parity, kSleepNs) && global_ns() - t0 <= kWaitNs) {
+    while (!mbar_try_wait(bar, parity) && global_ns() - t0 <= kWaitNs) {
     }
 }
 
