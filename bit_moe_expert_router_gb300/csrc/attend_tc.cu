@@ -10,8 +10,7 @@
 // Bound: the tensor pipe (4 D flops per pair and head) against the 2^x of the
 // special-function units and their surrounding instructions (one per pair and
 // head).  Per tile of 128 rows x 128 keys: S = Q K^T (operands in shared memory, 128 fp32
-// accumulator columns in tensor memory), a softmax warpgroup reads S (a thread
-// per row, so a row's maximum and sum need no exchange), writes P back over S as
+// accumulator columns in tensor memory), two softmax warpgroups read S and write P back over S as
 // packed 16-bit values, and O += P V takes P from tensor memory and V from shared
 // memory as an MN-major operand (rows of the cache are rows of K there, no transposition).
 //   D <= 128: two tiles of 128 rows per CTA share the keys' tiles; while one tile's
@@ -30,7 +29,9 @@
 // tile go through the workspace and the join.
 //
 // Warps: 0 MMA issue (one lane) and the tensor-memory allocation, 1 the K and V
-// tiles, 2-3 Q, then one warpgroup per row tile: softmax and output.
+// tiles, 2-3 Q, then two warpgroups per row tile: softmax and output, a thread for half
+// of a row's keys (64 of a tile's 128) and half of its output, so that the way from S to P is
+// half as long; the halves exchange their maxima through shared memory.
 // Every wait is bounded; a timeout sets the status word and every role leaves.
 #include <algorithm>
 
@@ -52,17 +53,18 @@ struct TcCfg {
     static constexpr int kKBlocks = kBlocks / KS;       // column blocks of a K slot (all 128 keys)
     static constexpr int kVKeys = kTcKeys / KS;         // keys of a V slot (all column blocks)
     static constexpr int kSlot = kTcKeys * DH * 2 / KS;
-    static constexpr int kSlots = DH == 256 ? 4 : DH == 128 ? 5 : 8;
+    static constexpr int kSlots = DH == 64 ? 8 : 4;
     static constexpr int kLook = NQ == 2 ? 1 : 2;       // K tiles ahead of V
     static constexpr int kQTile = 128 * DH * 2;
-    static constexpr int kThreads = 128 + 128 * NQ;
+    static constexpr int kThreads = 128 + 256 * NQ;
     static constexpr int kSCol = 0, kOCol = 256;        // two S (or P) buffers of 128 columns, then O
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = kOffQ + NQ * kQTile;
     static constexpr int kOffBars = kOffRing + kSlots * kSlot;
     static constexpr int kBars = 2 * kSlots + 6 + 3 * NQ + 2;
     static constexpr int kOffMisc = kOffBars + 8 * kBars;
-    static constexpr int kSmem = kOffMisc + 16 + 1024;
+    static constexpr int kOffEx = kOffMisc + 16;        // float [NQ][2][2][128]: what the two halves of a row exchange
+    static constexpr int kSmem = kOffEx + NQ * 2048 + 1024;
     static_assert(kOCol + NQ * DH <= 512, "tensor-memory columns");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -112,6 +114,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 template <typename T, int DH>
 __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     attend_tc_kernel(const AttendArgs a, int box_rows, const __grid_constant__ CUtensorMap kmap,
@@ -123,11 +131,11 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     uint64_t* full = bars;                    // [slots] the slot's bytes have landed
     uint64_t* empty = full + C::kSlots;       // [slots] MMA commit: the slot is read
     uint64_t* s_full = empty + C::kSlots;     // [2] MMA commit: S is there
-    uint64_t* p_full = s_full + 2;            // [2] four softmax warps: P is there, S is read
+    uint64_t* p_full = s_full + 2;            // [2] eight softmax warps: P is there, S is read
     uint64_t* q_full = p_full + 2;            // [NQ] the Q warps: Q is in shared memory
     uint64_t* q_free = q_full + C::NQ;        // [NQ] MMA commit: the tile's last S is there
     uint64_t* o_done = q_free + C::NQ;        // [2] MMA commit: P V is added (by P's buffer)
-    uint64_t* o_free = o_done + 2;            // [NQ] four softmax warps: the tile's O is read
+    uint64_t* o_free = o_done + 2;            // [NQ] eight softmax warps: the tile's O is read
     uint64_t* tail = o_free + C::NQ;          // the bytes of a V slot that is cleared by hand
     uint64_t* done = tail + 1;                // MMA commit: everything issued has finished
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -144,13 +152,13 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 4);
+            mbar_init(p_full + i, 8);
             mbar_init(o_done + i, 1);
         }
         for (int i = 0; i < C::NQ; ++i) {
             mbar_init(q_full + i, 2 / C::NQ);
             mbar_init(q_free + i, 1);
-            mbar_init(o_free + i, 4);
+            mbar_init(o_free + i, 8);
         }
         mbar_init(tail, 1);
         mbar_init(done, 1);
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     bool ok = true;
 
     if (warp < 4) {
-        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         if (warp == 0) {
             // ------------------------------------------------------------ MMA issue
             const bool leader = elect_one();
@@ -436,22 +444,33 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             }
         }
     } else {
-        // ---------------------------------------------------------------- softmax, one row per thread
-        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-        const int w = (warp - 4) / 4;               // the warpgroup's row tile
-        const int row = (tid & 127);                // tile row = tensor-memory lane
+        // ---------------------------------------------------------------- softmax, half a row per thread
+        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+        const int w = (warp - 4) / 8;               // the row tile
+        const int half = ((warp - 4) / 4) & 1;      // keys 64 half .. of a tile, columns DH / 2 half .. of O
+        const int row = tid & 127;                  // tile row = tensor-memory lane
         const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t o_col = tmem + lane_base + C::kOCol + DH * w;
+        const uint32_t o_col = tmem + lane_base + C::kOCol + DH * w + DH / 2 * half;
+        float* ex = reinterpret_cast<float*>(smem + C::kOffEx) + 512 * w + row;  // [parity][half]
+        const int ex_bar = 1 + 4 * w + (warp & 3);  // the two warps of the same rows
         const float sc = a.scale * kLog2e;
-        uint32_t tiles = 0;                         // key tiles of this warpgroup so far
+        uint32_t tiles = 0;                         // key tiles of this row tile so far
+        uint32_t swaps = 0;
+        // The other half's value.
+        auto exchange = [&](float x) {
+            float* at = ex + 256 * (swaps++ & 1);
+            at[128 * half] = x;
+            asm volatile("bar.sync %0, 64;\n" ::"r"(ex_bar) : "memory");
+            return at[128 * (half ^ 1)];
+        };
         // Tile t's S, P and P V: which buffer, and which phase of its barriers.  (One tile per CTA: P V of two
-        // tiles can be under way when this warpgroup has stored the second P, so they need a barrier each.)
+        // tiles can be under way when the second P is stored, so they need a barrier each.)
         auto buf_of = [&](uint32_t t) { return C::NQ == 2 ? w : static_cast<int>(t & 1); };
         auto phase_of = [&](uint32_t t) { return (C::NQ == 2 ? t : t >> 1) & 1; };
         while (ok && c.u < c.end) {
             const int n = deal_take(a, c);
             const int r0 = c.rt * C::kRows + 128 * w;
-            const int rows = min(c.s.q_len * kv.group - r0, 128);  // of this warpgroup
+            const int rows = min(c.s.q_len * kv.group - r0, 128);  // of this row tile
             if (rows <= 0) {
                 deal_next<C::kRows, kTcKeys>(a, c, n);
                 continue;
@@ -470,30 +489,31 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 if (!ok) break;
                 if (live) {
                     tc_fence_after();
-                    uint32_t v[128];
+                    uint32_t v[64];
                     const uint32_t s_col = tmem + lane_base + C::kSCol + 128 * buf;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, v + 32 * i);
+                    tmem_ld32(s_col + 64 * half, v);
+                    tmem_ld32(s_col + 64 * half + 32, v + 32);
                     tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_tie32(v + 32 * i);
-                    const int key0 = (c.first + c.off + j) * kTcKeys;
+                    tmem_tie<32>(v);
+                    tmem_tie<32>(v + 32);
+                    const int key0 = (c.first + c.off + j) * kTcKeys + 64 * half;
                     const int rel_hi = p_hi - key0, rel_lo = p_lo - key0;
-                    if (__any_sync(~0u, rel_hi < kTcKeys - 1 || rel_lo >= 0)) {
+                    if (__any_sync(~0u, rel_hi < 63 || rel_lo >= 0)) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i)
+                        for (int i = 0; i < 64; ++i)
                             if (i > rel_hi || i <= rel_lo) v[i] = __float_as_uint(kNegInf);
                     }
                     float mx[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(v[i]);
+                    for (int x = 0; x < 4; ++x) mx[x] = max3(__uint_as_float(v[x]), __uint_as_float(v[x + 4]), __uint_as_float(v[x + 8]));
 #pragma unroll
-                    for (int i = 4; i < 128; i += 8) {
+                    for (int i = 12; i < 60; i += 8)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mx[x] = fmaxf(mx[x], i + 4 + x < 128 ? fmaxf(__uint_as_float(v[i + x]), __uint_as_float(v[i + 4 + x])) : __uint_as_float(v[i + x]));
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], __uint_as_float(v[i + x]), __uint_as_float(v[i + 4 + x]));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(v[60 + x]));
+                    float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                    top = fmaxf(top, exchange(top));  // (S of both halves is read: P may be stored over it)
                     // (with m = -inf the difference is inf, or NaN if the row has seen nothing yet)
                     const bool grew = (top - m) * sc > 8.f;
                     if (j == 0) {
@@ -508,30 +528,30 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         const uint64_t f2 = pair(f, f);
                         l2 = mul2(l2, f2);
 #pragma unroll 1
-                        for (int i = 0; i < DH; i += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(o_col + i, o);
+                        for (int i = 0; i < DH / 2; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o_col + i, o);
                             tmem_ld_wait();
-                            tmem_tie32(o);
+                            tmem_tie<16>(o);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tmem_st32(o_col + i, o);
+                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tmem_st16(o_col + i, o);
                         }
                     }
                     const float base = m == kNegInf ? 0.f : m * sc;
                     const uint64_t sc2 = pair(sc, sc), nb2 = pair(-base, -base);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t pk[32];
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int e = 64 * h + 2 * i;
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = 32 * h + 2 * i;
                             const float2 x = unpair(fma2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nb2));
                             const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
                             l2 = add2(l2, pair(p0, p1));
                             pk[i] = Elem<T>::pack(p0, p1);  // the product's operand: 16 bits; the sum l is of the fp32 values
                         }
-                        tmem_st32(s_col + 32 * h, pk);
+                        tmem_st16(s_col + 32 * half + 16 * h, pk);
                     }
                     tmem_st_wait();
                     tc_fence_before();
@@ -545,28 +565,30 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const bool whole = n == c.n;
-            const float2 lp = unpair(l2);
-            const float l = lp.x + lp.y;
             const int tok = c.s.q0 + tok_i, head = c.h * kv.group + (r0 + min(row, rows - 1)) % kv.group;
-            bool bad = l != l;
+            bool bad = false;
             if (live) {
+                const float2 lp = unpair(l2);
+                float l = lp.x + lp.y;
+                l += exchange(l);
+                bad = l != l;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs;
+                T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + DH / 2 * half;
                 const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (c.u == u_begin ? 0 : 1)) * C::kRows + 128 * w + row;
-                float* pdst = a.part_o + prow * DH;
+                float* pdst = a.part_o + prow * DH + DH / 2 * half;
 #pragma unroll 1
-                for (int i = 0; i < DH; i += 32) {
+                for (int i = 0; i < DH / 2; i += 32) {
                     uint32_t o[32];
                     tmem_ld32(o_col + i, o);
                     tmem_ld_wait();
-                    tmem_tie32(o);
+                    tmem_tie<32>(o);
                     if (!mine) continue;
                     if (whole) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x) bad |= __uint_as_float(o[x]) != __uint_as_float(o[x]);
 #pragma unroll
                         for (int x = 0; x < 32; x += 8)
-                            if (i + x < kv.d) {
+                            if (DH / 2 * half + i + x < kv.d) {
                                 uint4 u;
                                 u.x = Elem<T>::pack(__uint_as_float(o[x]) * inv, __uint_as_float(o[x + 1]) * inv);
                                 u.y = Elem<T>::pack(__uint_as_float(o[x + 2]) * inv, __uint_as_float(o[x + 3]) * inv);
@@ -579,7 +601,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         for (int x = 0; x < 32; x += 4) *reinterpret_cast<uint4*>(pdst + i + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
                     }
                 }
-                if (mine) {
+                if (mine && half == 0) {
                     if (!whole) a.part_ml[prow] = make_float2(m == kNegInf ? kNegInf : m * sc, l);
                     else if (a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = l == 0.f ? kNegInf : (m * sc + log2f(l)) * kLn2;
                 }
@@ -587,11 +609,14 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free + w);
-            unsigned again = __ballot_sync(~0u, whole && mine && bad);
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                attend_row<T>(a, c.b, __shfl_sync(~0u, tok, src), __shfl_sync(~0u, head, src), __shfl_sync(~0u, pos, src));
+            if (live && whole) {
+                bad |= exchange(bad ? 1.f : 0.f) != 0.f;  // (and both halves of the row are stored)
+                unsigned again = half == 0 ? __ballot_sync(~0u, mine && bad) : 0;
+                while (again) {
+                    const int src = __ffs(again) - 1;
+                    again &= again - 1;
+                    attend_row<T>(a, c.b, __shfl_sync(~0u, tok, src), __shfl_sync(~0u, head, src), __shfl_sync(~0u, pos, src));
+                }
             }
             deal_next<C::kRows, kTcKeys>(a, c, n);
         }
