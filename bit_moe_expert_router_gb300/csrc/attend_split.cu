@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
 
     if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
     Cursor c;
-    deal_begin<kSplitRows, kKeys>(a, prefix, 16, c);
+    deal_begin<kSplitRows, kKeys>(a, prefix, 16, blockIdx.x, gridDim.x, c);
     if (a.split && threadIdx.x == 0) {
         BoundaryRec r;
         r.begin = c.u - c.off;

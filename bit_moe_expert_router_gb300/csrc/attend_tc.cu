@@ -17,6 +17,9 @@
 //     softmax runs the tensor pipe does the other's products.
 //   D <= 256: one tile (O takes 256 of the 512 columns); S is double-buffered, so the
 //     tensor pipe does the next keys' S while the softmax of this one runs.
+//   D > 64: CTAs work in pairs (cta_group::2): an MMA covers 256 rows, 128 of each CTA, and each CTA
+//     brings half of K (64 keys) and half of V (half the components), so the bytes that
+//     each SM takes from L2, and from its shared memory for an MMA, are halved.
 // The reference m is raised, and O rescaled, only when a row's maximum has grown
 // by more than 2^8 over it: P stays below 2^8 (exact enough in 16 bits: the rounding is relative)
 // and almost every tile leaves O alone.
@@ -46,25 +49,26 @@ constexpr int kTcKeys = 128;  // keys of a unit
 
 template <int DH>
 struct TcCfg {
-    static constexpr int NQ = DH == 256 ? 1 : 2;        // row tiles per CTA
-    static constexpr int kRows = 128 * NQ;
-    static constexpr int kBlocks = DH / 64;             // 64-component column blocks
-    static constexpr int KS = DH == 256 ? 2 : 1;        // ring slots of a K or V tile
-    static constexpr int kKBlocks = kBlocks / KS;       // column blocks of a K slot (all 128 keys)
-    static constexpr int kVKeys = kTcKeys / KS;         // keys of a V slot (all column blocks)
-    static constexpr int kSlot = kTcKeys * DH * 2 / KS;
-    static constexpr int kSlots = DH == 64 ? 8 : 4;
+    static constexpr int CG = DH == 64 ? 1 : 2;         // CTAs that share a tile of keys
+    static constexpr int NQ = DH == 256 ? 1 : 2;        // row tiles of 128 per CTA
+    static constexpr int kTile = 128 * CG;              // rows of a tile over its CTAs
+    static constexpr int kRows = kTile * NQ;
+    static constexpr int kKKeys = kTcKeys / CG;         // a CTA's share of K: these keys, all components,
+    static constexpr int kVCols = DH / CG;              // of V: all keys, these components
+    static constexpr int kKBlocks = DH / 64, kVBlocks = kVCols / 64;  // in column blocks of 64
+    static constexpr int kSlot = kKKeys * DH * 2;
+    static constexpr int kSlots = DH == 64 ? 10 : DH == 128 ? 9 : 5;
     static constexpr int kLook = NQ == 2 ? 1 : 2;       // K tiles ahead of V
     static constexpr int kQTile = 128 * DH * 2;
     static constexpr int kThreads = 128 + 256 * NQ;
     static constexpr int kSCol = 0, kOCol = 256;        // two S (or P) buffers of 128 columns, then O
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = kOffQ + NQ * kQTile;
-    static constexpr int kOffBars = kOffRing + kSlots * kSlot;
+    static constexpr int kOffEx = kOffRing + kSlots * kSlot;  // float [NQ][2][2][128]: what the halves of a row exchange
+    static constexpr int kOffBars = kOffEx + NQ * 2048;
     static constexpr int kBars = 2 * kSlots + 6 + 3 * NQ + 2;
     static constexpr int kOffMisc = kOffBars + 8 * kBars;
-    static constexpr int kOffEx = kOffMisc + 16;        // float [NQ][2][2][128]: what the two halves of a row exchange
-    static constexpr int kSmem = kOffEx + NQ * 2048 + 1024;
+    static constexpr int kSmem = kOffMisc + 16;
     static_assert(kOCol + NQ * DH <= 512, "tensor-memory columns");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -80,11 +84,11 @@ struct MmaFmt<__half> {
     static constexpr uint32_t v = 0;
 };
 
-// kind::f16 instruction descriptor: fp32 accumulator, A and B of one type, M = 128, N = n; b_mn: B is MN-major.
+// kind::f16 instruction descriptor: fp32 accumulator, A and B of one type, M = m, N = n; b_mn: B is MN-major.
 template <typename T>
-__device__ constexpr uint32_t idesc16(int n, bool b_mn) {
+__device__ constexpr uint32_t idesc16(int m, int n, bool b_mn) {
     return (1u << 4) | (MmaFmt<T>::v << 7) | (MmaFmt<T>::v << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
-           ((128u >> 4) << 24);
+           (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // Two fp32 operations in one instruction.
@@ -125,17 +129,19 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     attend_tc_kernel(const AttendArgs a, int box_rows, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
     using C = TcCfg<DH>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int CG = C::CG;
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
-    uint64_t* full = bars;                    // [slots] the slot's bytes have landed
+    // What the issuing CTA waits for is counted on its own barriers, by both CTAs of a pair; what it
+    // tells is committed to both CTAs' copies.
+    uint64_t* full = bars;                    // [slots] each CTA's loader: the slot's bytes have landed
     uint64_t* empty = full + C::kSlots;       // [slots] MMA commit: the slot is read
     uint64_t* s_full = empty + C::kSlots;     // [2] MMA commit: S is there
-    uint64_t* p_full = s_full + 2;            // [2] eight softmax warps: P is there, S is read
-    uint64_t* q_full = p_full + 2;            // [NQ] the Q warps: Q is in shared memory
+    uint64_t* p_full = s_full + 2;            // [2] each CTA's eight softmax warps: P is there, S is read
+    uint64_t* q_full = p_full + 2;            // [NQ] each CTA's Q warps: Q is in shared memory
     uint64_t* q_free = q_full + C::NQ;        // [NQ] MMA commit: the tile's last S is there
     uint64_t* o_done = q_free + C::NQ;        // [2] MMA commit: P V is added (by P's buffer)
-    uint64_t* o_free = o_done + 2;            // [NQ] eight softmax warps: the tile's O is read
+    uint64_t* o_free = o_done + 2;            // [NQ] each CTA's eight softmax warps: the tile's O is read
     uint64_t* tail = o_free + C::NQ;          // the bytes of a V slot that is cleared by hand
     uint64_t* done = tail + 1;                // MMA commit: everything issued has finished
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -145,20 +151,24 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     const Ctl ctl{abort_flag, a.hdr};
 
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (smem_u32(smem) & 1023u) {  // (the swizzled tiles' places; the same in every CTA)
+        if (tid == 0) atomicOr(&a.hdr->status, kDevTimeout);
+        return;
+    }
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(full + i, 1);
+            mbar_init(full + i, CG);
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 8);
+            mbar_init(p_full + i, 8 * CG);
             mbar_init(o_done + i, 1);
         }
         for (int i = 0; i < C::NQ; ++i) {
-            mbar_init(q_full + i, 2 / C::NQ);
+            mbar_init(q_full + i, 2 / C::NQ * CG);
             mbar_init(q_free + i, 1);
-            mbar_init(o_free + i, 8);
+            mbar_init(o_free + i, 8 * CG);
         }
         mbar_init(tail, 1);
         mbar_init(done, 1);
@@ -166,13 +176,11 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         if (blockIdx.x == 0) a.hdr->status = kDevOk;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tmem_holder)), "r"(512));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-    }
+    if (warp == 0) tmem_alloc<CG>(tmem_holder, 512);
+    const int rank = CG == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CG;
     Cursor c;
-    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, c);  // (scratch: the ring)
-    if (a.split && tid == 0) {
+    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, me, gridDim.x / CG, c);  // (scratch: the ring)
+    if (rank == 0 && tid == 0) {
         BoundaryRec r;
         r.begin = c.u - c.off;
         r.per = c.per;
@@ -182,12 +190,13 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         r.rt = c.rt;
         r.h = c.h;
         r.pad = 0;
-        a.recs[blockIdx.x] = r;
+        a.recs[me] = r;
     }
     clear_stray_rows<T>(a);
     tc_fence_before();
     fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
     __syncthreads();
+    if constexpr (CG == 2) cluster_sync();  // the peer's barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const uint32_t ring = smem_u32(smem + C::kOffRing);
@@ -197,59 +206,50 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     if (warp < 4) {
         if constexpr (C::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         if (warp == 0) {
+          if (rank == 0) {
             // ------------------------------------------------------------ MMA issue
             const bool leader = elect_one();
-            const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(ring), vd = sdesc_mn(ring, C::kVKeys * 128);
+            const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(ring), vd = sdesc_mn(ring, kTcKeys * 128);
             int slot = 0;                     // the next ring slot of K or V,
             uint32_t phase = 0;               // and the phase of its barrier
             uint32_t tiles[2] = {0, 0};       // key tiles so far, by warpgroup
             uint32_t items[2] = {0, 0};       // row tiles so far, by warpgroup
-            auto qk = [&](int w, int buf, int s) {  // S[buf] = Q[w] K^T, K in slots s ..
+            auto qk = [&](int w, int buf, int s) {  // S[buf] = Q[w] K^T, K in slot s
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < DH / 16; ++k) {
-                        const int blk = k / 4;
-                        mma_f16_ss(tmem + C::kSCol + 128 * buf, qd + ((w * C::kQTile + blk * 16384 + (k % 4) * 32) >> 4),
-                                   kd + ((s * C::kSlot + blk / C::kKBlocks * C::kSlot + blk % C::kKBlocks * 16384 + (k % 4) * 32) >> 4),
-                                   idesc16<T>(128, false), k > 0);
-                    }
-                    mma_commit(s_full + buf);
+                    for (int k = 0; k < DH / 16; ++k)
+                        mma_f16_ss<CG>(tmem + C::kSCol + 128 * buf, qd + ((w * C::kQTile + k / 4 * 16384 + k % 4 * 32) >> 4),
+                                       kd + ((s * C::kSlot + k / 4 * (C::kKKeys * 128) + k % 4 * 32) >> 4), idesc16<T>(C::kTile, kTcKeys, false),
+                                       k > 0);
+                    mma_commit<CG>(s_full + buf);
                 }
                 __syncwarp();
             };
-            auto pv = [&](int w, int buf, int s, bool first) {  // O[w] (+)= P[buf] V, V in slots s ..
+            auto pv = [&](int w, int buf, int s, bool first) {  // O[w] (+)= P[buf] V, V in slot s
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < kTcKeys / 16; ++k)
-                        mma_f16_ta(tmem + C::kOCol + DH * w, tmem + C::kSCol + 128 * buf + 8 * k,
-                                   vd + ((s * C::kSlot + k * 16 / C::kVKeys * C::kSlot + k * 16 % C::kVKeys * 128) >> 4), idesc16<T>(DH, true),
-                                   !first || k > 0);
-                    mma_commit(o_done + buf);
+                        mma_f16_ta<CG>(tmem + C::kOCol + DH * w, tmem + C::kSCol + 128 * buf + 8 * k, vd + ((s * C::kSlot + k * 2048) >> 4),
+                                       idesc16<T>(C::kTile, DH, true), !first || k > 0);
+                    mma_commit<CG>(o_done + buf);
                 }
                 __syncwarp();
             };
-            auto landed = [&](int s, uint32_t ph) {
-#pragma unroll
-                for (int i = 0; i < C::KS; ++i) ok = ok && wait_bar(full + s + i, ph, ctl);
-                ok = __all_sync(~0u, ok);
-            };
-            auto commit = [&](uint64_t* bar, int n) {
-                if (leader)
-                    for (int i = 0; i < n; ++i) mma_commit(bar + i);
+            auto commit = [&](uint64_t* bar) {
+                if (leader) mma_commit<CG>(bar);
                 __syncwarp();
             };
             auto wait = [&](uint64_t* bar, uint32_t ph) { ok = __all_sync(~0u, ok && wait_bar(bar, ph, ctl)); };
             auto advance = [&]() {
-                slot += C::KS;
-                if (slot == C::kSlots) slot = 0, phase ^= 1;
+                if (++slot == C::kSlots) slot = 0, phase ^= 1;
             };
             while (ok && c.u < c.end) {
                 const int n = deal_take(a, c);
                 const int rows = min(c.s.q_len * kv.group - c.rt * C::kRows, C::kRows);
-                const int act = C::NQ == 2 && rows > 128 ? 2 : 1;
+                const int act = C::NQ == 2 && rows > C::kTile ? 2 : 1;
                 if constexpr (C::NQ == 2) {
                     // slots: K0, then V(j), K(j + 1)
-                    landed(slot, phase);
+                    wait(full + slot, phase);
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         if (w >= act) break;
@@ -257,14 +257,14 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         qk(w, w, slot);
-                        if (n == 1) commit(q_free + w, 1);
+                        if (n == 1) commit(q_free + w);
                     }
                     if (!ok) break;
-                    commit(empty + slot, 1);
+                    commit(empty + slot);
                     advance();
                     for (int j = 0; j < n && ok; ++j) {
                         const int vs = slot;
-                        landed(slot, phase);
+                        wait(full + slot, phase);
                         advance();
                         const bool more = j + 1 < n;
                         const int ks = slot;
@@ -277,16 +277,16 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                             ++tiles[w];
                             tc_fence_after();
                             pv(w, w, vs, j == 0);
-                            if (w == act - 1) commit(empty + vs, 1);
+                            if (w == act - 1) commit(empty + vs);
                             if (more) {
-                                if (w == 0) landed(ks, phase);
+                                if (w == 0) wait(full + ks, phase);
                                 if (!ok) break;
                                 qk(w, w, ks);
-                                if (j + 2 == n) commit(q_free + w, 1);
+                                if (j + 2 == n) commit(q_free + w);
                             }
                         }
                         if (ok && more) {
-                            commit(empty + ks, 1);
+                            commit(empty + ks);
                             advance();
                         }
                     }
@@ -294,24 +294,24 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     // slots: K0, K1, then V(j), K(j + 2); S buffers alternate over all tiles
                     wait(q_full, items[0] & 1);
                     auto next_s = [&](int j) {
-                        landed(slot, phase);
+                        wait(full + slot, phase);
                         if (!ok) return;
                         tc_fence_after();
                         qk(0, (tiles[0] + j) & 1, slot);
-                        commit(empty + slot, C::KS);
-                        if (j + 1 == n) commit(q_free, 1);
+                        commit(empty + slot);
+                        if (j + 1 == n) commit(q_free);
                         advance();
                     };
                     for (int j = 0; j < min(n, 2) && ok; ++j) next_s(j);
                     for (int j = 0; j < n && ok; ++j) {
                         const uint32_t t = tiles[0] + j;
-                        landed(slot, phase);
+                        wait(full + slot, phase);
                         wait(p_full + (t & 1), (t >> 1) & 1);
                         if (j == 0) wait(o_free, (items[0] & 1) ^ 1);
                         if (!ok) break;
                         tc_fence_after();
                         pv(0, t & 1, slot, j == 0);
-                        commit(empty + slot, C::KS);
+                        commit(empty + slot);
                         advance();
                         if (j + 2 < n) next_s(j + 2);
                     }
@@ -320,16 +320,20 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 for (int w = 0; w < act; ++w) ++items[w];
                 deal_next<C::kRows, kTcKeys>(a, c, n);
             }
-            commit(done, 1);
-            drain_bar(done, 0);
+            if (leader) mma_commit_own<CG>(done);
+            __syncwarp();
+            drain_bar(done, 0, global_ns() + kWaitNs);
+          }
         } else if (warp == 1) {
             // ------------------------------------------------------------ K and V tiles
             int use = 0;
             uint32_t tails = 0;
-            const int boxes = kTcKeys / box_rows;  // <= 16; lane i brings box i of a tile
             int lo, hi;
-            auto where = [&](int unit, int& row, int& page) {  // this lane's box of tile `unit`
-                const int key = unit * kTcKeys + lane * box_rows;
+            int slot = 0;
+            uint32_t phase = 0;
+            // Lane i brings box i of `rows` rows (at most 16 boxes) from key `key0` on: where it lies.
+            auto where = [&](int key0, int boxes, int& row, int& page) {
+                const int key = key0 + lane * box_rows;
                 page = kv.n_pages;  // outside the map: zeros
                 row = 0;
                 if (lane < boxes && key < hi) {
@@ -338,62 +342,58 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     if (id >= 0) page = id;
                 }
             };
-            auto claim = [&]() {
-                ok = __all_sync(~0u, wait_bar(empty + use % C::kSlots, ((use / C::kSlots) & 1) ^ 1, ctl));
-                return use % C::kSlots;
+            auto advance = [&]() {
+                if (++slot == C::kSlots) slot = 0, phase ^= 1;
+                ++use;
             };
             auto load_k = [&](int unit) {
                 int row, page;
-                where(unit, row, page);
+                constexpr int kKeys = C::kKKeys;
+                const int boxes = kKeys / box_rows;
+                where(unit * kTcKeys + rank * kKeys, boxes, row, page);
+                ok = __all_sync(~0u, wait_bar(empty + slot, phase ^ 1, ctl));
+                if (!ok) return;
+                const uint32_t bar = leaders(full + slot);
+                if (lane == 0) mbar_expect_tx(bar, C::kSlot);
+                __syncwarp();
+                if (lane < boxes)
 #pragma unroll
-                for (int i = 0; i < C::KS; ++i) {
-                    const int s = claim();
-                    if (!ok) return;
-                    if (lane == 0) mbar_expect_tx(full + s, C::kSlot);
-                    __syncwarp();
-                    if (lane < boxes)
-#pragma unroll
-                        for (int b = 0; b < C::kKBlocks; ++b)
-                            tma_tile4d(ring + s * C::kSlot + b * 16384 + lane * box_rows * 128, &kmap, (i * C::kKBlocks + b) * 64, row, c.h, page,
-                                       full + s);
-                    ++use;
-                }
+                    for (int b = 0; b < C::kKBlocks; ++b)
+                        tma_tile4d<CG>(ring + slot * C::kSlot + (b * kKeys + lane * box_rows) * 128, &kmap, b * 64, row, c.h, page, bar);
+                advance();
             };
             auto load_v = [&](int unit) {
                 int row, page;
-                where(unit, row, page);
+                const int boxes = kTcKeys / box_rows;
+                where(unit * kTcKeys, boxes, row, page);
+                ok = __all_sync(~0u, wait_bar(empty + slot, phase ^ 1, ctl));
+                if (!ok) return;
+                const int last = hi - unit * kTcKeys;  // rows that some row of the tile sees
+                const bool cut = last > 0 && last < kTcKeys && last % box_rows != 0;
+                const uint32_t there = leaders(full + slot), bar = cut ? own_bar(tail) : there;
+                if (lane == 0) mbar_expect_tx(bar, C::kSlot);
+                __syncwarp();
+                if (lane < boxes)
 #pragma unroll
-                for (int i = 0; i < C::KS; ++i) {
-                    const int s = claim();
+                    for (int b = 0; b < C::kVBlocks; ++b)
+                        tma_tile4d<CG>(ring + slot * C::kSlot + (b * kTcKeys + lane * box_rows) * 128, &vmap, rank * C::kVCols + b * 64, row, c.h,
+                                       page, bar);
+                if (cut) {  // the box's rows behind the last visible one
+                    ok = __all_sync(~0u, wait_bar(tail, tails & 1, ctl));
                     if (!ok) return;
-                    const int key0 = unit * kTcKeys + i * C::kVKeys;
-                    const int last = hi - key0;  // rows that some row of the tile sees
-                    const bool cut = last > 0 && last < C::kVKeys && last % box_rows != 0;
-                    uint64_t* bar = cut ? tail : full + s;
-                    if (lane == 0) mbar_expect_tx(bar, C::kSlot);
-                    __syncwarp();
-                    const int first = lane * box_rows - i * C::kVKeys;  // the box's first row in this slot
-                    if (lane < boxes && first >= 0 && first < C::kVKeys)
-#pragma unroll
-                        for (int b = 0; b < C::kBlocks; ++b)
-                            tma_tile4d(ring + s * C::kSlot + b * (C::kVKeys * 128) + first * 128, &vmap, b * 64, row, c.h, page, bar);
-                    if (cut) {  // the box's rows behind the last visible one
-                        ok = __all_sync(~0u, wait_bar(tail, tails & 1, ctl));
-                        if (!ok) return;
-                        ++tails;
-                        const int end = (last + box_rows - 1) / box_rows * box_rows;
-                        const int per = (end - last) * 8;
-                        for (int x = lane; x < per * C::kBlocks; x += 32) {
-                            const int b = x / per, y = x - b * per;
-                            *reinterpret_cast<uint4*>(smem + C::kOffRing + s * C::kSlot + b * (C::kVKeys * 128) + last * 128 + y * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async_proxy();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(full + s);
+                    ++tails;
+                    const int end = (last + box_rows - 1) / box_rows * box_rows;
+                    const int per = (end - last) * 8;
+                    for (int x = lane; x < per * C::kVBlocks; x += 32) {
+                        const int b = x / per, y = x - b * per;
+                        *reinterpret_cast<uint4*>(smem + C::kOffRing + slot * C::kSlot + (b * kTcKeys + last) * 128 + y * 16) =
+                            make_uint4(0, 0, 0, 0);
                     }
-                    ++use;
+                    fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(there);
                 }
+                advance();
             };
             while (ok && c.u < c.end) {
                 const int n = deal_take(a, c);
@@ -407,9 +407,13 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 }
                 deal_next<C::kRows, kTcKeys>(a, c, n);
             }
-            // every copy issued above lands before the CTA leaves (a cut slot's bytes are counted on
-            // `tail`, and have been waited for)
-            for (int u = max(use - C::kSlots, 0); u < use; ++u) drain_bar(full + u % C::kSlots, (u / C::kSlots) & 1);
+            // Nothing is on its way to this CTA's memory when it leaves: every slot's last use has landed and been
+            // read (or, after a timeout, the limit has passed).
+            const uint64_t end = global_ns() + kWaitNs;
+            for (int u = max(use - C::kSlots, 0); u < use; ++u) {
+                if (rank == 0) drain_bar(full + u % C::kSlots, (u / C::kSlots) & 1, end);
+                drain_bar(empty + u % C::kSlots, (u / C::kSlots) & 1, end);
+            }
         } else {
             // ------------------------------------------------------------ Q: warp 2 + w brings row tile w (one tile: half each)
             const int w = C::NQ == 2 ? warp - 2 : 0;
@@ -419,29 +423,38 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const int x = lane % kCpr;
             while (ok && c.u < c.end) {
                 const int n = deal_take(a, c);
-                const int r0 = c.rt * C::kRows + 128 * w;
-                const int rows = min(c.s.q_len * kv.group - r0, 128);
-                if (rows > 0) {
+                const int all = c.s.q_len * kv.group - c.rt * C::kRows;
+                if (all > C::kTile * w) {
+                    const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
+                    const int rows = min(c.s.q_len * kv.group - r0, 128);
                     ok = __all_sync(~0u, wait_bar(q_free + w, (items & 1) ^ 1, ctl));
                     if (!ok) break;
                     ++items;
+                    // where the rows begin: each lane finds its rows' places once, then passes them round
+                    constexpr int kMine = C::NQ == 2 ? 128 : 64;  // this warp's rows
+                    const int first = C::NQ == 2 ? 0 : (warp - 2) * 64;
+#pragma unroll
+                    for (int g = 0; g < kMine; g += 32) {
+                        const int rr = r0 + max(min(first + g + lane, rows - 1), 0);
+                        const int64_t at = static_cast<int64_t>(c.s.q0 + rr / kv.group) * a.q_ts + (c.h * kv.group + rr % kv.group) * a.q_hs;
 #pragma unroll 8
-                    for (int i = 0; i < 128 / kPer / (2 / C::NQ); ++i) {
-                        const int r = (i + (C::NQ == 2 ? 0 : (warp - 2) * (64 / kPer))) * kPer + lane / kCpr;
-                        const bool in = r < rows && x * 8 < kv.d;
-                        const int rr = in ? r0 + r : r0;
-                        const int tok = c.s.q0 + rr / kv.group, head = c.h * kv.group + rr % kv.group;
-                        cp_async16(sq + (x / 8) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) << 4),
-                                   static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + (in ? x * 8 : 0), in ? 16 : 0);
+                        for (int i = 0; i < 32; i += kPer) {
+                            const int64_t from = __shfl_sync(~0u, at, i + lane / kCpr);
+                            const int r = first + g + i + lane / kCpr;
+                            const bool in = r < rows && x * 8 < kv.d;
+                            cp_async16(sq + (x / 8) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) << 4),
+                                       static_cast<const T*>(a.q) + (in ? from + x * 8 : 0), in ? 16 : 0);
+                        }
                     }
                     cp_async_commit();
                     cp_async_wait<0>();
                     fence_async_proxy();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(q_full + w);
+                    if (lane == 0) mbar_arrive(leaders(q_full + w));
                 }
                 deal_next<C::kRows, kTcKeys>(a, c, n);
             }
+            if (items) drain_bar(q_free + w, (items - 1) & 1, global_ns() + kWaitNs);  // (its arrival, too, has come)
         }
     } else {
         // ---------------------------------------------------------------- softmax, half a row per thread
@@ -469,15 +482,16 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         auto phase_of = [&](uint32_t t) { return (C::NQ == 2 ? t : t >> 1) & 1; };
         while (ok && c.u < c.end) {
             const int n = deal_take(a, c);
-            const int r0 = c.rt * C::kRows + 128 * w;
-            const int rows = min(c.s.q_len * kv.group - r0, 128);  // of this row tile
-            if (rows <= 0) {
+            const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
+            const int rows = min(c.s.q_len * kv.group - r0, 128);  // of this CTA's part of the row tile (may be none)
+            if (c.s.q_len * kv.group <= c.rt * C::kRows + C::kTile * w) {
                 deal_next<C::kRows, kTcKeys>(a, c, n);
                 continue;
             }
             const bool mine = row < rows;
             const bool live = (row & ~31) < rows;   // some row of the warp is one
-            const int tok_i = (r0 + min(row, rows - 1)) / kv.group;
+            const int r_in = r0 + max(min(row, rows - 1), 0);
+            const int tok_i = r_in / kv.group;
             const int pos = c.s.pos0 + tok_i;
             const int p_hi = min(pos, kv.cap - 1);
             const int p_lo = a.window > 0 ? pos - a.window : -1;
@@ -557,7 +571,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + buf);
+                if (lane == 0) mbar_arrive(leaders(p_full + buf));
             }
             if (!ok) break;
             // ------------------------------------------------------------ the tile's output
@@ -565,7 +579,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const bool whole = n == c.n;
-            const int tok = c.s.q0 + tok_i, head = c.h * kv.group + (r0 + min(row, rows - 1)) % kv.group;
+            const int tok = c.s.q0 + tok_i, head = c.h * kv.group + r_in % kv.group;
             bool bad = false;
             if (live) {
                 const float2 lp = unpair(l2);
@@ -574,7 +588,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 bad = l != l;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + DH / 2 * half;
-                const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (c.u == u_begin ? 0 : 1)) * C::kRows + 128 * w + row;
+                const int64_t prow = (2 * static_cast<int64_t>(me) + (c.u == u_begin ? 0 : 1)) * C::kRows + C::kTile * w + 128 * rank + row;
                 float* pdst = a.part_o + prow * DH + DH / 2 * half;
 #pragma unroll 1
                 for (int i = 0; i < DH / 2; i += 32) {
@@ -608,7 +622,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_free + w);
+            if (lane == 0) mbar_arrive(leaders(o_free + w));
             if (live && whole) {
                 bad |= exchange(bad ? 1.f : 0.f) != 0.f;  // (and both halves of the row are stored)
                 unsigned again = half == 0 ? __ballot_sync(~0u, mine && bad) : 0;
@@ -624,9 +638,10 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (CG == 2) cluster_sync();  // the peer has read this CTA's shared and tensor memory
     if (warp == 0) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512));
+        tmem_free<CG>(tmem, 512);
     }
 }
 
@@ -650,16 +665,27 @@ cudaError_t make_map(const KvArgs& kv, const void* base, int64_t ps, int64_t rs,
 template <typename T, int DH>
 cudaError_t launch_t(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st) {
     using C = TcCfg<DH>;
-    const int box = std::min(tc_box_rows(a.kv.page), C::kVKeys);
+    const int box = std::min(tc_box_rows(a.kv.page), C::kKKeys);
     CUtensorMap kmap, vmap;
     if (cudaError_t e = make_map(a.kv, a.kv.k, a.kv.k_ps, a.kv.k_rs, a.kv.k_hs, dtype, box, &kmap); e != cudaSuccess) return e;
     if (cudaError_t e = make_map(a.kv, a.kv.v, a.kv.v_ps, a.kv.v_rs, a.kv.v_hs, dtype, box, &vmap); e != cudaSuccess) return e;
     cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    attend_tc_kernel<T, DH><<<n_ctas, C::kThreads, C::kSmem, st>>>(a, box, kmap, vmap);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || n_ctas < 2) return e;
-    return launch_attend_join<T, C::kRows, DH, 1>(a, n_ctas, st);
+    const int groups = n_ctas / C::CG;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(groups * C::CG);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C::CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attend_tc_kernel<T, DH>, a, box, kmap, vmap);
+    if (e != cudaSuccess || groups < 2) return e;
+    return launch_attend_join<T, C::kRows, DH, 1>(a, groups, st);
 }
 
 template <typename T>
@@ -674,7 +700,13 @@ cudaError_t launch_e(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st
 }  // namespace
 
 int tc_box_rows(int page) { return std::min(page & -page, kTcKeys); }
-int tc_rows(int d) { return padded_dim(d) == 256 ? TcCfg<256>::kRows : TcCfg<128>::kRows; }
+int tc_part_rows(int d, int n_ctas) {
+    switch (padded_dim(d)) {
+        case 64: return 2 * (n_ctas / TcCfg<64>::CG) * TcCfg<64>::kRows;
+        case 128: return 2 * (n_ctas / TcCfg<128>::CG) * TcCfg<128>::kRows;
+        default: return 2 * (n_ctas / TcCfg<256>::CG) * TcCfg<256>::kRows;
+    }
+}
 
 cudaError_t launch_attend_tc(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st) {
     return dtype == 0 ? launch_e<__nv_bfloat16>(a, dtype, n_ctas, st) : launch_e<__half>(a, dtype, n_ctas, st);

@@ -71,7 +71,7 @@ cudaError_t launch_attend_split(const AttendArgs& a, int dtype, int n_ctas, int 
 
 // Attention on tcgen05; pages of a multiple of 8 positions.
 int tc_box_rows(int page);  // rows of a page that one TMA box takes
-int tc_rows(int d);         // rows of a tile
+int tc_part_rows(int d, int n_ctas);  // rows of all pieces
 cudaError_t launch_attend_tc(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st);
 
 }  // namespace moe

@@ -95,7 +95,7 @@ AttendLayout attend_layout(const moe_kv_batch_t* b) {
     AttendLayout L{};
     L.n_ctas = moe::num_sms();
     const int d = static_cast<int>(b->head_dim);
-    const size_t rows = 2 * static_cast<size_t>(L.n_ctas) * std::max(moe::kSplitRows, moe::tc_rows(d));
+    const size_t rows = std::max(2 * L.n_ctas * moe::kSplitRows, moe::tc_part_rows(d, L.n_ctas));
     size_t at = 0;
     auto take = [&](size_t bytes) { size_t here = at; at = (at + bytes + 255) & ~size_t(255); return here; };
     L.hdr = take(sizeof(moe::Header));

@@ -106,9 +106,10 @@ struct Cursor {
     SeqInfo s;
 };
 
-// Called by the whole block.  prefix: n_seqs + 1 shared words.  Sets `c` in every thread.
+// The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + 1 shared
+// words.  Sets `c` in every thread.
 template <int ROWS, int KEYS>
-__device__ void deal_begin(const AttendArgs& a, long long* prefix, long long min_per, Cursor& c) {
+__device__ void deal_begin(const AttendArgs& a, long long* prefix, long long min_per, int me, int all, Cursor& c) {
     using D = Deal<ROWS, KEYS>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int B = a.kv.n_seqs;
@@ -141,8 +142,8 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, long long min
     }
     __syncthreads();
     const long long total = prefix[B];
-    c.per = max((total + gridDim.x - 1) / gridDim.x, a.split ? min_per : 1LL);
-    c.u = min(static_cast<long long>(blockIdx.x) * c.per, total);
+    c.per = max((total + all - 1) / all, a.split ? min_per : 1LL);
+    c.u = min(me * c.per, total);
     c.end = min(c.u + c.per, total);
     c.b = c.rt = c.h = c.off = c.first = c.n = 0;
     if (c.u >= c.end) return;
