@@ -9,9 +9,8 @@ namespace moe {
 constexpr int kJoinWarps = 8;
 
 // Block (c, y) stands for the boundary before CTA c + 1; the rows of a tile that several boundaries cut
-// are dealt over their blocks.  A row is taken by WPR warps, which share its pieces (few rows and many
-// pieces: 8; many rows and two or three pieces: 1).  The sums' order is that of the pieces' CTAs, whatever
-// order they were finished in, so two runs give the same bits.
+// are dealt over their blocks.  A row is taken by WPR warps, which share its pieces.  The sums' order is that
+// of the pieces' CTAs, whatever order they were finished in, so two runs give the same bits.
 template <typename T, int ROWS, int DH, int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendArgs a) {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -30,7 +29,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     const int r0 = rec.rt * ROWS, rows = min(s.q_len * kv.group - r0, ROWS);
     auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
     const int step = c1 - c0;
-    for (int k = blockIdx.y * kGroups; cta - (c0 + 1) + k * step < rows; k += gridDim.y * kGroups) {
+    for (int k = 0; cta - (c0 + 1) + k * step < rows; k += kGroups) {
         const int r = cta - (c0 + 1) + (k + group) * step;
         float mm = kNegInf, ll = 0.f;
         float2 acc[kVec / 2];
@@ -93,11 +92,90 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     }
 }
 
+// The same for tiles of many rows and few pieces, which lie as [component / 4][row][4]: a block takes 32 rows of
+// a tile, a lane per row, the warps the components in turn; the rows are written through shared memory.
+template <typename T, int ROWS, int DH>
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const AttendArgs a) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    constexpr int kPad = DH / 2 + 1;  // words of a staged row (odd: a column of rows lies in different banks)
+    __shared__ uint32_t rows_out[32][kPad];
+    __shared__ unsigned bad_rows;
+    const int cta = blockIdx.x + 1;
+    const BoundaryRec rec = a.recs[cta];
+    if (!rec.cut) return;
+    const KvArgs& kv = a.kv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = static_cast<int>(rec.begin / rec.per), c1 = static_cast<int>((rec.begin + rec.n - 1) / rec.per);
+    const SeqInfo s = seq_info(kv, rec.b);
+    const int r0 = rec.rt * ROWS, rows = min(s.q_len * kv.group - r0, ROWS);
+    auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
+    const int step = c1 - c0;  // boundaries of the tile: blocks of 32 rows go round them
+    for (int g = (cta - (c0 + 1)) + step * blockIdx.y; 32 * g < rows; g += step * gridDim.y) {
+        const int r = 32 * g + lane;
+        float mm = kNegInf;
+        for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, a.part_ml[slot_of(p) * ROWS + r].x);
+        const float base = mm == kNegInf ? 0.f : mm;
+        float ll = 0.f;
+        for (int p = c0; p <= c1; ++p) {
+            const float2 v = a.part_ml[slot_of(p) * ROWS + r];
+            ll += v.y * exp2_fast(v.x - base);
+        }
+        if (threadIdx.x == 0) bad_rows = 0;
+        __syncthreads();
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        bool bad = ll != ll;
+        constexpr int kMine = DH / 4 / kJoinWarps;
+        float4 acc[kMine];
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = c0; p <= c1; ++p) {
+            const int64_t slot = slot_of(p);
+            const float f = exp2_fast(a.part_ml[slot * ROWS + r].x - base);
+            const float4* o = reinterpret_cast<const float4*>(a.part_o + slot * ROWS * DH) + r;
+#pragma unroll
+            for (int x = 0; x < kMine; ++x) {
+                const float4 v = o[(warp + kJoinWarps * x) * ROWS];
+                acc[x].x += v.x * f;
+                acc[x].y += v.y * f;
+                acc[x].z += v.z * f;
+                acc[x].w += v.w * f;
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) {
+            const float4 v = acc[x];
+            bad |= v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w;
+            rows_out[lane][2 * (warp + kJoinWarps * x)] = Elem<T>::pack(v.x * inv, v.y * inv);
+            rows_out[lane][2 * (warp + kJoinWarps * x) + 1] = Elem<T>::pack(v.z * inv, v.w * inv);
+        }
+        const unsigned bads = __ballot_sync(~0u, bad && r < rows);
+        if (lane == 0 && bads) atomicOr(&bad_rows, bads);
+        if (warp == 0 && r < rows && a.lse) {
+            const int tok = s.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
+            a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
+        }
+        __syncthreads();
+        const unsigned again = bad_rows;
+        for (int y = warp; y < 32 && 32 * g + y < rows; y += kJoinWarps) {
+            const int rr = r0 + 32 * g + y;
+            const int tok = s.q0 + rr / kv.group, head = rec.h * kv.group + rr % kv.group;
+            if (again >> y & 1) {
+                attend_row<T>(a, rec.b, tok, head, s.pos0 + rr / kv.group);
+                continue;
+            }
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs);
+#pragma unroll
+            for (int x = 0; x < DH / 64; ++x)
+                if (2 * (lane + 32 * x) < kv.d) dst[lane + 32 * x] = rows_out[y][lane + 32 * x];
+        }
+        __syncthreads();
+    }
+}
+
 // Launched while the first kernel runs (it waits for its end by itself), one column of blocks per boundary.
-template <typename T, int ROWS, int DH, int WPR>
-cudaError_t launch_attend_join(const AttendArgs& a, int n_ctas, cudaStream_t st) {
+inline cudaError_t launch_join(void (*kernel)(AttendArgs), const AttendArgs& a, dim3 grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n_ctas - 1, WPR > 1 ? 1 : ROWS / kJoinWarps);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -105,7 +183,15 @@ cudaError_t launch_attend_join(const AttendArgs& a, int n_ctas, cudaStream_t st)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, ROWS, DH, WPR>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+template <typename T, int ROWS, int DH, int WPR>
+cudaError_t launch_attend_join(const AttendArgs& a, int n_ctas, cudaStream_t st) {
+    return launch_join(attend_join_kernel<T, ROWS, DH, WPR>, a, dim3(n_ctas - 1), st);
+}
+template <typename T, int ROWS, int DH>
+cudaError_t launch_attend_join_rows(const AttendArgs& a, int n_ctas, cudaStream_t st) {
+    return launch_join(attend_join_rows_kernel<T, ROWS, DH>, a, dim3(n_ctas - 1, ROWS / 32), st);
 }
 
 }  // namespace moe

@@ -581,42 +581,67 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const bool whole = n == c.n;
             const int tok = c.s.q0 + tok_i, head = c.h * kv.group + r_in % kv.group;
             bool bad = false;
+            const int part = 2 * me + (c.u == u_begin ? 0 : 1), r_tile = C::kTile * w + 128 * rank + row;
             if (live) {
                 const float2 lp = unpair(l2);
                 float l = lp.x + lp.y;
                 l += exchange(l);
                 bad = l != l;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + DH / 2 * half;
-                const int64_t prow = (2 * static_cast<int64_t>(me) + (c.u == u_begin ? 0 : 1)) * C::kRows + C::kTile * w + 128 * rank + row;
-                float* pdst = a.part_o + prow * DH + DH / 2 * half;
+                if (whole) {
+                    // 32 columns (four 16-byte chunks) at a time, transposed over four lanes: a store instruction then
+                    // writes 64-byte pieces of 8 rows instead of 16-byte pieces of 32.
+                    const int64_t at = tok * a.o_ts + head * a.o_hs;
+                    T* dst[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        dst[x] = static_cast<T*>(a.out) + __shfl_sync(~0u, at, (lane & ~3) + x) + DH / 2 * half + (lane & 3) * 8;
 #pragma unroll 1
-                for (int i = 0; i < DH / 2; i += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(o_col + i, o);
-                    tmem_ld_wait();
-                    tmem_tie<32>(o);
-                    if (!mine) continue;
-                    if (whole) {
+                    for (int i = 0; i < DH / 2; i += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_col + i, o);
+                        tmem_ld_wait();
+                        tmem_tie<32>(o);
+                        uint32_t u[4][4];
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) bad |= __uint_as_float(o[x]) != __uint_as_float(o[x]);
+                        for (int x = 0; x < 16; ++x) {
+                            const float y = __uint_as_float(o[2 * x]), z = __uint_as_float(o[2 * x + 1]);
+                            bad |= y != y || z != z;
+                            u[x / 4][x % 4] = Elem<T>::pack(y * inv, z * inv);
+                        }
 #pragma unroll
-                        for (int x = 0; x < 32; x += 8)
-                            if (DH / 2 * half + i + x < kv.d) {
-                                uint4 u;
-                                u.x = Elem<T>::pack(__uint_as_float(o[x]) * inv, __uint_as_float(o[x + 1]) * inv);
-                                u.y = Elem<T>::pack(__uint_as_float(o[x + 2]) * inv, __uint_as_float(o[x + 3]) * inv);
-                                u.z = Elem<T>::pack(__uint_as_float(o[x + 4]) * inv, __uint_as_float(o[x + 5]) * inv);
-                                u.w = Elem<T>::pack(__uint_as_float(o[x + 6]) * inv, __uint_as_float(o[x + 7]) * inv);
-                                *reinterpret_cast<uint4*>(dst + i + x) = u;
+                        for (int b = 1; b <= 2; b *= 2)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                if (x & b) continue;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    const uint32_t got = __shfl_xor_sync(~0u, lane & b ? u[x][y] : u[x | b][y], b);
+                                    if (lane & b) u[x][y] = got;
+                                    else u[x | b][y] = got;
+                                }
                             }
-                    } else {
+                        if (DH / 2 * half + i + (lane & 3) * 8 < kv.d)
 #pragma unroll
-                        for (int x = 0; x < 32; x += 4) *reinterpret_cast<uint4*>(pdst + i + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                            for (int x = 0; x < 4; ++x)
+                                if ((row & ~3) + x < rows) *reinterpret_cast<uint4*>(dst[x] + i) = make_uint4(u[x][0], u[x][1], u[x][2], u[x][3]);
+                    }
+                } else {
+                    // a piece: rows side by side ([component / 4][row][4]), so that a warp's stores are contiguous
+                    float* dst = a.part_o + (static_cast<int64_t>(part) * C::kRows * DH) + (DH / 8 * half * C::kRows + r_tile) * 4;
+#pragma unroll 1
+                    for (int i = 0; i < DH / 2; i += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_col + i, o);
+                        tmem_ld_wait();
+                        tmem_tie<32>(o);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            *reinterpret_cast<uint4*>(dst + (i / 4 + x) * C::kRows * 4) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                     }
                 }
                 if (mine && half == 0) {
-                    if (!whole) a.part_ml[prow] = make_float2(m == kNegInf ? kNegInf : m * sc, l);
+                    if (!whole) a.part_ml[part * C::kRows + r_tile] = make_float2(m == kNegInf ? kNegInf : m * sc, l);
                     else if (a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = l == 0.f ? kNegInf : (m * sc + log2f(l)) * kLn2;
                 }
                 tc_fence_before();
@@ -685,7 +710,7 @@ cudaError_t launch_t(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, attend_tc_kernel<T, DH>, a, box, kmap, vmap);
     if (e != cudaSuccess || groups < 2) return e;
-    return launch_attend_join<T, C::kRows, DH, 1>(a, groups, st);
+    return launch_attend_join_rows<T, C::kRows, DH>(a, groups, st);
 }
 
 template <typename T>
