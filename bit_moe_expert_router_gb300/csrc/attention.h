@@ -33,7 +33,7 @@ struct AppendArgs {
     const int32_t* positions;
     int64_t table_rows;
     int rot, interleaved;
-    float eps, weight_offset;
+    float eps, weight_offset, inv_d;
 };
 
 struct AttendArgs {

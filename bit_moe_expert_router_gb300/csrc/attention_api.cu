@@ -129,7 +129,7 @@ MOE_API int moe_w4a8_kv_append(const moe_kv_batch_t* batch, const moe_head_prep_
     if (!prep || prep->rot_dim < 0 || prep->rot_dim % 2 != 0 || prep->rot_dim > batch->head_dim || !(prep->eps >= 0.f) ||
         !std::isfinite(prep->eps) || !std::isfinite(prep->weight_offset))
         return MOE_ERR_INVALID_ARG;
-    if (prep->rot_dim > 0 && (!prep->cos_sin || !aligned4(prep->cos_sin) || prep->table_rows < 1)) return MOE_ERR_INVALID_ARG;
+    if (prep->rot_dim > 0 && (!prep->cos_sin || !aligned16(prep->cos_sin) || prep->table_rows < 1)) return MOE_ERR_INVALID_ARG;
     for (const float* w : {prep->q_weight, prep->k_weight})
         if (w && !aligned16(w)) return MOE_ERR_INVALID_ARG;
     if (prep->positions && !aligned4(prep->positions)) return MOE_ERR_INVALID_ARG;
@@ -160,6 +160,7 @@ MOE_API int moe_w4a8_kv_append(const moe_kv_batch_t* batch, const moe_head_prep_
     a.interleaved = prep->interleaved != 0;
     a.eps = prep->eps;
     a.weight_offset = prep->weight_offset;
+    a.inv_d = 1.f / static_cast<float>(a.kv.d);
     return moe::cuda_status(moe::launch_kv_append(a, static_cast<int>(batch->dtype), static_cast<cudaStream_t>(stream)), "kv_append");
 }
 
