@@ -18,7 +18,6 @@ from . import binding
 from .binding import MoeError, alloc_workspace  # noqa: F401
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
-_INT32_MAX = 2 ** 31 - 1
 _lib = None
 
 
@@ -87,6 +86,7 @@ class KVBatch:
         binding._need(q_start, "q_start", torch.int32, (seqs + 1,))
         binding._need(kv_len, "kv_len", torch.int32, (seqs,))
         self.device = binding._one_device("KVBatch", (k_cache, v_cache, block_table, q_start, kv_len))
+        self._index = self.device.index
         self.dtype = k_cache.dtype
         self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), hkv, d
         self.k_cache, self.v_cache = k_cache, v_cache
@@ -113,14 +113,14 @@ class KVBatch:
 
     def _rows(self, t, name, n, heads):
         """(address, token stride, head stride) of a [n, heads, head_dim] tensor of this batch."""
-        if t.dtype is not self.dtype:
-            raise TypeError(f"{name}: dtype {t.dtype}, expected {self.dtype}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-        if t.shape != (n, heads, self.head_dim):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n, heads, self.head_dim)}")
-        ts, hs, es = t.stride()
-        if es != 1:
+        ts, hs, es = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (n, heads, self.head_dim) or es != 1:
+            if t.dtype is not self.dtype:
+                raise TypeError(f"{name}: dtype {t.dtype}, expected {self.dtype}")
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+            if t.shape != (n, heads, self.head_dim):
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n, heads, self.head_dim)}")
             raise ValueError(f"{name}: the components of a head must be contiguous")
         return t.data_ptr(), ts, hs
 
@@ -153,7 +153,11 @@ class HeadPrep:
         given = tuple(t for t in (cos_sin, q_weight, k_weight, positions) if t is not None)
         self.device = binding._one_device("HeadPrep", given) if given else None
         self.cos_sin, self.q_weight, self.k_weight, self.positions = cos_sin, q_weight, k_weight, positions
-        self.weight_dims = {w.numel() for w in (q_weight, k_weight) if w is not None}
+        dims = {w.numel() for w in (q_weight, k_weight) if w is not None}
+        if len(dims) > 1:
+            raise ValueError(f"q_weight and k_weight of different sizes: {sorted(dims)}")
+        self._weight_dim = dims.pop() if dims else 0
+        self._index = self.device.index if given else -1
         at = [None if t is None else t.data_ptr() for t in (cos_sin, q_weight, k_weight, positions)]
         self._c = _HeadPrep(at[0], rows, rot, int(interleaved), at[1], at[2], at[3], eps, weight_offset)
         self._p = ctypes.addressof(self._c)
@@ -194,14 +198,14 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda
     return (torch.cat([angle.cos(), angle.sin()], dim=1) * size).float().to(device)
 
 
-def _enqueue(fn: str, device, *args):
-    """Calls `fn` with `args` and the current stream of `device`, with that device current."""
-    call = getattr(_load(), fn)
-    if device.index == torch.cuda.current_device():
-        status = call(*args, torch.cuda.current_stream(device).cuda_stream)
+def _enqueue(fn: str, index: int, *args):
+    """Calls `fn` with `args` and the current stream of device `index`, with that device current."""
+    call = getattr(_lib or _load(), fn)
+    if torch._C._cuda_getDevice() == index:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            status = call(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != 0:
         raise MoeError(fn, status)
 
@@ -213,15 +217,15 @@ def moe_w4a8_kv_append(batch: KVBatch, prep: HeadPrep, q, k, v, q_out):
     multiples of 16 bytes.  q_out may be q.
     """
     n = q.shape[0]
-    if prep.device is not None and prep.device != batch.device:
+    hq, hkv = batch.n_q_heads, batch.n_kv_heads
+    if prep._index >= 0 and prep._index != batch._index:
         raise ValueError(f"HeadPrep is on {prep.device}, the cache on {batch.device}")
-    if prep.weight_dims and prep.weight_dims != {batch.head_dim}:
-        raise ValueError(f"norm weights of {sorted(prep.weight_dims)} components, heads of {batch.head_dim}")
+    if prep._weight_dim and prep._weight_dim != batch.head_dim:
+        raise ValueError(f"norm weights of {prep._weight_dim} components, heads of {batch.head_dim}")
     if prep.positions is not None and prep.positions.shape != (n,):
         raise ValueError(f"positions: shape {tuple(prep.positions.shape)}, expected {(n,)}")
-    _enqueue("moe_w4a8_kv_append", batch.device, batch._p, prep._p, n, *batch._rows(q, "q", n, batch.n_q_heads),
-             *batch._rows(k, "k", n, batch.n_kv_heads), *batch._rows(v, "v", n, batch.n_kv_heads),
-             *batch._rows(q_out, "q_out", n, batch.n_q_heads))
+    _enqueue("moe_w4a8_kv_append", batch._index, batch._p, prep._p, n, *batch._rows(q, "q", n, hq), *batch._rows(k, "k", n, hkv),
+             *batch._rows(v, "v", n, hkv), *batch._rows(q_out, "q_out", n, hq))
     return q_out
 
 
@@ -233,15 +237,16 @@ def moe_w4a8_paged_attention(batch: KVBatch, q, out, lse=None, scale: float | No
     them.  workspace: batch.alloc_workspace().
     """
     n = q.shape[0]
+    hq = batch.n_q_heads
+    at = None
     if lse is not None:
-        if lse.dtype is not torch.float32 or lse.shape != (n, batch.n_q_heads) or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous float32 tensor of shape {(n, batch.n_q_heads)}")
-        if lse.device != batch.device:
+        if lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape {(n, hq)}")
+        if lse.get_device() != batch._index:
             raise ValueError(f"lse is on {lse.device}, the cache on {batch.device}")
-    if workspace.device != batch.device:
+        at = lse.data_ptr()
+    if workspace.get_device() != batch._index:
         raise ValueError(f"workspace is on {workspace.device}, the cache on {batch.device}")
-    wp, wb = binding._ws_view(workspace)
-    _enqueue("moe_w4a8_paged_attention", batch.device, batch._p, n, *batch._rows(q, "q", n, batch.n_q_heads),
-             *batch._rows(out, "out", n, batch.n_q_heads), None if lse is None else lse.data_ptr(),
-             batch.head_dim ** -0.5 if scale is None else scale, window, wp, wb)
+    _enqueue("moe_w4a8_paged_attention", batch._index, batch._p, n, *batch._rows(q, "q", n, hq), *batch._rows(out, "out", n, hq),
+             at, batch.head_dim ** -0.5 if scale is None else scale, window, *binding._ws_view(workspace))
     return out
