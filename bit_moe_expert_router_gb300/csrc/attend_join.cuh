@@ -8,66 +8,77 @@ namespace moe {
 
 constexpr int kJoinWarps = 8;
 
-// Block (c, y) stands for the boundary before CTA c + 1; the rows of a tile that several boundaries cut
-// are dealt over their blocks.  A row is taken by WPR warps, which share its pieces.  The sums' order is that
-// of the pieces' CTAs, whatever order they were finished in, so two runs give the same bits.
-template <typename T, int ROWS, int DH, int WPR>
+// Block c stands for the boundary before CTA c + 1; the rows of a tile that several boundaries cut are dealt
+// over their blocks.  A row is taken by one warp, or by eight that share its pieces where they are
+// many.  The sums' order is that of the pieces' CTAs, whatever order they were finished in, so two
+// runs give the same bits.
+template <typename T, int ROWS, int DH>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendArgs a) {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    constexpr int kGroups = kJoinWarps / WPR;
-    constexpr int kVec = DH / 32;  // components per lane: 2 lane + 64 x, + 1
-    __shared__ float2 part[WPR > 1 ? kJoinWarps : 1][WPR > 1 ? DH / 2 : 1];
+    constexpr int kVec = DH / 64;  // pairs of components per lane: lane + 32 x
+    __shared__ float2 part[kJoinWarps][DH / 2];
     __shared__ float part_l[kJoinWarps];
     const int cta = blockIdx.x + 1;
     const BoundaryRec rec = a.recs[cta];
     if (!rec.cut) return;
     const KvArgs& kv = a.kv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int group = warp / WPR, wi = warp % WPR;
     const int c0 = static_cast<int>(rec.begin / rec.per), c1 = static_cast<int>((rec.begin + rec.n - 1) / rec.per);
-    const SeqInfo s = seq_info(kv, rec.b);
-    const int r0 = rec.rt * ROWS, rows = min(s.q_len * kv.group - r0, ROWS);
+    const int share = c1 - c0 + 1 > 8 ? kJoinWarps : 1;  // warps per row
+    const int wi = share > 1 ? warp : 0;
+    const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
     auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
     const int step = c1 - c0;
-    for (int k = 0; cta - (c0 + 1) + k * step < rows; k += kGroups) {
-        const int r = cta - (c0 + 1) + (k + group) * step;
+    for (int k = 0; cta - (c0 + 1) + k * step < rows; k += kJoinWarps / share) {
+        const int r = cta - (c0 + 1) + (k + (share > 1 ? 0 : warp)) * step;
         float mm = kNegInf, ll = 0.f;
-        float2 acc[kVec / 2];
+        float2 acc[kVec];
 #pragma unroll
-        for (int x = 0; x < kVec / 2; ++x) acc[x] = make_float2(0.f, 0.f);
+        for (int x = 0; x < kVec; ++x) acc[x] = make_float2(0.f, 0.f);
         if (r < rows) {
             for (int p = c0 + lane; p <= c1; p += 32) mm = fmaxf(mm, a.part_ml[slot_of(p) * ROWS + r].x);
+            constexpr int kAhead = 4;
+            for (int p0 = c0 + wi; p0 <= c1; p0 += kAhead * share) {
+                float2 v[kAhead], o[kAhead][kVec];
 #pragma unroll
-            for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
-            const float base = mm == kNegInf ? 0.f : mm;
-#pragma unroll 4
-            for (int p = c0 + wi; p <= c1; p += WPR) {
-                const int64_t slot = slot_of(p);
-                const float2 v = a.part_ml[slot * ROWS + r];
-                const float f = exp2_fast(v.x - base);
-                const float2* o = reinterpret_cast<const float2*>(a.part_o + (slot * ROWS + r) * DH) + lane;
-                ll += v.y * f;
+                for (int y = 0; y < kAhead; ++y) {
+                    const int p = min(p0 + y * share, c1);
+                    const int64_t at = slot_of(p) * ROWS + r;
+                    v[y] = a.part_ml[at];
 #pragma unroll
-                for (int x = 0; x < kVec / 2; ++x) {
-                    const float2 w = o[32 * x];
-                    acc[x].x += w.x * f;
-                    acc[x].y += w.y * f;
+                    for (int x = 0; x < kVec; ++x) o[y][x] = reinterpret_cast<const float2*>(a.part_o + at * DH)[lane + 32 * x];
+                }
+                if (p0 == c0 + wi) {
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
+                }
+                const float base = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) {
+                    if (p0 + y * share > c1) break;
+                    const float f = exp2_fast(v[y].x - base);
+                    ll += v[y].y * f;
+#pragma unroll
+                    for (int x = 0; x < kVec; ++x) {
+                        acc[x].x += o[y][x].x * f;
+                        acc[x].y += o[y][x].y * f;
+                    }
                 }
             }
         }
-        if constexpr (WPR > 1) {
+        if (share > 1) {  // (every warp of the block has the same row)
             __syncthreads();
 #pragma unroll
-            for (int x = 0; x < kVec / 2; ++x) part[warp][lane + 32 * x] = acc[x];
+            for (int x = 0; x < kVec; ++x) part[warp][lane + 32 * x] = acc[x];
             if (lane == 0) part_l[warp] = ll;
             __syncthreads();
-            if (wi == 0) {
+            if (warp == 0) {
 #pragma unroll
-                for (int w = 1; w < WPR; ++w) {
-                    ll += part_l[warp + w];
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    ll += part_l[w];
 #pragma unroll
-                    for (int x = 0; x < kVec / 2; ++x) {
-                        const float2 v = part[warp + w][lane + 32 * x];
+                    for (int x = 0; x < kVec; ++x) {
+                        const float2 v = part[w][lane + 32 * x];
                         acc[x].x += v.x;
                         acc[x].y += v.y;
                     }
@@ -75,18 +86,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
             }
         }
         if (wi != 0 || r >= rows) continue;
-        const int tok = s.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
+        const int tok = rec.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
         bool bad = ll != ll;
 #pragma unroll
-        for (int x = 0; x < kVec / 2; ++x) bad |= acc[x].x != acc[x].x || acc[x].y != acc[x].y;
+        for (int x = 0; x < kVec; ++x) bad |= acc[x].x != acc[x].x || acc[x].y != acc[x].y;
         if (__any_sync(~0u, bad)) {
-            attend_row<T>(a, rec.b, tok, head, s.pos0 + (r0 + r) / kv.group);
+            attend_row<T>(a, rec.b, tok, head, rec.pos0 + (r0 + r) / kv.group);
             continue;
         }
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + 2 * lane;
 #pragma unroll
-        for (int x = 0; x < kVec / 2; ++x)
+        for (int x = 0; x < kVec; ++x)
             if (2 * lane + 64 * x < kv.d) *reinterpret_cast<uint32_t*>(dst + 64 * x) = Elem<T>::pack(acc[x].x * inv, acc[x].y * inv);
         if (lane == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
     }
@@ -106,8 +117,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const
     const KvArgs& kv = a.kv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = static_cast<int>(rec.begin / rec.per), c1 = static_cast<int>((rec.begin + rec.n - 1) / rec.per);
-    const SeqInfo s = seq_info(kv, rec.b);
-    const int r0 = rec.rt * ROWS, rows = min(s.q_len * kv.group - r0, ROWS);
+    const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
     auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
     const int step = c1 - c0;  // boundaries of the tile: blocks of 32 rows go round them
     for (int g = (cta - (c0 + 1)) + step * blockIdx.y; 32 * g < rows; g += step * gridDim.y) {
@@ -151,16 +161,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const
         const unsigned bads = __ballot_sync(~0u, bad && r < rows);
         if (lane == 0 && bads) atomicOr(&bad_rows, bads);
         if (warp == 0 && r < rows && a.lse) {
-            const int tok = s.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
+            const int tok = rec.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
             a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
         }
         __syncthreads();
         const unsigned again = bad_rows;
         for (int y = warp; y < 32 && 32 * g + y < rows; y += kJoinWarps) {
             const int rr = r0 + 32 * g + y;
-            const int tok = s.q0 + rr / kv.group, head = rec.h * kv.group + rr % kv.group;
+            const int tok = rec.q0 + rr / kv.group, head = rec.h * kv.group + rr % kv.group;
             if (again >> y & 1) {
-                attend_row<T>(a, rec.b, tok, head, s.pos0 + rr / kv.group);
+                attend_row<T>(a, rec.b, tok, head, rec.pos0 + rr / kv.group);
                 continue;
             }
             uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs);
@@ -185,9 +195,9 @@ inline cudaError_t launch_join(void (*kernel)(AttendArgs), const AttendArgs& a, 
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
-template <typename T, int ROWS, int DH, int WPR>
+template <typename T, int ROWS, int DH>
 cudaError_t launch_attend_join(const AttendArgs& a, int n_ctas, cudaStream_t st) {
-    return launch_join(attend_join_kernel<T, ROWS, DH, WPR>, a, dim3(n_ctas - 1), st);
+    return launch_join(attend_join_kernel<T, ROWS, DH>, a, dim3(n_ctas - 1), st);
 }
 template <typename T, int ROWS, int DH>
 cudaError_t launch_attend_join_rows(const AttendArgs& a, int n_ctas, cudaStream_t st) {

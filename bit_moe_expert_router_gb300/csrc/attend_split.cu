@@ -14,28 +14,34 @@
 // 16-byte cp.async into its own ring (chunks XOR-swizzled by row so that
 // ldmatrix reads without bank conflicts), and keeps its own m, l, o; no
 // barrier inside a piece.  At a piece's end the warps' states are joined in
-// shared memory.  The pieces are equal shares of all (sequence, head, 16 keys)
-// units of the batch (the deal), so ragged lengths balance; pieces of one row tile go
-// to the workspace and a second kernel joins them in a fixed order.
+// shared memory, while the copies of the CTA's next piece are on their way: a
+// warp's copies run through its units of all pieces without a stop.  The pieces
+// come from the deal; pieces of one row tile go to the workspace and a second
+// kernel joins them in a fixed order.
 #include "attend_join.cuh"
 #include "attention_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kKeys = 16;  // keys of a unit: one warp's step
+constexpr int kKeys = 16;       // keys of a unit: one warp's step
+constexpr int kMinShare = 4;    // units of a CTA at least, where there are few,
+constexpr int kOwnPieces = 64;  // and at most for pieces that end with their tile
 
 template <int DH>
 struct SplitCfg {
     static constexpr int kWarps = DH == 256 ? 4 : 8;
-    static constexpr int kStages = DH == 64 ? 6 : 3;
+    static constexpr int kStages = DH == 64 ? 4 : 2;
     static constexpr int kCpr = DH / 8;                    // 16-byte chunks per row
     static constexpr int kTile = kKeys * DH;               // elements of K (or V) in a stage
     static constexpr int kQBytes = kSplitRows * DH * 2;
     static constexpr int kWarpBytes = kStages * 2 * kTile * 2;
-    static constexpr int kSmem = kQBytes + kWarps * kWarpBytes + kWarps * kSplitRows * 8;
+    static constexpr int kStateBytes = kSplitRows * DH * 4;  // a warp's state at the join
+    static constexpr int kOffRings = 2 * kQBytes;            // (the queries of this piece and of the next)
+    static constexpr int kOffState = kOffRings + kWarps * kWarpBytes;
+    static constexpr int kOffMl = kOffState + kWarps * kStateBytes;
+    static constexpr int kOffPrefix = kOffMl + kWarps * kSplitRows * 8;
     static constexpr bool kQRegs = DH <= 128;              // the queries' fragments stay in registers
-    static_assert(kWarpBytes >= kSplitRows * DH * 4, "a warp's ring holds its state at the join");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -87,70 +93,122 @@ struct Rows {
     }
 };
 
+// A warp's way through its keys: the unit whose copies come next, in its piece.
+template <bool ALIGNED>
+struct Feed {
+    Cursor c;
+    int unit, end;     // next unit of this warp in the piece, the piece's end
+    int hi;            // keys from here on no row of the tile sees
+    Rows<ALIGNED> rows;
+    template <int WARPS>
+    __device__ __forceinline__ void enter(const AttendArgs& a, int warp) {  // the cursor's piece, or a later one
+        while (c.u < c.end) {
+            int lo;
+            const int r0 = c.rt * kSplitRows;
+            key_range(a.kv, a.window, c.s, r0, min(r0 + kSplitRows, c.s.q_len * a.kv.group), lo, hi);
+            unit = c.first + c.off + warp;
+            end = c.first + c.off + c.take;
+            if (unit < end) {
+                rows.fetch(a.kv, c.b, unit, end);
+                return;
+            }
+            deal_next<kSplitRows, kKeys>(a, c);
+        }
+    }
+};
+
 template <typename T, int DH, bool ALIGNED>
 __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_kernel(const AttendArgs a) {
     using C = SplitCfg<DH>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    T* sq = reinterpret_cast<T*>(smem);
-    unsigned char* rings = smem + C::kQBytes;
-    float2* ml = reinterpret_cast<float2*>(rings + C::kWarps * C::kWarpBytes);  // [warps][rows]
-    long long* prefix = reinterpret_cast<long long*>(reinterpret_cast<unsigned char*>(ml) + C::kWarps * kSplitRows * 8);
+    float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);  // [warps][rows]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const KvArgs& kv = a.kv;
     const T* kc = static_cast<const T*>(kv.k);
     const T* vc = static_cast<const T*>(kv.v);
-    unsigned char* ring = rings + warp * C::kWarpBytes;
+    unsigned char* ring = smem + C::kOffRings + warp * C::kWarpBytes;
     const int chunks = kv.d / 8;
 
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     // components past D are never copied: zero once (rows of the ring, and of the queries)
-    if (kv.d < DH) {
-        for (int i = threadIdx.x; i < (C::kQBytes + C::kWarps * C::kWarpBytes) / 16; i += blockDim.x)
-            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-    }
+    if (kv.d < DH)
+        for (int i = threadIdx.x; i < C::kOffState / 16; i += blockDim.x) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
 
     if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
     Cursor c;
-    deal_begin<kSplitRows, kKeys>(a, prefix, 16, blockIdx.x, gridDim.x, c);
-    if (a.split && threadIdx.x == 0) {
-        BoundaryRec r;
-        r.begin = c.u - c.off;
-        r.per = c.per;
-        r.n = c.n;
-        r.cut = c.u < c.end && c.off > 0;
-        r.b = c.b;
-        r.rt = c.rt;
-        r.h = c.h;
-        r.pad = 0;
-        a.recs[blockIdx.x] = r;
-    }
+    deal_begin<kSplitRows, kKeys>(a, reinterpret_cast<long long*>(smem + C::kOffPrefix), kMinShare, kOwnPieces, blockIdx.x, gridDim.x, c);
     clear_stray_rows<T>(a);
     const float sc = a.scale * kLog2e;
     const long long u_begin = c.u;
 
-    while (c.u < c.end) {
-        const int taken = deal_take(a, c);
-        const int r0 = c.rt * kSplitRows;
-        const int rows = min(c.s.q_len * kv.group - r0, kSplitRows);
-        int lo, hi;
-        key_range(kv, a.window, c.s, r0, r0 + rows, lo, hi);
-        const int unit0 = c.first + c.off, unit1 = unit0 + taken;
-
-        // the queries of the tile
+    Feed<ALIGNED> feed;
+    feed.c = c;
+    feed.template enter<C::kWarps>(a, warp);
+    auto issue = [&](int stage) {
+        if (feed.c.u < feed.c.end) {
+            Rows<ALIGNED>& rw = feed.rows;
+            rw.settle(kv, feed.c.h);
+            unsigned char* sk = ring + stage * 2 * C::kTile * 2;
+            unsigned char* sv = sk + C::kTile * 2;
+            const int key0 = feed.unit * kKeys;
+            const int x = lane % C::kCpr;
+            constexpr int kRowsPer = 32 / C::kCpr;
+#pragma unroll
+            for (int i = 0; i < kKeys / kRowsPer; ++i) {
+                const int r = i * kRowsPer + lane / C::kCpr;
+                int64_t ko, vo;
+                bool ok;
+                if constexpr (ALIGNED) {
+                    ko = rw.k + r * kv.k_rs;
+                    vo = rw.v + r * kv.v_rs;
+                    ok = rw.ok;
+                } else {
+                    ko = __shfl_sync(~0u, rw.k, r);
+                    vo = __shfl_sync(~0u, rw.v, r);
+                    ok = __shfl_sync(~0u, rw.ok ? 1 : 0, r);
+                }
+                ok = ok && key0 + r < feed.hi;
+                if (x < chunks) {  // a key that no row sees is zeros: whatever the cache holds there stays out
+                    cp_async16(sk + chunk_at<C::kCpr>(r, x), kc + (ok ? ko + x * 8 : 0), ok ? 16 : 0);
+                    cp_async16(sv + chunk_at<C::kCpr>(r, x), vc + (ok ? vo + x * 8 : 0), ok ? 16 : 0);
+                }
+            }
+            feed.unit += C::kWarps;
+            if (feed.unit < feed.end) {
+                rw.fetch(kv, feed.c.b, feed.unit, feed.end);
+            } else {
+                deal_next<kSplitRows, kKeys>(a, feed.c);
+                feed.template enter<C::kWarps>(a, warp);
+            }
+        }
+        cp_async_commit();
+    };
+    // the queries of the cursor's tile; zeros past the rows
+    auto queries = [&](int buf) {
+        const int r0 = c.rt * kSplitRows, rows = min(c.s.q_len * kv.group - r0, kSplitRows);
         for (int i = threadIdx.x; i < kSplitRows * chunks; i += blockDim.x) {
             const int r = i / chunks, x = i - r * chunks;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int tok = c.s.q0 + (r0 + r) / kv.group, head = c.h * kv.group + (r0 + r) % kv.group;
-                w = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + x * 8);
-            }
-            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sq) + chunk_at<C::kCpr>(r, x)) = w;
+            const int rr = r0 + min(r, rows - 1);
+            const int tok = c.s.q0 + rr / kv.group, head = c.h * kv.group + rr % kv.group;
+            cp_async16(smem + buf * C::kQBytes + chunk_at<C::kCpr>(r, x), static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + x * 8,
+                       r < rows ? 16 : 0);
         }
-        __syncthreads();
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) issue(s);
+    int stage = 0, fill = C::kStages - 1, qb = 0;
+    if (c.u < c.end) queries(0);
+    cp_async_wait<0>();
+    __syncthreads();
+
+    while (c.u < c.end) {
+        const int r0 = c.rt * kSplitRows;
+        const int rows = min(c.s.q_len * kv.group - r0, kSplitRows);
+        const int unit0 = c.first + c.off, unit1 = unit0 + c.take;
         const int mat = lane >> 3, mrow = lane & 7;
         uint32_t qf[C::kQRegs ? DH / 16 : 1][4];
-        const uint32_t q_addr = smem_u32(sq);
+        const uint32_t q_addr = smem_u32(smem + qb * C::kQBytes);
         if constexpr (C::kQRegs) {
 #pragma unroll
             for (int ks = 0; ks < DH / 16; ++ks) ldsm4(qf[ks], q_addr + chunk_at<C::kCpr>((mat & 1) * 8 + mrow, ks * 2 + (mat >> 1)));
@@ -172,45 +230,6 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
         for (int n = 0; n < DH / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
 
-        Rows<ALIGNED> rw;
-        rw.fetch(kv, c.b, unit0 + warp, unit1);
-        int fetch_unit = unit0 + warp;  // the unit whose ids rw holds
-        auto issue = [&](int stage) {
-            if (fetch_unit < unit1) {
-                rw.settle(kv, c.h);
-                unsigned char* sk = ring + stage * 2 * C::kTile * 2;
-                unsigned char* sv = sk + C::kTile * 2;
-                const int key0 = fetch_unit * kKeys;
-                const int x = lane % C::kCpr;
-                constexpr int kRowsPer = 32 / C::kCpr;
-#pragma unroll
-                for (int i = 0; i < kKeys / kRowsPer; ++i) {
-                    const int r = i * kRowsPer + lane / C::kCpr;
-                    int64_t ko, vo;
-                    bool ok;
-                    if constexpr (ALIGNED) {
-                        ko = rw.k + r * kv.k_rs;
-                        vo = rw.v + r * kv.v_rs;
-                        ok = rw.ok;
-                    } else {
-                        ko = __shfl_sync(~0u, rw.k, r);
-                        vo = __shfl_sync(~0u, rw.v, r);
-                        ok = __shfl_sync(~0u, rw.ok ? 1 : 0, r);
-                    }
-                    ok = ok && key0 + r < hi;
-                    if (x < chunks) {  // a key that no row sees is zeros: whatever the cache holds there stays out
-                        cp_async16(sk + chunk_at<C::kCpr>(r, x), kc + (ok ? ko + x * 8 : 0), ok ? 16 : 0);
-                        cp_async16(sv + chunk_at<C::kCpr>(r, x), vc + (ok ? vo + x * 8 : 0), ok ? 16 : 0);
-                    }
-                }
-                fetch_unit += C::kWarps;
-                rw.fetch(kv, c.b, fetch_unit, unit1);
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int s = 0; s < C::kStages - 1; ++s) issue(s);
-        int stage = 0, fill = C::kStages - 1;
         for (int u = unit0 + warp; u < unit1; u += C::kWarps) {
             issue(fill);
             fill = fill + 1 == C::kStages ? 0 : fill + 1;
@@ -218,20 +237,20 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
             __syncwarp();
             const uint32_t sk = smem_u32(ring + stage * 2 * C::kTile * 2), sv = sk + C::kTile * 2;
             stage = stage + 1 == C::kStages ? 0 : stage + 1;
-            float s[2][4] = {};
+            float s[2][4] = {}, s2[2][4] = {};  // (two sums each: the products of one wait for one another)
 #pragma unroll
             for (int ks = 0; ks < DH / 16; ++ks) {
                 uint32_t kf[4];
                 ldsm4(kf, sk + chunk_at<C::kCpr>((mat >> 1) * 8 + mrow, ks * 2 + (mat & 1)));
+                uint32_t qv[4];
                 if constexpr (C::kQRegs) {
-                    mma16816<T>(s[0], qf[ks], kf[0], kf[1]);
-                    mma16816<T>(s[1], qf[ks], kf[2], kf[3]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) qv[x] = qf[ks][x];
                 } else {
-                    uint32_t qv[4];
                     ldsm4(qv, q_addr + chunk_at<C::kCpr>((mat & 1) * 8 + mrow, ks * 2 + (mat >> 1)));
-                    mma16816<T>(s[0], qv, kf[0], kf[1]);
-                    mma16816<T>(s[1], qv, kf[2], kf[3]);
                 }
+                mma16816<T>(ks & 1 ? s2[0] : s[0], qv, kf[0], kf[1]);
+                mma16816<T>(ks & 1 ? s2[1] : s[1], qv, kf[2], kf[3]);
             }
             const int key0 = u * kKeys;
             const bool masked = key0 + kKeys - 1 > min(all_hi, kv.cap - 1) || key0 <= all_lo;
@@ -240,7 +259,7 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float v = s[n][i] * sc;
+                    float v = (s[n][i] + s2[n][i]) * sc;
                     if (masked) {
                         const int key = key0 + n * 8 + (lane & 3) * 2 + (i & 1);
                         if (key > p_hi[i >> 1] || key <= p_lo[i >> 1]) v = kNegInf;
@@ -290,11 +309,9 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
             }
             __syncwarp();  // the stage is read before its next copies
         }
-        cp_async_wait<0>();
-        __syncwarp();
 
-        // this warp's state into its ring
-        float* so = reinterpret_cast<float*>(ring);  // [rows][DH]
+        // this warp's state
+        float* so = reinterpret_cast<float*>(smem + C::kOffState + warp * C::kStateBytes);  // [rows][DH]
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             l[x] += __shfl_xor_sync(~0u, l[x], 1);
@@ -307,9 +324,13 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
                     *reinterpret_cast<float2*>(so + r * DH + n * 8 + (lane & 3) * 2) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
             }
         }
-        __syncthreads();
-        const bool whole = taken == c.n;
+        const bool whole = c.whole();
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (c.u == u_begin ? 0 : 1);
+        const int q0 = c.s.q0, pos0 = c.s.pos0, h = c.h, b = c.b;
+        deal_next<kSplitRows, kKeys>(a, c);
+        qb ^= 1;
+        if (c.u < c.end) queries(qb);  // of the next piece
+        __syncthreads();
         // the join of the warps: a warp per row
         for (int r = warp; r < rows; r += C::kWarps) {
             float mw = kNegInf, lw = 0.f;
@@ -332,7 +353,7 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
             for (int w = 0; w < C::kWarps; ++w) {
                 const float fx = __shfl_sync(~0u, fw, w);
                 if (fx == 0.f) continue;
-                const float* p = reinterpret_cast<const float*>(rings + w * C::kWarpBytes) + r * DH + lane * 2;
+                const float* p = reinterpret_cast<const float*>(smem + C::kOffState + w * C::kStateBytes) + r * DH + lane * 2;
 #pragma unroll
                 for (int x = 0; x < DH / 64; ++x) {
                     const float2 v = *reinterpret_cast<const float2*>(p + x * 64);
@@ -341,13 +362,13 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
                 }
             }
             if (whole) {
-                const int tok = c.s.q0 + (r0 + r) / kv.group, head = c.h * kv.group + (r0 + r) % kv.group;
+                const int tok = q0 + (r0 + r) / kv.group, head = h * kv.group + (r0 + r) % kv.group;
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
                 bool bad = ll != ll;
 #pragma unroll
                 for (int x = 0; x < DH / 32; ++x) bad |= acc[x] != acc[x];
                 if (__any_sync(~0u, bad)) {
-                    attend_row<T>(a, c.b, tok, head, c.s.pos0 + (r0 + r) / kv.group);
+                    attend_row<T>(a, b, tok, head, pos0 + (r0 + r) / kv.group);
                     continue;
                 }
                 T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + lane * 2;
@@ -363,27 +384,22 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
                 if (lane == 0) a.part_ml[slot * kSplitRows + r] = make_float2(mm, ll);
             }
         }
+        cp_async_wait<0>();
         __syncthreads();
-        if (kv.d < DH) {  // the state overwrote the ring's zero columns
-            for (int i = threadIdx.x; i < C::kWarps * C::kWarpBytes / 16; i += blockDim.x)
-                reinterpret_cast<uint4*>(rings)[i] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-        }
-        deal_next<kSplitRows, kKeys>(a, c, taken);
     }
 }
 
 template <typename T, int DH, bool ALIGNED>
 cudaError_t launch_t(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
     using C = SplitCfg<DH>;
-    const int smem = C::kSmem + (a.kv.n_seqs + 1) * 8;
+    const int smem = C::kOffPrefix + (a.kv.n_seqs + 1) * 8;
     cudaError_t e = cudaFuncSetAttribute(attend_split_kernel<T, DH, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = a.split ? n_ctas : max(1, min(max_items, n_ctas * 8));
     attend_split_kernel<T, DH, ALIGNED><<<grid, C::kWarps * 32, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.split || grid < 2) return e;
-    return launch_attend_join<T, kSplitRows, DH, 8>(a, grid, st);
+    return launch_attend_join<T, kSplitRows, DH>(a, grid, st);
 }
 
 template <typename T, int DH>

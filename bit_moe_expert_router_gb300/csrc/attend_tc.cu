@@ -152,19 +152,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     if (warp == 0) tmem_alloc<CG>(tmem_holder, 512);
     const int rank = CG == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CG;
     Cursor c;
-    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, me, gridDim.x / CG, c);  // (scratch: the ring)
-    if (rank == 0 && tid == 0) {
-        BoundaryRec r;
-        r.begin = c.u - c.off;
-        r.per = c.per;
-        r.n = c.n;
-        r.cut = c.u < c.end && c.off > 0;
-        r.b = c.b;
-        r.rt = c.rt;
-        r.h = c.h;
-        r.pad = 0;
-        a.recs[me] = r;
-    }
+    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, 16, me, gridDim.x / CG, c);  // (scratch: the ring)
     clear_stray_rows<T>(a);
     tc_fence_before();
     fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
@@ -217,7 +205,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 if (++slot == C::kSlots) slot = 0, phase ^= 1;
             };
             while (ok && c.u < c.end) {
-                const int n = deal_take(a, c);
+                const int n = c.take;
                 const int rows = min(c.s.q_len * kv.group - c.rt * C::kRows, C::kRows);
                 const int act = C::NQ == 2 && rows > C::kTile ? 2 : 1;
                 if constexpr (C::NQ == 2) {
@@ -291,7 +279,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     tiles[0] += n;
                 }
                 for (int w = 0; w < act; ++w) ++items[w];
-                deal_next<C::kRows, kTcKeys>(a, c, n);
+                deal_next<C::kRows, kTcKeys>(a, c);
             }
             if (leader) mma_commit_own<CG>(done);
             __syncwarp();
@@ -369,7 +357,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 advance();
             };
             while (ok && c.u < c.end) {
-                const int n = deal_take(a, c);
+                const int n = c.take;
                 const int r0 = c.rt * C::kRows;
                 key_range(kv, a.window, c.s, r0, min(r0 + C::kRows, c.s.q_len * kv.group), lo, hi);
                 const int unit0 = c.first + c.off;
@@ -378,7 +366,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     load_v(unit0 + j);
                     if (ok && j + C::kLook < n) load_k(unit0 + j + C::kLook);
                 }
-                deal_next<C::kRows, kTcKeys>(a, c, n);
+                deal_next<C::kRows, kTcKeys>(a, c);
             }
             // Nothing is on its way to this CTA's memory when it leaves: every slot's last use has landed and been
             // read (or, after a timeout, the limit has passed).
@@ -395,7 +383,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             constexpr int kCpr = DH / 8, kPer = 32 / kCpr;  // chunks per row, rows per warp step
             const int x = lane % kCpr;
             while (ok && c.u < c.end) {
-                const int n = deal_take(a, c);
+                const int n = c.take;
                 const int all = c.s.q_len * kv.group - c.rt * C::kRows;
                 if (all > C::kTile * w) {
                     const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
@@ -425,7 +413,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(leaders(q_full + w));
                 }
-                deal_next<C::kRows, kTcKeys>(a, c, n);
+                deal_next<C::kRows, kTcKeys>(a, c);
             }
             if (items) drain_bar(q_free + w, (items - 1) & 1, global_ns() + kWaitNs);  // (its arrival, too, has come)
         }
@@ -454,11 +442,11 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         auto buf_of = [&](uint32_t t) { return C::NQ == 2 ? w : static_cast<int>(t & 1); };
         auto phase_of = [&](uint32_t t) { return (C::NQ == 2 ? t : t >> 1) & 1; };
         while (ok && c.u < c.end) {
-            const int n = deal_take(a, c);
+            const int n = c.take;
             const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
             const int rows = min(c.s.q_len * kv.group - r0, 128);  // of this CTA's part of the row tile (may be none)
             if (c.s.q_len * kv.group <= c.rt * C::kRows + C::kTile * w) {
-                deal_next<C::kRows, kTcKeys>(a, c, n);
+                deal_next<C::kRows, kTcKeys>(a, c);
                 continue;
             }
             const bool mine = row < rows;
@@ -551,7 +539,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
             if (!ok) break;
             tc_fence_after();
-            const bool whole = n == c.n;
+            const bool whole = c.whole();
             const int tok = c.s.q0 + tok_i, head = c.h * kv.group + r_in % kv.group;
             bool bad = false;
             const int part = 2 * me + (c.u == u_begin ? 0 : 1), r_tile = C::kTile * w + 128 * rank + row;
@@ -630,7 +618,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     attend_row<T>(a, c.b, __shfl_sync(~0u, tok, src), __shfl_sync(~0u, head, src), __shfl_sync(~0u, pos, src));
                 }
             }
-            deal_next<C::kRows, kTcKeys>(a, c, n);
+            deal_next<C::kRows, kTcKeys>(a, c);
         }
     }
 

@@ -51,13 +51,14 @@ struct AttendArgs {
     float2* part_ml;           // [2 * CTAs][tile rows]: running maximum (base 2), sum
 };
 
-// A row tile of the batch cut by CTA c's first unit: written by CTA c, read by the join.
+// What the join knows of the row tile that CTA c's share begins in: written by CTA c.
 struct BoundaryRec {
-    long long begin;   // the tile's first unit
-    long long per;     // units per CTA
-    int n;             // the tile's units
+    long long begin;   // where the tile begins in the line of units,
+    long long per;     // units of the line per CTA,
+    int n;             // and the tile's
     int cut;           // 1 if the tile began before CTA c
-    int b, rt, h, pad;
+    int rt, h;         // row tile and key/value head
+    int q0, q_len, pos0, b;  // the sequence: first token, tokens, first token's position, number
 };
 
 cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t st);

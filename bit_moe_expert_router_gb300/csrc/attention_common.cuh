@@ -107,49 +107,71 @@ __device__ __forceinline__ void key_range(const KvArgs& a, int window, const Seq
 // The batch's work is a line of units: sequence by sequence, row tile by row tile (ROWS rows of one
 // sequence's token-major (token, head of the group) rows), key/value head by head, key unit by key
 // unit (KEYS consecutive positions).  CTA c takes units [c per, (c + 1) per), so the grid's shares
-// differ by one unit at most however ragged the batch is; a tile that a share's end cuts is finished
-// by the join.  A tile whose rows see nothing counts as one unit (its rows still have to be written).
-template <int ROWS, int KEYS>
+// differ by one unit at most however ragged the batch is.  Where the tiles are few and the shares
+// short, each tile is cut into pieces of its own instead, one per CTA: a CTA that ends one tile and
+// begins another starts its copies twice, which then costs more than the balance gains.  Pieces of
+// a cut tile are put together by the join.  A tile whose rows see nothing counts as one unit (its
+// rows still have to be written).
 struct Deal {
-    static __device__ __forceinline__ int tiles(const KvArgs& a, const SeqInfo& s) {
-        return (s.q_len * a.group + ROWS - 1) / ROWS;
-    }
-    // First key unit and number of units of row tile rt.
-    static __device__ __forceinline__ int units(const AttendArgs& a, const SeqInfo& s, int rt, int& first) {
-        const int r1 = min((rt + 1) * ROWS, s.q_len * a.kv.group);
-        int lo, hi;
-        key_range(a.kv, a.window, s, rt * ROWS, r1, lo, hi);
-        first = lo / KEYS;
-        return max((hi + KEYS - 1) / KEYS - first, 1);
-    }
+    int split;           // 0: a tile is one unit of the line
+    long long piece;     // > 0: a tile of n units is cut into ceil(n / piece) pieces, the line's units
 };
+
+template <int ROWS>
+__device__ __forceinline__ int row_tiles(const KvArgs& a, const SeqInfo& s) {
+    return (s.q_len * a.group + ROWS - 1) / ROWS;
+}
+// First key unit and number of key units of row tile rt.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ int key_units(const AttendArgs& a, const SeqInfo& s, int rt, int& first) {
+    const int r1 = min((rt + 1) * ROWS, s.q_len * a.kv.group);
+    int lo, hi;
+    key_range(a.kv, a.window, s, rt * ROWS, r1, lo, hi);
+    first = lo / KEYS;
+    return max((hi + KEYS - 1) / KEYS - first, 1);
+}
+// What the tile counts for in the line.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ int tile_weight(const AttendArgs& a, const Deal& d, const SeqInfo& s, int rt) {
+    if (!d.split) return 1;
+    int first;
+    const int n = key_units<ROWS, KEYS>(a, s, rt, first);
+    return d.piece ? static_cast<int>((n + d.piece - 1) / d.piece) : n;
+}
 
 struct Cursor {
-    long long u, end;  // this CTA's next unit and its end
-    long long per;
-    int b, rt, h;      // the tile that unit `u` is in
-    int off;           // units of the tile before `u`
-    int first, n;      // the tile's first key unit and its number of units
+    long long u, end;  // the CTA's next place in the line, and its end
+    int b, rt, h;      // the tile there
+    int first, n;      // its first key unit and its key units
+    int off, take;     // the key units before this piece, and the piece's
     SeqInfo s;
+    Deal d;
+    __device__ __forceinline__ bool whole() const { return take == n; }
 };
 
-// The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + 1 shared
-// words.  Sets `c` in every thread.
+// prefix[b] = the line's length before sequence b, prefix[n_seqs] all of it.  Called by the whole block.
 template <int ROWS, int KEYS>
-__device__ void deal_begin(const AttendArgs& a, long long* prefix, long long min_per, int me, int all, Cursor& c) {
-    using D = Deal<ROWS, KEYS>;
+__device__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int B = a.kv.n_seqs;
-    for (int b = warp; b < B; b += warps) {
+    constexpr int kFew = 8;  // more tiles than this are summed by a warp
+    for (int b = threadIdx.x; b < B; b += blockDim.x) {
         const SeqInfo s = seq_info(a.kv, b);
-        const int nt = D::tiles(a.kv, s);
+        const int nt = row_tiles<ROWS>(a.kv, s);
         long long sum = 0;
-        for (int rt = lane; rt < nt; rt += 32) {
-            int first;
-            sum += a.split ? D::units(a, s, rt, first) : 1;
-        }
+        for (int rt = 0; rt < nt && nt <= kFew; ++rt) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
+        prefix[b + 1] = nt <= kFew ? sum * a.kv.hkv : -1;
+    }
+    __syncthreads();
+    for (int b = warp; b < B; b += warps) {
+        if (prefix[b + 1] >= 0) continue;
+        const SeqInfo s = seq_info(a.kv, b);
+        const int nt = row_tiles<ROWS>(a.kv, s);
+        long long sum = 0;
+        for (int rt = lane; rt < nt; rt += 32) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        __syncwarp();
         if (lane == 0) prefix[b + 1] = sum * a.kv.hkv;
     }
     __syncthreads();
@@ -168,68 +190,120 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, long long min
         }
     }
     __syncthreads();
-    const long long total = prefix[B];
-    c.per = max((total + all - 1) / all, a.split ? min_per : 1LL);
-    c.u = min(me * c.per, total);
-    c.end = min(c.u + c.per, total);
-    c.b = c.rt = c.h = c.off = c.first = c.n = 0;
-    if (c.u >= c.end) return;
-    int lo = 0, hi = B - 1;  // the sequence that holds unit u: the last b with prefix[b] <= u
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= c.u) lo = mid;
-        else hi = mid - 1;
-    }
-    c.b = lo;
-    c.s = seq_info(a.kv, lo);
-    const int nt = D::tiles(a.kv, c.s);
-    long long rel = c.u - prefix[lo];
-    for (int t0 = 0;; t0 += 32) {  // every warp walks the sequence's tiles, 32 at a time
-        int first = 0;
-        const int rt = t0 + lane;
-        const int n = rt < nt ? (a.split ? D::units(a, c.s, rt, first) : 1) : 0;
-        long long x = static_cast<long long>(n) * a.kv.hkv;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(~0u, x, o);
-            if (lane >= o) x += y;
-        }
-        const unsigned past = __ballot_sync(~0u, x > rel);
-        if (past || t0 + 32 >= nt) {
-            const int l = past ? __ffs(past) - 1 : 31;
-            const long long before = __shfl_sync(~0u, x - static_cast<long long>(n) * a.kv.hkv, l);
-            const int nl = max(__shfl_sync(~0u, n, l), 1);
-            rel -= before;
-            c.rt = min(t0 + l, nt - 1);
-            c.h = static_cast<int>(rel / nl);
-            c.off = static_cast<int>(rel - static_cast<long long>(c.h) * nl);
-            break;
-        }
-        rel -= __shfl_sync(~0u, x, 31);
-    }
-    c.n = D::units(a, c.s, c.rt, c.first);
 }
 
-// Units of the current tile that are this CTA's.
-__device__ __forceinline__ int deal_take(const AttendArgs& a, const Cursor& c) {
-    return a.split ? static_cast<int>(min(static_cast<long long>(c.n - c.off), c.end - c.u)) : c.n;
-}
-
-// Past the current tile.
+// The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + 1 shared
+// words.  A share has min_per units at least; tiles are cut one by one where that gives pieces of at
+// most own_pieces units.  Sets `c` in every thread, and this CTA's record of the tile that its share
+// begins in.
 template <int ROWS, int KEYS>
-__device__ __forceinline__ void deal_next(const AttendArgs& a, Cursor& c, int taken) {
-    using D = Deal<ROWS, KEYS>;
-    c.u += a.split ? taken : 1;
+__device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, int own_pieces, int me, int all, Cursor& c) {
+    const int lane = threadIdx.x & 31;
+    const int B = a.kv.n_seqs;
+    c.d.split = a.split;
+    c.d.piece = 0;
+    deal_prefix<ROWS, KEYS>(a, c.d, prefix);
+    long long total = prefix[B], per = 1;
+    if (a.split) {
+        per = max((total + all - 1) / all, static_cast<long long>(min_per));
+        if (B * a.kv.hkv * 4 <= all) {  // (tiles of one sequence and head are counted only where that may be few)
+            long long tiles = 0;
+            for (int b = lane; b < B; b += 32) tiles += row_tiles<ROWS>(a.kv, seq_info(a.kv, b));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(~0u, tiles, o);
+            tiles *= a.kv.hkv;
+            // pieces of p units: at most total / p + tiles of them
+            const long long p = tiles * 4 <= all ? max((total + all - tiles - 1) / (all - tiles), static_cast<long long>(min_per)) : 0;
+            if (p && p <= own_pieces) {
+                __syncthreads();  // (the total has been read)
+                c.d.piece = p;
+                deal_prefix<ROWS, KEYS>(a, c.d, prefix);
+                total = prefix[B];
+                per = 1;
+            }
+        }
+    } else {
+        per = (total + all - 1) / all;
+    }
+    c.u = min(me * per, total);
+    c.end = min(c.u + per, total);
+    c.b = c.rt = c.h = c.off = c.take = c.first = c.n = 0;
+    int idx = 0, weight = 0;
+    if (c.u < c.end) {
+        int lo = 0, hi = B - 1;  // the sequence that holds unit u: the last b with prefix[b] <= u
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= c.u) lo = mid;
+            else hi = mid - 1;
+        }
+        c.b = lo;
+        c.s = seq_info(a.kv, lo);
+        const int nt = row_tiles<ROWS>(a.kv, c.s);
+        long long rel = c.u - prefix[lo];
+        for (int t0 = 0;; t0 += 32) {  // every warp walks the sequence's tiles, 32 at a time
+            const int rt = t0 + lane;
+            const int n = rt < nt ? tile_weight<ROWS, KEYS>(a, c.d, c.s, rt) : 0;
+            long long x = static_cast<long long>(n) * a.kv.hkv;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o) x += y;
+            }
+            const unsigned past = __ballot_sync(~0u, x > rel);
+            if (past || t0 + 32 >= nt) {
+                const int l = past ? __ffs(past) - 1 : 31;
+                rel -= __shfl_sync(~0u, x - static_cast<long long>(n) * a.kv.hkv, l);
+                weight = max(__shfl_sync(~0u, n, l), 1);
+                c.rt = min(t0 + l, nt - 1);
+                c.h = static_cast<int>(rel / weight);
+                idx = static_cast<int>(rel - static_cast<long long>(c.h) * weight);
+                break;
+            }
+            rel -= __shfl_sync(~0u, x, 31);
+        }
+        c.n = key_units<ROWS, KEYS>(a, c.s, c.rt, c.first);
+        if (c.d.piece) {
+            c.off = static_cast<int>(static_cast<long long>(c.n) * idx / weight);
+            c.take = static_cast<int>(static_cast<long long>(c.n) * (idx + 1) / weight) - c.off;
+        } else if (a.split) {
+            c.off = idx;
+            c.take = static_cast<int>(min(static_cast<long long>(c.n - c.off), c.end - c.u));
+        } else {
+            c.take = c.n;
+        }
+    }
+    if (threadIdx.x == 0 && a.split) {
+        BoundaryRec r;
+        r.begin = c.u - idx;
+        r.per = per;
+        r.n = weight;
+        r.cut = idx > 0;
+        r.rt = c.rt;
+        r.h = c.h;
+        r.q0 = c.s.q0;
+        r.q_len = c.s.q_len;
+        r.pos0 = c.s.pos0;
+        r.b = c.b;
+        a.recs[me] = r;
+    }
+}
+
+// Past the current piece.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ void deal_next(const AttendArgs& a, Cursor& c) {
+    c.u += c.d.split && !c.d.piece ? c.take : 1;
     c.off = 0;
     if (c.u >= c.end) return;
-    if (++c.h < a.kv.hkv) return;
-    c.h = 0;
-    ++c.rt;
-    while (c.rt >= D::tiles(a.kv, c.s)) {  // ends at the sequence that holds unit u
-        c.s = seq_info(a.kv, ++c.b);
-        c.rt = 0;
+    if (++c.h == a.kv.hkv) {
+        c.h = 0;
+        ++c.rt;
+        while (c.rt >= row_tiles<ROWS>(a.kv, c.s)) {  // ends at the sequence that holds unit u
+            c.s = seq_info(a.kv, ++c.b);
+            c.rt = 0;
+        }
+        c.n = key_units<ROWS, KEYS>(a, c.s, c.rt, c.first);
     }
-    c.n = D::units(a, c.s, c.rt, c.first);
+    c.take = c.d.split ? static_cast<int>(min(static_cast<long long>(c.n), c.end - c.u)) : c.n;
 }
 
 // ---------------------------------------------------------------- the exact row
