@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     if (!rec.cut) return;
     const KvArgs& kv = a.kv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = static_cast<int>(rec.begin / rec.per), c1 = static_cast<int>((rec.begin + rec.n - 1) / rec.per);
+    const int c0 = static_cast<int>(div_line(rec.begin, rec.per)), c1 = static_cast<int>(div_line(rec.begin + rec.n - 1, rec.per));
     const int share = c1 - c0 + 1 > 8 ? kJoinWarps : 1;  // warps per row
     const int wi = share > 1 ? warp : 0;
     const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
@@ -86,12 +86,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
             }
         }
         if (wi != 0 || r >= rows) continue;
-        const int tok = rec.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
+        int i, g;
+        row_of(kv, r0 + r, i, g);
+        const int tok = rec.q0 + i, head = rec.h * kv.group + g;
         bool bad = ll != ll;
 #pragma unroll
         for (int x = 0; x < kVec; ++x) bad |= acc[x].x != acc[x].x || acc[x].y != acc[x].y;
         if (__any_sync(~0u, bad)) {
-            attend_row<T>(a, rec.b, tok, head, rec.pos0 + (r0 + r) / kv.group);
+            attend_row<T>(a, rec.b, tok, head, rec.pos0 + i);
             continue;
         }
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const
     if (!rec.cut) return;
     const KvArgs& kv = a.kv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = static_cast<int>(rec.begin / rec.per), c1 = static_cast<int>((rec.begin + rec.n - 1) / rec.per);
+    const int c0 = static_cast<int>(div_line(rec.begin, rec.per)), c1 = static_cast<int>(div_line(rec.begin + rec.n - 1, rec.per));
     const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
     auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
     const int step = c1 - c0;  // boundaries of the tile: blocks of 32 rows go round them
@@ -161,16 +163,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const
         const unsigned bads = __ballot_sync(~0u, bad && r < rows);
         if (lane == 0 && bads) atomicOr(&bad_rows, bads);
         if (warp == 0 && r < rows && a.lse) {
-            const int tok = rec.q0 + (r0 + r) / kv.group, head = rec.h * kv.group + (r0 + r) % kv.group;
+            int i, g;
+            row_of(kv, r0 + r, i, g);
+            const int tok = rec.q0 + i, head = rec.h * kv.group + g;
             a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
         }
         __syncthreads();
         const unsigned again = bad_rows;
         for (int y = warp; y < 32 && 32 * g + y < rows; y += kJoinWarps) {
-            const int rr = r0 + 32 * g + y;
-            const int tok = rec.q0 + rr / kv.group, head = rec.h * kv.group + rr % kv.group;
+            int i, hg;
+            row_of(kv, r0 + 32 * g + y, i, hg);
+            const int tok = rec.q0 + i, head = rec.h * kv.group + hg;
             if (again >> y & 1) {
-                attend_row<T>(a, rec.b, tok, head, rec.pos0 + rr / kv.group);
+                attend_row<T>(a, rec.b, tok, head, rec.pos0 + i);
                 continue;
             }
             uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs);

@@ -81,7 +81,7 @@ struct Rows {
     int id, at;    // the next unit's page and the key's (or first key's) row in it
     __device__ __forceinline__ void fetch(const KvArgs& a, int b, int unit, int end) {
         const int key = unit * kKeys + (ALIGNED ? 0 : (threadIdx.x & 15));
-        const int p = key / a.page;
+        const int p = div_by(key, a.by_page);
         at = key - p * a.page;
         id = unit < end ? page_id(a, b, p) : -1;
     }
@@ -188,9 +188,10 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
         const int r0 = c.rt * kSplitRows, rows = min(c.s.q_len * kv.group - r0, kSplitRows);
         for (int i = threadIdx.x; i < kSplitRows * chunks; i += blockDim.x) {
             const int r = i / chunks, x = i - r * chunks;
-            const int rr = r0 + min(r, rows - 1);
-            const int tok = c.s.q0 + rr / kv.group, head = c.h * kv.group + rr % kv.group;
-            cp_async16(smem + buf * C::kQBytes + chunk_at<C::kCpr>(r, x), static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + x * 8,
+            int tok, g;
+            row_of(kv, r0 + min(r, rows - 1), tok, g);
+            cp_async16(smem + buf * C::kQBytes + chunk_at<C::kCpr>(r, x),
+                       static_cast<const T*>(a.q) + (c.s.q0 + tok) * a.q_ts + (c.h * kv.group + g) * a.q_hs + x * 8,
                        r < rows ? 16 : 0);
         }
         cp_async_commit();
@@ -218,12 +219,12 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int r = (lane >> 2) + 8 * x;
-            const int p = c.s.pos0 + (r0 + min(r, rows - 1)) / kv.group;
+            const int p = c.s.pos0 + div_by(r0 + min(r, rows - 1), kv.by_group);
             p_hi[x] = min(p, kv.cap - 1);
             p_lo[x] = a.window > 0 ? p - a.window : -1;
         }
-        const int all_hi = c.s.pos0 + r0 / kv.group;                                          // every row sees keys <= all_hi
-        const int all_lo = a.window > 0 ? c.s.pos0 + (r0 + rows - 1) / kv.group - a.window : -1;  // and > all_lo
+        const int all_hi = c.s.pos0 + div_by(r0, kv.by_group);                                          // every row sees keys <= all_hi
+        const int all_lo = a.window > 0 ? c.s.pos0 + div_by(r0 + rows - 1, kv.by_group) - a.window : -1;  // and > all_lo
 
         float o[DH / 8][4];
 #pragma unroll
@@ -362,13 +363,15 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
                 }
             }
             if (whole) {
-                const int tok = q0 + (r0 + r) / kv.group, head = h * kv.group + (r0 + r) % kv.group;
+                int i, g;
+                row_of(kv, r0 + r, i, g);
+                const int tok = q0 + i, head = h * kv.group + g;
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
                 bool bad = ll != ll;
 #pragma unroll
                 for (int x = 0; x < DH / 32; ++x) bad |= acc[x] != acc[x];
                 if (__any_sync(~0u, bad)) {
-                    attend_row<T>(a, b, tok, head, pos0 + (r0 + r) / kv.group);
+                    attend_row<T>(a, b, tok, head, pos0 + i);
                     continue;
                 }
                 T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + lane * 2;

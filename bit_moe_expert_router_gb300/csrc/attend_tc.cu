@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 page = kv.n_pages;  // outside the map: zeros
                 row = 0;
                 if (lane < boxes && key < hi) {
-                    const int p = key / kv.page, id = page_id(kv, c.b, p);
+                    const int p = div_by(key, kv.by_page), id = page_id(kv, c.b, p);
                     row = key - p * kv.page;
                     if (id >= 0) page = id;
                 }
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             constexpr int kCpr = DH / 8, kPer = 32 / kCpr;  // chunks per row, rows per warp step
             const int x = lane % kCpr;
             while (ok && c.u < c.end) {
-                const int n = c.take;
+
                 const int all = c.s.q_len * kv.group - c.rt * C::kRows;
                 if (all > C::kTile * w) {
                     const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
@@ -396,8 +396,9 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     const int first = C::NQ == 2 ? 0 : (warp - 2) * 64;
 #pragma unroll
                     for (int g = 0; g < kMine; g += 32) {
-                        const int rr = r0 + max(min(first + g + lane, rows - 1), 0);
-                        const int64_t at = static_cast<int64_t>(c.s.q0 + rr / kv.group) * a.q_ts + (c.h * kv.group + rr % kv.group) * a.q_hs;
+                        int tok, hg;
+                        row_of(kv, r0 + max(min(first + g + lane, rows - 1), 0), tok, hg);
+                        const int64_t at = static_cast<int64_t>(c.s.q0 + tok) * a.q_ts + (c.h * kv.group + hg) * a.q_hs;
 #pragma unroll 8
                         for (int i = 0; i < 32; i += kPer) {
                             const int64_t from = __shfl_sync(~0u, at, i + lane / kCpr);
@@ -452,7 +453,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const bool mine = row < rows;
             const bool live = (row & ~31) < rows;   // some row of the warp is one
             const int r_in = r0 + max(min(row, rows - 1), 0);
-            const int tok_i = r_in / kv.group;
+            int tok_i, hg;
+            row_of(kv, r_in, tok_i, hg);
             const int pos = c.s.pos0 + tok_i;
             const int p_hi = min(pos, kv.cap - 1);
             const int p_lo = a.window > 0 ? pos - a.window : -1;
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const bool whole = c.whole();
-            const int tok = c.s.q0 + tok_i, head = c.h * kv.group + r_in % kv.group;
+            const int tok = c.s.q0 + tok_i, head = c.h * kv.group + hg;
             bool bad = false;
             const int part = 2 * me + (c.u == u_begin ? 0 : 1), r_tile = C::kTile * w + 128 * rank + row;
             if (live) {

@@ -9,6 +9,17 @@ namespace moe {
 
 struct Header;
 
+// Division of 0 <= n < 2^31 by a fixed 1 <= d < 2^31 by multiplication: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + high word of n m) >> s.
+struct Divisor {
+    uint32_t mul, shift;
+};
+inline Divisor make_divisor(int d) {
+    uint32_t s = 0;
+    while ((int64_t(1) << s) < d) ++s;
+    return {static_cast<uint32_t>(((((uint64_t(1) << s) - d) << 32) / d) + 1), s};
+}
+
 // A paged cache and its ragged batch, as the kernels take it.
 struct KvArgs {
     void* k;
@@ -20,6 +31,7 @@ struct KvArgs {
     const int32_t* kv_len;     // [n_seqs]
     int n_tokens, n_seqs, hq, hkv, group, d, page, n_pages, width;
     int cap;                   // positions a row of the table can hold
+    Divisor by_page, by_group;
 };
 
 struct AppendArgs {

@@ -81,6 +81,8 @@ moe::KvArgs kv_args(const moe_kv_batch_t* b, int64_t n_tokens) {
     a.width = static_cast<int>(b->table_width);
     const __int128 cap = static_cast<__int128>(b->table_width) * b->page_size;
     a.cap = static_cast<int>(cap < kI32 - 512 ? cap : kI32 - 512);  // a last tile's end stays in range
+    a.by_page = moe::make_divisor(a.page);
+    a.by_group = moe::make_divisor(a.group);
     return a;
 }
 

@@ -73,6 +73,20 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
 
 // ---------------------------------------------------------------- the ragged batch
+__device__ __forceinline__ int div_by(int n, const Divisor& d) {
+    return static_cast<int>((__umulhi(n, d.mul) + static_cast<uint32_t>(n)) >> d.shift);
+}
+// A quotient of the line's units: almost always of 32-bit numbers, which is several times shorter.
+__device__ __forceinline__ long long div_line(long long n, long long d) {
+    if (((n | d) >> 32) == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+    return n / d;
+}
+// Row r of a sequence's (token, head of the group) rows.
+__device__ __forceinline__ void row_of(const KvArgs& a, int r, int& tok, int& g) {
+    tok = div_by(r, a.by_group);
+    g = r - tok * a.group;
+}
+
 struct SeqInfo {
     int q0;     // first token
     int q_len;
@@ -97,7 +111,7 @@ __device__ __forceinline__ int page_id(const KvArgs& a, int b, int idx) {
 
 // Keys [lo, hi) that rows [r0, r1) (row = token * group + head of the group) see, at least one of them.
 __device__ __forceinline__ void key_range(const KvArgs& a, int window, const SeqInfo& s, int r0, int r1, int& lo, int& hi) {
-    const int p0 = s.pos0 + r0 / a.group, p1 = s.pos0 + (r1 - 1) / a.group;
+    const int p0 = s.pos0 + div_by(r0, a.by_group), p1 = s.pos0 + div_by(r1 - 1, a.by_group);
     hi = min(p1, a.cap - 1) + 1;
     lo = window > 0 ? max(p0 - window + 1, 0) : 0;
     if (hi <= lo) lo = hi = 0;
@@ -114,7 +128,7 @@ __device__ __forceinline__ void key_range(const KvArgs& a, int window, const Seq
 // rows still have to be written).
 struct Deal {
     int split;           // 0: a tile is one unit of the line
-    long long piece;     // > 0: a tile of n units is cut into ceil(n / piece) pieces, the line's units
+    int piece;           // > 0: a tile of n units is cut into ceil(n / piece) pieces, the line's units
 };
 
 template <int ROWS>
@@ -136,7 +150,7 @@ __device__ __forceinline__ int tile_weight(const AttendArgs& a, const Deal& d, c
     if (!d.split) return 1;
     int first;
     const int n = key_units<ROWS, KEYS>(a, s, rt, first);
-    return d.piece ? static_cast<int>((n + d.piece - 1) / d.piece) : n;
+    return d.piece ? static_cast<int>(static_cast<unsigned>(n + d.piece - 1) / static_cast<unsigned>(d.piece)) : n;
 }
 
 struct Cursor {
@@ -151,7 +165,7 @@ struct Cursor {
 
 // prefix[b] = the line's length before sequence b, prefix[n_seqs] all of it.  Called by the whole block.
 template <int ROWS, int KEYS>
-__device__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix) {
+__device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int B = a.kv.n_seqs;
     constexpr int kFew = 8;  // more tiles than this are summed by a warp
@@ -205,7 +219,7 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
     deal_prefix<ROWS, KEYS>(a, c.d, prefix);
     long long total = prefix[B], per = 1;
     if (a.split) {
-        per = max((total + all - 1) / all, static_cast<long long>(min_per));
+        per = max(div_line(total + all - 1, all), static_cast<long long>(min_per));
         if (B * a.kv.hkv * 4 <= all) {  // (tiles of one sequence and head are counted only where that may be few)
             long long tiles = 0;
             for (int b = lane; b < B; b += 32) tiles += row_tiles<ROWS>(a.kv, seq_info(a.kv, b));
@@ -213,17 +227,17 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
             for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(~0u, tiles, o);
             tiles *= a.kv.hkv;
             // pieces of p units: at most total / p + tiles of them
-            const long long p = tiles * 4 <= all ? max((total + all - tiles - 1) / (all - tiles), static_cast<long long>(min_per)) : 0;
+            const long long p = tiles * 4 <= all ? max(div_line(total + all - tiles - 1, all - tiles), static_cast<long long>(min_per)) : 0;
             if (p && p <= own_pieces) {
                 __syncthreads();  // (the total has been read)
-                c.d.piece = p;
+                c.d.piece = static_cast<int>(p);
                 deal_prefix<ROWS, KEYS>(a, c.d, prefix);
                 total = prefix[B];
                 per = 1;
             }
         }
     } else {
-        per = (total + all - 1) / all;
+        per = div_line(total + all - 1, all);
     }
     c.u = min(me * per, total);
     c.end = min(c.u + per, total);
@@ -255,7 +269,7 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
                 rel -= __shfl_sync(~0u, x - static_cast<long long>(n) * a.kv.hkv, l);
                 weight = max(__shfl_sync(~0u, n, l), 1);
                 c.rt = min(t0 + l, nt - 1);
-                c.h = static_cast<int>(rel / weight);
+                c.h = static_cast<int>(div_line(rel, weight));
                 idx = static_cast<int>(rel - static_cast<long long>(c.h) * weight);
                 break;
             }
@@ -263,8 +277,8 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
         }
         c.n = key_units<ROWS, KEYS>(a, c.s, c.rt, c.first);
         if (c.d.piece) {
-            c.off = static_cast<int>(static_cast<long long>(c.n) * idx / weight);
-            c.take = static_cast<int>(static_cast<long long>(c.n) * (idx + 1) / weight) - c.off;
+            c.off = static_cast<int>(div_line(static_cast<long long>(c.n) * idx, weight));
+            c.take = static_cast<int>(div_line(static_cast<long long>(c.n) * (idx + 1), weight)) - c.off;
         } else if (a.split) {
             c.off = idx;
             c.take = static_cast<int>(min(static_cast<long long>(c.n - c.off), c.end - c.u));
@@ -332,8 +346,8 @@ __device__ __noinline__ void attend_row(const AttendArgs& a, int b, int token, i
     const float c = a.scale * kLog2e;
     float m = kNegInf, l = 0.f;
     for (int j = lo; j < hi; ++j) {
-        const int id = page_id(a.kv, b, j / a.kv.page);
-        const int64_t row = j % a.kv.page;
+        const int at = div_by(j, a.kv.by_page), id = page_id(a.kv, b, at);
+        const int64_t row = j - at * a.kv.page;
         uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
         if (on && id >= 0) {
             kw = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.k) + id * a.kv.k_ps + row * a.kv.k_rs + hk * a.kv.k_hs + lane * 8);

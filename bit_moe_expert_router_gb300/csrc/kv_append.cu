@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
     int64_t row = 0;
     int id = -1;
     if (pos >= 0 && pos < a.kv.cap) {
-        const int p = static_cast<unsigned>(pos) / static_cast<unsigned>(a.kv.page);
+        const int p = div_by(pos, a.kv.by_page);
         id = page_id(a.kv, b, p);
         row = pos - p * a.kv.page;
     }
