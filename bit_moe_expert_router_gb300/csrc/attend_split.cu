@@ -31,17 +31,18 @@ constexpr int kOwnPieces = 64;  // and at most for pieces that end with their ti
 template <int DH>
 struct SplitCfg {
     static constexpr int kWarps = DH == 256 ? 4 : 8;
-    static constexpr int kStages = DH == 64 ? 4 : 2;
+    static constexpr int kStages = DH == 64 ? 6 : 3;
     static constexpr int kCpr = DH / 8;                    // 16-byte chunks per row
     static constexpr int kTile = kKeys * DH;               // elements of K (or V) in a stage
     static constexpr int kQBytes = kSplitRows * DH * 2;
     static constexpr int kWarpBytes = kStages * 2 * kTile * 2;
-    static constexpr int kStateBytes = kSplitRows * DH * 4;  // a warp's state at the join
-    static constexpr int kOffRings = 2 * kQBytes;            // (the queries of this piece and of the next)
-    static constexpr int kOffState = kOffRings + kWarps * kWarpBytes;
-    static constexpr int kOffMl = kOffState + kWarps * kStateBytes;
-    static constexpr int kOffPrefix = kOffMl + kWarps * kSplitRows * 8;
+    static constexpr int kStageBytes = 2 * kTile * 2;
+    static constexpr int kOffRings = 2 * kQBytes;          // (the queries of this piece and of the next)
+    static constexpr int kOffMl = kOffRings + kWarps * kWarpBytes;
+    static constexpr int kOffStage = kOffMl + kWarps * kSplitRows * 8;
+    static constexpr int kOffPrefix = kOffStage + kWarps * 4;
     static constexpr bool kQRegs = DH <= 128;              // the queries' fragments stay in registers
+    static_assert(kStageBytes >= kSplitRows * DH * 4, "a stage holds a warp's state at the join");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -126,13 +127,14 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
     const KvArgs& kv = a.kv;
     const T* kc = static_cast<const T*>(kv.k);
     const T* vc = static_cast<const T*>(kv.v);
+    int* ml_stage = reinterpret_cast<int*>(smem + C::kOffStage);  // [warps]
     unsigned char* ring = smem + C::kOffRings + warp * C::kWarpBytes;
     const int chunks = kv.d / 8;
 
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     // components past D are never copied: zero once (rows of the ring, and of the queries)
     if (kv.d < DH)
-        for (int i = threadIdx.x; i < C::kOffState / 16; i += blockDim.x) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < C::kOffMl / 16; i += blockDim.x) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
 
     if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
     Cursor c;
@@ -311,8 +313,9 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
             __syncwarp();  // the stage is read before its next copies
         }
 
-        // this warp's state
-        float* so = reinterpret_cast<float*>(smem + C::kOffState + warp * C::kStateBytes);  // [rows][DH]
+        // this warp's state, in the stage whose copies come next (the others' are under way)
+        ml_stage[warp] = fill;
+        float* so = reinterpret_cast<float*>(ring + fill * C::kStageBytes);  // [rows][DH]
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             l[x] += __shfl_xor_sync(~0u, l[x], 1);
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
             for (int w = 0; w < C::kWarps; ++w) {
                 const float fx = __shfl_sync(~0u, fw, w);
                 if (fx == 0.f) continue;
-                const float* p = reinterpret_cast<const float*>(smem + C::kOffState + w * C::kStateBytes) + r * DH + lane * 2;
+                const float* p = reinterpret_cast<const float*>(smem + C::kOffRings + w * C::kWarpBytes + ml_stage[w] * C::kStageBytes) + r * DH + lane * 2;
 #pragma unroll
                 for (int x = 0; x < DH / 64; ++x) {
                     const float2 v = *reinterpret_cast<const float2*>(p + x * 64);
@@ -389,6 +392,10 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
         }
         cp_async_wait<0>();
         __syncthreads();
+        if (kv.d < DH) {  // the state overwrote the stage's zero columns
+            for (int i = lane; i < C::kStageBytes / 16; i += 32) reinterpret_cast<uint4*>(ring + fill * C::kStageBytes)[i] = make_uint4(0, 0, 0, 0);
+            __syncwarp();
+        }
     }
 }
 
