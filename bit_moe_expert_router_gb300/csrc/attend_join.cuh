@@ -105,13 +105,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     }
 }
 
-// The same for tiles of many rows and few pieces, which lie as [component / 4][row][4]: a block takes 32 rows of
-// a tile, a lane per row, the warps the components in turn; the rows are written through shared memory.
+// The same for tiles of many rows, which lie as [component / 4][row][4]: a block takes 32 rows and 64
+// components of a tile, a lane per row, two fours of components per warp; the rows are written through shared
+// memory.
 template <typename T, int ROWS, int DH>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const AttendArgs a) {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    constexpr int kPad = DH / 2 + 1;  // words of a staged row (odd: a column of rows lies in different banks)
-    __shared__ uint32_t rows_out[32][kPad];
+    constexpr int kSlices = DH / 64;
+    __shared__ uint32_t rows_out[32][33];  // (odd: a column of rows lies in different banks)
     __shared__ unsigned bad_rows;
     const int cta = blockIdx.x + 1;
     const BoundaryRec rec = a.recs[cta];
@@ -121,52 +122,50 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const
     const int c0 = static_cast<int>(div_line(rec.begin, rec.per)), c1 = static_cast<int>(div_line(rec.begin + rec.n - 1, rec.per));
     const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
     auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
-    const int step = c1 - c0;  // boundaries of the tile: blocks of 32 rows go round them
-    for (int g = (cta - (c0 + 1)) + step * blockIdx.y; 32 * g < rows; g += step * gridDim.y) {
+    const int step = c1 - c0;  // boundaries of the tile: its parts go round them
+    for (int v = (cta - (c0 + 1)) + step * blockIdx.y; v / kSlices * 32 < rows; v += step * gridDim.y) {
+        const int g = v / kSlices, col = v % kSlices * 64;  // rows 32 g .., components col ..
         const int r = 32 * g + lane;
         float mm = kNegInf;
+#pragma unroll 4
         for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, a.part_ml[slot_of(p) * ROWS + r].x);
         const float base = mm == kNegInf ? 0.f : mm;
-        float ll = 0.f;
-        for (int p = c0; p <= c1; ++p) {
-            const float2 v = a.part_ml[slot_of(p) * ROWS + r];
-            ll += v.y * exp2_fast(v.x - base);
-        }
         if (threadIdx.x == 0) bad_rows = 0;
-        __syncthreads();
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        bool bad = ll != ll;
-        constexpr int kMine = DH / 4 / kJoinWarps;
-        float4 acc[kMine];
-#pragma unroll
-        for (int x = 0; x < kMine; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float ll = 0.f;
+        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
         for (int p = c0; p <= c1; ++p) {
             const int64_t slot = slot_of(p);
-            const float f = exp2_fast(a.part_ml[slot * ROWS + r].x - base);
-            const float4* o = reinterpret_cast<const float4*>(a.part_o + slot * ROWS * DH) + r;
-#pragma unroll
-            for (int x = 0; x < kMine; ++x) {
-                const float4 v = o[(warp + kJoinWarps * x) * ROWS];
-                acc[x].x += v.x * f;
-                acc[x].y += v.y * f;
-                acc[x].z += v.z * f;
-                acc[x].w += v.w * f;
-            }
+            const float2 ml = a.part_ml[slot * ROWS + r];
+            const float4* o = reinterpret_cast<const float4*>(a.part_o + slot * ROWS * DH) + (col / 4 + 2 * warp) * ROWS + r;
+            const float4 x = o[0], y = o[ROWS];
+            const float f = exp2_fast(ml.x - base);
+            ll += ml.y * f;
+            acc[0].x += x.x * f;
+            acc[0].y += x.y * f;
+            acc[0].z += x.z * f;
+            acc[0].w += x.w * f;
+            acc[1].x += y.x * f;
+            acc[1].y += y.y * f;
+            acc[1].z += y.z * f;
+            acc[1].w += y.w * f;
         }
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        bool bad = ll != ll;
+        __syncthreads();
 #pragma unroll
-        for (int x = 0; x < kMine; ++x) {
-            const float4 v = acc[x];
-            bad |= v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w;
-            rows_out[lane][2 * (warp + kJoinWarps * x)] = Elem<T>::pack(v.x * inv, v.y * inv);
-            rows_out[lane][2 * (warp + kJoinWarps * x) + 1] = Elem<T>::pack(v.z * inv, v.w * inv);
+        for (int x = 0; x < 2; ++x) {
+            const float4 o = acc[x];
+            bad |= o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w;
+            rows_out[lane][4 * warp + 2 * x] = Elem<T>::pack(o.x * inv, o.y * inv);
+            rows_out[lane][4 * warp + 2 * x + 1] = Elem<T>::pack(o.z * inv, o.w * inv);
         }
         const unsigned bads = __ballot_sync(~0u, bad && r < rows);
         if (lane == 0 && bads) atomicOr(&bad_rows, bads);
-        if (warp == 0 && r < rows && a.lse) {
-            int i, g;
-            row_of(kv, r0 + r, i, g);
-            const int tok = rec.q0 + i, head = rec.h * kv.group + g;
-            a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
+        if (warp == 0 && col == 0 && r < rows && a.lse) {
+            int i, hg;
+            row_of(kv, r0 + r, i, hg);
+            a.lse[static_cast<int64_t>(rec.q0 + i) * kv.hq + rec.h * kv.group + hg] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
         }
         __syncthreads();
         const unsigned again = bad_rows;
@@ -175,13 +174,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const
             row_of(kv, r0 + 32 * g + y, i, hg);
             const int tok = rec.q0 + i, head = rec.h * kv.group + hg;
             if (again >> y & 1) {
-                attend_row<T>(a, rec.b, tok, head, rec.pos0 + i);
+                attend_row<T>(a, rec.b, tok, head, rec.pos0 + i, col, col + 64);
                 continue;
             }
-            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs);
-#pragma unroll
-            for (int x = 0; x < DH / 64; ++x)
-                if (2 * (lane + 32 * x) < kv.d) dst[lane + 32 * x] = rows_out[y][lane + 32 * x];
+            if (col + 2 * lane < kv.d)
+                reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col)[lane] = rows_out[y][lane];
         }
         __syncthreads();
     }
@@ -206,7 +203,7 @@ cudaError_t launch_attend_join(const AttendArgs& a, int n_ctas, cudaStream_t st)
 }
 template <typename T, int ROWS, int DH>
 cudaError_t launch_attend_join_rows(const AttendArgs& a, int n_ctas, cudaStream_t st) {
-    return launch_join(attend_join_rows_kernel<T, ROWS, DH>, a, dim3(n_ctas - 1, ROWS / 32), st);
+    return launch_join(attend_join_rows_kernel<T, ROWS, DH>, a, dim3(n_ctas - 1, ROWS / 32 * (DH / 64) / 2), st);
 }
 
 }  // namespace moe

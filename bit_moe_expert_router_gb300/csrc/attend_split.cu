@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kKeys = 16;       // keys of a unit: one warp's step
 constexpr int kMinShare = 4;    // units of a CTA at least, where there are few,
+constexpr int kExtra = 4;       // what a tile's beginning and end count for
 constexpr int kOwnPieces = 64;  // and at most for pieces that end with their tile
 
 template <int DH>
@@ -138,10 +139,9 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
 
     if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
     Cursor c;
-    deal_begin<kSplitRows, kKeys>(a, reinterpret_cast<long long*>(smem + C::kOffPrefix), kMinShare, kOwnPieces, blockIdx.x, gridDim.x, c);
+    deal_begin<kSplitRows, kKeys>(a, reinterpret_cast<long long*>(smem + C::kOffPrefix), kMinShare, kOwnPieces, kExtra, blockIdx.x, gridDim.x, c);
     clear_stray_rows<T>(a);
     const float sc = a.scale * kLog2e;
-    const long long u_begin = c.u;
 
     Feed<ALIGNED> feed;
     feed.c = c;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
             }
         }
         const bool whole = c.whole();
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (c.u == u_begin ? 0 : 1);
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (c.u == c.begin ? 0 : 1);
         const int q0 = c.s.q0, pos0 = c.s.pos0, h = c.h, b = c.b;
         deal_next<kSplitRows, kKeys>(a, c);
         qb ^= 1;

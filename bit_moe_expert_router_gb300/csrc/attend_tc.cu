@@ -58,6 +58,7 @@ struct TcCfg {
     static constexpr int kKBlocks = DH / 64, kVBlocks = kVCols / 64;  // in column blocks of 64
     static constexpr int kSlot = kKKeys * DH * 2;
     static constexpr int kSlots = DH == 64 ? 10 : DH == 128 ? 9 : 5;
+    static constexpr int kExtra = 3;                    // key tiles that a row tile's beginning and end count for
     static constexpr int kLook = NQ == 2 ? 1 : 2;       // K tiles ahead of V
     static constexpr int kQTile = 128 * DH * 2;
     static constexpr int kThreads = 128 + 256 * NQ;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     if (warp == 0) tmem_alloc<CG>(tmem_holder, 512);
     const int rank = CG == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CG;
     Cursor c;
-    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, 16, me, gridDim.x / CG, c);  // (scratch: the ring)
+    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, 16, C::kExtra, me, gridDim.x / CG, c);  // (scratch: the ring)
     clear_stray_rows<T>(a);
     tc_fence_before();
     fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
@@ -161,7 +162,6 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const uint32_t ring = smem_u32(smem + C::kOffRing);
-    const long long u_begin = c.u;
     bool ok = true;
 
     if (warp < 4) {
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const bool whole = c.whole();
             const int tok = c.s.q0 + tok_i, head = c.h * kv.group + hg;
             bool bad = false;
-            const int part = 2 * me + (c.u == u_begin ? 0 : 1), r_tile = C::kTile * w + 128 * rank + row;
+            const int part = 2 * me + (c.u == c.begin ? 0 : 1), r_tile = C::kTile * w + 128 * rank + row;
             if (live) {
                 const float2 lp = unpair(l2);
                 float l = lp.x + lp.y;
@@ -559,18 +559,25 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         dst[x] = static_cast<T*>(a.out) + __shfl_sync(~0u, at, (lane & ~3) + x) + DH / 2 * half + (lane & 3) * 8;
-#pragma unroll 1
+                    uint64_t t2 = pair(0.f, 0.f);  // 0 times every value: NaN where one is not finite
+                    const uint64_t inv2 = pair(inv, inv), zero2 = pair(0.f, 0.f);
+                    uint32_t o[2][16];
+                    tmem_ld16(o_col, o[0]);
+#pragma unroll
                     for (int i = 0; i < DH / 2; i += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_col + i, o);
-                        tmem_ld_wait();
-                        tmem_tie<32>(o);
                         uint32_t u[4][4];
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const float y = __uint_as_float(o[2 * x]), z = __uint_as_float(o[2 * x + 1]);
-                            bad |= y != y || z != z;
-                            u[x / 4][x % 4] = Elem<T>::pack(y * inv, z * inv);
+                        for (int y = 0; y < 2; ++y) {
+                            tmem_ld_wait();
+                            tmem_tie<16>(o[y]);
+                            if (i + 16 * y + 16 < DH / 2) tmem_ld16(o_col + i + 16 * y + 16, o[y ^ 1]);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const uint64_t v = pair(__uint_as_float(o[y][2 * x]), __uint_as_float(o[y][2 * x + 1]));
+                                t2 = fma2(v, zero2, t2);
+                                const float2 f = unpair(mul2(v, inv2));
+                                u[2 * y + x / 4][x % 4] = Elem<T>::pack(f.x, f.y);
+                            }
                         }
 #pragma unroll
                         for (int b = 1; b <= 2; b *= 2)
@@ -589,18 +596,22 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                             for (int x = 0; x < 4; ++x)
                                 if ((row & ~3) + x < rows) *reinterpret_cast<uint4*>(dst[x] + i) = make_uint4(u[x][0], u[x][1], u[x][2], u[x][3]);
                     }
+                    const float2 t = unpair(t2);
+                    bad |= t.x != t.x || t.y != t.y;
                 } else {
                     // a piece: rows side by side ([component / 4][row][4]), so that a warp's stores are contiguous
                     float* dst = a.part_o + (static_cast<int64_t>(part) * C::kRows * DH) + (DH / 8 * half * C::kRows + r_tile) * 4;
-#pragma unroll 1
-                    for (int i = 0; i < DH / 2; i += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_col + i, o);
-                        tmem_ld_wait();
-                        tmem_tie<32>(o);
+                    uint32_t o[2][16];
+                    tmem_ld16(o_col, o[0]);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            *reinterpret_cast<uint4*>(dst + (i / 4 + x) * C::kRows * 4) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    for (int i = 0; i < DH / 2; i += 16) {
+                        const int y = i / 16 & 1;
+                        tmem_ld_wait();
+                        tmem_tie<16>(o[y]);
+                        if (i + 16 < DH / 2) tmem_ld16(o_col + i + 16, o[y ^ 1]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            *reinterpret_cast<uint4*>(dst + (i / 4 + x) * C::kRows * 4) = make_uint4(o[y][4 * x], o[y][4 * x + 1], o[y][4 * x + 2], o[y][4 * x + 3]);
                     }
                 }
                 if (mine && half == 0) {

@@ -124,10 +124,12 @@ __device__ __forceinline__ void key_range(const KvArgs& a, int window, const Seq
 // differ by one unit at most however ragged the batch is.  Where the tiles are few and the shares
 // short, each tile is cut into pieces of its own instead, one per CTA: a CTA that ends one tile and
 // begins another starts its copies twice, which then costs more than the balance gains.  Pieces of
-// a cut tile are put together by the join.  A tile whose rows see nothing counts as one unit (its
-// rows still have to be written).
+// a cut tile are put together by the join.  A tile whose rows see nothing has one unit (its rows
+// still have to be written), and each tile counts `extra` units more at its end, for what a CTA spends on
+// beginning and ending it.
 struct Deal {
     int split;           // 0: a tile is one unit of the line
+    int extra;
     int piece;           // > 0: a tile of n units is cut into ceil(n / piece) pieces, the line's units
 };
 
@@ -150,18 +152,31 @@ __device__ __forceinline__ int tile_weight(const AttendArgs& a, const Deal& d, c
     if (!d.split) return 1;
     int first;
     const int n = key_units<ROWS, KEYS>(a, s, rt, first);
-    return d.piece ? static_cast<int>(static_cast<unsigned>(n + d.piece - 1) / static_cast<unsigned>(d.piece)) : n;
+    return d.piece ? static_cast<int>(static_cast<unsigned>(n + d.piece - 1) / static_cast<unsigned>(d.piece)) : n + d.extra;
 }
 
 struct Cursor {
     long long u, end;  // the CTA's next place in the line, and its end
+    long long begin;   // where it began
     int b, rt, h;      // the tile there
     int first, n;      // its first key unit and its key units
     int off, take;     // the key units before this piece, and the piece's
+    int pass;          // how far the piece reaches in the line
     SeqInfo s;
     Deal d;
     __device__ __forceinline__ bool whole() const { return take == n; }
 };
+
+// The keys of the piece that begins at `off` of its tile (none where that is in the tile's extra units).
+__device__ __forceinline__ void deal_take(Cursor& c) {
+    if (!c.d.split) {
+        c.take = c.n;
+        c.pass = 1;
+        return;
+    }
+    c.pass = static_cast<int>(min(static_cast<long long>(c.n + c.d.extra - c.off), c.end - c.u));
+    c.take = max(min(c.n, c.off + c.pass) - c.off, 0);
+}
 
 // prefix[b] = the line's length before sequence b, prefix[n_seqs] all of it.  Called by the whole block.
 template <int ROWS, int KEYS>
@@ -206,15 +221,36 @@ __device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, 
     __syncthreads();
 }
 
+// Past the current piece, to the next one that has keys.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ void deal_next(const AttendArgs& a, Cursor& c) {
+    do {
+        c.u += c.pass;
+        c.off = 0;
+        if (c.u >= c.end) return;
+        if (++c.h == a.kv.hkv) {
+            c.h = 0;
+            ++c.rt;
+            while (c.rt >= row_tiles<ROWS>(a.kv, c.s)) {  // ends at the sequence that holds unit u
+                c.s = seq_info(a.kv, ++c.b);
+                c.rt = 0;
+            }
+            c.n = key_units<ROWS, KEYS>(a, c.s, c.rt, c.first);
+        }
+        deal_take(c);
+    } while (c.take == 0);
+}
+
 // The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + 1 shared
 // words.  A share has min_per units at least; tiles are cut one by one where that gives pieces of at
 // most own_pieces units.  Sets `c` in every thread, and this CTA's record of the tile that its share
 // begins in.
 template <int ROWS, int KEYS>
-__device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, int own_pieces, int me, int all, Cursor& c) {
+__device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, int own_pieces, int extra, int me, int all, Cursor& c) {
     const int lane = threadIdx.x & 31;
     const int B = a.kv.n_seqs;
     c.d.split = a.split;
+    c.d.extra = extra;
     c.d.piece = 0;
     deal_prefix<ROWS, KEYS>(a, c.d, prefix);
     long long total = prefix[B], per = 1;
@@ -239,9 +275,9 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
     } else {
         per = div_line(total + all - 1, all);
     }
-    c.u = min(me * per, total);
+    c.u = c.begin = min(me * per, total);
     c.end = min(c.u + per, total);
-    c.b = c.rt = c.h = c.off = c.take = c.first = c.n = 0;
+    c.b = c.rt = c.h = c.off = c.take = c.pass = c.first = c.n = 0;
     int idx = 0, weight = 0;
     if (c.u < c.end) {
         int lo = 0, hi = B - 1;  // the sequence that holds unit u: the last b with prefix[b] <= u
@@ -279,19 +315,18 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
         if (c.d.piece) {
             c.off = static_cast<int>(div_line(static_cast<long long>(c.n) * idx, weight));
             c.take = static_cast<int>(div_line(static_cast<long long>(c.n) * (idx + 1), weight)) - c.off;
-        } else if (a.split) {
-            c.off = idx;
-            c.take = static_cast<int>(min(static_cast<long long>(c.n - c.off), c.end - c.u));
+            c.pass = 1;
         } else {
-            c.take = c.n;
+            c.off = a.split ? idx : 0;
+            deal_take(c);
         }
     }
     if (threadIdx.x == 0 && a.split) {
         BoundaryRec r;
         r.begin = c.u - idx;
         r.per = per;
-        r.n = weight;
-        r.cut = idx > 0;
+        r.n = c.d.piece ? weight : c.n;
+        r.cut = idx > 0 && idx < r.n;
         r.rt = c.rt;
         r.h = c.h;
         r.q0 = c.s.q0;
@@ -300,33 +335,16 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
         r.b = c.b;
         a.recs[me] = r;
     }
-}
-
-// Past the current piece.
-template <int ROWS, int KEYS>
-__device__ __forceinline__ void deal_next(const AttendArgs& a, Cursor& c) {
-    c.u += c.d.split && !c.d.piece ? c.take : 1;
-    c.off = 0;
-    if (c.u >= c.end) return;
-    if (++c.h == a.kv.hkv) {
-        c.h = 0;
-        ++c.rt;
-        while (c.rt >= row_tiles<ROWS>(a.kv, c.s)) {  // ends at the sequence that holds unit u
-            c.s = seq_info(a.kv, ++c.b);
-            c.rt = 0;
-        }
-        c.n = key_units<ROWS, KEYS>(a, c.s, c.rt, c.first);
-    }
-    c.take = c.d.split ? static_cast<int>(min(static_cast<long long>(c.n), c.end - c.u)) : c.n;
+    if (c.u < c.end && c.take == 0) deal_next<ROWS, KEYS>(a, c);
 }
 
 // ---------------------------------------------------------------- the exact row
 // One (token, head) row over the positions it sees and no others, by one warp.  The tiled kernels
 // multiply the values of a masked position by a weight of zero, which is no zero where the value is
 // not finite; a row that ends with a NaN is therefore taken again here.  (A row whose NaN is its own
-// comes out the same.)
+// comes out the same.)  Writes components [col0, col1), and lse with component 0.
 template <typename T>
-__device__ __noinline__ void attend_row(const AttendArgs& a, int b, int token, int head, int pos) {
+__device__ __noinline__ void attend_row(const AttendArgs& a, int b, int token, int head, int pos, int col0 = 0, int col1 = 256) {
     const int lane = threadIdx.x & 31;
     const bool on = lane * 8 < a.kv.d;
     const int hk = head / a.kv.group;
@@ -376,7 +394,7 @@ __device__ __noinline__ void attend_row(const AttendArgs& a, int b, int token, i
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (on) {
+    if (on && lane * 8 >= col0 && lane * 8 < col1) {
         uint4 w;
         w.x = Elem<T>::pack(o[0] * inv, o[1] * inv);
         w.y = Elem<T>::pack(o[2] * inv, o[3] * inv);
@@ -384,7 +402,7 @@ __device__ __noinline__ void attend_row(const AttendArgs& a, int b, int token, i
         w.w = Elem<T>::pack(o[6] * inv, o[7] * inv);
         *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + lane * 8) = w;
     }
-    if (lane == 0 && a.lse) a.lse[static_cast<int64_t>(token) * a.kv.hq + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    if (lane == 0 && col0 == 0 && a.lse) a.lse[static_cast<int64_t>(token) * a.kv.hq + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
 }
 
 // Rows of the tokens that belong to no sequence: zeros, and -inf.  Called by the whole grid.
