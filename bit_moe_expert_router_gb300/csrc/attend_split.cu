@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
     if (kv.d < DH)
         for (int i = threadIdx.x; i < C::kOffMl / 16; i += blockDim.x) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
 
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
+    if (a.lead && blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
     Cursor c;
     deal_begin<kSplitRows, kKeys>(a, reinterpret_cast<long long*>(smem + C::kOffPrefix), kMinShare, kOwnPieces, kExtra, blockIdx.x, gridDim.x, c);
     clear_stray_rows<T>(a);
@@ -407,14 +407,21 @@ cudaError_t launch_t(const AttendArgs& a, int n_ctas, int max_items, cudaStream_
     if (e != cudaSuccess) return e;
     const int grid = a.split ? n_ctas : max(1, min(max_items, n_ctas * 8));
     attend_split_kernel<T, DH, ALIGNED><<<grid, C::kWarps * 32, smem, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !a.split || grid < 2) return e;
-    return launch_attend_join<T, kSplitRows, DH>(a, grid, st);
+    return cudaGetLastError();
 }
 
 template <typename T, int DH>
 cudaError_t launch_d(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
     return a.kv.page % kKeys == 0 ? launch_t<T, DH, true>(a, n_ctas, max_items, st) : launch_t<T, DH, false>(a, n_ctas, max_items, st);
+}
+
+template <typename T>
+cudaError_t launch_j(const AttendArgs& a, int n_ctas, cudaStream_t st) {
+    switch (padded_dim(a.kv.d)) {
+        case 64: return launch_attend_join<T, kSplitRows, 64>(a, n_ctas, st);
+        case 128: return launch_attend_join<T, kSplitRows, 128>(a, n_ctas, st);
+        default: return launch_attend_join<T, kSplitRows, 256>(a, n_ctas, st);
+    }
 }
 
 template <typename T>
@@ -427,6 +434,11 @@ cudaError_t launch_e(const AttendArgs& a, int n_ctas, int max_items, cudaStream_
 }
 
 }  // namespace
+
+cudaError_t launch_attend_split_join(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st) {
+    if (!a.split || n_ctas < 2) return cudaSuccess;
+    return dtype == 0 ? launch_j<__nv_bfloat16>(a, n_ctas, st) : launch_j<__half>(a, n_ctas, st);
+}
 
 cudaError_t launch_attend_split(const AttendArgs& a, int dtype, int n_ctas, int max_items, cudaStream_t st) {
     return dtype == 0 ? launch_e<__nv_bfloat16>(a, n_ctas, max_items, st) : launch_e<__half>(a, n_ctas, max_items, st);

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         mbar_init(tail, 1);
         mbar_init(done, 1);
         *abort_flag = 0;
-        if (blockIdx.x == 0) a.hdr->status = kDevOk;
+        if (a.lead && blockIdx.x == 0) a.hdr->status = kDevOk;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 0) tmem_alloc<CG>(tmem_holder, 512);
@@ -638,6 +638,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();  // the peer has read this CTA's shared and tensor memory
+    // (started beside the kernel before it: not to be complete before that is, for what waits for this one)
+    if (a.follows && tid == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (warp == 0) {
         tc_fence_after();
         tmem_free<CG>(tmem, 512);
@@ -676,15 +678,21 @@ cudaError_t launch_t(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = C::CG;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend_tc_kernel<T, DH>, a, box, kmap, vmap);
-    if (e != cudaSuccess || groups < 2) return e;
-    return launch_attend_join_rows<T, C::kRows, DH>(a, groups, st);
+    cfg.numAttrs = a.follows ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, attend_tc_kernel<T, DH>, a, box, kmap, vmap);
+}
+
+template <typename T, int DH>
+cudaError_t launch_j(const AttendArgs& a, int n_ctas, cudaStream_t st) {
+    const int groups = n_ctas / TcCfg<DH>::CG;
+    return groups < 2 ? cudaSuccess : launch_attend_join_rows<T, TcCfg<DH>::kRows, DH>(a, groups, st);
 }
 
 template <typename T>
@@ -704,6 +712,15 @@ int tc_part_rows(int d, int n_ctas) {
         case 64: return 2 * (n_ctas / TcCfg<64>::CG) * TcCfg<64>::kRows;
         case 128: return 2 * (n_ctas / TcCfg<128>::CG) * TcCfg<128>::kRows;
         default: return 2 * (n_ctas / TcCfg<256>::CG) * TcCfg<256>::kRows;
+    }
+}
+
+cudaError_t launch_attend_tc_join(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st) {
+    const bool bf = dtype == 0;
+    switch (padded_dim(a.kv.d)) {
+        case 64: return bf ? launch_j<__nv_bfloat16, 64>(a, n_ctas, st) : launch_j<__half, 64>(a, n_ctas, st);
+        case 128: return bf ? launch_j<__nv_bfloat16, 128>(a, n_ctas, st) : launch_j<__half, 128>(a, n_ctas, st);
+        default: return bf ? launch_j<__nv_bfloat16, 256>(a, n_ctas, st) : launch_j<__half, 256>(a, n_ctas, st);
     }
 }
 

@@ -57,6 +57,9 @@ struct AttendArgs {
     float scale;
     int window;                // 0: none
     int split;                 // pieces of a row tile may go to several CTAs
+    int rows_lo, rows_hi;      // the sequences of so many rows per key/value head are this kernel's
+    int lead;                  // of two kernels for one batch: this one clears the status and the stray rows
+    int follows;               // launched beside the kernel before it
     Header* hdr;               // workspace: the status word
     struct BoundaryRec* recs;  // workspace: one per CTA
     float* part_o;             // [2 * CTAs][tile rows][padded D]
@@ -81,10 +84,12 @@ inline int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // Attention on mma.sync with the keys split over the warps of the GPU.
 constexpr int kSplitRows = 16;
 cudaError_t launch_attend_split(const AttendArgs& a, int dtype, int n_ctas, int max_items, cudaStream_t st);
+cudaError_t launch_attend_split_join(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st);
 
 // Attention on tcgen05; pages of a multiple of 8 positions.
 int tc_box_rows(int page);  // rows of a page that one TMA box takes
 int tc_part_rows(int d, int n_ctas);  // rows of all pieces
 cudaError_t launch_attend_tc(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st);
+cudaError_t launch_attend_tc_join(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st);
 
 }  // namespace moe

@@ -86,24 +86,26 @@ moe::KvArgs kv_args(const moe_kv_batch_t* b, int64_t n_tokens) {
     return a;
 }
 
-// Workspace of attend: the status word, boundary records, then the pieces' sums and accumulators (laid out
-// for the engine with the larger row tiles; the other uses the front of each).
+// Workspace of attend: the status word, then for each engine (both may run for one batch) boundary records and
+// the pieces' sums and accumulators.
 struct AttendLayout {
     int n_ctas;
-    size_t hdr, recs, ml, o, total;
+    size_t hdr, recs[2], ml[2], o[2], total;
 };
 
 AttendLayout attend_layout(const moe_kv_batch_t* b) {
     AttendLayout L{};
     L.n_ctas = moe::num_sms();
     const int d = static_cast<int>(b->head_dim);
-    const size_t rows = std::max(2 * L.n_ctas * moe::kSplitRows, moe::tc_part_rows(d, L.n_ctas));
     size_t at = 0;
     auto take = [&](size_t bytes) { size_t here = at; at = (at + bytes + 255) & ~size_t(255); return here; };
     L.hdr = take(sizeof(moe::Header));
-    L.recs = take(sizeof(moe::BoundaryRec) * L.n_ctas);
-    L.ml = take(sizeof(float2) * rows);
-    L.o = take(sizeof(float) * rows * moe::padded_dim(d));
+    for (int e = 0; e < 2; ++e) {
+        const size_t rows = e == 0 ? 2 * L.n_ctas * moe::kSplitRows : moe::tc_part_rows(d, L.n_ctas);
+        L.recs[e] = take(sizeof(moe::BoundaryRec) * L.n_ctas);
+        L.ml[e] = take(sizeof(float2) * rows);
+        L.o[e] = take(sizeof(float) * rows * moe::padded_dim(d));
+    }
     L.total = at;
     return L;
 }
@@ -120,6 +122,11 @@ bool use_tc(const moe_kv_batch_t* b, int64_t rows) {
 // Up to this many positions a row tile stays with one CTA: the pieces' way through memory and the second
 // kernel cost more than the keys' streaming by one CTA.
 constexpr int64_t kWholeKeys = 768;
+
+#define MOE_ATTEND(call)                                                         \
+    do {                                                                         \
+        if (int rc = moe::cuda_status((call), "paged_attention")) return rc;     \
+    } while (0)
 
 }  // namespace
 
@@ -194,20 +201,44 @@ MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_toke
     a.window = static_cast<int>(std::min<int64_t>(window, kI32));
     char* ws = static_cast<char*>(workspace);
     a.hdr = moe::ws_at<moe::Header>(workspace, L.hdr);
-    a.recs = reinterpret_cast<moe::BoundaryRec*>(ws + L.recs);
-    a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
-    a.part_o = reinterpret_cast<float*>(ws + L.o);
-    const int64_t rows = std::min(batch->max_q_len, n_tokens) * a.kv.group;
-    if (use_tc(batch, rows)) {
-        a.split = 1;
-        return moe::cuda_status(moe::launch_attend_tc(a, static_cast<int>(batch->dtype), L.n_ctas, static_cast<cudaStream_t>(stream)),
-                                "paged_attention");
+    a.lead = 1;
+    a.rows_hi = static_cast<int>(kI32);
+    auto pieces = [&](int e) {
+        a.recs = reinterpret_cast<moe::BoundaryRec*>(ws + L.recs[e]);
+        a.part_ml = reinterpret_cast<float2*>(ws + L.ml[e]);
+        a.part_o = reinterpret_cast<float*>(ws + L.o[e]);
+    };
+    const int dtype = static_cast<int>(batch->dtype);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t max_q = std::min(batch->max_q_len, n_tokens);
+    const int64_t rows = max_q * a.kv.group;
+    if (!use_tc(batch, rows)) {
+        const int64_t tiles = (rows + moe::kSplitRows - 1) / moe::kSplitRows;
+        const int64_t items = std::min<int64_t>(batch->n_seqs * tiles * a.kv.hkv, int64_t(1) << 30);
+        const int64_t keys = std::min<int64_t>(std::min(batch->max_kv_len, window > 0 ? window + tiles * moe::kSplitRows : kI32), a.kv.cap);
+        a.split = keys > kWholeKeys;
+        pieces(0);
+        MOE_ATTEND(moe::launch_attend_split(a, dtype, L.n_ctas, static_cast<int>(items), st));
+        MOE_ATTEND(moe::launch_attend_split_join(a, dtype, L.n_ctas, st));
+        return MOE_OK;
     }
-    const int64_t tiles = (rows + moe::kSplitRows - 1) / moe::kSplitRows;
-    const int64_t items = std::min<int64_t>(batch->n_seqs * tiles * a.kv.hkv, int64_t(1) << 30);
-    const int64_t keys = std::min<int64_t>(std::min(batch->max_kv_len, window > 0 ? window + tiles * moe::kSplitRows : kI32), a.kv.cap);
-    a.split = keys > kWholeKeys;
-    return moe::cuda_status(moe::launch_attend_split(a, static_cast<int>(batch->dtype), L.n_ctas, static_cast<int>(items),
-                                                     static_cast<cudaStream_t>(stream)),
-                            "paged_attention");
+    // Sequences of few rows among longer ones (decoding requests beside a chunk) go to the split engine: a tile of
+    // 256 or 512 rows that they fill by a few streams their keys at less than half its rate.
+    a.split = 1;
+    moe::AttendArgs few = a;
+    const bool mixed = n_tokens <= (batch->n_seqs - 1) * max_q + moe::kSplitRows / a.kv.group;  // (there may be some)
+    if (mixed) {
+        pieces(0);
+        few = a;
+        few.rows_hi = moe::kSplitRows;
+        few.lead = 0;
+        MOE_ATTEND(moe::launch_attend_split(few, dtype, L.n_ctas, 0, st));
+        a.rows_lo = moe::kSplitRows + 1;
+        a.follows = 1;
+    }
+    pieces(1);
+    MOE_ATTEND(moe::launch_attend_tc(a, dtype, L.n_ctas, st));
+    if (mixed) MOE_ATTEND(moe::launch_attend_split_join(few, dtype, L.n_ctas, st));
+    MOE_ATTEND(moe::launch_attend_tc_join(a, dtype, L.n_ctas, st));
+    return MOE_OK;
 }

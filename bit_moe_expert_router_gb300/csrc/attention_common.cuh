@@ -134,8 +134,9 @@ struct Deal {
 };
 
 template <int ROWS>
-__device__ __forceinline__ int row_tiles(const KvArgs& a, const SeqInfo& s) {
-    return (s.q_len * a.group + ROWS - 1) / ROWS;
+__device__ __forceinline__ int row_tiles(const AttendArgs& a, const SeqInfo& s) {
+    const int rows = s.q_len * a.kv.group;
+    return rows < a.rows_lo || rows > a.rows_hi ? 0 : (rows + ROWS - 1) / ROWS;
 }
 // First key unit and number of key units of row tile rt.
 template <int ROWS, int KEYS>
@@ -183,25 +184,27 @@ template <int ROWS, int KEYS>
 __device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int B = a.kv.n_seqs;
-    constexpr int kFew = 8;  // more tiles than this are summed by a warp
+    constexpr int kFew = 8;                    // more tiles than this are summed by warps,
+    constexpr long long kOpen = -(1LL << 60);  // from this on
     for (int b = threadIdx.x; b < B; b += blockDim.x) {
         const SeqInfo s = seq_info(a.kv, b);
-        const int nt = row_tiles<ROWS>(a.kv, s);
+        const int nt = row_tiles<ROWS>(a, s);
         long long sum = 0;
         for (int rt = 0; rt < nt && nt <= kFew; ++rt) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
-        prefix[b + 1] = nt <= kFew ? sum * a.kv.hkv : -1;
+        prefix[b + 1] = nt <= kFew ? sum * a.kv.hkv : kOpen;
     }
     __syncthreads();
-    for (int b = warp; b < B; b += warps) {
+    const int each = max(warps / B, 1);  // warps for one sequence
+    for (int i = warp; i < B * each; i += warps) {
+        const int b = each > 1 ? i / each : i;
         if (prefix[b + 1] >= 0) continue;
         const SeqInfo s = seq_info(a.kv, b);
-        const int nt = row_tiles<ROWS>(a.kv, s);
+        const int nt = row_tiles<ROWS>(a, s);
         long long sum = 0;
-        for (int rt = lane; rt < nt; rt += 32) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
+        for (int rt = (i - b * each) * 32 + lane; rt < nt; rt += 32 * each) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        __syncwarp();
-        if (lane == 0) prefix[b + 1] = sum * a.kv.hkv;
+        if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(prefix + b + 1), static_cast<unsigned long long>(sum * a.kv.hkv));
     }
     __syncthreads();
     if (warp == 0) {
@@ -209,6 +212,7 @@ __device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, 
         if (lane == 0) prefix[0] = 0;
         for (int b0 = 0; b0 < B; b0 += 32) {
             long long x = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
+            if (x < 0) x -= kOpen;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(~0u, x, o);
@@ -231,7 +235,7 @@ __device__ __forceinline__ void deal_next(const AttendArgs& a, Cursor& c) {
         if (++c.h == a.kv.hkv) {
             c.h = 0;
             ++c.rt;
-            while (c.rt >= row_tiles<ROWS>(a.kv, c.s)) {  // ends at the sequence that holds unit u
+            while (c.rt >= row_tiles<ROWS>(a, c.s)) {  // ends at the sequence that holds unit u
                 c.s = seq_info(a.kv, ++c.b);
                 c.rt = 0;
             }
@@ -258,7 +262,7 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
         per = max(div_line(total + all - 1, all), static_cast<long long>(min_per));
         if (B * a.kv.hkv * 4 <= all) {  // (tiles of one sequence and head are counted only where that may be few)
             long long tiles = 0;
-            for (int b = lane; b < B; b += 32) tiles += row_tiles<ROWS>(a.kv, seq_info(a.kv, b));
+            for (int b = lane; b < B; b += 32) tiles += row_tiles<ROWS>(a, seq_info(a.kv, b));
 #pragma unroll
             for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(~0u, tiles, o);
             tiles *= a.kv.hkv;
@@ -288,7 +292,7 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
         }
         c.b = lo;
         c.s = seq_info(a.kv, lo);
-        const int nt = row_tiles<ROWS>(a.kv, c.s);
+        const int nt = row_tiles<ROWS>(a, c.s);
         long long rel = c.u - prefix[lo];
         for (int t0 = 0;; t0 += 32) {  // every warp walks the sequence's tiles, 32 at a time
             const int rt = t0 + lane;
@@ -408,6 +412,7 @@ __device__ __noinline__ void attend_row(const AttendArgs& a, int b, int token, i
 // Rows of the tokens that belong to no sequence: zeros, and -inf.  Called by the whole grid.
 template <typename T>
 __device__ void clear_stray_rows(const AttendArgs& a) {
+    if (!a.lead) return;
     const int s0 = min(max(__ldg(a.kv.q_start), 0), a.kv.n_tokens);
     const int s1 = min(max(__ldg(a.kv.q_start + a.kv.n_seqs), s0), a.kv.n_tokens);
     const int stray = s0 + a.kv.n_tokens - s1;
