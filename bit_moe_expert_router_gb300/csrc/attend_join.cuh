@@ -14,7 +14,7 @@ constexpr int kJoinWarps = 8;
 // runs give the same bits.
 template <typename T, int ROWS, int DH>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendArgs a) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    wait_for_stream();
     constexpr int kVec = DH / 64;  // pairs of components per lane: lane + 32 x
     __shared__ float2 part[kJoinWarps][DH / 2];
     __shared__ float part_l[kJoinWarps];
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
 // memory.
 template <typename T, int ROWS, int DH>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const AttendArgs a) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    wait_for_stream();
     constexpr int kSlices = DH / 64;
     __shared__ uint32_t rows_out[32][33];  // (odd: a column of rows lies in different banks)
     __shared__ unsigned bad_rows;
@@ -184,26 +184,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const
     }
 }
 
-// Launched while the first kernel runs (it waits for its end by itself), one column of blocks per boundary.
-inline cudaError_t launch_join(void (*kernel)(AttendArgs), const AttendArgs& a, dim3 grid, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-}
 template <typename T, int ROWS, int DH>
 cudaError_t launch_attend_join(const AttendArgs& a, int n_ctas, cudaStream_t st) {
-    return launch_join(attend_join_kernel<T, ROWS, DH>, a, dim3(n_ctas - 1), st);
+    return launch_in_stream(attend_join_kernel<T, ROWS, DH>, dim3(n_ctas - 1), kJoinWarps * 32, 0, 1, st, a);
 }
 template <typename T, int ROWS, int DH>
 cudaError_t launch_attend_join_rows(const AttendArgs& a, int n_ctas, cudaStream_t st) {
-    return launch_join(attend_join_rows_kernel<T, ROWS, DH>, a, dim3(n_ctas - 1, ROWS / 32 * (DH / 64) / 2), st);
+    return launch_in_stream(attend_join_rows_kernel<T, ROWS, DH>, dim3(n_ctas - 1, ROWS / 32 * (DH / 64) / 2), kJoinWarps * 32, 0, 1, st, a);
 }
 
 }  // namespace moe

@@ -132,11 +132,11 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
     unsigned char* ring = smem + C::kOffRings + warp * C::kWarpBytes;
     const int chunks = kv.d / 8;
 
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     // components past D are never copied: zero once (rows of the ring, and of the queries)
     if (kv.d < DH)
         for (int i = threadIdx.x; i < C::kOffMl / 16; i += blockDim.x) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
 
+    wait_for_stream();
     if (a.lead && blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
     Cursor c;
     deal_begin<kSplitRows, kKeys>(a, reinterpret_cast<long long*>(smem + C::kOffPrefix), kMinShare, kOwnPieces, kExtra, blockIdx.x, gridDim.x, c);
@@ -402,12 +402,11 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
 template <typename T, int DH, bool ALIGNED>
 cudaError_t launch_t(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
     using C = SplitCfg<DH>;
-    const int smem = C::kOffPrefix + (a.kv.n_seqs + 1) * 8;
+    const int smem = C::kOffPrefix + (a.kv.n_seqs + 2) * 8;
     cudaError_t e = cudaFuncSetAttribute(attend_split_kernel<T, DH, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = a.split ? n_ctas : max(1, min(max_items, n_ctas * 8));
-    attend_split_kernel<T, DH, ALIGNED><<<grid, C::kWarps * 32, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_in_stream(attend_split_kernel<T, DH, ALIGNED>, dim3(grid), C::kWarps * 32, smem, 1, st, a);
 }
 
 template <typename T, int DH>

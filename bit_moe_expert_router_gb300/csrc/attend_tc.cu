@@ -124,7 +124,6 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     const KvArgs& kv = a.kv;
     const Ctl ctl{abort_flag, a.hdr};
 
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (smem_u32(smem) & 1023u) {  // (the swizzled tiles' places; the same in every CTA)
         if (tid == 0) atomicOr(&a.hdr->status, kDevTimeout);
         return;
@@ -147,10 +146,12 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         mbar_init(tail, 1);
         mbar_init(done, 1);
         *abort_flag = 0;
-        if (a.lead && blockIdx.x == 0) a.hdr->status = kDevOk;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 0) tmem_alloc<CG>(tmem_holder, 512);
+    if (a.follows) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // beside the split kernel, which has waited
+    else wait_for_stream();
+    if (a.lead && blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
     const int rank = CG == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CG;
     Cursor c;
     deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, 16, C::kExtra, me, gridDim.x / CG, c);  // (scratch: the ring)
@@ -673,20 +674,7 @@ cudaError_t launch_t(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st
     cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int groups = n_ctas / C::CG;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(groups * C::CG);
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C::CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.follows ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attend_tc_kernel<T, DH>, a, box, kmap, vmap);
+    return launch_in_stream(attend_tc_kernel<T, DH>, dim3(groups * C::CG), C::kThreads, C::kSmem, C::CG, st, a, box, kmap, vmap);
 }
 
 template <typename T, int DH>

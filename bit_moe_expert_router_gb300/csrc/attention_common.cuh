@@ -68,6 +68,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Every kernel here is launched beside the end of the one before it in the stream: it waits for that one's
+// end (and with it for all before) first, and only then lets the next be launched, so that what a kernel may
+// rely on when it starts is complete.
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;\ngriddepcontrol.launch_dependents;\n" ::: "memory");
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
@@ -179,9 +186,10 @@ __device__ __forceinline__ void deal_take(Cursor& c) {
     c.take = max(min(c.n, c.off + c.pass) - c.off, 0);
 }
 
-// prefix[b] = the line's length before sequence b, prefix[n_seqs] all of it.  Called by the whole block.
+// prefix[b] = the line's length before sequence b, prefix[n_seqs] all of it; adds the sequences' row tiles to
+// *tiles.  Called by the whole block.
 template <int ROWS, int KEYS>
-__device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix) {
+__device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix, int* tiles) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int B = a.kv.n_seqs;
     constexpr int kFew = 8;                    // more tiles than this are summed by warps,
@@ -192,6 +200,7 @@ __device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, 
         long long sum = 0;
         for (int rt = 0; rt < nt && nt <= kFew; ++rt) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
         prefix[b + 1] = nt <= kFew ? sum * a.kv.hkv : kOpen;
+        if (nt) atomicAdd(tiles, nt);
     }
     __syncthreads();
     const int each = max(warps / B, 1);  // warps for one sequence
@@ -245,7 +254,7 @@ __device__ __forceinline__ void deal_next(const AttendArgs& a, Cursor& c) {
     } while (c.take == 0);
 }
 
-// The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + 1 shared
+// The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + 2 shared
 // words.  A share has min_per units at least; tiles are cut one by one where that gives pieces of at
 // most own_pieces units.  Sets `c` in every thread, and this CTA's record of the tile that its share
 // begins in.
@@ -256,22 +265,21 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
     c.d.split = a.split;
     c.d.extra = extra;
     c.d.piece = 0;
-    deal_prefix<ROWS, KEYS>(a, c.d, prefix);
+    int* tiles_found = reinterpret_cast<int*>(prefix + B + 1);
+    if (threadIdx.x == 0) *tiles_found = 0;
+    __syncthreads();
+    deal_prefix<ROWS, KEYS>(a, c.d, prefix, tiles_found);
     long long total = prefix[B], per = 1;
     if (a.split) {
         per = max(div_line(total + all - 1, all), static_cast<long long>(min_per));
-        if (B * a.kv.hkv * 4 <= all) {  // (tiles of one sequence and head are counted only where that may be few)
-            long long tiles = 0;
-            for (int b = lane; b < B; b += 32) tiles += row_tiles<ROWS>(a, seq_info(a.kv, b));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(~0u, tiles, o);
-            tiles *= a.kv.hkv;
+        const long long tiles = static_cast<long long>(*tiles_found) * a.kv.hkv;
+        if (tiles * 4 <= all) {
             // pieces of p units: at most total / p + tiles of them
-            const long long p = tiles * 4 <= all ? max(div_line(total + all - tiles - 1, all - tiles), static_cast<long long>(min_per)) : 0;
-            if (p && p <= own_pieces) {
+            const long long p = max(div_line(total + all - tiles - 1, all - tiles), static_cast<long long>(min_per));
+            if (p <= own_pieces) {
                 __syncthreads();  // (the total has been read)
                 c.d.piece = static_cast<int>(p);
-                deal_prefix<ROWS, KEYS>(a, c.d, prefix);
+                deal_prefix<ROWS, KEYS>(a, c.d, prefix, tiles_found);
                 total = prefix[B];
                 per = 1;
             }
@@ -426,6 +434,25 @@ __device__ void clear_stray_rows(const AttendArgs& a) {
         if (a.lse)
             for (int x = threadIdx.x; x < a.kv.hq; x += blockDim.x) a.lse[static_cast<int64_t>(t) * a.kv.hq + x] = kNegInf;
     }
+}
+
+// Launches `kernel` as above, in clusters of `cluster` blocks.
+template <typename... Params, typename... Args>
+cudaError_t launch_in_stream(void (*kernel)(Params...), dim3 grid, int block, size_t smem, int cluster, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace moe

@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
     };
     uint4 raw[BATCH][C];
     enter();
+    wait_for_stream();
     load(raw, 0);  // under way while the token's place is looked up
 
     const int b = find_seq(a.kv, t);
@@ -318,9 +319,8 @@ cudaError_t launch_m(const AppendArgs& a, cudaStream_t st) {
     const int parts = many ? (rounds + kRoundsPerWarp - 1) / kRoundsPerWarp : rounds;
     const int per = (rounds + parts - 1) / parts;
     const dim3 grid((a.kv.n_tokens + kAppendThreads / 32 - 1) / (kAppendThreads / 32), parts);
-    if (many) kv_append_kernel<T, LPH, C, kBatch / C, TURN><<<grid, kAppendThreads, 0, st>>>(a, per);
-    else kv_append_kernel<T, LPH, C, 1, TURN><<<grid, kAppendThreads, 0, st>>>(a, per);
-    return cudaGetLastError();
+    auto kernel = many ? kv_append_kernel<T, LPH, C, kBatch / C, TURN> : kv_append_kernel<T, LPH, C, 1, TURN>;
+    return launch_in_stream(kernel, grid, kAppendThreads, 0, 1, st, a, per);
 }
 
 template <typename T, int LPH, int C>
