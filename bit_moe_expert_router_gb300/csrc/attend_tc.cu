@@ -59,18 +59,20 @@ struct TcCfg {
     static constexpr int kSlot = kKKeys * DH * 2;
     static constexpr int kSlots = DH == 64 ? 10 : DH == 128 ? 9 : 5;
     static constexpr int kExtra = 3;                    // key tiles that a row tile's beginning and end count for
-    static constexpr int kLook = NQ == 2 ? 1 : 2;       // K tiles ahead of V
+    static constexpr bool kOwnP = DH == 64;             // P has columns of its own, so S is free once it is read
+    static constexpr int kLook = NQ == 2 && !kOwnP ? 1 : 2;  // K tiles ahead of V
     static constexpr int kQTile = 128 * DH * 2;
     static constexpr int kThreads = 128 + 256 * NQ;
-    static constexpr int kSCol = 0, kOCol = 256;        // two S (or P) buffers of 128 columns, then O
+    static constexpr int kSCol = 0, kOCol = 256;        // two S buffers of 128 columns, then O
+    static constexpr int kPCol = kOwnP ? kOCol + NQ * DH : kSCol, kPStep = kOwnP ? 64 : 128;  // P, by buffer
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = kOffQ + NQ * kQTile;
     static constexpr int kOffEx = kOffRing + kSlots * kSlot;  // float [NQ][2][2][128]: what the halves of a row exchange
     static constexpr int kOffBars = kOffEx + NQ * 2048;
-    static constexpr int kBars = 2 * kSlots + 6 + 3 * NQ + 2;
+    static constexpr int kBars = 2 * kSlots + 8 + 3 * NQ + 2;
     static constexpr int kOffMisc = kOffBars + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 16;
-    static_assert(kOCol + NQ * DH <= 512, "tensor-memory columns");
+    static_assert((kOwnP ? kPCol + 2 * kPStep : kOCol + NQ * DH) <= 512, "tensor-memory columns");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -112,7 +114,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     uint64_t* empty = full + C::kSlots;       // [slots] MMA commit: the slot is read
     uint64_t* s_full = empty + C::kSlots;     // [2] MMA commit: S is there
     uint64_t* p_full = s_full + 2;            // [2] each CTA's eight softmax warps: P is there, S is read
-    uint64_t* q_full = p_full + 2;            // [NQ] each CTA's Q warps: Q is in shared memory
+    uint64_t* s_read = p_full + 2;            // [2] (P in its own columns) the same warps: S is read
+    uint64_t* q_full = s_read + 2;            // [NQ] each CTA's Q warps: Q is in shared memory
     uint64_t* q_free = q_full + C::NQ;        // [NQ] MMA commit: the tile's last S is there
     uint64_t* o_done = q_free + C::NQ;        // [2] MMA commit: P V is added (by P's buffer)
     uint64_t* o_free = o_done + 2;            // [NQ] each CTA's eight softmax warps: the tile's O is read
@@ -136,6 +139,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 8 * CG);
+            mbar_init(s_read + i, 8 * CG);
             mbar_init(o_done + i, 1);
         }
         for (int i = 0; i < C::NQ; ++i) {
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < kTcKeys / 16; ++k)
-                        mma_f16_ta<CG>(tmem + C::kOCol + DH * w, tmem + C::kSCol + 128 * buf + 8 * k, vd + ((s * C::kSlot + k * 2048) >> 4),
+                        mma_f16_ta<CG>(tmem + C::kOCol + DH * w, tmem + C::kPCol + C::kPStep * buf + 8 * k, vd + ((s * C::kSlot + k * 2048) >> 4),
                                        idesc16<T>(C::kTile, DH, true), !first || k > 0);
                     mma_commit<CG>(o_done + buf);
                 }
@@ -209,7 +213,43 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 const int n = c.take;
                 const int rows = min(c.s.q_len * kv.group - c.rt * C::kRows, C::kRows);
                 const int act = C::NQ == 2 && rows > C::kTile ? 2 : 1;
-                if constexpr (C::NQ == 2) {
+                if constexpr (C::kOwnP) {
+                    // slots: K0, K1, then V(j), K(j + 2); S of the next keys while the softmax of these runs
+                    auto next_s = [&](int j) {
+                        wait(full + slot, phase);
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            if (w >= act) break;
+                            if (j == 0) wait(q_full + w, items[w] & 1);
+                            else wait(s_read + w, (tiles[w] + j - 1) & 1);
+                            if (!ok) return;
+                            tc_fence_after();
+                            qk(w, w, slot);
+                            if (j + 1 == n) commit(q_free + w);
+                        }
+                        commit(empty + slot);
+                        advance();
+                    };
+                    next_s(0);
+                    for (int j = 0; j < n && ok; ++j) {
+                        if (j + 1 < n) next_s(j + 1);
+                        if (ok) wait(full + slot, phase);
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            if (w >= act || !ok) break;
+                            wait(p_full + w, (tiles[w] + j) & 1);
+                            if (j == 0) wait(o_free + w, (items[w] & 1) ^ 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            pv(w, w, slot, j == 0);
+                        }
+                        if (!ok) break;
+                        commit(empty + slot);
+                        advance();
+                    }
+                    // the last S's reading is not waited for above: P of the same tile follows it
+                    for (int w = 0; w < act; ++w) tiles[w] += n;
+                } else if constexpr (C::NQ == 2) {
                     // slots: K0, then V(j), K(j + 1)
                     wait(full + slot, phase);
 #pragma unroll
@@ -474,6 +514,11 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     tmem_ld_wait();
                     tmem_tie<32>(v);
                     tmem_tie<32>(v + 32);
+                    if constexpr (C::kOwnP) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(leaders(s_read + buf));
+                    }
                     const int key0 = (c.first + c.off + j) * kTcKeys + 64 * half;
                     const int rel_hi = p_hi - key0, rel_lo = p_lo - key0;
                     if (__any_sync(~0u, rel_hi < 63 || rel_lo >= 0)) {
@@ -516,6 +561,11 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                             tmem_st16(o_col + i, o);
                         }
                     }
+                    if constexpr (C::kOwnP) {  // the product before has read its P
+                        if (j > 0) ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
                     const float base = m == kNegInf ? 0.f : m * sc;
                     const uint64_t sc2 = pair(sc, sc), nb2 = pair(-base, -base);
 #pragma unroll
@@ -529,10 +579,15 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                             l2 = add2(l2, pair(p0, p1));
                             pk[i] = Elem<T>::pack(p0, p1);  // the product's operand: 16 bits; the sum l is of the fp32 values
                         }
-                        tmem_st16(s_col + 32 * half + 16 * h, pk);
+                        tmem_st16(tmem + lane_base + C::kPCol + C::kPStep * buf + 32 * half + 16 * h, pk);
                     }
                     tmem_st_wait();
                     tc_fence_before();
+                } else if constexpr (C::kOwnP) {
+                    if (lane == 0) mbar_arrive(leaders(s_read + buf));
+                    // (S may be two tiles ahead of P: not to count for this tile's P before the last one's is complete)
+                    if (j > 0) ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
+                    if (!ok) break;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(leaders(p_full + buf));
