@@ -102,8 +102,8 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
-    attend_tc_kernel(const AttendArgs a, int box_rows, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap) {
+    attend_tc_kernel(const AttendArgs a, int box_rows, int q_boxes, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
     using C = TcCfg<DH>;
     constexpr int CG = C::CG;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -432,6 +432,21 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     ok = __all_sync(~0u, wait_bar(q_free + w, (items & 1) ^ 1, ctl));
                     if (!ok) break;
                     ++items;
+                    if (q_boxes) {  // (heads of a group, tokens): the tile's rows in order, as boxes of 64 components
+                        constexpr int kMineBlocks = C::NQ == 2 ? DH / 64 : DH / 128;  // (one tile: half the components each)
+                        const int b0 = C::NQ == 2 ? 0 : (warp - 2) * kMineBlocks;
+                        if (lane == 0) {
+                            const uint32_t bar = leaders(q_full + w);
+                            mbar_expect_tx(bar, kMineBlocks * 16384);
+#pragma unroll
+                            for (int b = 0; b < kMineBlocks; ++b)
+                                tma_tile3d<CG>(smem_u32(sq) + (b0 + b) * 16384, &qmap, (b0 + b) * 64, c.h * kv.group,
+                                               c.s.q0 + div_by(r0, kv.by_group), bar);
+                        }
+                        __syncwarp();
+                        deal_next<C::kRows, kTcKeys>(a, c);
+                        continue;
+                    }
                     // where the rows begin: each lane finds its rows' places once, then passes them round
                     constexpr int kMine = C::NQ == 2 ? 128 : 64;  // this warp's rows
                     const int first = C::NQ == 2 ? 0 : (warp - 2) * 64;
@@ -702,6 +717,22 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     }
 }
 
+// The queries [tokens][heads][D] as a 3-D map (component, head, token), boxes of 64 components x the heads of
+// a group x as many tokens as make 128 rows.
+cudaError_t make_qmap(const AttendArgs& a, int dtype, CUtensorMap* map) {
+    Encode encode = nullptr;
+    if (cudaError_t e = get_encode(&encode); e != cudaSuccess) return e;
+    const KvArgs& kv = a.kv;
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kv.d), static_cast<cuuint64_t>(kv.hq), static_cast<cuuint64_t>(kv.n_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kv.hq > 1 ? 2 * a.q_hs : 16), static_cast<cuuint64_t>(kv.n_tokens > 1 ? 2 * a.q_ts : 16)};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(kv.group), static_cast<cuuint32_t>(128 / kv.group)};
+    const CUresult r = encode(map, dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(a.q), dims,
+                              strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // The cache [pages][page_size][heads][D] as a 4-D map (component, row, head, page), boxes of 64 components x
 // `box` rows in 128-byte-swizzled rows.  Anything outside reads zeros: components past D, the page past the last.
 cudaError_t make_map(const KvArgs& kv, const void* base, int64_t ps, int64_t rs, int64_t hs, int dtype, int box, CUtensorMap* map) {
@@ -726,10 +757,17 @@ cudaError_t launch_t(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st
     CUtensorMap kmap, vmap;
     if (cudaError_t e = make_map(a.kv, a.kv.k, a.kv.k_ps, a.kv.k_rs, a.kv.k_hs, dtype, box, &kmap); e != cudaSuccess) return e;
     if (cudaError_t e = make_map(a.kv, a.kv.v, a.kv.v_ps, a.kv.v_rs, a.kv.v_hs, dtype, box, &vmap); e != cudaSuccess) return e;
+    // Queries by TMA where the heads of a group divide a tile (then a tile begins with a token) and the strides fit a
+    // map; else row by row.
+    const int64_t most = int64_t(1) << 39;
+    const bool q_boxes = 128 % a.kv.group == 0 && (a.kv.hq == 1 || (a.q_hs > 0 && a.q_hs < most)) && (a.kv.n_tokens == 1 || (a.q_ts > 0 && a.q_ts < most));
+    CUtensorMap qmap = kmap;
+    if (q_boxes)
+        if (cudaError_t e = make_qmap(a, dtype, &qmap); e != cudaSuccess) return e;
     cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int groups = n_ctas / C::CG;
-    return launch_in_stream(attend_tc_kernel<T, DH>, dim3(groups * C::CG), C::kThreads, C::kSmem, C::CG, st, a, box, kmap, vmap);
+    return launch_in_stream(attend_tc_kernel<T, DH>, dim3(groups * C::CG), C::kThreads, C::kSmem, C::CG, st, a, box, q_boxes ? 1 : 0, kmap, vmap, qmap);
 }
 
 template <typename T, int DH>

@@ -164,6 +164,22 @@ __device__ __forceinline__ void tma_tile4d(uint32_t dst, const CUtensorMap* map,
             : "memory");
 }
 
+// The same for a 3-D box.
+template <int CG>
+__device__ __forceinline__ void tma_tile3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+}
+
 // One arrival on `bar` (CG = 2: on both CTAs' copies) when every MMA issued so far has finished.
 template <int CG>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
