@@ -536,10 +536,15 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     }
                     const int key0 = (c.first + c.off + j) * kTcKeys + 64 * half;
                     const int rel_hi = p_hi - key0, rel_lo = p_lo - key0;
-                    if (__any_sync(~0u, rel_hi < 63 || rel_lo >= 0)) {
+                    if (__any_sync(~0u, rel_hi < 63)) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i)
-                            if (i > rel_hi || i <= rel_lo) v[i] = __float_as_uint(kNegInf);
+                            if (i > rel_hi) v[i] = __float_as_uint(kNegInf);
+                    }
+                    if (__any_sync(~0u, rel_lo >= 0)) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i <= rel_lo) v[i] = __float_as_uint(kNegInf);
                     }
                     float mx[4];
 #pragma unroll
