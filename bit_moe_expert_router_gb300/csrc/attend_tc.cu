@@ -31,8 +31,8 @@
 // stays out of the sums.  Work is dealt in equal shares of 128-key units; the pieces of a cut
 // tile go through the workspace and the join.
 //
-// Warps: 0 MMA issue (one lane) and the tensor-memory allocation, 1 the K and V
-// tiles, 2-3 Q, then two warpgroups per row tile: softmax and output, a thread for half
+// Warps: 0 MMA issue (one lane) and the tensor-memory allocation, 1 the K tiles, 3 the
+// V tiles (a box takes its lane about 100 cycles to issue, and pages of 16 make 16 boxes a tile), 2 Q, then two warpgroups per row tile: softmax and output, a thread for half
 // of a row's keys (64 of a tile's 128) and half of its output, so that the way from S to P is
 // half as long; the halves exchange their maxima through shared memory.
 // Every wait is bounded; a timeout sets the status word and every role leaves.
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             mbar_init(o_done + i, 1);
         }
         for (int i = 0; i < C::NQ; ++i) {
-            mbar_init(q_full + i, 2 / C::NQ * CG);
+            mbar_init(q_full + i, CG);
             mbar_init(q_free + i, 1);
             mbar_init(o_free + i, 8 * CG);
         }
@@ -326,13 +326,11 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             __syncwarp();
             drain_bar(done, 0, global_ns() + kWaitNs);
           }
-        } else if (warp == 1) {
-            // ------------------------------------------------------------ K and V tiles
-            int use = 0;
+        } else if (warp == 1 || warp == 3) {
+            // ------------------------------------------------------------ K tiles (warp 1), V tiles (warp 3)
+            int base = 0;             // ring slots taken before this piece
             uint32_t tails = 0;
             int lo, hi;
-            int slot = 0;
-            uint32_t phase = 0;
             // Lane i brings box i of `rows` rows (at most 16 boxes) from key `key0` on: where it lies.
             auto where = [&](int key0, int boxes, int& row, int& page) {
                 const int key = key0 + lane * box_rows;
@@ -344,16 +342,18 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     if (id >= 0) page = id;
                 }
             };
-            auto advance = [&]() {
-                if (++slot == C::kSlots) slot = 0, phase ^= 1;
-                ++use;
+            // The slot of use `use` of the ring, free.
+            auto claim = [&](int use) {
+                const int slot = use % C::kSlots;
+                ok = __all_sync(~0u, wait_bar(empty + slot, (use / C::kSlots & 1) ^ 1, ctl));
+                return slot;
             };
-            auto load_k = [&](int unit) {
+            auto load_k = [&](int unit, int use) {
                 int row, page;
                 constexpr int kKeys = C::kKKeys;
                 const int boxes = kKeys / box_rows;
                 where(unit * kTcKeys + rank * kKeys, boxes, row, page);
-                ok = __all_sync(~0u, wait_bar(empty + slot, phase ^ 1, ctl));
+                const int slot = claim(use);
                 if (!ok) return;
                 const uint32_t bar = leaders(full + slot);
                 if (lane == 0) mbar_expect_tx(bar, C::kSlot);
@@ -362,13 +362,12 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 #pragma unroll
                     for (int b = 0; b < C::kKBlocks; ++b)
                         tma_tile4d<CG>(ring + slot * C::kSlot + (b * kKeys + lane * box_rows) * 128, &kmap, b * 64, row, c.h, page, bar);
-                advance();
             };
-            auto load_v = [&](int unit) {
+            auto load_v = [&](int unit, int use) {
                 int row, page;
                 const int boxes = kTcKeys / box_rows;
                 where(unit * kTcKeys, boxes, row, page);
-                ok = __all_sync(~0u, wait_bar(empty + slot, phase ^ 1, ctl));
+                const int slot = claim(use);
                 if (!ok) return;
                 const int last = hi - unit * kTcKeys;  // rows that some row of the tile sees
                 const bool cut = last > 0 && last < kTcKeys && last % box_rows != 0;
@@ -395,70 +394,65 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(there);
                 }
-                advance();
             };
             while (ok && c.u < c.end) {
                 const int n = c.take;
                 const int r0 = c.rt * C::kRows;
                 key_range(kv, a.window, c.s, r0, min(r0 + C::kRows, c.s.q_len * kv.group), lo, hi);
                 const int unit0 = c.first + c.off;
-                for (int j = 0; j < min(n, C::kLook) && ok; ++j) load_k(unit0 + j);
+                // (in the ring, K is kLook tiles ahead of V)
                 for (int j = 0; j < n && ok; ++j) {
-                    load_v(unit0 + j);
-                    if (ok && j + C::kLook < n) load_k(unit0 + j + C::kLook);
+                    if (warp == 1) load_k(unit0 + j, base + j + max(j - C::kLook + 1, 0));
+                    else load_v(unit0 + j, base + j + min(j + C::kLook, n));
                 }
+                base += 2 * n;
                 deal_next<C::kRows, kTcKeys>(a, c);
             }
             // Nothing is on its way to this CTA's memory when it leaves: every slot's last use has landed and been
             // read (or, after a timeout, the limit has passed).
             const uint64_t end = global_ns() + kWaitNs;
-            for (int u = max(use - C::kSlots, 0); u < use; ++u) {
+            for (int u = max(base - C::kSlots, 0); u < base; ++u) {
                 if (rank == 0) drain_bar(full + u % C::kSlots, (u / C::kSlots) & 1, end);
                 drain_bar(empty + u % C::kSlots, (u / C::kSlots) & 1, end);
             }
         } else {
-            // ------------------------------------------------------------ Q: warp 2 + w brings row tile w (one tile: half each)
-            const int w = C::NQ == 2 ? warp - 2 : 0;
-            uint8_t* sq = smem + C::kOffQ + w * C::kQTile;
-            uint32_t items = 0;
+            // ------------------------------------------------------------ Q
+            uint32_t items[2] = {0, 0};
             constexpr int kCpr = DH / 8, kPer = 32 / kCpr;  // chunks per row, rows per warp step
             const int x = lane % kCpr;
             while (ok && c.u < c.end) {
-
                 const int all = c.s.q_len * kv.group - c.rt * C::kRows;
-                if (all > C::kTile * w) {
+#pragma unroll 1
+                for (int w = 0; w < C::NQ; ++w) {
+                    if (all <= C::kTile * w || !ok) break;
+                    uint8_t* sq = smem + C::kOffQ + w * C::kQTile;
                     const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
                     const int rows = min(c.s.q_len * kv.group - r0, 128);
-                    ok = __all_sync(~0u, wait_bar(q_free + w, (items & 1) ^ 1, ctl));
+                    ok = __all_sync(~0u, wait_bar(q_free + w, (items[w] & 1) ^ 1, ctl));
                     if (!ok) break;
-                    ++items;
+                    ++items[w];
                     if (q_boxes) {  // (heads of a group, tokens): the tile's rows in order, as boxes of 64 components
-                        constexpr int kMineBlocks = C::NQ == 2 ? DH / 64 : DH / 128;  // (one tile: half the components each)
-                        const int b0 = C::NQ == 2 ? 0 : (warp - 2) * kMineBlocks;
                         if (lane == 0) {
                             const uint32_t bar = leaders(q_full + w);
-                            mbar_expect_tx(bar, kMineBlocks * 16384);
+                            mbar_expect_tx(bar, C::kQTile);
 #pragma unroll
-                            for (int b = 0; b < kMineBlocks; ++b)
-                                tma_tile3d<CG>(smem_u32(sq) + (b0 + b) * 16384, &qmap, (b0 + b) * 64, c.h * kv.group,
+                            for (int b = 0; b < DH / 64; ++b)
+                                tma_tile3d<CG>(smem_u32(sq) + b * 16384, &qmap, b * 64, c.h * kv.group,
                                                c.s.q0 + div_by(r0, kv.by_group), bar);
                         }
                         __syncwarp();
-                        deal_next<C::kRows, kTcKeys>(a, c);
                         continue;
                     }
                     // where the rows begin: each lane finds its rows' places once, then passes them round
-                    constexpr int kMine = C::NQ == 2 ? 128 : 64;  // this warp's rows
-                    const int first = C::NQ == 2 ? 0 : (warp - 2) * 64;
-#pragma unroll
-                    for (int g = 0; g < kMine; g += 32) {
+#pragma unroll 1
+                    for (int g = 0; g < 128; g += 32) {
                         int tok, hg;
-                        row_of(kv, r0 + max(min(first + g + lane, rows - 1), 0), tok, hg);
+                        row_of(kv, r0 + max(min(g + lane, rows - 1), 0), tok, hg);
                         const int64_t at = static_cast<int64_t>(c.s.q0 + tok) * a.q_ts + (c.h * kv.group + hg) * a.q_hs;
 #pragma unroll 8
                         for (int i = 0; i < 32; i += kPer) {
                             const int64_t from = __shfl_sync(~0u, at, i + lane / kCpr);
-                            const int r = first + g + i + lane / kCpr;
+                            const int r = g + i + lane / kCpr;
                             const bool in = r < rows && x * 8 < kv.d;
                             cp_async16(sq + (x / 8) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) << 4),
                                        static_cast<const T*>(a.q) + (in ? from + x * 8 : 0), in ? 16 : 0);
@@ -472,7 +466,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 }
                 deal_next<C::kRows, kTcKeys>(a, c);
             }
-            if (items) drain_bar(q_free + w, (items - 1) & 1, global_ns() + kWaitNs);  // (its arrival, too, has come)
+            for (int w = 0; w < C::NQ; ++w)
+                if (items[w]) drain_bar(q_free + w, (items[w] - 1) & 1, global_ns() + kWaitNs);  // (its arrival, too, has come)
         }
     } else {
         // ---------------------------------------------------------------- softmax, half a row per thread
