@@ -14,9 +14,11 @@
 // packed 16-bit values, and O += P V takes P from tensor memory and V from shared
 // memory as an MN-major operand (rows of the cache are rows of K there, no transposition).
 //   D <= 128: two tiles of 128 rows per CTA share the keys' tiles; while one tile's
-//     softmax runs the tensor pipe does the other's products.
+//     softmax runs the tensor pipe does the other's products.  (D <= 64 has columns to spare: P gets its
+//     own, and S of the next keys follows as soon as S is read.)
 //   D <= 256: one tile (O takes 256 of the 512 columns); S is double-buffered, so the
-//     tensor pipe does the next keys' S while the softmax of this one runs.
+//     tensor pipe does the next keys' S while the softmax of this one runs; so too with D <= 128 where
+//     the rows fill one tile only.
 //   D > 64: CTAs work in pairs (cta_group::2): an MMA covers 256 rows, 128 of each CTA, and each CTA
 //     brings half of K (64 keys) and half of V (half the components), so the bytes that
 //     each SM takes from L2, and from its shared memory for an MMA, are halved.
@@ -60,7 +62,8 @@ struct TcCfg {
     static constexpr int kSlots = DH == 64 ? 10 : DH == 128 ? 9 : 5;
     static constexpr int kExtra = 3;                    // key tiles that a row tile's beginning and end count for
     static constexpr bool kOwnP = DH == 64;             // P has columns of its own, so S is free once it is read
-    static constexpr int kLook = NQ == 2 && !kOwnP ? 1 : 2;  // K tiles ahead of V
+    // K tiles ahead of V, by the row tiles that have rows
+    static __device__ constexpr int look(int act) { return act == 2 && !kOwnP ? 1 : 2; }
     static constexpr int kQTile = 128 * DH * 2;
     static constexpr int kThreads = 128 + 256 * NQ;
     static constexpr int kSCol = 0, kOCol = 256;        // two S buffers of 128 columns, then O
@@ -167,6 +170,20 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const uint32_t ring = smem_u32(smem + C::kOffRing);
+    // Row tiles of the CTA (pair) that have rows, of the cursor's.
+    auto active = [&]() { return C::NQ == 2 && c.s.q_len * kv.group - c.rt * C::kRows > C::kTile ? 2 : 1; };
+    // The two S (P) buffers.  Two row tiles have one each; one alone alternates between them (except where P has columns
+    // of its own), beginning each piece with the first, so that S of the next keys is ready when the softmax of these ends.
+    // uses: of each buffer, before the piece; tile j of the piece is use uses[b] + (alternating ? j / 2 : j) of its buffer b.
+    auto alternates = [&](int act) { return act == 1 && !C::kOwnP; };
+    auto buf_of = [&](int w, int act, int j) { return alternates(act) ? j & 1 : w; };
+    auto use_of = [&](uint32_t uses0, uint32_t uses1, int w, int act, int j) {
+        return (buf_of(w, act, j) ? uses1 : uses0) + (alternates(act) ? j >> 1 : j);
+    };
+    auto count_uses = [&](uint32_t& uses0, uint32_t& uses1, int act, int n) {
+        uses0 += alternates(act) ? (n + 1) / 2 : n;
+        uses1 += alternates(act) ? n / 2 : act == 2 ? n : 0;
+    };
     bool ok = true;
 
     if (warp < 4) {
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(ring), vd = sdesc_mn(ring, kTcKeys * 128);
             int slot = 0;                     // the next ring slot of K or V,
             uint32_t phase = 0;               // and the phase of its barrier
-            uint32_t tiles[2] = {0, 0};       // key tiles so far, by warpgroup
+            uint32_t uses0 = 0, uses1 = 0;    // of the S buffers, before this piece
             uint32_t items[2] = {0, 0};       // row tiles so far, by warpgroup
             auto qk = [&](int w, int buf, int s) {  // S[buf] = Q[w] K^T, K in slot s
                 if (leader) {
@@ -211,8 +228,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             };
             while (ok && c.u < c.end) {
                 const int n = c.take;
-                const int rows = min(c.s.q_len * kv.group - c.rt * C::kRows, C::kRows);
-                const int act = C::NQ == 2 && rows > C::kTile ? 2 : 1;
+                const int act = active();
                 if constexpr (C::kOwnP) {
                     // slots: K0, K1, then V(j), K(j + 2); S of the next keys while the softmax of these runs
                     auto next_s = [&](int j) {
@@ -221,7 +237,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         for (int w = 0; w < 2; ++w) {
                             if (w >= act) break;
                             if (j == 0) wait(q_full + w, items[w] & 1);
-                            else wait(s_read + w, (tiles[w] + j - 1) & 1);
+                            else wait(s_read + w, ((w ? uses1 : uses0) + j - 1) & 1);
                             if (!ok) return;
                             tc_fence_after();
                             qk(w, w, slot);
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
                             if (w >= act || !ok) break;
-                            wait(p_full + w, (tiles[w] + j) & 1);
+                            wait(p_full + w, ((w ? uses1 : uses0) + j) & 1);
                             if (j == 0) wait(o_free + w, (items[w] & 1) ^ 1);
                             if (!ok) break;
                             tc_fence_after();
@@ -247,9 +263,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         commit(empty + slot);
                         advance();
                     }
-                    // the last S's reading is not waited for above: P of the same tile follows it
-                    for (int w = 0; w < act; ++w) tiles[w] += n;
-                } else if constexpr (C::NQ == 2) {
+                    // (the last S's reading is not waited for above: P of the same tile follows it)
+                } else if (act == 2) {
                     // slots: K0, then V(j), K(j + 1)
                     wait(full + slot, phase);
 #pragma unroll
@@ -273,10 +288,9 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
                             if (w >= act) break;
-                            wait(p_full + w, tiles[w] & 1);
+                            wait(p_full + w, ((w ? uses1 : uses0) + j) & 1);
                             if (j == 0) wait(o_free + w, (items[w] & 1) ^ 1);
                             if (!ok) break;
-                            ++tiles[w];
                             tc_fence_after();
                             pv(w, w, vs, j == 0);
                             if (w == act - 1) commit(empty + vs);
@@ -293,32 +307,31 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         }
                     }
                 } else {
-                    // slots: K0, K1, then V(j), K(j + 2); S buffers alternate over all tiles
+                    // slots: K0, K1, then V(j), K(j + 2)
                     wait(q_full, items[0] & 1);
                     auto next_s = [&](int j) {
                         wait(full + slot, phase);
                         if (!ok) return;
                         tc_fence_after();
-                        qk(0, (tiles[0] + j) & 1, slot);
+                        qk(0, j & 1, slot);
                         commit(empty + slot);
                         if (j + 1 == n) commit(q_free);
                         advance();
                     };
                     for (int j = 0; j < min(n, 2) && ok; ++j) next_s(j);
                     for (int j = 0; j < n && ok; ++j) {
-                        const uint32_t t = tiles[0] + j;
                         wait(full + slot, phase);
-                        wait(p_full + (t & 1), (t >> 1) & 1);
+                        wait(p_full + (j & 1), use_of(uses0, uses1, 0, act, j) & 1);
                         if (j == 0) wait(o_free, (items[0] & 1) ^ 1);
                         if (!ok) break;
                         tc_fence_after();
-                        pv(0, t & 1, slot, j == 0);
+                        pv(0, j & 1, slot, j == 0);
                         commit(empty + slot);
                         advance();
                         if (j + 2 < n) next_s(j + 2);
                     }
-                    tiles[0] += n;
                 }
+                count_uses(uses0, uses1, act, n);
                 for (int w = 0; w < act; ++w) ++items[w];
                 deal_next<C::kRows, kTcKeys>(a, c);
             }
@@ -400,10 +413,10 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 const int r0 = c.rt * C::kRows;
                 key_range(kv, a.window, c.s, r0, min(r0 + C::kRows, c.s.q_len * kv.group), lo, hi);
                 const int unit0 = c.first + c.off;
-                // (in the ring, K is kLook tiles ahead of V)
+                const int look = C::look(active());  // (in the ring, K is so many tiles ahead of V)
                 for (int j = 0; j < n && ok; ++j) {
-                    if (warp == 1) load_k(unit0 + j, base + j + max(j - C::kLook + 1, 0));
-                    else load_v(unit0 + j, base + j + min(j + C::kLook, n));
+                    if (warp == 1) load_k(unit0 + j, base + j + max(j - look + 1, 0));
+                    else load_v(unit0 + j, base + j + min(j + look, n));
                 }
                 base += 2 * n;
                 deal_next<C::kRows, kTcKeys>(a, c);
@@ -480,7 +493,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         float* ex = reinterpret_cast<float*>(smem + C::kOffEx) + 512 * w + row;  // [parity][half]
         const int ex_bar = 1 + 4 * w + (warp & 3);  // the two warps of the same rows
         const float sc = a.scale * kLog2e;
-        uint32_t tiles = 0;                         // key tiles of this row tile so far
+        uint32_t uses0 = 0, uses1 = 0;              // of the S buffers, before this piece
         uint32_t swaps = 0;
         // The other half's value.
         auto exchange = [&](float x) {
@@ -489,15 +502,17 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             asm volatile("bar.sync %0, 64;\n" ::"r"(ex_bar) : "memory");
             return at[128 * (half ^ 1)];
         };
-        // Tile t's S, P and P V: which buffer, and which phase of its barriers.  (One tile per CTA: P V of two
-        // tiles can be under way when the second P is stored, so they need a barrier each.)
-        auto buf_of = [&](uint32_t t) { return C::NQ == 2 ? w : static_cast<int>(t & 1); };
-        auto phase_of = [&](uint32_t t) { return (C::NQ == 2 ? t : t >> 1) & 1; };
         while (ok && c.u < c.end) {
             const int n = c.take;
             const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
             const int rows = min(c.s.q_len * kv.group - r0, 128);  // of this CTA's part of the row tile (may be none)
-            if (c.s.q_len * kv.group <= c.rt * C::kRows + C::kTile * w) {
+            const int act = active();
+            if (w >= act) {
+                // (the other row tile alternates: this one's buffer is gone through with it, or its next wait would not
+                // know one phase of the barrier from another)
+                if (alternates(act))
+                    for (int j = 1; j < n && ok; j += 2) ok = __all_sync(~0u, wait_bar(s_full + w, use_of(uses0, uses1, w, act, j) & 1, ctl));
+                count_uses(uses0, uses1, act, n);
                 deal_next<C::kRows, kTcKeys>(a, c);
                 continue;
             }
@@ -511,9 +526,14 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const int p_lo = a.window > 0 ? pos - a.window : -1;
             float m = kNegInf;                       // the reference, in units of S
             uint64_t l2 = pair(0.f, 0.f);
-            for (int j = 0; j < n; ++j, ++tiles) {
-                const int buf = buf_of(tiles);
-                ok = __all_sync(~0u, wait_bar(s_full + buf, phase_of(tiles), ctl));
+            // (P V of two tiles can be under way when an alternating row tile has stored the second P: a barrier each)
+            auto added = [&](int j) {  // P V of tile j
+                ok = __all_sync(~0u, wait_bar(o_done + buf_of(w, act, j), use_of(uses0, uses1, w, act, j) & 1, ctl));
+                return ok;
+            };
+            for (int j = 0; j < n; ++j) {
+                const int buf = buf_of(w, act, j);
+                ok = __all_sync(~0u, wait_bar(s_full + buf, use_of(uses0, uses1, w, act, j) & 1, ctl));
                 if (!ok) break;
                 if (live) {
                     tc_fence_after();
@@ -558,8 +578,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         m = top;
                     } else if (__any_sync(~0u, grew)) {
                         // O is rescaled between the products: the one before has to be there
-                        ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
-                        if (!ok) break;
+                        if (!added(j - 1)) break;
                         tc_fence_after();
                         const float f = grew ? (m == kNegInf ? 0.f : exp2_fast((m - top) * sc)) : 1.f;
                         if (grew) m = top;
@@ -577,8 +596,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         }
                     }
                     if constexpr (C::kOwnP) {  // the product before has read its P
-                        if (j > 0) ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
-                        if (!ok) break;
+                        if (j > 0 && !added(j - 1)) break;
                         tc_fence_after();
                     }
                     const float base = m == kNegInf ? 0.f : m * sc;
@@ -601,16 +619,15 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 } else if constexpr (C::kOwnP) {
                     if (lane == 0) mbar_arrive(leaders(s_read + buf));
                     // (S may be two tiles ahead of P: not to count for this tile's P before the last one's is complete)
-                    if (j > 0) ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
-                    if (!ok) break;
+                    if (j > 0 && !added(j - 1)) break;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(leaders(p_full + buf));
             }
             if (!ok) break;
             // ------------------------------------------------------------ the tile's output
-            ok = __all_sync(~0u, wait_bar(o_done + buf_of(tiles - 1), phase_of(tiles - 1), ctl));
-            if (!ok) break;
+            if (!added(n - 1)) break;
+            count_uses(uses0, uses1, act, n);
             tc_fence_after();
             const bool whole = c.whole();
             const int tok = c.s.q0 + tok_i, head = c.h * kv.group + hg;
