@@ -19,6 +19,8 @@ from .binding import MoeError, alloc_workspace  # noqa: F401
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 _lib = None
+# the current device, and the handle of its current stream, without the objects torch.cuda makes of them
+_device, _stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 class _KVBatch(ctypes.Structure):
@@ -113,16 +115,18 @@ class KVBatch:
 
     def _rows(self, t, name, n, heads):
         """(address, token stride, head stride) of a [n, heads, head_dim] tensor of this batch."""
-        ts, hs, es = t.stride() if t.dim() == 3 else (0, 0, 0)
-        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (n, heads, self.head_dim) or es != 1:
-            if t.dtype is not self.dtype:
-                raise TypeError(f"{name}: dtype {t.dtype}, expected {self.dtype}")
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-            if t.shape != (n, heads, self.head_dim):
-                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n, heads, self.head_dim)}")
-            raise ValueError(f"{name}: the components of a head must be contiguous")
-        return t.data_ptr(), ts, hs
+        # (one test on the way of every call; what was wrong is found out below)
+        if t.shape == (n, heads, self.head_dim) and t.dtype is self.dtype and t.get_device() == self._index:
+            ts, hs, es = t.stride()
+            if es == 1:
+                return t.data_ptr(), ts, hs
+        if t.dtype is not self.dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {self.dtype}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+        if t.shape != (n, heads, self.head_dim):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n, heads, self.head_dim)}")
+        raise ValueError(f"{name}: the components of a head must be contiguous")
 
 
 class HeadPrep:
@@ -200,12 +204,8 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda
 
 def _enqueue(fn: str, index: int, *args):
     """Calls `fn` with `args` and the current stream of device `index`, with that device current."""
-    call = getattr(_lib or _load(), fn)
-    if torch._C._cuda_getDevice() == index:
-        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        status = getattr(_load(), fn)(*args, _stream(index))
     if status != 0:
         raise MoeError(fn, status)
 
@@ -224,9 +224,22 @@ def moe_w4a8_kv_append(batch: KVBatch, prep: HeadPrep, q, k, v, q_out):
         raise ValueError(f"norm weights of {prep._weight_dim} components, heads of {batch.head_dim}")
     if prep.positions is not None and prep.positions.shape != (n,):
         raise ValueError(f"positions: shape {tuple(prep.positions.shape)}, expected {(n,)}")
-    _enqueue("moe_w4a8_kv_append", batch._index, batch._p, prep._p, n, *batch._rows(q, "q", n, hq), *batch._rows(k, "k", n, hkv),
-             *batch._rows(v, "v", n, hkv), *batch._rows(q_out, "q_out", n, hq))
+    args = (batch._p, prep._p, n, *batch._rows(q, "q", n, hq), *batch._rows(k, "k", n, hkv), *batch._rows(v, "v", n, hkv),
+            *batch._rows(q_out, "q_out", n, hq))
+    if _lib is None or _device() != batch._index:
+        _enqueue("moe_w4a8_kv_append", batch._index, *args)
+    elif status := _lib.moe_w4a8_kv_append(*args, _stream(batch._index)):
+        raise MoeError("moe_w4a8_kv_append", status)
     return q_out
+
+
+def _aligned(ws):
+    """(address, bytes) of the 256-byte aligned part of a workspace."""
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        binding._need(ws, "workspace", torch.uint8)
+    base = ws.data_ptr()
+    at = (base + 255) & -256
+    return at, ws.numel() - (at - base)
 
 
 def moe_w4a8_paged_attention(batch: KVBatch, q, out, lse=None, scale: float | None = None, window: int = 0, *, workspace):
@@ -247,6 +260,10 @@ def moe_w4a8_paged_attention(batch: KVBatch, q, out, lse=None, scale: float | No
         at = lse.data_ptr()
     if workspace.get_device() != batch._index:
         raise ValueError(f"workspace is on {workspace.device}, the cache on {batch.device}")
-    _enqueue("moe_w4a8_paged_attention", batch._index, batch._p, n, *batch._rows(q, "q", n, hq), *batch._rows(out, "out", n, hq),
-             at, batch.head_dim ** -0.5 if scale is None else scale, window, *binding._ws_view(workspace))
+    args = (batch._p, n, *batch._rows(q, "q", n, hq), *batch._rows(out, "out", n, hq), at,
+            batch.head_dim ** -0.5 if scale is None else scale, window, *_aligned(workspace))
+    if _lib is None or _device() != batch._index:
+        _enqueue("moe_w4a8_paged_attention", batch._index, *args)
+    elif status := _lib.moe_w4a8_paged_attention(*args, _stream(batch._index)):
+        raise MoeError("moe_w4a8_paged_attention", status)
     return out

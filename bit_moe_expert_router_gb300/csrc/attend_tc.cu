@@ -174,16 +174,9 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     auto active = [&]() { return C::NQ == 2 && c.s.q_len * kv.group - c.rt * C::kRows > C::kTile ? 2 : 1; };
     // The two S (P) buffers.  Two row tiles have one each; one alone alternates between them (except where P has columns
     // of its own), beginning each piece with the first, so that S of the next keys is ready when the softmax of these ends.
-    // uses: of each buffer, before the piece; tile j of the piece is use uses[b] + (alternating ? j / 2 : j) of its buffer b.
+    // uses: bit b is the parity of the times buffer b has been used, the phase of its barriers.
     auto alternates = [&](int act) { return act == 1 && !C::kOwnP; };
     auto buf_of = [&](int w, int act, int j) { return alternates(act) ? j & 1 : w; };
-    auto use_of = [&](uint32_t uses0, uint32_t uses1, int w, int act, int j) {
-        return (buf_of(w, act, j) ? uses1 : uses0) + (alternates(act) ? j >> 1 : j);
-    };
-    auto count_uses = [&](uint32_t& uses0, uint32_t& uses1, int act, int n) {
-        uses0 += alternates(act) ? (n + 1) / 2 : n;
-        uses1 += alternates(act) ? n / 2 : act == 2 ? n : 0;
-    };
     bool ok = true;
 
     if (warp < 4) {
@@ -195,7 +188,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(ring), vd = sdesc_mn(ring, kTcKeys * 128);
             int slot = 0;                     // the next ring slot of K or V,
             uint32_t phase = 0;               // and the phase of its barrier
-            uint32_t uses0 = 0, uses1 = 0;    // of the S buffers, before this piece
+            uint32_t uses = 0;                // of the S buffers, by the tiles whose P V is issued
             uint32_t items[2] = {0, 0};       // row tiles so far, by warpgroup
             auto qk = [&](int w, int buf, int s) {  // S[buf] = Q[w] K^T, K in slot s
                 if (leader) {
@@ -237,7 +230,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         for (int w = 0; w < 2; ++w) {
                             if (w >= act) break;
                             if (j == 0) wait(q_full + w, items[w] & 1);
-                            else wait(s_read + w, ((w ? uses1 : uses0) + j - 1) & 1);
+                            else wait(s_read + w, uses >> w & 1);
                             if (!ok) return;
                             tc_fence_after();
                             qk(w, w, slot);
@@ -253,11 +246,12 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
                             if (w >= act || !ok) break;
-                            wait(p_full + w, ((w ? uses1 : uses0) + j) & 1);
+                            wait(p_full + w, uses >> w & 1);
                             if (j == 0) wait(o_free + w, (items[w] & 1) ^ 1);
                             if (!ok) break;
                             tc_fence_after();
                             pv(w, w, slot, j == 0);
+                            uses ^= 1u << w;
                         }
                         if (!ok) break;
                         commit(empty + slot);
@@ -288,11 +282,12 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
                             if (w >= act) break;
-                            wait(p_full + w, ((w ? uses1 : uses0) + j) & 1);
+                            wait(p_full + w, uses >> w & 1);
                             if (j == 0) wait(o_free + w, (items[w] & 1) ^ 1);
                             if (!ok) break;
                             tc_fence_after();
                             pv(w, w, vs, j == 0);
+                            uses ^= 1u << w;
                             if (w == act - 1) commit(empty + vs);
                             if (more) {
                                 if (w == 0) wait(full + ks, phase);
@@ -321,17 +316,17 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     for (int j = 0; j < min(n, 2) && ok; ++j) next_s(j);
                     for (int j = 0; j < n && ok; ++j) {
                         wait(full + slot, phase);
-                        wait(p_full + (j & 1), use_of(uses0, uses1, 0, act, j) & 1);
+                        wait(p_full + (j & 1), uses >> (j & 1) & 1);
                         if (j == 0) wait(o_free, (items[0] & 1) ^ 1);
                         if (!ok) break;
                         tc_fence_after();
                         pv(0, j & 1, slot, j == 0);
+                        uses ^= 1u << (j & 1);
                         commit(empty + slot);
                         advance();
                         if (j + 2 < n) next_s(j + 2);
                     }
                 }
-                count_uses(uses0, uses1, act, n);
                 for (int w = 0; w < act; ++w) ++items[w];
                 deal_next<C::kRows, kTcKeys>(a, c);
             }
@@ -493,7 +488,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         float* ex = reinterpret_cast<float*>(smem + C::kOffEx) + 512 * w + row;  // [parity][half]
         const int ex_bar = 1 + 4 * w + (warp & 3);  // the two warps of the same rows
         const float sc = a.scale * kLog2e;
-        uint32_t uses0 = 0, uses1 = 0;              // of the S buffers, before this piece
+        uint32_t uses = 0;                          // of the S buffers, before this tile
         uint32_t swaps = 0;
         // The other half's value.
         auto exchange = [&](float x) {
@@ -511,8 +506,10 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 // (the other row tile alternates: this one's buffer is gone through with it, or its next wait would not
                 // know one phase of the barrier from another)
                 if (alternates(act))
-                    for (int j = 1; j < n && ok; j += 2) ok = __all_sync(~0u, wait_bar(s_full + w, use_of(uses0, uses1, w, act, j) & 1, ctl));
-                count_uses(uses0, uses1, act, n);
+                    for (int j = 1; j < n && ok; j += 2) {
+                        ok = __all_sync(~0u, wait_bar(s_full + w, uses >> w & 1, ctl));
+                        uses ^= 1u << w;
+                    }
                 deal_next<C::kRows, kTcKeys>(a, c);
                 continue;
             }
@@ -527,13 +524,13 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             float m = kNegInf;                       // the reference, in units of S
             uint64_t l2 = pair(0.f, 0.f);
             // (P V of two tiles can be under way when an alternating row tile has stored the second P: a barrier each)
-            auto added = [&](int j) {  // P V of tile j
-                ok = __all_sync(~0u, wait_bar(o_done + buf_of(w, act, j), use_of(uses0, uses1, w, act, j) & 1, ctl));
+            auto added = [&](int j) {  // P V of tile j, the last one counted in `uses`
+                ok = __all_sync(~0u, wait_bar(o_done + buf_of(w, act, j), (uses >> buf_of(w, act, j) & 1) ^ 1, ctl));
                 return ok;
             };
             for (int j = 0; j < n; ++j) {
                 const int buf = buf_of(w, act, j);
-                ok = __all_sync(~0u, wait_bar(s_full + buf, use_of(uses0, uses1, w, act, j) & 1, ctl));
+                ok = __all_sync(~0u, wait_bar(s_full + buf, uses >> buf & 1, ctl));
                 if (!ok) break;
                 if (live) {
                     tc_fence_after();
@@ -623,11 +620,12 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(leaders(p_full + buf));
+                uses ^= 1u << buf;
             }
             if (!ok) break;
             // ------------------------------------------------------------ the tile's output
             if (!added(n - 1)) break;
-            count_uses(uses0, uses1, act, n);
+            if (act == 2) uses ^= (n & 1u) << (w ^ 1);  // (the other row tile's)
             tc_fence_after();
             const bool whole = c.whole();
             const int tok = c.s.q0 + tok_i, head = c.h * kv.group + hg;

@@ -110,10 +110,16 @@ AttendLayout attend_layout(const moe_kv_batch_t* b) {
     return L;
 }
 
-// The tcgen05 engine takes batches whose row tiles fill more than one tile of the split engine, from pages that
-// TMA boxes of whole 8-row groups divide.
+// The tcgen05 engine takes batches whose rows fill more than one 16-row tile of the split engine, from pages that
+// TMA boxes of whole 8-row groups divide.  Two of those tiles go to the split engine too where the caches' visible part is
+// small (it reads it once for each): 4 sequences of 5 tokens (20 rows) at 500 positions of 8 heads of 128, 8 MB,
+// 12.5 us against 19.5; 4 of 3 tokens (24 rows) at 6000 positions of 2 heads of 256, 49 MB, 35 us against 25.
+constexpr int64_t kSmallCache = 16 << 20;
+
 bool use_tc(const moe_kv_batch_t* b, int64_t rows) {
     if (rows <= moe::kSplitRows || moe::tc_box_rows(static_cast<int>(b->page_size)) < 8) return false;
+    const int64_t keys = std::min<int64_t>(b->max_kv_len, kI32) * std::min<int64_t>(b->n_seqs, kMaxSeqs);
+    if (rows <= 2 * moe::kSplitRows && keys <= kSmallCache / (4 * b->n_kv_heads * b->head_dim)) return false;
     for (int64_t s : {b->k_page_stride, b->k_row_stride, b->k_head_stride, b->v_page_stride, b->v_row_stride, b->v_head_stride})
         if (s == 0 || s >= int64_t(1) << 39) return false;  // what a tensor map can hold
     return true;
