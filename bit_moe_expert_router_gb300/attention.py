@@ -100,15 +100,18 @@ class KVBatch:
                            ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], k_cache.data_ptr(), v_cache.data_ptr(),
                            block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr())
         self._p = ctypes.addressof(self._c)
-        self.workspace_size()  # refuses sizes and strides that the operators refuse
+        lib = _load()
+        if _device() == self._index:
+            self._workspace = lib.moe_w4a8_paged_attention_workspace_size(self._p)
+        else:
+            with torch.cuda.device(self._index):
+                self._workspace = lib.moe_w4a8_paged_attention_workspace_size(self._p)
+        if self._workspace == 0:  # sizes or strides that the operators refuse
+            raise MoeError("moe_w4a8_paged_attention_workspace_size", 1)
 
     def workspace_size(self) -> int:
         """Bytes of workspace of moe_w4a8_paged_attention for this batch, whatever its tokens."""
-        with torch.cuda.device(self.device):
-            n = _load().moe_w4a8_paged_attention_workspace_size(self._p)
-        if n == 0:
-            raise MoeError("moe_w4a8_paged_attention_workspace_size", 1)
-        return n
+        return self._workspace
 
     def alloc_workspace(self) -> torch.Tensor:
         return alloc_workspace(self.workspace_size(), self.device)
