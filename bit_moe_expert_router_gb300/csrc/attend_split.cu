@@ -137,6 +137,10 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
         for (int i = threadIdx.x; i < C::kOffMl / 16; i += blockDim.x) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
 
     wait_for_stream();
+    // a small table is brought near while the lengths are: its entries are the next to be waited for
+    if (static_cast<int64_t>(kv.n_seqs) * kv.width <= 1024)
+        for (int i = threadIdx.x * 8; i < kv.n_seqs * kv.width; i += blockDim.x * 8)
+            asm volatile("prefetch.global.L1 [%0];\n" ::"l"(kv.table + i));
     if (a.lead && blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
     Cursor c;
     deal_begin<kSplitRows, kKeys>(a, reinterpret_cast<long long*>(smem + C::kOffPrefix), kMinShare, kOwnPieces, kExtra, blockIdx.x, gridDim.x, c);
@@ -150,29 +154,35 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
         if (feed.c.u < feed.c.end) {
             Rows<ALIGNED>& rw = feed.rows;
             rw.settle(kv, feed.c.h);
-            unsigned char* sk = ring + stage * 2 * C::kTile * 2;
-            unsigned char* sv = sk + C::kTile * 2;
+            unsigned char* sk = ring + stage * C::kStageBytes;
             const int key0 = feed.unit * kKeys;
-            const int x = lane % C::kCpr;
+            const bool all = key0 + kKeys <= feed.hi && rw.ok;  // (ALIGNED: every key of the unit is read)
             constexpr int kRowsPer = 32 / C::kCpr;
+            const int x = lane % C::kCpr, row0 = lane / C::kCpr;
+            // chunk_at(i kRowsPer + row0, x), its row's low bits apart: row0 is below kRowsPer
+            unsigned char* at = sk + row0 * C::kCpr * 16;
+            const int xs = x ^ (row0 & 7);
+            const T *kp = kc + rw.k + row0 * kv.k_rs + x * 8, *vp = vc + rw.v + row0 * kv.v_rs + x * 8;
+            const int64_t k_step = kRowsPer * kv.k_rs, v_step = kRowsPer * kv.v_rs;
 #pragma unroll
             for (int i = 0; i < kKeys / kRowsPer; ++i) {
-                const int r = i * kRowsPer + lane / C::kCpr;
-                int64_t ko, vo;
+                const int r = i * kRowsPer + row0;
                 bool ok;
                 if constexpr (ALIGNED) {
-                    ko = rw.k + r * kv.k_rs;
-                    vo = rw.v + r * kv.v_rs;
-                    ok = rw.ok;
+                    ok = all || (rw.ok && key0 + r < feed.hi);
                 } else {
-                    ko = __shfl_sync(~0u, rw.k, r);
-                    vo = __shfl_sync(~0u, rw.v, r);
-                    ok = __shfl_sync(~0u, rw.ok ? 1 : 0, r);
+                    ok = __shfl_sync(~0u, rw.ok ? 1 : 0, r) && key0 + r < feed.hi;
+                    kp = kc + __shfl_sync(~0u, rw.k, r) + x * 8;
+                    vp = vc + __shfl_sync(~0u, rw.v, r) + x * 8;
                 }
-                ok = ok && key0 + r < feed.hi;
                 if (x < chunks) {  // a key that no row sees is zeros: whatever the cache holds there stays out
-                    cp_async16(sk + chunk_at<C::kCpr>(r, x), kc + (ok ? ko + x * 8 : 0), ok ? 16 : 0);
-                    cp_async16(sv + chunk_at<C::kCpr>(r, x), vc + (ok ? vo + x * 8 : 0), ok ? 16 : 0);
+                    unsigned char* to = at + i * kRowsPer * C::kCpr * 16 + ((xs ^ (i * kRowsPer & 7)) << 4);
+                    cp_async16(to, kp, ok ? 16 : 0);
+                    cp_async16(to + C::kTile * 2, vp, ok ? 16 : 0);
+                }
+                if constexpr (ALIGNED) {
+                    kp += k_step;
+                    vp += v_step;
                 }
             }
             feed.unit += C::kWarps;
