@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
 template <typename T, int DH, bool ALIGNED>
 cudaError_t launch_t(const AttendArgs& a, int n_ctas, int max_items, cudaStream_t st) {
     using C = SplitCfg<DH>;
-    const int smem = C::kOffPrefix + (a.kv.n_seqs + 2) * 8;
+    const int smem = C::kOffPrefix + (a.kv.n_seqs + kDealWords) * 8;
     cudaError_t e = cudaFuncSetAttribute(attend_split_kernel<T, DH, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = a.split ? n_ctas : max(1, min(max_items, n_ctas * 8));

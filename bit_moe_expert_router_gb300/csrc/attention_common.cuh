@@ -254,100 +254,166 @@ __device__ __forceinline__ void deal_next(const AttendArgs& a, Cursor& c) {
     } while (c.take == 0);
 }
 
-// The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + 2 shared
-// words.  A share has min_per units at least; tiles are cut one by one where that gives pieces of at
+// Inclusive sums over a warp's lanes.
+__device__ __forceinline__ long long lane_sums(long long x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, x, o);
+        if ((threadIdx.x & 31) >= o) x += y;
+    }
+    return x;
+}
+
+constexpr int kDealWords = 32;  // shared words of deal_begin beside one per sequence
+
+// The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + kDealWords
+// shared words.  A share has min_per units at least; tiles are cut one by one where that gives pieces of at
 // most own_pieces units.  Sets `c` in every thread, and this CTA's record of the tile that its share
-// begins in.
+// begins in.  Batches of up to 32 sequences (where the time until a CTA knows its share counts) are dealt
+// by one warp, a lane per sequence: 2.2 us from the kernel's start for 8 sequences, against 3.3 with the block.
 template <int ROWS, int KEYS>
 __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, int own_pieces, int extra, int me, int all, Cursor& c) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int B = a.kv.n_seqs;
     c.d.split = a.split;
     c.d.extra = extra;
     c.d.piece = 0;
-    int* tiles_found = reinterpret_cast<int*>(prefix + B + 1);
-    if (threadIdx.x == 0) *tiles_found = 0;
-    __syncthreads();
-    deal_prefix<ROWS, KEYS>(a, c.d, prefix, tiles_found);
-    long long total = prefix[B], per = 1;
-    if (a.split) {
+    c.b = c.rt = c.h = c.off = c.take = c.pass = c.first = c.n = 0;
+    long long total = 0, per = 1, rel = 0;
+    int nt = 0;  // row tiles of the sequence that the share begins in
+    // Units per CTA; true if the tiles are to be cut one by one instead, into pieces of c.d.piece.
+    auto cut = [&](long long tiles) {
+        if (!a.split) {
+            per = div_line(total + all - 1, all);
+            return false;
+        }
         per = max(div_line(total + all - 1, all), static_cast<long long>(min_per));
-        const long long tiles = static_cast<long long>(*tiles_found) * a.kv.hkv;
-        if (tiles * 4 <= all) {
-            // pieces of p units: at most total / p + tiles of them
-            const long long p = max(div_line(total + all - tiles - 1, all - tiles), static_cast<long long>(min_per));
-            if (p <= own_pieces) {
-                __syncthreads();  // (the total has been read)
-                c.d.piece = static_cast<int>(p);
-                deal_prefix<ROWS, KEYS>(a, c.d, prefix, tiles_found);
-                total = prefix[B];
-                per = 1;
+        if (tiles * 4 > all) return false;
+        // pieces of p units: at most total / p + tiles of them
+        const long long p = max(div_line(total + all - tiles - 1, all - tiles), static_cast<long long>(min_per));
+        if (p > own_pieces) return false;
+        c.d.piece = static_cast<int>(p);
+        per = 1;
+        return true;
+    };
+    auto place = [&]() {
+        c.u = c.begin = min(me * per, total);
+        c.end = min(c.u + per, total);
+    };
+    if (B <= 32) {
+        if (warp == 0) {
+            SeqInfo s = {0, 0, 0};
+            int own = 0;
+            if (lane < B) {
+                s = seq_info(a.kv, lane);
+                own = row_tiles<ROWS>(a, s);
+            }
+            auto length = [&]() {  // of this lane's sequence in the line
+                constexpr int kFew = 4;  // more tiles than this are summed by the warp
+                long long sum = 0;
+                for (int rt = 0; rt < own && own <= kFew; ++rt) sum += tile_weight<ROWS, KEYS>(a, c.d, s, rt);
+                for (unsigned many = __ballot_sync(~0u, own > kFew); many; many &= many - 1) {
+                    const int src = __ffs(many) - 1, n = __shfl_sync(~0u, own, src);
+                    const SeqInfo o = {__shfl_sync(~0u, s.q0, src), __shfl_sync(~0u, s.q_len, src), __shfl_sync(~0u, s.pos0, src)};
+                    long long part = 0;
+                    for (int rt = lane; rt < n; rt += 32) part += tile_weight<ROWS, KEYS>(a, c.d, o, rt);
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) part += __shfl_xor_sync(~0u, part, x);
+                    if (lane == src) sum = part;
+                }
+                return sum * a.kv.hkv;
+            };
+            long long len = length(), sums = lane_sums(len);
+            total = __shfl_sync(~0u, sums, 31);
+            if (cut(static_cast<long long>(__reduce_add_sync(~0u, own)) * a.kv.hkv)) {
+                len = length();
+                sums = lane_sums(len);
+                total = __shfl_sync(~0u, sums, 31);
+            }
+            place();
+            if (c.u < c.end) {
+                c.b = __ffs(__ballot_sync(~0u, sums > c.u)) - 1;
+                rel = c.u - __shfl_sync(~0u, sums - len, c.b);
+                c.s = {__shfl_sync(~0u, s.q0, c.b), __shfl_sync(~0u, s.q_len, c.b), __shfl_sync(~0u, s.pos0, c.b)};
+                nt = __shfl_sync(~0u, own, c.b);
             }
         }
     } else {
-        per = div_line(total + all - 1, all);
-    }
-    c.u = c.begin = min(me * per, total);
-    c.end = min(c.u + per, total);
-    c.b = c.rt = c.h = c.off = c.take = c.pass = c.first = c.n = 0;
-    int idx = 0, weight = 0;
-    if (c.u < c.end) {
-        int lo = 0, hi = B - 1;  // the sequence that holds unit u: the last b with prefix[b] <= u
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= c.u) lo = mid;
-            else hi = mid - 1;
+        int* tiles_found = reinterpret_cast<int*>(prefix + B + 1);
+        if (threadIdx.x == 0) *tiles_found = 0;
+        __syncthreads();
+        deal_prefix<ROWS, KEYS>(a, c.d, prefix, tiles_found);
+        total = prefix[B];
+        const long long tiles = static_cast<long long>(*tiles_found) * a.kv.hkv;
+        __syncthreads();  // (the total has been read)
+        if (cut(tiles)) {
+            deal_prefix<ROWS, KEYS>(a, c.d, prefix, tiles_found);
+            total = prefix[B];
         }
-        c.b = lo;
-        c.s = seq_info(a.kv, lo);
-        const int nt = row_tiles<ROWS>(a, c.s);
-        long long rel = c.u - prefix[lo];
-        for (int t0 = 0;; t0 += 32) {  // every warp walks the sequence's tiles, 32 at a time
-            const int rt = t0 + lane;
-            const int n = rt < nt ? tile_weight<ROWS, KEYS>(a, c.d, c.s, rt) : 0;
-            long long x = static_cast<long long>(n) * a.kv.hkv;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(~0u, x, o);
-                if (lane >= o) x += y;
+        place();
+        if (warp == 0 && c.u < c.end) {
+            int lo = 0, hi = B - 1;  // the sequence that holds unit u: the last b with prefix[b] <= u
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (prefix[mid] <= c.u) lo = mid;
+                else hi = mid - 1;
             }
-            const unsigned past = __ballot_sync(~0u, x > rel);
-            if (past || t0 + 32 >= nt) {
-                const int l = past ? __ffs(past) - 1 : 31;
-                rel -= __shfl_sync(~0u, x - static_cast<long long>(n) * a.kv.hkv, l);
-                weight = max(__shfl_sync(~0u, n, l), 1);
-                c.rt = min(t0 + l, nt - 1);
-                c.h = static_cast<int>(div_line(rel, weight));
-                idx = static_cast<int>(rel - static_cast<long long>(c.h) * weight);
-                break;
+            c.b = lo;
+            c.s = seq_info(a.kv, lo);
+            nt = row_tiles<ROWS>(a, c.s);
+            rel = c.u - prefix[lo];
+        }
+    }
+    Cursor* shared = reinterpret_cast<Cursor*>(prefix + B + 2);
+    static_assert(sizeof(Cursor) + 2 * 8 <= kDealWords * 8, "deal_begin's shared words");
+    if (warp == 0) {
+        int idx = 0, weight = 0;
+        if (c.u < c.end) {
+            for (int t0 = 0;; t0 += 32) {  // the sequence's tiles, 32 at a time
+                const int rt = t0 + lane;
+                const int n = rt < nt ? tile_weight<ROWS, KEYS>(a, c.d, c.s, rt) : 0;
+                const long long x = lane_sums(static_cast<long long>(n) * a.kv.hkv);
+                const unsigned past = __ballot_sync(~0u, x > rel);
+                if (past || t0 + 32 >= nt) {
+                    const int l = past ? __ffs(past) - 1 : 31;
+                    rel -= __shfl_sync(~0u, x - static_cast<long long>(n) * a.kv.hkv, l);
+                    weight = max(__shfl_sync(~0u, n, l), 1);
+                    c.rt = min(t0 + l, nt - 1);
+                    c.h = static_cast<int>(div_line(rel, weight));
+                    idx = static_cast<int>(rel - static_cast<long long>(c.h) * weight);
+                    break;
+                }
+                rel -= __shfl_sync(~0u, x, 31);
             }
-            rel -= __shfl_sync(~0u, x, 31);
+            c.n = key_units<ROWS, KEYS>(a, c.s, c.rt, c.first);
+            if (c.d.piece) {
+                c.off = static_cast<int>(div_line(static_cast<long long>(c.n) * idx, weight));
+                c.take = static_cast<int>(div_line(static_cast<long long>(c.n) * (idx + 1), weight)) - c.off;
+                c.pass = 1;
+            } else {
+                c.off = a.split ? idx : 0;
+                deal_take(c);
+            }
         }
-        c.n = key_units<ROWS, KEYS>(a, c.s, c.rt, c.first);
-        if (c.d.piece) {
-            c.off = static_cast<int>(div_line(static_cast<long long>(c.n) * idx, weight));
-            c.take = static_cast<int>(div_line(static_cast<long long>(c.n) * (idx + 1), weight)) - c.off;
-            c.pass = 1;
-        } else {
-            c.off = a.split ? idx : 0;
-            deal_take(c);
+        if (lane == 0 && a.split) {
+            BoundaryRec r;
+            r.begin = c.u - idx;
+            r.per = per;
+            r.n = c.d.piece ? weight : c.n;
+            r.cut = idx > 0 && idx < r.n;
+            r.rt = c.rt;
+            r.h = c.h;
+            r.q0 = c.s.q0;
+            r.q_len = c.s.q_len;
+            r.pos0 = c.s.pos0;
+            r.b = c.b;
+            a.recs[me] = r;
         }
+        if (c.u < c.end && c.take == 0) deal_next<ROWS, KEYS>(a, c);
+        if (lane == 0) *shared = c;
     }
-    if (threadIdx.x == 0 && a.split) {
-        BoundaryRec r;
-        r.begin = c.u - idx;
-        r.per = per;
-        r.n = c.d.piece ? weight : c.n;
-        r.cut = idx > 0 && idx < r.n;
-        r.rt = c.rt;
-        r.h = c.h;
-        r.q0 = c.s.q0;
-        r.q_len = c.s.q_len;
-        r.pos0 = c.s.pos0;
-        r.b = c.b;
-        a.recs[me] = r;
-    }
-    if (c.u < c.end && c.take == 0) deal_next<ROWS, KEYS>(a, c);
+    __syncthreads();
+    c = *shared;
 }
 
 // ---------------------------------------------------------------- the exact row
