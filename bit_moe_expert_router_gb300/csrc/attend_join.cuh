@@ -126,29 +126,42 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_rows_kernel(const
     for (int v = (cta - (c0 + 1)) + step * blockIdx.y; v / kSlices * 32 < rows; v += step * gridDim.y) {
         const int g = v / kSlices, col = v % kSlices * 64;  // rows 32 g .., components col ..
         const int r = 32 * g + lane;
-        float mm = kNegInf;
-#pragma unroll 4
-        for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, a.part_ml[slot_of(p) * ROWS + r].x);
-        const float base = mm == kNegInf ? 0.f : mm;
         if (threadIdx.x == 0) bad_rows = 0;
-        float ll = 0.f;
+        // pieces four at a time (two or three are usual), their loads all under way at once; the sums are
+        // rescaled between the fours
+        float mm = kNegInf, ll = 0.f;
         float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-        for (int p = c0; p <= c1; ++p) {
-            const int64_t slot = slot_of(p);
-            const float2 ml = a.part_ml[slot * ROWS + r];
-            const float4* o = reinterpret_cast<const float4*>(a.part_o + slot * ROWS * DH) + (col / 4 + 2 * warp) * ROWS + r;
-            const float4 x = o[0], y = o[ROWS];
-            const float f = exp2_fast(ml.x - base);
-            ll += ml.y * f;
-            acc[0].x += x.x * f;
-            acc[0].y += x.y * f;
-            acc[0].z += x.z * f;
-            acc[0].w += x.w * f;
-            acc[1].x += y.x * f;
-            acc[1].y += y.y * f;
-            acc[1].z += y.z * f;
-            acc[1].w += y.w * f;
+        auto add = [](float4& to, const float4& x, float f) {
+            to.x += x.x * f;
+            to.y += x.y * f;
+            to.z += x.z * f;
+            to.w += x.w * f;
+        };
+        for (int p0 = c0; p0 <= c1; p0 += 4) {
+            float2 ml[4];
+            float4 x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t slot = slot_of(min(p0 + i, c1));
+                ml[i] = a.part_ml[slot * ROWS + r];
+                const float4* o = reinterpret_cast<const float4*>(a.part_o + slot * ROWS * DH) + (col / 4 + 2 * warp) * ROWS + r;
+                x[i] = o[0];
+                y[i] = o[ROWS];
+            }
+            const float top = fmaxf(mm, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));  // (the last may count twice)
+            const float base = top == kNegInf ? 0.f : top, f0 = exp2_fast(mm - base);
+            mm = top;
+            ll *= f0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) acc[i] = make_float4(acc[i].x * f0, acc[i].y * f0, acc[i].z * f0, acc[i].w * f0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (p0 + i > c1) break;
+                const float f = exp2_fast(ml[i].x - base);
+                ll += ml[i].y * f;
+                add(acc[0], x[i], f);
+                add(acc[1], y[i], f);
+            }
         }
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         bool bad = ll != ll;
