@@ -33,10 +33,15 @@
 // stays out of the sums.  Work is dealt in equal shares of 128-key units; the pieces of a cut
 // tile go through the workspace and the join.
 //
-// Warps: 0 MMA issue (one lane) and the tensor-memory allocation, 1 the K tiles, 3 the
-// V tiles (a box takes its lane about 100 cycles to issue, and pages of 16 make 16 boxes a tile), 2 Q, then two warpgroups per row tile: softmax and output, a thread for half
-// of a row's keys (64 of a tile's 128) and half of its output, so that the way from S to P is
-// half as long; the halves exchange their maxima through shared memory.
+// Warps: 0 MMA issue (one lane) and the tensor-memory allocation, 1 the K tiles, 3 the V tiles (a
+// box takes its lane about 100 cycles to issue, and pages of 16 make 16 boxes a tile), 2 Q, then two
+// warpgroups per row tile: softmax and output, a thread for half of a row's keys (64 of a tile's 128)
+// and half of its output, so that the way from S to P is half as long; the halves exchange their
+// maxima through shared memory.
+// Measured: 8192-token prompt, 16 / 2 heads of 256: 330 us, 1.66 PFLOP/s, 86% of the tensor pipe's cycles;
+// 4096 tokens of 32 / 8 heads of 128 140 us, 0.98 PFLOP/s (softmax, P, P V and the next Q K in a chain); heads of
+// 64 107 us, 0.64 PFLOP/s.  Alternating S buffers for a single row tile: 32 sequences of 8 tokens at 8000
+// positions 343 -> 244 us, for which that 4096-token prompt went from 142 to 146 when it came.
 // Every wait is bounded; a timeout sets the status word and every role leaves.
 #include <algorithm>
 
@@ -60,7 +65,10 @@ struct TcCfg {
     static constexpr int kKBlocks = DH / 64, kVBlocks = kVCols / 64;  // in column blocks of 64
     static constexpr int kSlot = kKKeys * DH * 2;
     static constexpr int kSlots = DH == 64 ? 10 : DH == 128 ? 9 : 5;
-    static constexpr int kExtra = 3;                    // key tiles that a row tile's beginning and end count for
+    // Key tiles that a row tile's beginning and end count for.  A 4096-token prompt of 32 / 8 heads of 128 takes 140 us,
+    // without it 224 (heads of 64 107 and 207, 16 / 2 of 256 100 and 164): the first row tiles are short,
+    // so an equal share of keys holds many of them.
+    static constexpr int kExtra = 3;
     static constexpr bool kOwnP = DH == 64;             // P has columns of its own, so S is free once it is read
     // K tiles ahead of V, by the row tiles that have rows
     static __device__ constexpr int look(int act) { return act == 2 && !kOwnP ? 1 : 2; }
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     if (a.lead && blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
     const int rank = CG == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CG;
     Cursor c;
-    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, 16, C::kExtra, me, gridDim.x / CG, c);  // (scratch: the ring)
+    deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, C::kExtra, me, gridDim.x / CG, c);  // (scratch: the ring)
     clear_stray_rows<T>(a);
     tc_fence_before();
     fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA

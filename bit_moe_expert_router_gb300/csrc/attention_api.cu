@@ -126,7 +126,9 @@ bool use_tc(const moe_kv_batch_t* b, int64_t rows) {
 }
 
 // Up to this many positions a row tile stays with one CTA: the pieces' way through memory and the second
-// kernel cost more than the keys' streaming by one CTA.
+// kernel cost more than the keys' streaming by one CTA.  32 / 8 heads of 128, whole | split: one sequence of 100
+// positions 5.9 | 9.3 us, 760 11.3 | 8.9, 1500 17.1 | 9.6; eight sequences of 760 11.9 | 13.6, of 1000 15.8 | 15.8.
+// (One sequence would gain from a lower bound, eight from a higher one.)
 constexpr int64_t kWholeKeys = 768;
 
 #define MOE_ATTEND(call)                                                         \
@@ -229,7 +231,8 @@ MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_toke
         return MOE_OK;
     }
     // Sequences of few rows among longer ones (decoding requests beside a chunk) go to the split engine: a tile of
-    // 256 or 512 rows that they fill by a few streams their keys at less than half its rate.
+    // 256 or 512 rows that they fill by a few streams their keys at less than half its rate: a chunk among
+    // decoding requests 132 us, all on the tcgen05 engine 172.
     a.split = 1;
     moe::AttendArgs few = a;
     const bool mixed = n_tokens <= (batch->n_seqs - 1) * max_q + moe::kSplitRows / a.kv.group;  // (there may be some)

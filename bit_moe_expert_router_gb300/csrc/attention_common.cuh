@@ -128,16 +128,12 @@ __device__ __forceinline__ void key_range(const KvArgs& a, int window, const Seq
 // The batch's work is a line of units: sequence by sequence, row tile by row tile (ROWS rows of one
 // sequence's token-major (token, head of the group) rows), key/value head by head, key unit by key
 // unit (KEYS consecutive positions).  CTA c takes units [c per, (c + 1) per), so the grid's shares
-// differ by one unit at most however ragged the batch is.  Where the tiles are few and the shares
-// short, each tile is cut into pieces of its own instead, one per CTA: a CTA that ends one tile and
-// begins another starts its copies twice, which then costs more than the balance gains.  Pieces of
-// a cut tile are put together by the join.  A tile whose rows see nothing has one unit (its rows
-// still have to be written), and each tile counts `extra` units more at its end, for what a CTA spends on
-// beginning and ending it.
+// differ by one unit at most however ragged the batch is.  Pieces of a cut tile are put together by the
+// join.  A tile whose rows see nothing has one unit (its rows still have to be written), and each tile
+// counts `extra` units more at its end, for what a CTA spends on beginning and ending it.
 struct Deal {
     int split;           // 0: a tile is one unit of the line
     int extra;
-    int piece;           // > 0: a tile of n units is cut into ceil(n / piece) pieces, the line's units
 };
 
 template <int ROWS>
@@ -160,7 +156,7 @@ __device__ __forceinline__ int tile_weight(const AttendArgs& a, const Deal& d, c
     if (!d.split) return 1;
     int first;
     const int n = key_units<ROWS, KEYS>(a, s, rt, first);
-    return d.piece ? static_cast<int>(static_cast<unsigned>(n + d.piece - 1) / static_cast<unsigned>(d.piece)) : n + d.extra;
+    return n + d.extra;
 }
 
 struct Cursor {
@@ -186,10 +182,9 @@ __device__ __forceinline__ void deal_take(Cursor& c) {
     c.take = max(min(c.n, c.off + c.pass) - c.off, 0);
 }
 
-// prefix[b] = the line's length before sequence b, prefix[n_seqs] all of it; adds the sequences' row tiles to
-// *tiles.  Called by the whole block.
+// prefix[b] = the line's length before sequence b, prefix[n_seqs] all of it.  Called by the whole block.
 template <int ROWS, int KEYS>
-__device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix, int* tiles) {
+__device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int B = a.kv.n_seqs;
     constexpr int kFew = 8;                    // more tiles than this are summed by warps,
@@ -200,7 +195,6 @@ __device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, 
         long long sum = 0;
         for (int rt = 0; rt < nt && nt <= kFew; ++rt) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
         prefix[b + 1] = nt <= kFew ? sum * a.kv.hkv : kOpen;
-        if (nt) atomicAdd(tiles, nt);
     }
     __syncthreads();
     const int each = max(warps / B, 1);  // warps for one sequence
@@ -267,36 +261,20 @@ __device__ __forceinline__ long long lane_sums(long long x) {
 constexpr int kDealWords = 32;  // shared words of deal_begin beside one per sequence
 
 // The share of CTA (or pair of CTAs) `me` of `all`.  Called by the whole block.  prefix: n_seqs + kDealWords
-// shared words.  A share has min_per units at least; tiles are cut one by one where that gives pieces of at
-// most own_pieces units.  Sets `c` in every thread, and this CTA's record of the tile that its share
-// begins in.  Batches of up to 32 sequences (where the time until a CTA knows its share counts) are dealt
+// shared words.  A share has min_per units at least.  Sets `c` in every thread, and this CTA's record of the
+// tile that its share begins in.  Batches of up to 32 sequences (where the time until a CTA knows its share counts) are dealt
 // by one warp, a lane per sequence: 2.2 us from the kernel's start for 8 sequences, against 3.3 with the block.
 template <int ROWS, int KEYS>
-__device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, int own_pieces, int extra, int me, int all, Cursor& c) {
+__device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, int extra, int me, int all, Cursor& c) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int B = a.kv.n_seqs;
     c.d.split = a.split;
     c.d.extra = extra;
-    c.d.piece = 0;
     c.b = c.rt = c.h = c.off = c.take = c.pass = c.first = c.n = 0;
     long long total = 0, per = 1, rel = 0;
     int nt = 0;  // row tiles of the sequence that the share begins in
-    // Units per CTA; true if the tiles are to be cut one by one instead, into pieces of c.d.piece.
-    auto cut = [&](long long tiles) {
-        if (!a.split) {
-            per = div_line(total + all - 1, all);
-            return false;
-        }
-        per = max(div_line(total + all - 1, all), static_cast<long long>(min_per));
-        if (tiles * 4 > all) return false;
-        // pieces of p units: at most total / p + tiles of them
-        const long long p = max(div_line(total + all - tiles - 1, all - tiles), static_cast<long long>(min_per));
-        if (p > own_pieces) return false;
-        c.d.piece = static_cast<int>(p);
-        per = 1;
-        return true;
-    };
     auto place = [&]() {
+        per = max(div_line(total + all - 1, all), static_cast<long long>(a.split ? min_per : 0));
         c.u = c.begin = min(me * per, total);
         c.end = min(c.u + per, total);
     };
@@ -323,13 +301,8 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
                 }
                 return sum * a.kv.hkv;
             };
-            long long len = length(), sums = lane_sums(len);
+            const long long len = length(), sums = lane_sums(len);
             total = __shfl_sync(~0u, sums, 31);
-            if (cut(static_cast<long long>(__reduce_add_sync(~0u, own)) * a.kv.hkv)) {
-                len = length();
-                sums = lane_sums(len);
-                total = __shfl_sync(~0u, sums, 31);
-            }
             place();
             if (c.u < c.end) {
                 c.b = __ffs(__ballot_sync(~0u, sums > c.u)) - 1;
@@ -339,17 +312,8 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
             }
         }
     } else {
-        int* tiles_found = reinterpret_cast<int*>(prefix + B + 1);
-        if (threadIdx.x == 0) *tiles_found = 0;
-        __syncthreads();
-        deal_prefix<ROWS, KEYS>(a, c.d, prefix, tiles_found);
+        deal_prefix<ROWS, KEYS>(a, c.d, prefix);
         total = prefix[B];
-        const long long tiles = static_cast<long long>(*tiles_found) * a.kv.hkv;
-        __syncthreads();  // (the total has been read)
-        if (cut(tiles)) {
-            deal_prefix<ROWS, KEYS>(a, c.d, prefix, tiles_found);
-            total = prefix[B];
-        }
         place();
         if (warp == 0 && c.u < c.end) {
             int lo = 0, hi = B - 1;  // the sequence that holds unit u: the last b with prefix[b] <= u
@@ -367,7 +331,7 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
     Cursor* shared = reinterpret_cast<Cursor*>(prefix + B + 2);
     static_assert(sizeof(Cursor) + 2 * 8 <= kDealWords * 8, "deal_begin's shared words");
     if (warp == 0) {
-        int idx = 0, weight = 0;
+        int idx = 0;
         if (c.u < c.end) {
             for (int t0 = 0;; t0 += 32) {  // the sequence's tiles, 32 at a time
                 const int rt = t0 + lane;
@@ -377,7 +341,7 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
                 if (past || t0 + 32 >= nt) {
                     const int l = past ? __ffs(past) - 1 : 31;
                     rel -= __shfl_sync(~0u, x - static_cast<long long>(n) * a.kv.hkv, l);
-                    weight = max(__shfl_sync(~0u, n, l), 1);
+                    const int weight = max(__shfl_sync(~0u, n, l), 1);
                     c.rt = min(t0 + l, nt - 1);
                     c.h = static_cast<int>(div_line(rel, weight));
                     idx = static_cast<int>(rel - static_cast<long long>(c.h) * weight);
@@ -386,20 +350,14 @@ __device__ void deal_begin(const AttendArgs& a, long long* prefix, int min_per, 
                 rel -= __shfl_sync(~0u, x, 31);
             }
             c.n = key_units<ROWS, KEYS>(a, c.s, c.rt, c.first);
-            if (c.d.piece) {
-                c.off = static_cast<int>(div_line(static_cast<long long>(c.n) * idx, weight));
-                c.take = static_cast<int>(div_line(static_cast<long long>(c.n) * (idx + 1), weight)) - c.off;
-                c.pass = 1;
-            } else {
-                c.off = a.split ? idx : 0;
-                deal_take(c);
-            }
+            c.off = a.split ? idx : 0;
+            deal_take(c);
         }
         if (lane == 0 && a.split) {
             BoundaryRec r;
             r.begin = c.u - idx;
             r.per = per;
-            r.n = c.d.piece ? weight : c.n;
+            r.n = c.n;
             r.cut = idx > 0 && idx < r.n;
             r.rt = c.rt;
             r.h = c.h;

@@ -13,6 +13,10 @@
 // 3 or 4 shuffles.  A rotated pair lies in one lane (interleaved, and halves of 128) or in
 // two lanes whose distance is the same for the whole head (halves), which
 // costs four shuffles of the packed elements.
+//
+// Measured: 8192 tokens 40.6 us, 4.2 TB/s; a copy of as many bytes takes 26.7 us.  Other shapes (64 threads a
+// block, 5 to 24 rounds a warp, 2 chunks in flight, 5 to 8 blocks an SM) took 39.4 to 48.5.  Streaming stores
+// would give 2048 mixed tokens 0.7 us, but the keys are read next.
 #include <algorithm>
 
 #include "attention_common.cuh"
@@ -23,6 +27,8 @@ namespace {
 constexpr int kAppendThreads = 128;
 constexpr int kRoundsPerWarp = 12;
 constexpr int kBatch = 4;  // chunks a lane has in flight, and as many of the next rounds
+// From this many rounds on warps take several: 1024 tokens of 16 / 2 heads of 256 7.3 us, one each 10.0 (8192
+// 40.6 and 66); below it 64 tokens take 2.6 us with one each, 6.4 with several.
 constexpr int64_t kManyRounds = 64 * 152;
 
 // The sequence that token t belongs to (its index b with q_start[b] <= t < q_start[b + 1]), or -1.
