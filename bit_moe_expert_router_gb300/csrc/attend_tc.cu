@@ -794,9 +794,11 @@ cudaError_t launch_t(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st
 }
 
 template <typename T, int DH>
-cudaError_t launch_j(const AttendArgs& a, int n_ctas, cudaStream_t st) {
+cudaError_t launch_j(const AttendArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
+    constexpr int kRows = TcCfg<DH>::kRows;
     const int groups = n_ctas / TcCfg<DH>::CG;
-    return groups < 2 ? cudaSuccess : launch_attend_join_rows<T, TcCfg<DH>::kRows, DH>(a, groups, st);
+    const int64_t tiles = a.kv.n_seqs * ((rows + kRows - 1) / kRows) * a.kv.hkv;
+    return groups < 2 ? cudaSuccess : launch_attend_join_rows<T, kRows, DH>(a, groups, tiles, st);
 }
 
 template <typename T>
@@ -819,12 +821,12 @@ int tc_part_rows(int d, int n_ctas) {
     }
 }
 
-cudaError_t launch_attend_tc_join(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st) {
+cudaError_t launch_attend_tc_join(const AttendArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
     const bool bf = dtype == 0;
     switch (padded_dim(a.kv.d)) {
-        case 64: return bf ? launch_j<__nv_bfloat16, 64>(a, n_ctas, st) : launch_j<__half, 64>(a, n_ctas, st);
-        case 128: return bf ? launch_j<__nv_bfloat16, 128>(a, n_ctas, st) : launch_j<__half, 128>(a, n_ctas, st);
-        default: return bf ? launch_j<__nv_bfloat16, 256>(a, n_ctas, st) : launch_j<__half, 256>(a, n_ctas, st);
+        case 64: return bf ? launch_j<__nv_bfloat16, 64>(a, rows, n_ctas, st) : launch_j<__half, 64>(a, rows, n_ctas, st);
+        case 128: return bf ? launch_j<__nv_bfloat16, 128>(a, rows, n_ctas, st) : launch_j<__half, 128>(a, rows, n_ctas, st);
+        default: return bf ? launch_j<__nv_bfloat16, 256>(a, rows, n_ctas, st) : launch_j<__half, 256>(a, rows, n_ctas, st);
     }
 }
 

@@ -90,6 +90,7 @@ cudaError_t launch_attend_split_join(const AttendArgs& a, int dtype, int n_ctas,
 int tc_box_rows(int page);  // rows of a page that one TMA box takes
 int tc_part_rows(int d, int n_ctas);  // rows of all pieces
 cudaError_t launch_attend_tc(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st);
-cudaError_t launch_attend_tc_join(const AttendArgs& a, int dtype, int n_ctas, cudaStream_t st);
+// rows: of a sequence per key/value head, at most
+cudaError_t launch_attend_tc_join(const AttendArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st);
 
 }  // namespace moe

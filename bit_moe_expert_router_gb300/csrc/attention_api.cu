@@ -248,6 +248,6 @@ MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_toke
     pieces(1);
     MOE_ATTEND(moe::launch_attend_tc(a, dtype, L.n_ctas, st));
     if (mixed) MOE_ATTEND(moe::launch_attend_split_join(few, dtype, L.n_ctas, st));
-    MOE_ATTEND(moe::launch_attend_tc_join(a, dtype, L.n_ctas, st));
+    MOE_ATTEND(moe::launch_attend_tc_join(a, dtype, rows, L.n_ctas, st));
     return MOE_OK;
 }
