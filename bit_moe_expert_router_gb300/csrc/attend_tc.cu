@@ -80,7 +80,7 @@ struct TcCfg {
     static constexpr int kOffRing = kOffQ + NQ * kQTile;
     static constexpr int kOffEx = kOffRing + kSlots * kSlot;  // float [NQ][2][2][128]: what the halves of a row exchange
     static constexpr int kOffBars = kOffEx + NQ * 2048;
-    static constexpr int kBars = 2 * kSlots + 8 + 3 * NQ + 2;
+    static constexpr int kBars = 2 * kSlots + 11 + 3 * NQ + 2;
     static constexpr int kOffMisc = kOffBars + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 16;
     static_assert((kOwnP ? kPCol + 2 * kPStep : kOCol + NQ * DH) <= 512, "tensor-memory columns");
@@ -123,13 +123,14 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     // tells is committed to both CTAs' copies.
     uint64_t* full = bars;                    // [slots] each CTA's loader: the slot's bytes have landed
     uint64_t* empty = full + C::kSlots;       // [slots] MMA commit: the slot is read
-    uint64_t* s_full = empty + C::kSlots;     // [2] MMA commit: S is there
-    uint64_t* p_full = s_full + 2;            // [2] each CTA's eight softmax warps: P is there, S is read
-    uint64_t* s_read = p_full + 2;            // [2] (P in its own columns) the same warps: S is read
+    // ([3]: an S buffer's uses by its own row tile, two, and those of the second buffer by a row tile that alternates)
+    uint64_t* s_full = empty + C::kSlots;     // [3] MMA commit: S is there
+    uint64_t* p_full = s_full + 3;            // [3] each CTA's eight softmax warps: P is there, S is read
+    uint64_t* s_read = p_full + 3;            // [2] (P in its own columns) the same warps: S is read
     uint64_t* q_full = s_read + 2;            // [NQ] each CTA's Q warps: Q is in shared memory
     uint64_t* q_free = q_full + C::NQ;        // [NQ] MMA commit: the tile's last S is there
-    uint64_t* o_done = q_free + C::NQ;        // [2] MMA commit: P V is added (by P's buffer)
-    uint64_t* o_free = o_done + 2;            // [NQ] each CTA's eight softmax warps: the tile's O is read
+    uint64_t* o_done = q_free + C::NQ;        // [3] MMA commit: P V is added
+    uint64_t* o_free = o_done + 3;            // [NQ] each CTA's eight softmax warps: the tile's O is read
     uint64_t* tail = o_free + C::NQ;          // the bytes of a V slot that is cleared by hand
     uint64_t* done = tail + 1;                // MMA commit: everything issued has finished
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -147,10 +148,10 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             mbar_init(full + i, CG);
             mbar_init(empty + i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 8 * CG);
-            mbar_init(s_read + i, 8 * CG);
+            if (i < 2) mbar_init(s_read + i, 8 * CG);
             mbar_init(o_done + i, 1);
         }
         for (int i = 0; i < C::NQ; ++i) {
@@ -182,9 +183,12 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     auto active = [&]() { return C::NQ == 2 && c.s.q_len * kv.group - c.rt * C::kRows > C::kTile ? 2 : 1; };
     // The two S (P) buffers.  Two row tiles have one each; one alone alternates between them (except where P has columns
     // of its own), beginning each piece with the first, so that S of the next keys is ready when the softmax of these ends.
-    // uses: bit b is the parity of the times buffer b has been used, the phase of its barriers.
-    auto alternates = [&](int act) { return act == 1 && !C::kOwnP; };
-    auto buf_of = [&](int w, int act, int j) { return alternates(act) ? j & 1 : w; };
+    // Barriers go by who uses a buffer (set 0 and 1: a row tile its own, 2: the first row tile the second buffer), so
+    // that their phases are waited for by the warps that the next phase waits for: none can be missed, however
+    // late the second row tile's warps are in the piece before.
+    // uses: bit s is the parity of the times that set s has been used, the phase of its barriers.
+    auto buf_of = [&](int w, int act, int j) { return act == 1 && !C::kOwnP ? j & 1 : w; };
+    auto set_of = [&](int w, int act, int j) { return act == 1 && !C::kOwnP ? (j & 1) * 2 : w; };
     bool ok = true;
 
     if (warp < 4) {
@@ -196,26 +200,26 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(ring), vd = sdesc_mn(ring, kTcKeys * 128);
             int slot = 0;                     // the next ring slot of K or V,
             uint32_t phase = 0;               // and the phase of its barrier
-            uint32_t uses = 0;                // of the S buffers, by the tiles whose P V is issued
+            uint32_t uses = 0;                // of the sets, by the tiles whose P V is issued
             uint32_t items[2] = {0, 0};       // row tiles so far, by warpgroup
-            auto qk = [&](int w, int buf, int s) {  // S[buf] = Q[w] K^T, K in slot s
+            auto qk = [&](int w, int buf, int set, int s) {  // S[buf] = Q[w] K^T, K in slot s
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < DH / 16; ++k)
                         mma_f16_ss<CG>(tmem + C::kSCol + 128 * buf, qd + ((w * C::kQTile + k / 4 * 16384 + k % 4 * 32) >> 4),
                                        kd + ((s * C::kSlot + k / 4 * (C::kKKeys * 128) + k % 4 * 32) >> 4), idesc16<T>(C::kTile, kTcKeys, false),
                                        k > 0);
-                    mma_commit<CG>(s_full + buf);
+                    mma_commit<CG>(s_full + set);
                 }
                 __syncwarp();
             };
-            auto pv = [&](int w, int buf, int s, bool first) {  // O[w] (+)= P[buf] V, V in slot s
+            auto pv = [&](int w, int buf, int set, int s, bool first) {  // O[w] (+)= P[buf] V, V in slot s
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < kTcKeys / 16; ++k)
                         mma_f16_ta<CG>(tmem + C::kOCol + DH * w, tmem + C::kPCol + C::kPStep * buf + 8 * k, vd + ((s * C::kSlot + k * 2048) >> 4),
                                        idesc16<T>(C::kTile, DH, true), !first || k > 0);
-                    mma_commit<CG>(o_done + buf);
+                    mma_commit<CG>(o_done + set);
                 }
                 __syncwarp();
             };
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                             else wait(s_read + w, uses >> w & 1);
                             if (!ok) return;
                             tc_fence_after();
-                            qk(w, w, slot);
+                            qk(w, w, w, slot);
                             if (j + 1 == n) commit(q_free + w);
                         }
                         commit(empty + slot);
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                             if (j == 0) wait(o_free + w, (items[w] & 1) ^ 1);
                             if (!ok) break;
                             tc_fence_after();
-                            pv(w, w, slot, j == 0);
+                            pv(w, w, w, slot, j == 0);
                             uses ^= 1u << w;
                         }
                         if (!ok) break;
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         wait(q_full + w, items[w] & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        qk(w, w, slot);
+                        qk(w, w, w, slot);
                         if (n == 1) commit(q_free + w);
                     }
                     if (!ok) break;
@@ -294,13 +298,13 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                             if (j == 0) wait(o_free + w, (items[w] & 1) ^ 1);
                             if (!ok) break;
                             tc_fence_after();
-                            pv(w, w, vs, j == 0);
+                            pv(w, w, w, vs, j == 0);
                             uses ^= 1u << w;
                             if (w == act - 1) commit(empty + vs);
                             if (more) {
                                 if (w == 0) wait(full + ks, phase);
                                 if (!ok) break;
-                                qk(w, w, ks);
+                                qk(w, w, w, ks);
                                 if (j + 2 == n) commit(q_free + w);
                             }
                         }
@@ -316,20 +320,21 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                         wait(full + slot, phase);
                         if (!ok) return;
                         tc_fence_after();
-                        qk(0, j & 1, slot);
+                        qk(0, j & 1, (j & 1) * 2, slot);
                         commit(empty + slot);
                         if (j + 1 == n) commit(q_free);
                         advance();
                     };
                     for (int j = 0; j < min(n, 2) && ok; ++j) next_s(j);
                     for (int j = 0; j < n && ok; ++j) {
+                        const int set = (j & 1) * 2;
                         wait(full + slot, phase);
-                        wait(p_full + (j & 1), uses >> (j & 1) & 1);
+                        wait(p_full + set, uses >> set & 1);
                         if (j == 0) wait(o_free, (items[0] & 1) ^ 1);
                         if (!ok) break;
                         tc_fence_after();
-                        pv(0, j & 1, slot, j == 0);
-                        uses ^= 1u << (j & 1);
+                        pv(0, j & 1, set, slot, j == 0);
+                        uses ^= 1u << set;
                         commit(empty + slot);
                         advance();
                         if (j + 2 < n) next_s(j + 2);
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         float* ex = reinterpret_cast<float*>(smem + C::kOffEx) + 512 * w + row;  // [parity][half]
         const int ex_bar = 1 + 4 * w + (warp & 3);  // the two warps of the same rows
         const float sc = a.scale * kLog2e;
-        uint32_t uses = 0;                          // of the S buffers, before this tile
+        uint32_t uses = 0;                          // of the sets, before this tile
         uint32_t swaps = 0;
         // The other half's value.
         auto exchange = [&](float x) {
@@ -511,13 +516,6 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const int rows = min(c.s.q_len * kv.group - r0, 128);  // of this CTA's part of the row tile (may be none)
             const int act = active();
             if (w >= act) {
-                // (the other row tile alternates: this one's buffer is gone through with it, or its next wait would not
-                // know one phase of the barrier from another)
-                if (alternates(act))
-                    for (int j = 1; j < n && ok; j += 2) {
-                        ok = __all_sync(~0u, wait_bar(s_full + w, uses >> w & 1, ctl));
-                        uses ^= 1u << w;
-                    }
                 deal_next<C::kRows, kTcKeys>(a, c);
                 continue;
             }
@@ -533,12 +531,13 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             uint64_t l2 = pair(0.f, 0.f);
             // (P V of two tiles can be under way when an alternating row tile has stored the second P: a barrier each)
             auto added = [&](int j) {  // P V of tile j, the last one counted in `uses`
-                ok = __all_sync(~0u, wait_bar(o_done + buf_of(w, act, j), (uses >> buf_of(w, act, j) & 1) ^ 1, ctl));
+                const int set = set_of(w, act, j);
+                ok = __all_sync(~0u, wait_bar(o_done + set, (uses >> set & 1) ^ 1, ctl));
                 return ok;
             };
             for (int j = 0; j < n; ++j) {
-                const int buf = buf_of(w, act, j);
-                ok = __all_sync(~0u, wait_bar(s_full + buf, uses >> buf & 1, ctl));
+                const int buf = buf_of(w, act, j), set = set_of(w, act, j);
+                ok = __all_sync(~0u, wait_bar(s_full + set, uses >> set & 1, ctl));
                 if (!ok) break;
                 if (live) {
                     tc_fence_after();
@@ -627,13 +626,12 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     if (j > 0 && !added(j - 1)) break;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(leaders(p_full + buf));
-                uses ^= 1u << buf;
+                if (lane == 0) mbar_arrive(leaders(p_full + set));
+                uses ^= 1u << set;
             }
             if (!ok) break;
             // ------------------------------------------------------------ the tile's output
             if (!added(n - 1)) break;
-            if (act == 2) uses ^= (n & 1u) << (w ^ 1);  // (the other row tile's)
             tc_fence_after();
             const bool whole = c.whole();
             const int tok = c.s.q0 + tok_i, head = c.h * kv.group + hg;
