@@ -82,7 +82,8 @@ struct TcCfg {
     static constexpr int kOffBars = kOffEx + NQ * 2048;
     static constexpr int kBars = 2 * kSlots + 11 + 3 * NQ + 2;
     static constexpr int kOffMisc = kOffBars + 8 * kBars;
-    static constexpr int kSmem = kOffMisc + 16;
+    static constexpr int kOffStart = kOffMisc + 16;     // the cursor at the share's beginning
+    static constexpr int kSmem = kOffStart + sizeof(Cursor);
     static_assert((kOwnP ? kPCol + 2 * kPStep : kOCol + NQ * DH) <= 512, "tensor-memory columns");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -109,6 +110,37 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
+}
+
+// Of the rows of a softmax warp in the whole tiles from `c` on, those that ended with a NaN, taken again one by one
+// (every second: the warp of the rows' other half has the others).  A row can take as long as its context is long:
+// this comes after all the pieces, when no role waits for the warp.
+template <typename T, int DH>
+__device__ __noinline__ void retake_rows(const AttendArgs& a, Cursor c, int rank, int w, int quarter, int half) {
+    using C = TcCfg<DH>;
+    const KvArgs& kv = a.kv;
+    const int lane = threadIdx.x & 31;
+    while (c.u < c.end) {
+        const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
+        const int rows = c.whole() ? min(c.s.q_len * kv.group - r0, 32 * quarter + 32) : 0;
+        for (int r = 32 * quarter + half; r < rows; r += 2) {
+            int tok, hg;
+            row_of(kv, r0 + r, tok, hg);
+            const int head = c.h * kv.group + hg;
+            bool odd = false;
+            if (lane * 8 < kv.d) {
+                const uint4 o = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + (c.s.q0 + tok) * a.o_ts + head * a.o_hs + lane * 8);
+                const uint32_t o4[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = Elem<T>::unpack(o4[i]);
+                    odd |= f.x != f.x || f.y != f.y;
+                }
+            }
+            if (__any_sync(~0u, odd)) attend_row<T>(a, c.b, c.s.q0 + tok, head, c.s.pos0 + tok);
+        }
+        deal_next<C::kRows, kTcKeys>(a, c);
+    }
 }
 
 template <typename T, int DH>
@@ -171,6 +203,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     const int rank = CG == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CG;
     Cursor c;
     deal_begin<C::kRows, kTcKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 2, C::kExtra, me, gridDim.x / CG, c);  // (scratch: the ring)
+    if (tid == 0) *reinterpret_cast<Cursor*>(smem + C::kOffStart) = c;
     clear_stray_rows<T>(a);
     tc_fence_before();
     fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
@@ -503,6 +536,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         const float sc = a.scale * kLog2e;
         uint32_t uses = 0;                          // of the sets, before this tile
         uint32_t swaps = 0;
+        bool odd = false;                           // some row of the warp ended with a NaN
         // The other half's value.
         auto exchange = [&](float x) {
             float* at = ex + 256 * (swaps++ & 1);
@@ -714,16 +748,12 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(leaders(o_free + w));
-            if (live && whole) {
-                bad |= exchange(bad ? 1.f : 0.f) != 0.f;  // (and both halves of the row are stored)
-                unsigned again = half == 0 ? __ballot_sync(~0u, mine && bad) : 0;
-                while (again) {
-                    const int src = __ffs(again) - 1;
-                    again &= again - 1;
-                    attend_row<T>(a, c.b, __shfl_sync(~0u, tok, src), __shfl_sync(~0u, head, src), __shfl_sync(~0u, pos, src));
-                }
-            }
+            odd |= __any_sync(~0u, mine && bad && whole);
             deal_next<C::kRows, kTcKeys>(a, c);
+        }
+        if (ok) {
+            odd |= exchange(odd ? 1.f : 0.f) != 0.f;  // (and both halves of the rows are stored)
+            if (odd) retake_rows<T, DH>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w, warp & 3, half);
         }
     }
 

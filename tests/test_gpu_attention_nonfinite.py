@@ -43,3 +43,14 @@ def test_one_row_tile_after_two_with_values_that_one_token_sees(d):
     for i, n in enumerate(c.kv_len):
         c.spoil_value(i, n - 1, math.nan if i % 4 < 2 else math.inf, comp=i % d)
     c.check()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lengths", [([200] * 90, [200] * 90), ([300, 20, 1], [2000, 1500, 1700])])
+def test_values_that_later_tokens_see(lengths, d):
+    """Whole row tiles, several to a CTA, and tiles in pieces: rows before the place keep their values, rows after it have NaN (or
+    the infinity) in that component alone."""
+    c = Batch(*lengths, 8, 2, d, 16, seed=43)
+    for i, (n, total) in enumerate(zip(*lengths)):
+        c.spoil_value(i, total - n + (2 * n) // 3, (math.nan, math.inf, -math.inf)[i % 3], head=i % 2, comp=(7 * i) % d)
+    c.check()
