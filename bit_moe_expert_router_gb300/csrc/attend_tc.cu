@@ -47,6 +47,7 @@
 
 #include "attend_join.cuh"
 #include "attention_common.cuh"
+#include "pair_exchange.h"
 #include "tcgen05.cuh"
 
 namespace moe {
@@ -78,7 +79,7 @@ struct TcCfg {
     static constexpr int kPCol = kOwnP ? kOCol + NQ * DH : kSCol, kPStep = kOwnP ? 64 : 128;  // P, by buffer
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = kOffQ + NQ * kQTile;
-    static constexpr int kOffEx = kOffRing + kSlots * kSlot;  // float [NQ][2][2][128]: what the halves of a row exchange
+    static constexpr int kOffEx = kOffRing + kSlots * kSlot;  // [NQ][2][2][128]: what the halves of a row exchange
     static constexpr int kOffBars = kOffEx + NQ * 2048;
     static constexpr int kBars = 2 * kSlots + 11 + 3 * NQ + 2;
     static constexpr int kOffMisc = kOffBars + 8 * kBars;
@@ -105,6 +106,13 @@ __device__ constexpr uint32_t idesc16(int m, int n, bool b_mn) {
     return (1u << 4) | (MmaFmt<T>::v << 7) | (MmaFmt<T>::v << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
 }
+
+// The meeting of the two softmax warps of the same rows, at a named barrier.
+struct WarpPairBarrier {
+    int id;
+    __device__ __forceinline__ void sync() { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
+    __device__ __forceinline__ void arrive() { asm volatile("bar.arrive %0, 64;\n" ::"r"(id) : "memory"); }
+};
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
@@ -531,18 +539,16 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         const int row = tid & 127;                  // tile row = tensor-memory lane
         const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t o_col = tmem + lane_base + C::kOCol + DH * w + DH / 2 * half;
-        float* ex = reinterpret_cast<float*>(smem + C::kOffEx) + 512 * w + row;  // [parity][half]
-        const int ex_bar = 1 + 4 * w + (warp & 3);  // the two warps of the same rows
+        PairExchange<WarpPairBarrier> other{reinterpret_cast<uint32_t*>(smem + C::kOffEx) + 512 * w + row, 128, half, 0, {1 + 4 * w + (warp & 3)}};
         const float sc = a.scale * kLog2e;
         uint32_t uses = 0;                          // of the sets, before this tile
-        uint32_t swaps = 0;
         bool odd = false;                           // some row of the warp ended with a NaN
-        // The other half's value.
-        auto exchange = [&](float x) {
-            float* at = ex + 256 * (swaps++ & 1);
-            at[128 * half] = x;
-            asm volatile("bar.sync %0, 64;\n" ::"r"(ex_bar) : "memory");
-            return at[128 * (half ^ 1)];
+        bool left = false;                          // the other half's warp has left
+        // The other half's value in x's place; false: it has left, and so does this one.
+        auto exchange = [&](float& x) {
+            left = __any_sync(~0u, !other.swap(x));
+            ok = !left;
+            return ok;
         };
         while (ok && c.u < c.end) {
             const int n = c.take;
@@ -609,7 +615,9 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(v[60 + x]));
                     float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                    top = fmaxf(top, exchange(top));  // (S of both halves is read: P may be stored over it)
+                    float top2 = top;
+                    if (!exchange(top2)) break;  // (S of both halves is read: P may be stored over it)
+                    top = fmaxf(top, top2);
                     // (with m = -inf the difference is inf, or NaN if the row has seen nothing yet)
                     const bool grew = (top - m) * sc > 8.f;
                     if (j == 0) {
@@ -663,9 +671,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 if (lane == 0) mbar_arrive(leaders(p_full + set));
                 uses ^= 1u << set;
             }
-            if (!ok) break;
+            if (!ok || !added(n - 1)) break;
             // ------------------------------------------------------------ the tile's output
-            if (!added(n - 1)) break;
             tc_fence_after();
             const bool whole = c.whole();
             const int tok = c.s.q0 + tok_i, head = c.h * kv.group + hg;
@@ -673,8 +680,9 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             const int part = 2 * me + (c.u == c.begin ? 0 : 1), r_tile = C::kTile * w + 128 * rank + row;
             if (live) {
                 const float2 lp = unpair(l2);
-                float l = lp.x + lp.y;
-                l += exchange(l);
+                float l = lp.x + lp.y, l_other = l;
+                if (!exchange(l_other)) break;
+                l += l_other;
                 bad = l != l;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 if (whole) {
@@ -751,9 +759,10 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             odd |= __any_sync(~0u, mine && bad && whole);
             deal_next<C::kRows, kTcKeys>(a, c);
         }
-        if (ok) {
-            odd |= exchange(odd ? 1.f : 0.f) != 0.f;  // (and both halves of the rows are stored)
-            if (odd) retake_rows<T, DH>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w, warp & 3, half);
+        if (!ok && !left) other.leave();
+        float odds = odd ? 1.f : 0.f;
+        if (ok && exchange(odds)) {  // (and both halves of the rows are stored)
+            if (odd || odds != 0.f) retake_rows<T, DH>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w, warp & 3, half);
         }
     }
 
