@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
           }
         } else if (warp == 1 || warp == 3) {
             // ------------------------------------------------------------ K tiles (warp 1), V tiles (warp 3)
-            int base = 0;             // ring slots taken before this piece
+            int base = 0;             // ring slots taken before this piece,
+            int top = 0;              // and by this warp's latest copies
             uint32_t tails = 0;
             int lo, hi;
             // Lane i brings box i of `rows` rows (at most 16 boxes) from key `key0` on: where it lies.
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 where(unit * kTcKeys + rank * kKeys, boxes, row, page);
                 const int slot = claim(use);
                 if (!ok) return;
+                top = use + 1;
                 const uint32_t bar = leaders(full + slot);
                 if (lane == 0) mbar_expect_tx(bar, C::kSlot);
                 __syncwarp();
@@ -431,6 +433,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 where(unit * kTcKeys, boxes, row, page);
                 const int slot = claim(use);
                 if (!ok) return;
+                top = use + 1;
                 const int last = hi - unit * kTcKeys;  // rows that some row of the tile sees
                 const bool cut = last > 0 && last < kTcKeys && last % box_rows != 0;
                 const uint32_t there = leaders(full + slot), bar = cut ? own_bar(tail) : there;
@@ -471,9 +474,11 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                 deal_next<C::kRows, kTcKeys>(a, c);
             }
             // Nothing is on its way to this CTA's memory when it leaves: every slot's last use has landed and been
-            // read (or, after a timeout, the limit has passed).
+            // read (or, after a timeout, the limit has passed), those of a piece that was given up among them.
+            // (Both CTAs' copies count on the first one's barriers, and a pair leaves together.)
+            top = max(top, base);
             const uint64_t end = global_ns() + kWaitNs;
-            for (int u = max(base - C::kSlots, 0); u < base; ++u) {
+            for (int u = max(top - C::kSlots, 0); u < top; ++u) {
                 if (rank == 0) drain_bar(full + u % C::kSlots, (u / C::kSlots) & 1, end);
                 drain_bar(empty + u % C::kSlots, (u / C::kSlots) & 1, end);
             }
