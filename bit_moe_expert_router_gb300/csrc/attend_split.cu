@@ -234,10 +234,10 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
             const int r = (lane >> 2) + 8 * x;
             const int p = c.s.pos0 + div_by(r0 + min(r, rows - 1), kv.by_group);
             p_hi[x] = min(p, kv.cap - 1);
-            p_lo[x] = a.window > 0 ? p - a.window : -1;
+            p_lo[x] = before_window(a.window, p);
         }
         const int all_hi = c.s.pos0 + div_by(r0, kv.by_group);                                          // every row sees keys <= all_hi
-        const int all_lo = a.window > 0 ? c.s.pos0 + div_by(r0 + rows - 1, kv.by_group) - a.window : -1;  // and > all_lo
+        const int all_lo = before_window(a.window, c.s.pos0 + div_by(r0 + rows - 1, kv.by_group));  // and > all_lo
 
         float o[DH / 8][4];
 #pragma unroll

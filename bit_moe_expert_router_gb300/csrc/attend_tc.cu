@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             row_of(kv, r_in, tok_i, hg);
             const int pos = c.s.pos0 + tok_i;
             const int p_hi = min(pos, kv.cap - 1);
-            const int p_lo = a.window > 0 ? pos - a.window : -1;
+            const int p_lo = before_window(a.window, pos);
             float m = kNegInf;                       // the reference, in units of S
             uint64_t l2 = pair(0.f, 0.f);
             // (P V of two tiles can be under way when an alternating row tile has stored the second P: a barrier each)

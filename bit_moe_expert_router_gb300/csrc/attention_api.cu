@@ -206,7 +206,7 @@ MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_toke
     a.o_ts = out_token_stride;
     a.o_hs = out_head_stride;
     a.scale = scale;
-    a.window = static_cast<int>(std::min<int64_t>(window, kI32));
+    a.window = window >= kI32 ? 0 : static_cast<int>(window);  // (no position is as far from another)
     char* ws = static_cast<char*>(workspace);
     a.hdr = moe::ws_at<moe::Header>(workspace, L.hdr);
     a.lead = 1;
@@ -223,7 +223,7 @@ MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_toke
     if (!use_tc(batch, rows)) {
         const int64_t tiles = (rows + moe::kSplitRows - 1) / moe::kSplitRows;
         const int64_t items = std::min<int64_t>(batch->n_seqs * tiles * a.kv.hkv, int64_t(1) << 30);
-        const int64_t keys = std::min<int64_t>(std::min(batch->max_kv_len, window > 0 ? window + tiles * moe::kSplitRows : kI32), a.kv.cap);
+        const int64_t keys = std::min<int64_t>(std::min(batch->max_kv_len, a.window > 0 ? a.window + tiles * moe::kSplitRows : kI32), a.kv.cap);
         a.split = keys > kWholeKeys;
         pieces(0);
         MOE_ATTEND(moe::launch_attend_split(a, dtype, L.n_ctas, static_cast<int>(items), st));

@@ -116,11 +116,15 @@ __device__ __forceinline__ int page_id(const KvArgs& a, int b, int idx) {
     return id >= 0 && id < a.n_pages ? id : -1;
 }
 
+// The last position that a window ending at position p leaves out, or -1: not below, so that what is taken from it stays
+// in 32 bits whatever the window (p may be negative).
+__device__ __forceinline__ int before_window(int window, int p) { return window > 0 && p >= window ? p - window : -1; }
+
 // Keys [lo, hi) that rows [r0, r1) (row = token * group + head of the group) see, at least one of them.
 __device__ __forceinline__ void key_range(const KvArgs& a, int window, const SeqInfo& s, int r0, int r1, int& lo, int& hi) {
     const int p0 = s.pos0 + div_by(r0, a.by_group), p1 = s.pos0 + div_by(r1 - 1, a.by_group);
     hi = min(p1, a.cap - 1) + 1;
-    lo = window > 0 ? max(p0 - window + 1, 0) : 0;
+    lo = before_window(window, p0) + 1;
     if (hi <= lo) lo = hi = 0;
 }
 
@@ -396,7 +400,7 @@ __device__ __noinline__ void attend_row(const AttendArgs& a, int b, int token, i
         }
     }
     const int hi = min(pos, a.kv.cap - 1) + 1;
-    const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const int lo = before_window(a.window, pos) + 1;
     const float c = a.scale * kLog2e;
     float m = kNegInf, l = 0.f;
     for (int j = lo; j < hi; ++j) {
