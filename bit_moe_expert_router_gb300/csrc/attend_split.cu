@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(SplitCfg<DH>::kWarps * 32, 1) attend_split_ker
     if (kv.d < DH)
         for (int i = threadIdx.x; i < C::kOffMl / 16; i += blockDim.x) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
 
-    wait_for_stream();
+    if (a.lead) wait_for_stream();
+    else wait_and_hand_on();  // the tcgen05 kernel of the same batch comes next
     // a small table is brought near while the lengths are: its entries are the next to be waited for
     if (static_cast<int64_t>(kv.n_seqs) * kv.width <= 1024)
         for (int i = threadIdx.x * 8; i < kv.n_seqs * kv.width; i += blockDim.x * 8)

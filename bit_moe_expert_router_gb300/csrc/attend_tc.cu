@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 0) tmem_alloc<CG>(tmem_holder, 512);
-    if (a.follows) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // beside the split kernel, which has waited
+    if (a.follows) begin_beside();  // the split kernel has waited
     else wait_for_stream();
     if (a.lead && blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
     const int rank = CG == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CG;

@@ -75,6 +75,15 @@ __device__ __forceinline__ void wait_for_stream() {
     asm volatile("griddepcontrol.wait;\ngriddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
+// The same where the next kernel begins beside this one and does not wait for it: it relies on what was complete when this one
+// began.  The wait makes that visible to this grid; the fences, here before the launch and there at its beginning
+// (begin_beside), carry it on, with the launch in the place of a flag that is written and read.  That a launch orders as
+// much as such a flag does is taken for granted: the instructions' description says when the next may start, and no more.
+__device__ __forceinline__ void wait_and_hand_on() {
+    asm volatile("griddepcontrol.wait;\nfence.acq_rel.gpu;\ngriddepcontrol.launch_dependents;\n" ::: "memory");
+}
+__device__ __forceinline__ void begin_beside() { asm volatile("fence.acq_rel.gpu;\ngriddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
