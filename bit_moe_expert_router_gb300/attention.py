@@ -109,6 +109,17 @@ class KVBatch:
         if self._workspace == 0:  # sizes or strides that the operators refuse
             raise MoeError("moe_w4a8_paged_attention_workspace_size", 1)
 
+    @property
+    def max_q_len(self) -> int:
+        """The bound on a sequence's new tokens.  May be set between calls: it is a hint to the next one."""
+        return self._c.max_q_len
+
+    @max_q_len.setter
+    def max_q_len(self, n: int):
+        if n < 1:
+            raise ValueError(f"max_q_len {n}: at least 1")
+        self._c.max_q_len = n
+
     def workspace_size(self) -> int:
         """Bytes of workspace of moe_w4a8_paged_attention for this batch, whatever its tokens."""
         return self._workspace

@@ -42,25 +42,27 @@ class ServingLayer:
         self.k_cache, self.v_cache = (torch.empty(cache, dtype=torch.bfloat16, device=dev) for _ in range(2))
         self.prep = attention.HeadPrep(attention.rope_table(pages_per_seq * page_size, rot_dim or head_dim, base, device=dev),
                                        q_weight=w["q_norm"], k_weight=w["k_norm"])
-        self._batches, self._workspaces = {}, {}
+        self._batch = attention.KVBatch(self.k_cache, self.v_cache, self.block_table, self.q_start, self.kv_len, n_q_heads=self.hq, max_q_len=1)
+        self._attend_workspace, self._moe_workspaces = self._batch.alloc_workspace(), {}
 
     def batch(self, max_q_len: int) -> attention.KVBatch:
-        """The handle for steps of at most max_q_len new tokens per sequence (kept: they are few)."""
-        if max_q_len not in self._batches:
-            self._batches[max_q_len] = attention.KVBatch(self.k_cache, self.v_cache, self.block_table, self.q_start, self.kv_len,
-                                                         n_q_heads=self.hq, max_q_len=max_q_len)
-        return self._batches[max_q_len]
+        """The layer's one handle, set for a step of at most max_q_len new tokens per sequence."""
+        self._batch.max_q_len = max_q_len
+        return self._batch
 
     def dims(self, tokens: int) -> binding.Dims:
         w13, w2 = self.w["w13"], self.w["w2"]
         return binding.Dims(tokens, w2.shape[1], w13.shape[1] // 2, w13.shape[0] - self.n_shared, self.n_shared, self.top_k, self.group)
 
     def workspaces(self, tokens: int, batch):
-        if tokens not in self._workspaces:
-            d = self.dims(tokens)
-            self._workspaces[tokens] = (batch.alloc_workspace(),
-                                        binding.alloc_workspace(binding.moe_w4a8_forward_bf16_workspace_size(d), self.k_cache.device))
-        return self._workspaces[tokens]
+        """(attention's, the experts') for a step of `tokens`.  Attention's does not depend on them.  The experts' is that of
+        the next power of two, so all of them together are less than four times what the largest step needs; they are kept, because
+        a captured graph holds their addresses."""
+        size = 1 << (tokens - 1).bit_length()
+        if size not in self._moe_workspaces:
+            need = binding.moe_w4a8_forward_bf16_workspace_size(self.dims(size))
+            self._moe_workspaces[size] = binding.alloc_workspace(need, self.k_cache.device)
+        return self._attend_workspace, self._moe_workspaces[size]
 
     def forward(self, x, max_q_len: int):
         """x [tokens, H] bf16, the new tokens of all sequences in order; q_start and kv_len hold the step's lengths."""
