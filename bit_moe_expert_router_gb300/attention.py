@@ -253,7 +253,7 @@ def _aligned(ws):
         binding._need(ws, "workspace", torch.uint8)
     base = ws.data_ptr()
     at = (base + 255) & -256
-    return at, ws.numel() - (at - base)
+    return at, max(0, ws.numel() - (at - base))
 
 
 def moe_w4a8_paged_attention(batch: KVBatch, q, out, lse=None, scale: float | None = None, window: int = 0, *, workspace):

@@ -177,7 +177,7 @@ def _ws_view(ws: torch.Tensor):
     _need(ws, "workspace", torch.uint8)
     base = ws.data_ptr()
     aligned = (base + 255) & ~255
-    return ctypes.c_void_p(aligned), ws.numel() - (aligned - base)
+    return ctypes.c_void_p(aligned), max(0, ws.numel() - (aligned - base))
 
 
 def _bank_shapes(d: Dims):
