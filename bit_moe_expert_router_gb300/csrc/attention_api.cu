@@ -235,7 +235,7 @@ MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_toke
     // decoding requests 132 us (128 since), all on the tcgen05 engine 172.
     a.split = 1;
     moe::AttendArgs few = a;
-    const bool mixed = n_tokens <= (batch->n_seqs - 1) * max_q + moe::kSplitRows / a.kv.group;  // (there may be some)
+    const bool mixed = a.kv.group <= moe::kSplitRows && n_tokens <= (batch->n_seqs - 1) * max_q + moe::kSplitRows / a.kv.group;  // (there may be some)
     if (mixed) {
         pieces(0);
         few = a;
