@@ -200,8 +200,8 @@ template <int ROWS, int KEYS>
 __device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, long long* prefix) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int B = a.kv.n_seqs;
-    constexpr int kFew = 8;                    // more tiles than this are summed by warps,
-    constexpr long long kOpen = -(1LL << 60);  // from this on
+    constexpr int kFew = 8;           // more tiles than this are summed by a warp
+    constexpr long long kOpen = -1;
     for (int b = threadIdx.x; b < B; b += blockDim.x) {
         const SeqInfo s = seq_info(a.kv, b);
         const int nt = row_tiles<ROWS>(a, s);
@@ -210,17 +210,15 @@ __device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, 
         prefix[b + 1] = nt <= kFew ? sum * a.kv.hkv : kOpen;
     }
     __syncthreads();
-    const int each = max(warps / B, 1);  // warps for one sequence
-    for (int i = warp; i < B * each; i += warps) {
-        const int b = each > 1 ? i / each : i;
-        if (prefix[b + 1] >= 0) continue;
+    for (int b = warp; b < B; b += warps) {
+        if (prefix[b + 1] != kOpen) continue;
         const SeqInfo s = seq_info(a.kv, b);
         const int nt = row_tiles<ROWS>(a, s);
         long long sum = 0;
-        for (int rt = (i - b * each) * 32 + lane; rt < nt; rt += 32 * each) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
+        for (int rt = lane; rt < nt; rt += 32) sum += tile_weight<ROWS, KEYS>(a, d, s, rt);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(prefix + b + 1), static_cast<unsigned long long>(sum * a.kv.hkv));
+        if (lane == 0) prefix[b + 1] = sum * a.kv.hkv;
     }
     __syncthreads();
     if (warp == 0) {
@@ -228,7 +226,6 @@ __device__ __forceinline__ void deal_prefix(const AttendArgs& a, const Deal& d, 
         if (lane == 0) prefix[0] = 0;
         for (int b0 = 0; b0 < B; b0 += 32) {
             long long x = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
-            if (x < 0) x -= kOpen;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(~0u, x, o);
