@@ -83,8 +83,6 @@
 // K order: the weight unpack turns a packed word (codes 0..7) into fp16
 // pairs (0,4) (1,5) (2,6) (3,7); the token rows are converted to fp16 in
 // the same order by the prep kernels, so both operands agree on K.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
@@ -92,6 +90,7 @@
 #include <mutex>
 
 #include "prefill.h"
+#include "tcgen05.cuh"
 
 namespace moe {
 namespace {
@@ -131,7 +130,6 @@ constexpr int kBarWords = kAStages + 2 * kBStages + 2 * kAcc + 1 + 2 * kRaw;
 constexpr int kOffMisc = kOffBars + 8 * kBarWords;              // tmem holder, abort flag, warp sums
 constexpr int kSmemUsed = kOffMisc + 4 * (2 + kNumWarps + 1);
 constexpr int kSmemTc = kSmemUsed + 1024;                      // + room to align the base to 1024 bytes
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSleepNs = 20000;  // longest sleep inside one barrier test
 static_assert(kAcc * kTileN + kAStages * kACols <= kTmemCols, "tensor-memory columns");
 
@@ -140,91 +138,20 @@ static_assert(kOffRaw % 1024 == 0 && kOffColp % 16 == 0 && kOffBars % 8 == 0, "r
 static_assert(kRawStage == 128 * 64, "raw stage: 128 rows of 64 packed bytes");
 static_assert((kOffB + kBStages * kBStage) >> 4 < (1 << 14), "B stages addressable by a matrix descriptor");
 
-__device__ __forceinline__ uint64_t global_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(count));
-}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// The same test, but the thread may sleep in the instruction for up to `ns` nanoseconds (it is
-// woken when the phase completes): a waiting warp then takes no issue slots from the warps
-// doing the work.
-__device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, uint32_t ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-        : "memory");
-    return ok != 0;
 }
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-struct Ctl {
-    volatile int* abort;
-    Header* hdr;
-};
-
-// Bounded wait for phase `parity` of `bar`; false if the CTA aborted or the
-// wait ran out (then the abort flag and the status word are set).
-__device__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        if (mbar_wait_sleep(bar, parity, kSleepNs)) return true;
-        if ((it & 7) == 7) {
-            if (*c.abort) return false;
-            const uint64_t t = global_ns();
-            if (t0 == 0) {
-                t0 = t;
-            } else if (t - t0 > kWaitNs) {
-                *c.abort = 1;
-                atomicOr(&c.hdr->status, kDevTimeout);
-                return false;
-            }
-        }
-    }
-}
-
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFF);
-    d |= static_cast<uint64_t>(1) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
+// The bounded wait of every role here: the thread sleeps in the barrier test.
+__device__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) { return moe::wait_bar<kSleepNs>(bar, parity, c); }
 
 // kind::f16 instruction descriptor: fp32 accumulator, fp16 A and B, both
 // K-major, M = 128, N = n (a multiple of 16).
 __device__ __forceinline__ uint32_t idesc_f16(int n) {
     return (1u << 4) | (0u << 7) | (0u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
-}
-
-// MMA with the A operand read from tensor memory (lane = row, K along the columns)
-// and B from shared memory (descriptor).
-__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
 }
 
 // TMA: 2-D box at (x, y) of `map` -> shared memory, completion counted on `bar`.
@@ -239,43 +166,12 @@ __device__ __forceinline__ void tma_tile2d(void* dst, const CUtensorMap* map, in
 // a few ulp from z / (1 + exp(-z))).
 __device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
-
-// 16 consecutive 32-bit tensor-memory columns of this thread's lane (no wait).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
-}
 // 8 consecutive 32-bit tensor-memory columns of this thread's lane (no wait).
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-
-
-// 32 consecutive 32-bit tensor-memory columns of this thread's lane <- v (no wait).
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-
 // Eight packed int4 codes (element e at bits 4e) -> fp16 pairs (0,4) (1,5) (2,6) (3,7).
 // A nibble n of a two's-complement code c satisfies n ^ 8 = c + 8.  Placed in
 // the low 4 mantissa bits of fp16 0x6400 (1024) it gives 1024 + c + 8, so
@@ -644,16 +540,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t ta = tmem + kACol0 + kACols * sa, td = tmem + b * kTileN;
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)  // K = 16 per MMA: 8 A columns, 32 bytes of a B row
-                        mma_f16_ta(td, ta + 8 * kk, bd + static_cast<uint64_t>(((kk >> 2) * kBAtom + 32 * (kk & 3)) >> 4),
+                        mma_f16_ta<1>(td, ta + 8 * kk, bd + static_cast<uint64_t>(((kk >> 2) * kBAtom + 32 * (kk & 3)) >> 4),
                                    idesc, (sub > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(empty + sb);
+                    mma_commit<1>(empty + sb);
                     if (sub == span - 1) {
-                        mma_commit(accf + b);
+                        mma_commit<1>(accf + b);
                         ++grp;
                     }
                 }
             }
-            mma_commit(done);  // arrives once every MMA issued above has completed
+            mma_commit<1>(done);  // arrives once every MMA issued above has completed
             const uint64_t t0 = global_ns();
             while (!mbar_try_wait(done, 0)) {
                 if (global_ns() - t0 > kWaitNs) {
@@ -1021,24 +917,6 @@ __global__ void prep_h16_kernel(const float* __restrict__ h, uint32_t* __restric
             }
         }
     }
-}
-
-using Encode = PFN_cuTensorMapEncodeTiled_v12000;
-
-cudaError_t get_encode(Encode* out) {
-    static Encode encode = nullptr;
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!encode) {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return e;
-        if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorSymbolNotFound;
-        encode = reinterpret_cast<Encode>(fn);
-    }
-    *out = encode;
-    return cudaSuccess;
 }
 
 // Tensor map of the B rows of one launch: fp16 [b_rows][K], boxes of 64 values by 192 rows,

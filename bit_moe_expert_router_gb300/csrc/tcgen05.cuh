@@ -1,5 +1,5 @@
 // Device wrappers of the tcgen05, TMA and mbarrier instructions of the
-// attention kernel, the bounded barrier wait, and the host's way to the
+// tcgen05 kernels, the bounded barrier wait, and the host's way to the
 // tensor-map encoder.
 #pragma once
 
@@ -48,6 +48,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// The same test, but the thread may sleep in the instruction for up to `ns` nanoseconds (it is
+// woken when the phase completes): a waiting warp then takes no issue slots from the warps
+// doing the work.
+__device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -67,12 +79,15 @@ struct Ctl {
 };
 
 // Bounded wait for phase `parity` of `bar`; false if the CTA aborted or the
-// wait ran out (then the abort flag and the status word are set).
+// wait ran out (then the abort flag and the status word are set).  SLEEP: how
+// many nanoseconds a test may sleep, 0 for not at all.
+template <uint32_t SLEEP = 0>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
+    constexpr uint32_t kTests = SLEEP ? 8 : 64;  // between looks at the flag and the clock
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63) == 63) {
+        if (SLEEP ? mbar_wait_sleep(bar, parity, SLEEP) : mbar_try_wait(bar, parity)) return true;
+        if (it % kTests == kTests - 1) {
             if (*c.abort) return false;
             const uint64_t t = global_ns();
             if (t0 == 0) {
