@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
     uint64_t* done = tail + 1;                // MMA commit: everything issued has finished
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+    int* odd = abort_flag + 1;                // some row of a whole tile ended with a NaN
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const KvArgs& kv = a.kv;
     const Ctl ctl{abort_flag, a.hdr};
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         }
         mbar_init(tail, 1);
         mbar_init(done, 1);
-        *abort_flag = 0;
+        *abort_flag = *odd = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 0) tmem_alloc<CG>(tmem_holder, 512);
@@ -547,14 +548,8 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
         PairExchange<WarpPairBarrier> other{reinterpret_cast<uint32_t*>(smem + C::kOffEx) + 512 * w + row, 128, half, 0, {1 + 4 * w + (warp & 3)}};
         const float sc = a.scale * kLog2e;
         uint32_t uses = 0;                          // of the sets, before this tile
-        bool odd = false;                           // some row of the warp ended with a NaN
-        bool left = false;                          // the other half's warp has left
         // The other half's value in x's place; false: it has left, and so does this one.
-        auto exchange = [&](float& x) {
-            left = __any_sync(~0u, !other.swap(x));
-            ok = !left;
-            return ok;
-        };
+        auto exchange = [&](float& x) { return ok = __all_sync(~0u, other.swap(x)); };
         while (ok && c.u < c.end) {
             const int n = c.take;
             const int r0 = c.rt * C::kRows + C::kTile * w + 128 * rank;
@@ -621,29 +616,33 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
                     for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(v[60 + x]));
                     float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                     float top2 = top;
-                    if (!exchange(top2)) break;  // (S of both halves is read: P may be stored over it)
+                    const bool there = other.swap(top2);  // (S of both halves is read: P may be stored over it)
                     top = fmaxf(top, top2);
-                    // (with m = -inf the difference is inf, or NaN if the row has seen nothing yet)
+                    // (with m = -inf, as at the piece's beginning, the difference is inf, or NaN if the row has seen nothing yet)
                     const bool grew = (top - m) * sc > 8.f;
-                    if (j == 0) {
-                        m = top;
-                    } else if (__any_sync(~0u, grew)) {
-                        // O is rescaled between the products: the one before has to be there
-                        if (!added(j - 1)) break;
-                        tc_fence_after();
-                        const float f = grew ? (m == kNegInf ? 0.f : exp2_fast((m - top) * sc)) : 1.f;
-                        if (grew) m = top;
-                        const uint64_t f2 = pair(f, f);
-                        l2 = mul2(l2, f2);
+                    if (__any_sync(~0u, grew || !there)) {  // (one vote: whether the other has left is looked at where it is rare)
+                        if (!(ok = __all_sync(~0u, there))) break;
+                        float f = 1.f;
+                        if (grew) {
+                            f = m == kNegInf ? 0.f : exp2_fast((m - top) * sc);
+                            m = top;
+                        }
+                        if (j > 0) {
+                            // O is rescaled between the products: the one before has to be there
+                            if (!added(j - 1)) break;
+                            tc_fence_after();
+                            const uint64_t f2 = pair(f, f);
+                            l2 = mul2(l2, f2);
 #pragma unroll 1
-                        for (int i = 0; i < DH / 2; i += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(o_col + i, o);
-                            tmem_ld_wait();
-                            tmem_tie<16>(o);
+                            for (int i = 0; i < DH / 2; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(o_col + i, o);
+                                tmem_ld_wait();
+                                tmem_tie<16>(o);
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tmem_st16(o_col + i, o);
+                                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                                tmem_st16(o_col + i, o);
+                            }
                         }
                     }
                     if constexpr (C::kOwnP) {  // the product before has read its P
@@ -761,13 +760,14 @@ __global__ void __launch_bounds__(TcCfg<DH>::kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(leaders(o_free + w));
-            odd |= __any_sync(~0u, mine && bad && whole);
+            if (mine && bad && whole) *odd = 1;
             deal_next<C::kRows, kTcKeys>(a, c);
         }
-        if (!ok && !left) other.leave();
-        float odds = odd ? 1.f : 0.f;
-        if (ok && exchange(odds)) {  // (and both halves of the rows are stored)
-            if (odd || odds != 0.f) retake_rows<T, DH>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w, warp & 3, half);
+        float end = 0.f;
+        if (!ok) {
+            other.leave();
+        } else if (exchange(end)) {  // (both halves of the rows are stored, and what they set in `odd`)
+            if (*odd) retake_rows<T, DH>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w, warp & 3, half);
         }
     }
 

@@ -41,7 +41,7 @@ struct PairExchange {
         memcpy(&x, &bits, 4);
         return bits != kLeftMark;
     }
-    // Once, by a warp that leaves by itself (not by one that found the mark), whatever the other does.
+    // Once, by a warp that leaves, whatever the other does or has done.
     MOE_HD void leave() {
         at[2 * lanes * (swaps & 1) + lanes * half] = kLeftMark;
         meet.arrive();

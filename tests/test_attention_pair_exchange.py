@@ -53,15 +53,15 @@ constexpr int kTiles = 3, kKeys = 3, kWaits = kTiles * (2 * kKeys + 1);
 void side(int half, uint32_t* places, State* state, bool live, bool* wrong) {
     moe::PairExchange<Meet> other{places, 1, half, 0, {state}};
     int waits = 0, step = 0;
-    bool ok = true, left = false;
+    bool ok = true;
     auto wait = [&] { return ok = waits++ != fail_at[half]; };
     auto exchange = [&] {
         const float nan = std::numeric_limits<float>::quiet_NaN();
         float x = step % 5 == 4 ? nan : 1000.f * half + step;  // (scores may be NaN)
-        left = !other.swap(x);
-        if (!left && !(step % 5 == 4 ? x != x : x == 1000.f * (half ^ 1) + step)) *wrong = true;
+        const bool there = other.swap(x);
+        if (there && !(step % 5 == 4 ? x != x : x == 1000.f * (half ^ 1) + step)) *wrong = true;
         ++step;
-        return ok = !left;
+        return ok = there;
     };
     for (int t = 0; ok && t < kTiles; ++t) {
         const bool has_rows = live || t != 1;  // a tile whose rows are none: waits without swaps
@@ -73,8 +73,8 @@ void side(int half, uint32_t* places, State* state, bool live, bool* wrong) {
         if (!ok || !wait()) break;                               // the last P V
         if (has_rows && !exchange()) break;                      // the sums
     }
-    if (!ok && !left) other.leave();
-    if (ok) exchange();
+    if (!ok) other.leave();
+    else exchange();
 }
 
 int main() {
