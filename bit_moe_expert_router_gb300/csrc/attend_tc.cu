@@ -38,11 +38,13 @@
 // warpgroups per row tile: softmax and output, a thread for half of a row's keys (64 of a tile's 128)
 // and half of its output, so that the way from S to P is half as long; the halves exchange their
 // maxima through shared memory.
-// Measured: 8192-token prompt, 16 / 2 heads of 256: 330 us, 1.66 PFLOP/s, 86% of the tensor pipe's cycles;
-// 4096 tokens of 32 / 8 heads of 128 140 us, 0.98 PFLOP/s (softmax, P, P V and the next Q K in a chain); heads of
-// 64 107 us, 0.64 PFLOP/s.  Alternating S buffers for a single row tile: 32 sequences of 8 tokens at 8000
+// Measured: 8192-token prompt, 16 / 2 heads of 256: 332 to 340 us by the card, 1.65 PFLOP/s, 86% of the tensor pipe's
+// cycles; 4096 tokens of 32 / 8 heads of 128 139 us, 0.99 PFLOP/s (softmax, P, P V and the next Q K in a chain); heads
+// of 64 107 us, 0.64 PFLOP/s.  At 64 and 128 components the 96 registers a thread do not hold everything: 56 bytes of
+// stack, 468 and 524 bytes of spill loads (none at 256).  Alternating S buffers for a single row tile: 32 sequences of 8 tokens at 8000
 // positions 343 -> 244 us, for which that 4096-token prompt went from 142 to 146 when it came.
-// Every wait is bounded; a timeout sets the status word and every role leaves.
+// Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
+// its own copies in flight.  The softmax warps' exchange is ended by the warp that leaves (pair_exchange.h).
 #include <algorithm>
 
 #include "attend_join.cuh"

@@ -232,7 +232,7 @@ MOE_API int moe_w4a8_paged_attention(const moe_kv_batch_t* batch, int64_t n_toke
     }
     // Sequences of few rows among longer ones (decoding requests beside a chunk) go to the split engine: a tile of
     // 256 or 512 rows that they fill by a few streams their keys at less than half its rate: a chunk among
-    // decoding requests 132 us (128 since), all on the tcgen05 engine 172.
+    // decoding requests 132 us (131 now), all on the tcgen05 engine 172.
     a.split = 1;
     moe::AttendArgs few = a;
     const bool mixed = a.kv.group <= moe::kSplitRows && n_tokens <= (batch->n_seqs - 1) * max_q + moe::kSplitRows / a.kv.group;  // (there may be some)

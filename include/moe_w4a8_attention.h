@@ -23,8 +23,11 @@
  *            lse[t][h] = log sum_j exp(scale q[t][h] . K_j).
  *
  * Everything between the inputs and the single rounding of each output is
- * fp32, except that attend's weights exp(s - max) are rounded to the
- * element type as operands of the matrix units (their sum is not).
+ * fp32, except that attend's weights are rounded to the element type as
+ * operands of the matrix units (their sum is not).  A weight is exp(s - m)
+ * for a reference m that may lag behind the row's maximum by a factor of up
+ * to 2^8; in fp16 a weight below 2^-14 is rounded to a multiple of 2^-24, so
+ * off by 2^-25 at most, and one below 2^-25 counts in the sum alone.
  *
  * Edge cases.  A row that sees no position (position below zero, kv_len 0)
  * gives out = 0 and lse = -inf; append treats a token at a position below
@@ -32,7 +35,9 @@
  * stored.  Tokens outside [q_start[0], q_start[B]) belong to no sequence
  * and give q_out = 0, out = 0, lse = -inf.  Cache rows past kv_len are
  * never part of a result, whatever they hold; a NaN or an infinity at a
- * position that a row does not see does not reach that row.  A page id
+ * position that a row does not see does not reach that row; a row that ends
+ * with a NaN is for that taken again key by key, about half a microsecond
+ * each, at the end of the call.  Any window of 2^31 - 1 or more is none.  A page id
  * outside [0, n_pages) is never dereferenced: append stores nothing there,
  * attend reads zeros.  Positions at table_width * page_size and beyond do
  * not exist.  q_start entries are clamped into [0, n_tokens].
