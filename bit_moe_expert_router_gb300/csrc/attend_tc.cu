@@ -91,24 +91,6 @@ struct TcCfg {
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-template <typename T>
-struct MmaFmt;
-template <>
-struct MmaFmt<__nv_bfloat16> {
-    static constexpr uint32_t v = 1;
-};
-template <>
-struct MmaFmt<__half> {
-    static constexpr uint32_t v = 0;
-};
-
-// kind::f16 instruction descriptor: fp32 accumulator, A and B of one type, M = m, N = n; b_mn: B is MN-major.
-template <typename T>
-__device__ constexpr uint32_t idesc16(int m, int n, bool b_mn) {
-    return (1u << 4) | (MmaFmt<T>::v << 7) | (MmaFmt<T>::v << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(m >> 4) << 24);
-}
-
 // The meeting of the two softmax warps of the same rows, at a named barrier.
 struct WarpPairBarrier {
     int id;

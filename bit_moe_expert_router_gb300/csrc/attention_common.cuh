@@ -41,6 +41,24 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+template <typename T>
+struct MmaFmt;
+template <>
+struct MmaFmt<__nv_bfloat16> {
+    static constexpr uint32_t v = 1;
+};
+template <>
+struct MmaFmt<__half> {
+    static constexpr uint32_t v = 0;
+};
+
+// kind::f16 instruction descriptor: fp32 accumulator, A and B of one type, M = m, N = n; a_mn, b_mn: A, B is MN-major.
+template <typename T>
+__device__ constexpr uint32_t idesc16(int m, int n, bool b_mn, bool a_mn = false) {
+    return (1u << 4) | (MmaFmt<T>::v << 7) | (MmaFmt<T>::v << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
     uint64_t r;
@@ -116,6 +134,27 @@ __device__ __forceinline__ SeqInfo seq_info(const KvArgs& a, int b) {
     s.q_len = max(e - s.q0, 0);
     s.pos0 = max(__ldg(a.kv_len + b), 0) - s.q_len;
     return s;
+}
+
+// The sequence that token t belongs to (its index b with q_start[b] <= t < q_start[b + 1]), or -1.
+// A decoding batch has one token per sequence, so b = t is tried first; else a 32-way search.
+__device__ __forceinline__ int find_seq(const KvArgs& a, int t) {
+    const int lane = threadIdx.x & 31;
+    const int guess = min(t, a.n_seqs - 1);
+    if (__ldg(a.q_start + guess) <= t && t < __ldg(a.q_start + guess + 1)) return guess;
+    int lo = 0, n = a.n_seqs;  // the first b of [lo, lo + n) with q_start[b + 1] > t
+    while (n > 0) {
+        const int step = (n + 31) / 32;
+        const int j = min((lane + 1) * step, n) - 1;
+        const unsigned past = __ballot_sync(~0u, __ldg(a.q_start + lo + j + 1) > t);
+        if (!past) return -1;
+        const int f = __ffs(past) - 1;
+        const int at = f * step;
+        n = min(step, n - at);
+        lo += at;
+        if (step == 1) break;
+    }
+    return __ldg(a.q_start + lo) <= t ? lo : -1;
 }
 
 // Page id of `idx` of sequence b, or -1 where there is none to read.

@@ -31,27 +31,6 @@ constexpr int kBatch = 4;  // chunks a lane has in flight, and as many of the ne
 // 40.6 and 66); below it 64 tokens take 2.6 us with one each, 6.4 with several.
 constexpr int64_t kManyRounds = 64 * 152;
 
-// The sequence that token t belongs to (its index b with q_start[b] <= t < q_start[b + 1]), or -1.
-// A decoding batch has one token per sequence, so b = t is tried first; else a 32-way search.
-__device__ __forceinline__ int find_seq(const KvArgs& a, int t) {
-    const int lane = threadIdx.x & 31;
-    const int guess = min(t, a.n_seqs - 1);
-    if (__ldg(a.q_start + guess) <= t && t < __ldg(a.q_start + guess + 1)) return guess;
-    int lo = 0, n = a.n_seqs;  // the first b of [lo, lo + n) with q_start[b + 1] > t
-    while (n > 0) {
-        const int step = (n + 31) / 32;
-        const int j = min((lane + 1) * step, n) - 1;
-        const unsigned past = __ballot_sync(~0u, __ldg(a.q_start + lo + j + 1) > t);
-        if (!past) return -1;
-        const int f = __ffs(past) - 1;
-        const int at = f * step;
-        n = min(step, n - at);
-        lo += at;
-        if (step == 1) break;
-    }
-    return __ldg(a.q_start + lo) <= t ? lo : -1;
-}
-
 // How the rotation finds a component's partner and its angle.
 enum Turn {
     kPairs,    // neighbours, whole chunks rotated: the partner is in the same chunk
