@@ -1,34 +1,700 @@
-// Latent attention, a warp for each (token, head) row: the keys one after
-// another with a running maximum and sum.
+// Latent attention on the fifth-generation tensor cores: every head of a layer
+// reads the same cache row, as its key with all components and as its value
+// with the first Dc.
+//
+// The mathematics, per (token, head) row: one pass over the keys with a running
+// reference m and sum l, s_j = scale q . x_j, p_j = 2^(s_j log2 e - m),
+// o = sum p_j x_j[0 .. Dc), the row is o / l.
+//
+// Bound: HBM while the rows are few (a row of the cache, 2 (Dc + R) bytes, does 2 (2 Dc + R) flops per head: the ridge is at
+// about 130 heads), the tensor pipe beyond.  A CTA takes a tile of ROWS = 16, 32 or 64 (token, head) rows, token-major,
+// against tiles of 64 keys, which come by TMA straight from the pages and are read from shared memory by both
+// products, so a cache row is brought once:
+//   S = Q X^T       64 rows (of which ROWS count) x 64 keys, A = Q and B = X both along the components; fp32 in tensor
+//                   memory, two buffers, so that the next keys' S is computed during this one's softmax
+//   O^T += X^T P^T  turned over: 128 components of the latent part x ROWS rows, four times, A = X along the keys' other
+//                   direction (no transposition is needed), B = P.  The accumulator takes 4 ROWS columns of tensor memory,
+//                   where O of 128 rows x 512 components alone would fill all of it.
+// A softmax thread has the matrix-fragment places of S (two rows, 16 keys each), four lanes a row.  P goes to shared memory in
+// 16 bits.  The reference m is raised, and O rescaled, only when a row's maximum has grown by more than 2^8 over it.
+//
+// The keys' tile is a ring of pairs of 64-component blocks (a pair is what one product of 128 components reads) and a
+// ring of tail blocks (the components behind the last pair); a pair is free as soon as its part of O^T is issued.  Pages
+// that are not there and rows past the last visible one read zeros, and rows behind it inside a box are cleared by hand.  Work
+// is dealt in equal shares of 64-key units; the pieces of a cut tile go through the workspace and the join.
+//
+// Warps: 0 MMA issue (one lane) and the tensor-memory allocation, 1 the keys, 2 and 3 the queries, 4 to 7 softmax and
+// output.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
+// its own copies in flight.  The softmax warps meet at a barrier once per tile, whatever became of their waits, and leave
+// together.
+#include <algorithm>
+
 #include "latent_common.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(128) attend_latent_kernel(const LatentArgs a) {
-    wait_for_stream();
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = kDevOk;  // (nothing here waits)
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(a.kv.n_tokens) * a.kv.hq) return;
-    const int t = static_cast<int>(row / a.kv.hq), head = static_cast<int>(row % a.kv.hq);
-    const int b = find_seq(a.kv, t);
-    int pos = -1;
-    if (b >= 0) {
-        const SeqInfo s = seq_info(a.kv, b);
-        pos = s.pos0 + t - s.q0;
+constexpr int kLatKeys = 64;  // keys of a unit
+constexpr int kMinShare = 2;  // units of a CTA at least, where there are few
+constexpr int kExtra = 2;     // units that a tile's beginning and end count for
+constexpr int kJoinWarps = 8;
+
+template <int ROWS>
+struct LatCfg {
+    static constexpr int kBlock = kLatKeys * 128, kPair = 2 * kBlock;  // bytes
+    static constexpr int kQBlock = ROWS * 128;                         // ROWS queries of 64 components
+    static constexpr int kQ = (2 * kMaxLatent / 128 + 1) * kQBlock;
+    static constexpr int kP = ROWS * 128;
+    static constexpr int kPairs = ROWS == 64 ? 8 : ROWS == 32 ? 10 : 11, kTails = ROWS == 64 ? 2 : 3;
+    static constexpr int kThreads = 256;
+    static constexpr int kOCol = 0, kSCol = 4 * ROWS, kCols = 512;
+    static constexpr int kOffQ = 0;
+    // (S is of 64 rows of Q: where ROWS is less, the MMA reads what lies behind them, at most 6 KB behind Q's end, into
+    // rows of S that are never looked at)
+    static constexpr int kOffP = kQ;
+    static constexpr int kOffPairs = kOffP + kP;
+    static constexpr int kOffTails = kOffPairs + kPairs * kPair;
+    static constexpr int kOffBars = kOffTails + kTails * kBlock;
+    static constexpr int kBars = 2 * kPairs + 2 * kTails + 9;
+    static constexpr int kOffAt = (kOffBars + 8 * kBars + 15) & ~15;   // [ROWS] where an output row begins
+    static constexpr int kOffFactor = kOffAt + 8 * ROWS;               // [ROWS] what O's rows are multiplied by
+    static constexpr int kOffMisc = kOffFactor + 4 * ROWS;
+    static constexpr int kOffStart = kOffMisc + 16;                    // the cursor at the share's beginning
+    static constexpr int kSmem = kOffStart + sizeof(Cursor);
+    static_assert(kSCol + 2 * kLatKeys <= kCols, "tensor-memory columns");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kPairs >= kMaxLatent / 128, "a tile of keys fits the ring");
+};
+
+// 16 lanes x 64 columns of 32 bits, as the accumulator fragments of eight 16 x 8 matrices (no wait).
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+
+// Barrier 1 of the 128 softmax threads: plain, or with the OR of a predicate.
+__device__ __forceinline__ void softmax_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, 128;\n" ::: "memory");
+}
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    __syncwarp();
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r) : "r"(static_cast<uint32_t>(x)) : "memory");
+    return r != 0;
+}
+
+// A place in a ring of N slots, and the phase of its barrier.
+template <int N>
+struct Place {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) slot = 0, phase ^= 1;
     }
-    latent_row<T>(a, max(b, 0), t, head, pos);
+};
+
+// The rows of the CTA's whole tiles that ended with a NaN, taken again one by one by the softmax warps.
+template <typename T, int ROWS>
+__device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int warp) {
+    const int lane = threadIdx.x & 31;
+    while (c.u < c.end) {
+        const int r0 = c.rt * ROWS;
+        const int rows = c.whole() ? min(c.s.q_len * a.kv.group - r0, ROWS) : 0;
+        for (int r = warp; r < rows; r += 4) {
+            int tok, head;
+            row_of(a.kv, r0 + r, tok, head);
+            bool odd = false;
+            for (int e = lane * 8; e < a.kv.d; e += 256) {
+                const uint4 o = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + (c.s.q0 + tok) * a.o_ts + head * a.o_hs + e);
+                const uint32_t o4[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = Elem<T>::unpack(o4[i]);
+                    odd |= f.x != f.x || f.y != f.y;
+                }
+            }
+            if (__any_sync(~0u, odd)) latent_row<T>(a, c.b, c.s.q0 + tok, head, c.s.pos0 + tok);
+        }
+        deal_next<ROWS, kLatKeys>(a, c);
+    }
+}
+
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
+    attend_latent_kernel(const LatentArgs a, int box_rows, const __grid_constant__ CUtensorMap map) {
+    using C = LatCfg<ROWS>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t* full_p = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [pairs] the bytes have landed
+    uint64_t* empty_p = full_p + C::kPairs;  // [pairs] MMA commit: the pair is read
+    uint64_t* full_t = empty_p + C::kPairs;  // [tails]
+    uint64_t* empty_t = full_t + C::kTails;  // [tails]
+    uint64_t* s_full = empty_t + C::kTails;  // [2] MMA commit: S is there
+    uint64_t* p_full = s_full + 2;           // the softmax warps: P is there, S is read
+    uint64_t* o_done = p_full + 1;           // MMA commit: the tile's O is added, P is read
+    uint64_t* o_free = o_done + 1;           // the softmax warps: the piece's O is read
+    uint64_t* q_full = o_free + 1;           // the two warps of the queries
+    uint64_t* q_free = q_full + 1;           // MMA commit: the piece's last S is there
+    uint64_t* cut_in = q_free + 1;           // the bytes of a tile that is cleared by hand
+    uint64_t* done = cut_in + 1;             // MMA commit: everything issued has finished
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+    int* odd = abort_flag + 1;               // some row of a whole tile ended with a NaN
+    int64_t* row_at = reinterpret_cast<int64_t*>(smem + C::kOffAt);
+    float* factor = reinterpret_cast<float*>(smem + C::kOffFactor);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const KvArgs& kv = a.kv;
+    const Ctl ctl{abort_flag, a.hdr};
+
+    if (smem_u32(smem) & 1023u) {  // (the swizzled tiles' places; the same in every CTA)
+        if (tid == 0) atomicOr(&a.hdr->status, kDevTimeout);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < C::kPairs; ++i) {
+            mbar_init(full_p + i, 1);
+            mbar_init(empty_p + i, 1);
+        }
+        for (int i = 0; i < C::kTails; ++i) {
+            mbar_init(full_t + i, 1);
+            mbar_init(empty_t + i, 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(s_full + 1, 1);
+        mbar_init(p_full, 4);
+        mbar_init(o_done, 1);
+        mbar_init(o_free, 4);
+        mbar_init(q_full, 2);
+        mbar_init(q_free, 1);
+        mbar_init(cut_in, 1);
+        mbar_init(done, 1);
+        *abort_flag = *odd = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 0) tmem_alloc<1>(tmem_holder, C::kCols);
+    wait_for_stream();
+    if (blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
+    Cursor c;
+    deal_begin<ROWS, kLatKeys>(a, reinterpret_cast<long long*>(smem + C::kOffPairs), kMinShare, kExtra, blockIdx.x, gridDim.x, c);  // (scratch: the ring)
+    if (tid == 0) *reinterpret_cast<Cursor*>(smem + C::kOffStart) = c;
+    clear_stray_rows<T>(a);  // (kv.d is what the outputs have)
+    tc_fence_before();
+    fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const int pairs = (kv.d + 127) / 128;        // of a key: 128 components each, the latent part's last one may reach behind it
+    const bool tail = a.dk > 128 * pairs;        // components behind the pairs
+    bool ok = true;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            // ------------------------------------------------------------ MMA issue, by one lane
+            const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(smem_u32(smem + C::kOffPairs)), td = sdesc(smem_u32(smem + C::kOffTails));
+            const uint64_t vd = sdesc_mn(smem_u32(smem + C::kOffPairs), C::kBlock), pd = sdesc(smem_u32(smem + C::kOffP));
+            Place<C::kPairs> sp, vp;             // the next pair of S, of O
+            Place<C::kTails> st;
+            uint32_t ts = 0, to = 0, items = 0;  // tiles so far whose S, whose O is issued; pieces
+            while (ok && c.u < c.end) {
+                const int n = c.take;
+                int js = 0, part = 0, jo = 0;    // the tile whose S is next and its next part; the one whose O is next
+                uint64_t t0 = 0;
+                for (uint32_t idle = 0; jo < n;) {
+                    bool did = false;
+                    if (jo < js && mbar_test(p_full, to & 1) && (jo > 0 || mbar_test(o_free, (items & 1) ^ 1))) {
+                        tc_fence_after();
+                        for (int x = 0; x < pairs; ++x) {
+#pragma unroll
+                            for (int k = 0; k < kLatKeys / 16; ++k)
+                                mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, vd + ((vp.slot * C::kPair + k * 2048) >> 4), pd + ((k * 32) >> 4),
+                                              idesc16<T>(128, ROWS, false, true), jo > 0 || k > 0);
+                            mma_commit<1>(empty_p + vp.slot);
+                            vp.next();
+                        }
+                        mma_commit<1>(o_done);
+                        ++jo;
+                        ++to;
+                        did = true;
+                    } else if (js < n && js <= jo + 1 && (js > 0 || part > 0 || mbar_test(q_full, items & 1)) &&
+                               mbar_test(part < pairs ? full_p + sp.slot : full_t + st.slot, part < pairs ? sp.phase : st.phase)) {
+                        // (S of tile js goes where S of tile js - 2 was, which is read when that one's P is there)
+                        tc_fence_after();
+                        const uint64_t qp = qd + ((2 * part * C::kQBlock) >> 4);
+                        const uint64_t kp = part < pairs ? kd + ((sp.slot * C::kPair) >> 4) : td + ((st.slot * C::kBlock) >> 4);
+                        const uint32_t s_col = tmem + C::kSCol + kLatKeys * (ts & 1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_f16_ss<1>(s_col, qp + k * 2, kp + k * 2, idesc16<T>(64, kLatKeys, false), part > 0 || k > 0);
+                        if (part < pairs) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_ss<1>(s_col, qp + (C::kQBlock >> 4) + k * 2, kp + (C::kBlock >> 4) + k * 2, idesc16<T>(64, kLatKeys, false), 1);
+                            sp.next();
+                        } else {
+                            mma_commit<1>(empty_t + st.slot);
+                            st.next();
+                        }
+                        if (++part == pairs + tail) {
+                            mma_commit<1>(s_full + (ts & 1));
+                            part = 0;
+                            ++ts;
+                            if (++js == n) mma_commit<1>(q_free);
+                        }
+                        did = true;
+                    }
+                    if (did) {
+                        idle = 0;
+                        t0 = 0;
+                    } else if (++idle % 64 == 0) {
+                        if (*ctl.abort) {
+                            ok = false;
+                            break;
+                        }
+                        const uint64_t now = global_ns();
+                        if (t0 == 0) {
+                            t0 = now;
+                        } else if (now - t0 > kWaitNs) {
+                            *ctl.abort = 1;
+                            atomicOr(&ctl.hdr->status, kDevTimeout);
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
+                ++items;
+                deal_next<ROWS, kLatKeys>(a, c);
+            }
+            mma_commit<1>(done);
+            drain_bar(done, 0, global_ns() + kWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- the keys
+        Place<C::kPairs> pp;
+        Place<C::kTails> tp;
+        int uses_p = 0, uses_t = 0;  // slots filled so far
+        uint32_t cuts = 0;
+        const uint32_t ring = smem_u32(smem + C::kOffPairs), tring = smem_u32(smem + C::kOffTails);
+        const int boxes = kLatKeys / box_rows;    // of a block, 8 at most
+        const int bx = lane % boxes, blk = lane / boxes;
+        auto claim = [&](uint64_t* empty, uint32_t phase) { return ok = __all_sync(~0u, wait_bar(empty, phase ^ 1, ctl)); };
+        while (ok && c.u < c.end) {
+            int lo, hi;
+            const int r0 = c.rt * ROWS;
+            key_range(kv, 0, c.s, r0, min(r0 + ROWS, c.s.q_len * kv.group), lo, hi);
+            for (int j = 0; j < c.take && ok; ++j) {
+                const int key0 = (c.first + c.off + j) * kLatKeys, key = key0 + bx * box_rows;
+                int page = kv.n_pages, row = 0;   // outside the map: zeros
+                if (key < hi) {
+                    const int p = div_by(key, kv.by_page), id = page_id(kv, c.b, p);
+                    row = key - p * kv.page;
+                    if (id >= 0) page = id;
+                }
+                const int last = hi - key0;       // rows that some row of the tile sees
+                const bool cut = last > 0 && last < kLatKeys && last % box_rows != 0;
+                auto copy = [&](int x, uint32_t dst, int blocks, uint64_t* bar) {
+                    if (lane == 0) mbar_expect_tx(own_bar(bar), blocks * C::kBlock);
+                    __syncwarp();
+                    if (blk < blocks) tma_tile3d<1>(dst + blk * C::kBlock + bx * box_rows * 128, &map, x + 64 * blk, row, page, own_bar(bar));
+                };
+                if (!cut) {
+                    for (int x = 0; x < pairs && claim(empty_p + pp.slot, pp.phase); ++x) {
+                        copy(128 * x, ring + pp.slot * C::kPair, 2, full_p + pp.slot);
+                        pp.next();
+                        ++uses_p;
+                    }
+                } else {  // the boxes' rows behind the last visible one are cleared before the products may read them
+                    auto q = pp;
+                    for (int x = 0; x < pairs && claim(empty_p + q.slot, q.phase); ++x) q.next();
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(own_bar(cut_in), pairs * C::kPair);
+                    __syncwarp();
+                    q = pp;
+                    for (int x = 0; x < pairs; ++x) {
+                        if (blk < 2)
+                            tma_tile3d<1>(ring + q.slot * C::kPair + blk * C::kBlock + bx * box_rows * 128, &map, 128 * x + 64 * blk, row, page, own_bar(cut_in));
+                        q.next();
+                    }
+                }
+                if (ok && tail && claim(empty_t + tp.slot, tp.phase)) {
+                    copy(128 * pairs, tring + tp.slot * C::kBlock, 1, full_t + tp.slot);
+                    tp.next();
+                    ++uses_t;
+                }
+                if (cut) {
+                    // (also when the tail was not to be had: these copies are under way)
+                    const bool in = __all_sync(~0u, wait_bar(cut_in, cuts & 1, ctl));
+                    if (!in) drain_bar(cut_in, cuts & 1, global_ns() + kWaitNs);
+                    ok = ok && in;
+                    if (!ok) break;
+                    ++cuts;
+                    const int end = (last + box_rows - 1) / box_rows * box_rows, per = (end - last) * 8;
+                    for (int x = 0; x < pairs; ++x) {
+                        uint8_t* at = smem + C::kOffPairs + pp.slot * C::kPair + last * 128;
+                        for (int y = lane; y < 2 * per; y += 32)
+                            *reinterpret_cast<uint4*>(at + (y >= per ? C::kBlock + (y - per) * 16 : y * 16)) = make_uint4(0, 0, 0, 0);
+                        fence_async_proxy();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(own_bar(full_p + pp.slot));
+                        pp.next();
+                        ++uses_p;
+                    }
+                }
+            }
+            deal_next<ROWS, kLatKeys>(a, c);
+        }
+        // Nothing is on its way to this CTA's memory when it leaves: every slot's last use has landed and been read (or,
+        // after a timeout, the limit has passed).
+        const uint64_t end = global_ns() + kWaitNs;
+        for (int u = max(uses_p - C::kPairs, 0); u < uses_p; ++u) {
+            drain_bar(full_p + u % C::kPairs, (u / C::kPairs) & 1, end);
+            drain_bar(empty_p + u % C::kPairs, (u / C::kPairs) & 1, end);
+        }
+        for (int u = max(uses_t - C::kTails, 0); u < uses_t; ++u) {
+            drain_bar(full_t + u % C::kTails, (u / C::kTails) & 1, end);
+            drain_bar(empty_t + u % C::kTails, (u / C::kTails) & 1, end);
+        }
+    } else if (warp < 4) {
+        // ---------------------------------------------------------------- the queries, half of the rows each
+        uint32_t items = 0;
+        const int chunks = (2 * pairs + tail) * 8;  // of a row, zeros past its components
+        while (ok && c.u < c.end) {
+            ok = __all_sync(~0u, wait_bar(q_free, (items & 1) ^ 1, ctl));
+            if (!ok) break;
+            ++items;
+            const int r0 = c.rt * ROWS, rows = min(c.s.q_len * kv.group - r0, ROWS);
+            for (int r = (warp - 2) * (ROWS / 2); r < (warp - 1) * (ROWS / 2); ++r) {
+                int tok, head;
+                row_of(kv, r0 + min(r, rows - 1), tok, head);
+                const T* src = static_cast<const T*>(a.q) + (c.s.q0 + tok) * a.q_ts + head * a.q_hs;
+                uint8_t* dst = smem + C::kOffQ + r * 128;
+                for (int x = lane; x < chunks; x += 32) {
+                    const bool in = r < rows && x * 8 < a.dk;
+                    cp_async16(dst + (x / 8) * C::kQBlock + (((x & 7) ^ (r & 7)) << 4), src + (in ? x * 8 : 0), in ? 16 : 0);
+                }
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(own_bar(q_full));
+            deal_next<ROWS, kLatKeys>(a, c);
+        }
+        if (items) drain_bar(q_free, (items - 1) & 1, global_ns() + kWaitNs);  // (its arrival, too, has come)
+    } else {
+        // ---------------------------------------------------------------- softmax and output
+        const int w = warp - 4;                   // S: rows 16 w ..; O^T: components 32 w .. of each 128
+        const uint32_t lane_base = static_cast<uint32_t>(32 * w) << 16;
+        const float sc = a.scale * kLog2e;
+        uint32_t t = 0;                           // tiles so far
+        while (ok && c.u < c.end) {
+            const int n = c.take;
+            const int r0 = c.rt * ROWS, rows = min(c.s.q_len * kv.group - r0, ROWS);
+            const bool live = 16 * w < rows;
+            int pos[2];                           // of this thread's rows: 16 w + lane / 4, and 8 on
+#pragma unroll
+            for (int x = 0; x < 2; ++x) pos[x] = min(c.s.pos0 + div_by(r0 + min(16 * w + lane / 4 + 8 * x, rows - 1), kv.by_group), kv.cap - 1);
+            const int all = min(c.s.pos0 + div_by(r0 + min(16 * w, rows - 1), kv.by_group), kv.cap - 1);  // every row of the warp sees keys <= all
+            if (tid - 128 < rows) {
+                int tok, head;
+                row_of(kv, r0 + tid - 128, tok, head);
+                row_at[tid - 128] = (c.s.q0 + tok) * a.o_ts + head * a.o_hs;
+            }
+            float m[2] = {kNegInf, kNegInf};      // the references, in units of S
+            float l[2] = {0.f, 0.f};              // this thread's part of the sums
+            for (int j = 0; j < n; ++j, ++t) {
+                if (ok) ok = __all_sync(~0u, wait_bar(s_full + (t & 1), t >> 1 & 1, ctl));
+                uint32_t v[32];
+                float top[2] = {kNegInf, kNegInf};
+                bool grew = false;
+                if (ok && live) {
+                    tc_fence_after();
+                    tmem_ld_frag(tmem + lane_base + C::kSCol + kLatKeys * (t & 1), v);
+                    tmem_ld_wait();
+                    tmem_tie<32>(v);
+                    const int key0 = (c.first + c.off + j) * kLatKeys;
+                    if (key0 + kLatKeys - 1 > all) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (key0 + 8 * (i / 4) + 2 * (lane & 3) + (i & 1) > pos[i >> 1 & 1]) v[i] = __float_as_uint(kNegInf);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top[i >> 1 & 1] = fmaxf(top[i >> 1 & 1], __uint_as_float(v[i]));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 1));
+                        top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 2));
+                        grew |= (top[x] - m[x]) * sc > 8.f;  // (m = -inf: inf, or NaN if the row has seen nothing yet)
+                    }
+                }
+                if (softmax_any(grew || !ok)) {
+                    ok = !softmax_any(!ok);
+                    if (!ok) break;
+                    if (live) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float f = 1.f;
+                            if ((top[x] - m[x]) * sc > 8.f) {
+                                f = m[x] == kNegInf ? 0.f : exp2_fast((m[x] - top[x]) * sc);
+                                m[x] = top[x];
+                            }
+                            l[x] *= f;
+                            if ((lane & 3) == 0) factor[16 * w + lane / 4 + 8 * x] = f;
+                        }
+                    }
+                    if (j > 0) {  // O is rescaled between the products: the one before has to be there
+                        softmax_sync();
+                        ok = __all_sync(~0u, wait_bar(o_done, (t & 1) ^ 1, ctl));
+                        if (ok) {
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int x = 0; x < pairs * ROWS; x += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tmem + lane_base + C::kOCol + x, o);
+                                tmem_ld_wait();
+                                tmem_tie<16>(o);
+#pragma unroll
+                                for (int y = 0; y < 16; ++y)
+                                    if (x % ROWS + y < rows) o[y] = __float_as_uint(__uint_as_float(o[y]) * factor[x % ROWS + y]);
+                                tmem_st16(tmem + lane_base + C::kOCol + x, o);
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                }
+                if (ok && j > 0) ok = __all_sync(~0u, wait_bar(o_done, (t & 1) ^ 1, ctl));  // P before is read
+                if (ok && live) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float base = m[x] == kNegInf ? 0.f : m[x] * sc;
+                        const int r = 16 * w + lane / 4 + 8 * x;
+                        uint8_t* at = smem + C::kOffP + r * 128 + (lane & 3) * 4;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float p0 = exp2_fast(fmaf(__uint_as_float(v[4 * i + 2 * x]), sc, -base));
+                            const float p1 = exp2_fast(fmaf(__uint_as_float(v[4 * i + 2 * x + 1]), sc, -base));
+                            l[x] += p0 + p1;
+                            // the product's operand: 16 bits; the sum l is of the fp32 values
+                            *reinterpret_cast<uint32_t*>(at + ((i ^ (r & 7)) << 4)) = Elem<T>::pack(p0, p1);
+                        }
+                    }
+                    fence_async_proxy();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(own_bar(p_full));
+            }
+            if (ok) ok = __all_sync(~0u, wait_bar(o_done, (t & 1) ^ 1, ctl));
+            if (softmax_any(!ok)) {
+                ok = false;
+                break;
+            }
+            // ------------------------------------------------------------ the tile's output
+            tc_fence_after();
+            const bool whole = c.whole();
+            const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (c.u == c.begin ? 0 : 1);
+            if (live) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    l[x] += __shfl_xor_sync(~0u, l[x], 1);
+                    l[x] += __shfl_xor_sync(~0u, l[x], 2);
+                    const int r = 16 * w + lane / 4 + 8 * x;
+                    if ((lane & 3) != 0 || r >= rows) continue;
+                    factor[r] = l[x] == 0.f ? 0.f : 1.f / l[x];
+                    if (l[x] != l[x]) *odd = 1;
+                    if (!whole) {
+                        a.part_ml[part * ROWS + r] = make_float2(m[x] == kNegInf ? kNegInf : m[x] * sc, l[x]);
+                    } else if (a.lse) {
+                        int tok, head;
+                        row_of(kv, r0 + r, tok, head);
+                        a.lse[static_cast<int64_t>(c.s.q0 + tok) * kv.hq + head] = l[x] == 0.f ? kNegInf : (m[x] * sc + log2f(l[x])) * kLn2;
+                    }
+                }
+            }
+            softmax_sync();
+            bool bad = false;
+            for (int x = 0; x < pairs; ++x) {
+                const int e = 128 * x + 32 * w + lane;    // this thread's component
+#pragma unroll 1
+                for (int y = 0; y < rows; y += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tmem + lane_base + C::kOCol + ROWS * x + y, o);
+                    tmem_ld_wait();
+                    tmem_tie<16>(o);
+                    if (whole) {
+#pragma unroll
+                        for (int r = 0; r < 16; r += 2) {
+                            // two rows: the even lane of a pair writes both lanes' components of the first, the odd lane of the second
+                            if (y + r >= rows) break;
+                            const float f0 = __uint_as_float(o[r]) * factor[y + r], f1 = __uint_as_float(o[r + 1]) * factor[min(y + r + 1, rows - 1)];
+                            bad |= f0 != f0 || (f1 != f1 && y + r + 1 < rows);
+                            const float got = __shfl_xor_sync(~0u, lane & 1 ? f0 : f1, 1);
+                            const int rr = y + r + (lane & 1);
+                            if (rr < rows && (e & ~1) < kv.d)
+                                *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row_at[rr] + (e & ~1)) =
+                                    lane & 1 ? Elem<T>::pack(got, f1) : Elem<T>::pack(f0, got);
+                        }
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (y + r < rows) a.part_o[(part * ROWS + y + r) * (128 * pairs) + e] = __uint_as_float(o[r]);
+                    }
+                }
+            }
+            tc_fence_before();
+            if (bad) *odd = 1;
+            softmax_sync();                           // (`factor` and `row_at` are read)
+            if (lane == 0) mbar_arrive(own_bar(o_free));
+            deal_next<ROWS, kLatKeys>(a, c);
+        }
+        if (ok && *odd) retake_rows<T, ROWS>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), w);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_free<1>(tmem, C::kCols);
+    }
+}
+
+// The join of the pieces of a cut tile.  Block c stands for the boundary before CTA c + 1; the (row, 128 components) items of a
+// tile that several boundaries cut are dealt over their blocks, a warp for an item, or eight that share its pieces where
+// they are many.  The sums' order is that of the pieces' CTAs, so two runs give the same bits.
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const LatentArgs a) {
+    wait_for_stream();
+    __shared__ float4 part[kJoinWarps][32];
+    __shared__ float part_l[kJoinWarps];
+    const int cta = blockIdx.x + 1;
+    const BoundaryRec rec = a.recs[cta];
+    if (!rec.cut) return;
+    const KvArgs& kv = a.kv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pairs = (kv.d + 127) / 128;
+    const int c0 = static_cast<int>(div_line(rec.begin, rec.per)), c1 = static_cast<int>(div_line(rec.begin + rec.n - 1, rec.per));
+    const int share = c1 - c0 + 1 > 8 ? kJoinWarps : 1;  // warps of an item
+    const int wi = share > 1 ? warp : 0;
+    const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
+    auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
+    const int step = c1 - c0;
+    for (int k = 0; cta - (c0 + 1) + k * step < rows * pairs; k += kJoinWarps / share) {
+        const int item = cta - (c0 + 1) + (k + (share > 1 ? 0 : warp)) * step;
+        const int r = item / pairs, col = item % pairs * 128;
+        float mm = kNegInf, ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            for (int p = c0 + lane; p <= c1; p += 32) mm = fmaxf(mm, a.part_ml[slot_of(p) * ROWS + r].x);
+            constexpr int kAhead = 8;
+            for (int p0 = c0 + wi; p0 <= c1; p0 += kAhead * share) {
+                float2 v[kAhead];
+                float4 o[kAhead];
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) {
+                    const int64_t at = slot_of(min(p0 + y * share, c1)) * ROWS + r;
+                    v[y] = a.part_ml[at];
+                    o[y] = reinterpret_cast<const float4*>(a.part_o + at * (128 * pairs) + col)[lane];
+                }
+                if (p0 == c0 + wi) {
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
+                }
+                const float base = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) {
+                    if (p0 + y * share > c1) break;
+                    const float f = exp2_fast(v[y].x - base);
+                    ll += v[y].y * f;
+                    acc.x += o[y].x * f;
+                    acc.y += o[y].y * f;
+                    acc.z += o[y].z * f;
+                    acc.w += o[y].w * f;
+                }
+            }
+        }
+        if (share > 1) {  // (every warp of the block has the same item)
+            __syncthreads();
+            part[warp][lane] = acc;
+            if (lane == 0) part_l[warp] = ll;
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    const float4 v = part[w][lane];
+                    ll += part_l[w];
+                    acc.x += v.x;
+                    acc.y += v.y;
+                    acc.z += v.z;
+                    acc.w += v.w;
+                }
+            }
+        }
+        if (wi != 0 || r >= rows) continue;
+        int i, head;
+        row_of(kv, r0 + r, i, head);
+        const int tok = rec.q0 + i;
+        const bool bad = ll != ll || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w;
+        if (__any_sync(~0u, bad)) {
+            latent_row<T>(a, rec.b, tok, head, rec.pos0 + i, col, col + 128);
+            continue;
+        }
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        if (col + 4 * lane < kv.d)
+            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col + 4 * lane) =
+                make_uint2(Elem<T>::pack(acc.x * inv, acc.y * inv), Elem<T>::pack(acc.z * inv, acc.w * inv));
+        if (lane == 0 && col == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
+    }
+}
+
+// The cache [pages][page_size][Dc + R] as a 3-D map (component, row, page), boxes of 64 components x `box` rows in
+// 128-byte-swizzled rows.  Anything outside reads zeros: components past the row's, the page past the last.
+cudaError_t make_map(const LatentArgs& a, int dtype, int box, CUtensorMap* map) {
+    Encode encode = nullptr;
+    if (cudaError_t e = get_encode(&encode); e != cudaSuccess) return e;
+    const KvArgs& kv = a.kv;
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.dk), static_cast<cuuint64_t>(kv.page), static_cast<cuuint64_t>(kv.n_pages)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * kv.k_rs), static_cast<cuuint64_t>(kv.n_pages > 1 ? 2 * kv.k_ps : 16)};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 1};
+    const CUresult r = encode(map, dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, kv.k, dims, strides, boxes, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename T, int ROWS>
+cudaError_t launch_r(const LatentArgs& a, int dtype, int n_ctas, cudaStream_t st) {
+    using C = LatCfg<ROWS>;
+    const int box = std::min(a.kv.page & -a.kv.page, kLatKeys);
+    CUtensorMap map;
+    if (cudaError_t e = make_map(a, dtype, box, &map); e != cudaSuccess) return e;
+    cudaError_t e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_in_stream(attend_latent_kernel<T, ROWS>, dim3(n_ctas), C::kThreads, C::kSmem, 1, st, a, box, map);
+    if (e != cudaSuccess || !a.split || n_ctas < 2) return e;
+    return launch_in_stream(latent_join_kernel<T, ROWS>, dim3(n_ctas - 1), kJoinWarps * 32, 0, 1, st, a);
+}
+
+template <typename T>
+cudaError_t launch_t(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
+    if (rows <= 16) return launch_r<T, 16>(a, dtype, n_ctas, st);
+    if (rows <= 32) return launch_r<T, 32>(a, dtype, n_ctas, st);
+    return launch_r<T, 64>(a, dtype, n_ctas, st);
 }
 
 }  // namespace
 
 int latent_part_rows(int n_ctas) { return 2 * n_ctas * 64; }
 
-cudaError_t launch_latent(const LatentArgs& a, int dtype, int64_t, int, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.kv.n_tokens) * a.kv.hq + 3) / 4));
-    return dtype == 0 ? launch_in_stream(attend_latent_kernel<__nv_bfloat16>, grid, 128, 0, 1, st, a)
-                      : launch_in_stream(attend_latent_kernel<__half>, grid, 128, 0, 1, st, a);
+cudaError_t launch_latent(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
+    return dtype == 0 ? launch_t<__nv_bfloat16>(a, dtype, rows, n_ctas, st) : launch_t<__half>(a, dtype, rows, n_ctas, st);
 }
 
 }  // namespace moe
