@@ -22,7 +22,7 @@ from __future__ import annotations
 
 __all__ = ["moe_w4a8_forward", "moe_w4a8_route", "moe_w4a8_gemm1_partials", "moe_w4a8_gemm2_partials",
            "moe_w4a8_workspace_size", "moe_w4a8_version", "moe_w4a8_status_string", "moe_w4a8_forward_noalloc",
-           "Dims", "MoeError"]
+           "Dims", "MoeError", "moe_w4a8_route_scored", "RouteRule", "moe_w4a8_forward_bf16_routed"]
 _ATTENTION = ["moe_w4a8_kv_append", "moe_w4a8_paged_attention", "KVBatch", "HeadPrep", "rope_table"]
 _LATENT = ["moe_w4a8_latent_append", "moe_w4a8_latent_attention", "LatentBatch"]
 __all__ += _ATTENTION + _LATENT

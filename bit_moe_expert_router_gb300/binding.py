@@ -74,13 +74,16 @@ def _load():
     lib.moe_w4a8_forward_bf16_workspace_size.restype = sz
     lib.moe_w4a8_forward_bf16.argtypes = [p, p, p, p, p, p, dp, p, p, sz, p]
     lib.moe_w4a8_forward_w2w4.argtypes = [p, p, p, p, p, p, p, p, dp, p, p, sz, p]
+    lib.moe_w4a8_forward_bf16_routed.argtypes = [p, p, p, p, p, p, p, dp, p, p, sz, p]
+    lib.moe_w4a8_route_scored.argtypes = [p, i64, p, i64, i64, p, p, p, p]
     lib.moe_w4a8_mixed_bank_layout.argtypes = [p, dp, p, p, p, p]
     lib.moe_w4a8_forward_w2w4_compact.argtypes = [p, p, p, p, p, p, p, p, p, p, dp, p, p, sz, p]
     for name in ("moe_w4a8_forward", "moe_w4a8_forward_debug", "moe_w4a8_route", "moe_w4a8_gemm1_partials",
                  "moe_w4a8_gemm2_partials", "moe_w4a8_forward_noalloc", "moe_w4a8_device_status",
                  "moe_w4a8_selftest_barrier_timeout", "moe_w4a8_forward_host", "moe_w4a8_forward_bf16",
                  "moe_w4a8_forward_w2w4", "moe_w4a8_debug_routing", "moe_w4a8_forward_routed",
-                 "moe_w4a8_mixed_bank_layout", "moe_w4a8_forward_w2w4_compact"):
+                 "moe_w4a8_mixed_bank_layout", "moe_w4a8_forward_w2w4_compact", "moe_w4a8_forward_bf16_routed",
+                 "moe_w4a8_route_scored"):
         getattr(lib, name).restype = ctypes.c_int
     if lib.moe_w4a8_version() != ABI_VERSION:
         raise RuntimeError(f"{LIB_PATH}: ABI version {lib.moe_w4a8_version()} != {ABI_VERSION}")
@@ -276,6 +279,26 @@ def moe_w4a8_forward_bf16(x_bf16, router_logits, w13_packed, w13_scale, w2_packe
     return out
 
 
+def moe_w4a8_forward_bf16_routed(x_bf16, topk_ids, topk_w, w13_packed, w13_scale, w2_packed, w2_scale, d: Dims, out,
+                                 workspace: torch.Tensor):
+    """moe_w4a8_forward_bf16 with the routing supplied by the caller (moe_w4a8_route_scored's, for example)."""
+    s13, s13s, s2, s2s = _bank_shapes(d)
+    _need(x_bf16, "x_bf16", torch.bfloat16, (d.T, d.H))
+    _need(topk_ids, "topk_ids", torch.int32, (d.T, d.top_k))
+    _need(topk_w, "topk_w", torch.float32, (d.T, d.top_k))
+    _need(w13_packed, "w13_packed", torch.uint8, s13)
+    _need(w13_scale, "w13_scale", torch.float32, s13s)
+    _need(w2_packed, "w2_packed", torch.uint8, s2)
+    _need(w2_scale, "w2_scale", torch.float32, s2s)
+    _need(out, "out", torch.float32, (d.T, d.H))
+    wp, wb = _ws_view(workspace)
+    _call("moe_w4a8_forward_bf16_routed", (x_bf16, topk_ids, topk_w, w13_packed, w13_scale, w2_packed, w2_scale, out,
+                                           workspace),
+          _ptr(x_bf16), _ptr(topk_ids), _ptr(topk_w), _ptr(w13_packed), _ptr(w13_scale), _ptr(w2_packed),
+          _ptr(w2_scale), ctypes.byref(d), _ptr(out), wp, wb)
+    return out
+
+
 def moe_w4a8_forward_w2w4(x_q, x_scale, router_logits, w13_packed, w13_scale, w2_packed, w2_scale, slot_bits,
                           d: Dims, out, workspace: torch.Tensor):
     """The layer on a mixed 2/4-bit bank: slot_bits (uint8 CUDA tensor [E+S], 2 or 4) gives each slot's width.
@@ -386,6 +409,70 @@ def moe_w4a8_route(router_logits, d: Dims, topk_ids, topk_w, counts, offsets, pe
     _call("moe_w4a8_route", (router_logits, topk_ids, topk_w, counts, offsets, perm, inv, workspace),
           _ptr(router_logits), ctypes.byref(d), _ptr(topk_ids), _ptr(topk_w), _ptr(counts), _ptr(offsets),
           _ptr(perm), _ptr(inv), wp, wb)
+
+
+class _RouteRule(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("n_experts", "top_k", "score", "n_groups", "topk_groups", "group_top", "renormalise")]
+    _fields_ += [("scale", ctypes.c_float)]
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class RouteRule:
+    """How moe_w4a8_route_scored chooses experts.
+
+    score: "softmax" or "sigmoid" of the logits.  n_groups > 1: the experts are that many runs of equal length, of which the
+    topk_groups best are kept, by their best expert (group_top 1) or the sum of their two best (2).  renormalise: the top_k
+    weights are divided by their sum.  scale: what they are multiplied by in the end.
+    """
+
+    def __init__(self, n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+                 renormalise: bool = True, scale: float = 1.0):
+        if score not in _SCORES:
+            raise ValueError(f"score {score!r}: one of {sorted(_SCORES)}")
+        self.n_experts, self.top_k = int(n_experts), int(top_k)
+        self._c = _RouteRule(n_experts, top_k, _SCORES[score], n_groups, topk_groups, group_top, int(renormalise), scale)
+        self._p = ctypes.addressof(self._c)
+        # what the operator refuses, it refuses here: a call without tokens enqueues nothing
+        _check("moe_w4a8_route_scored", _load().moe_w4a8_route_scored(self._p, 0, None, self.n_experts, 0, None, None, None, None))
+
+
+def moe_w4a8_route_scored(router_logits, rule: RouteRule, topk_ids, topk_w, bias=None):
+    """The experts of each token by their scores, and their weights (see the header).
+
+    router_logits [tokens, n_experts] float32, bfloat16 or float16, any token stride; bias [n_experts] float32, added to the
+    scores for the choice alone, or None; topk_ids [tokens, top_k] int32, topk_w [tokens, top_k] float32.
+    """
+    dtype = _LOGITS.get(router_logits.dtype)
+    if dtype is None:
+        raise TypeError(f"router_logits: dtype {router_logits.dtype}, expected one of {list(_LOGITS)}")
+    if not router_logits.is_cuda:
+        raise ValueError("router_logits must be a CUDA tensor")
+    if router_logits.dim() != 2 or router_logits.shape[1] != rule.n_experts:
+        raise ValueError(f"router_logits: shape {tuple(router_logits.shape)}, expected [tokens, {rule.n_experts}]")
+    n = router_logits.shape[0]
+    stride, last = router_logits.stride()
+    if last != 1 and rule.n_experts > 1:
+        raise ValueError("router_logits: a token's logits must be contiguous")
+    index = router_logits.get_device()
+    for t, name, want, shape in ((topk_ids, "topk_ids", torch.int32, (n, rule.top_k)), (topk_w, "topk_w", torch.float32, (n, rule.top_k)),
+                                 (bias, "bias", torch.float32, (rule.n_experts,))):
+        if t is None and name == "bias":
+            continue
+        if t is None or t.dtype is not want or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+            _need(t, name, want, shape)
+            raise ValueError(f"{name} is on {t.device}, router_logits on {router_logits.device}")
+    args = (rule._p, n, router_logits.data_ptr(), stride if n > 1 else max(stride, rule.n_experts), dtype,
+            None if bias is None else bias.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr())
+    if torch._C._cuda_getDevice() == index:
+        status = _load().moe_w4a8_route_scored(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = _load().moe_w4a8_route_scored(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        raise MoeError("moe_w4a8_route_scored", status)
 
 
 def moe_w4a8_forward_routed(x_q, x_scale, topk_ids, topk_w, w13_packed, w13_scale, w2_packed, w2_scale, d: Dims,

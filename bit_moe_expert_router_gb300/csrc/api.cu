@@ -5,11 +5,13 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include "decode.h"
 #include "kernels.h"
 #include "moe_w4a8.h"
 #include "prefill.h"
+#include "route_scored.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
 
@@ -476,6 +478,28 @@ MOE_API size_t moe_w4a8_forward_bf16_workspace_size(const moe_dims_t* d) {
     return bf16_stage_total(d, layout_of(d));
 }
 
+namespace {
+// The layer from bf16 activations; the routing from the logits, or supplied (logits null).
+int forward_bf16(const uint16_t* x_bf16, const float* router_logits, const int32_t* ids_in, const float* wts_in,
+                 const uint8_t* w13_packed, const float* w13_scale, const uint8_t* w2_packed, const float* w2_scale,
+                 const moe_dims_t* d, float* out, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+    const WsLayout L = layout_of(d);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < bf16_stage_total(d, L)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const Views v = views(workspace, L);
+    moe::DecodePlan pl;
+    if (decode_forward_plan(d, &pl))  // the fused kernel quantises the activations itself
+        return run_decode(nullptr, nullptr, router_logits, w13_packed, w13_scale, w2_packed, w2_scale, d, out, v, pl,
+                          nullptr, st, x_bf16, nullptr, false, ids_in, wts_in);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int8_t* x_q = reinterpret_cast<int8_t*>(ws + bf16_stage_xq(L));
+    float* x_scale = reinterpret_cast<float*>(ws + bf16_stage_xs(d, L));
+    MOE_CUDA(moe::launch_quantize_bf16(x_bf16, d->T, d->H, x_q, x_scale, st));
+    return run_layer(x_q, x_scale, router_logits, w13_packed, w13_scale, w2_packed, w2_scale, d, out, L, v, st,
+                     MOE_ENGINE_AUTO, nullptr, false, ids_in, wts_in);
+}
+}  // namespace
+
 MOE_API int moe_w4a8_forward_bf16(const uint16_t* x_bf16, const float* router_logits, const uint8_t* w13_packed,
                                   const float* w13_scale, const uint8_t* w2_packed, const float* w2_scale,
                                   const moe_dims_t* d, float* out, void* workspace, size_t workspace_bytes,
@@ -484,20 +508,20 @@ MOE_API int moe_w4a8_forward_bf16(const uint16_t* x_bf16, const float* router_lo
     MOE_TRY(check_ptrs({w13_packed, w13_scale, w2_packed, w2_scale}));
     if (d->T == 0) return MOE_OK;
     MOE_TRY(check_ptrs({x_bf16, router_logits, out}));
-    const WsLayout L = layout_of(d);
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_ERR_INVALID_ARG;
-    if (workspace_bytes < bf16_stage_total(d, L)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const Views v = views(workspace, L);
-    moe::DecodePlan pl;
-    if (decode_forward_plan(d, &pl))  // the fused kernel quantises the activations itself
-        return run_decode(nullptr, nullptr, router_logits, w13_packed, w13_scale, w2_packed, w2_scale, d, out, v, pl,
-                          nullptr, st, x_bf16);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    int8_t* x_q = reinterpret_cast<int8_t*>(ws + bf16_stage_xq(L));
-    float* x_scale = reinterpret_cast<float*>(ws + bf16_stage_xs(d, L));
-    MOE_CUDA(moe::launch_quantize_bf16(x_bf16, d->T, d->H, x_q, x_scale, st));
-    return run_layer(x_q, x_scale, router_logits, w13_packed, w13_scale, w2_packed, w2_scale, d, out, L, v, st);
+    return forward_bf16(x_bf16, router_logits, nullptr, nullptr, w13_packed, w13_scale, w2_packed, w2_scale, d, out,
+                        workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+MOE_API int moe_w4a8_forward_bf16_routed(const uint16_t* x_bf16, const int32_t* topk_ids, const float* topk_w,
+                                         const uint8_t* w13_packed, const float* w13_scale, const uint8_t* w2_packed,
+                                         const float* w2_scale, const moe_dims_t* d, float* out, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    MOE_TRY(check_dims(d));
+    MOE_TRY(check_ptrs({w13_packed, w13_scale, w2_packed, w2_scale}));
+    if (d->T == 0) return MOE_OK;
+    MOE_TRY(check_ptrs({x_bf16, topk_ids, topk_w, out}));
+    return forward_bf16(x_bf16, nullptr, topk_ids, topk_w, w13_packed, w13_scale, w2_packed, w2_scale, d, out, workspace,
+                        workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 MOE_API int moe_w4a8_forward_w2w4(const int8_t* x_q, const float* x_scale, const float* router_logits,
@@ -602,6 +626,45 @@ MOE_API int moe_w4a8_forward_routed(const int8_t* x_q, const float* x_scale, con
     return run_layer(x_q, x_scale, nullptr, w13_packed, w13_scale, w2_packed, w2_scale, d, out, L,
                      views(workspace, L), static_cast<cudaStream_t>(stream), MOE_ENGINE_AUTO, nullptr, false, topk_ids,
                      topk_w);
+}
+
+MOE_API int moe_w4a8_route_scored(const moe_route_rule_t* r, int64_t n_tokens, const void* router_logits,
+                                  int64_t logits_stride, int64_t logits_dtype, const float* bias, int32_t* topk_ids,
+                                  float* topk_w, void* stream) {
+    if (!r) return MOE_ERR_INVALID_ARG;
+    for (int64_t v : {r->n_experts, r->top_k, r->n_groups, r->topk_groups})
+        if (v < 1) return MOE_ERR_INVALID_ARG;
+    if (r->top_k > r->n_experts || r->n_experts % r->n_groups != 0 || r->topk_groups > r->n_groups || n_tokens < 0)
+        return MOE_ERR_INVALID_ARG;
+    const int64_t size = r->n_experts / r->n_groups;
+    if (r->group_top < 1 || r->group_top > 2 || r->group_top > size || (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) ||
+        logits_dtype < MOE_LOGITS_FP32 || logits_dtype > MOE_LOGITS_FP16 || logits_stride < r->n_experts || !std::isfinite(r->scale))
+        return MOE_ERR_INVALID_ARG;
+    if (r->n_experts > moe::kMaxExperts || r->top_k > moe::kMaxTopK || (r->n_groups & (r->n_groups - 1)) != 0 || r->n_groups > 32 ||
+        n_tokens > (int64_t(1) << 24))
+        return MOE_ERR_UNSUPPORTED;
+    if (r->top_k > r->topk_groups * size) return MOE_ERR_INVALID_ARG;
+    if (bias) MOE_TRY(check_ptrs({bias}));
+    if (n_tokens == 0) return MOE_OK;
+    MOE_TRY(check_ptrs({router_logits, topk_ids, topk_w}));
+    moe::RouteScoredArgs a{};
+    a.logits = router_logits;
+    a.bias = bias;
+    a.ids = topk_ids;
+    a.wts = topk_w;
+    a.T = n_tokens;
+    a.E = r->n_experts;
+    a.stride = logits_stride;
+    a.k = static_cast<int>(r->top_k);
+    a.dtype = static_cast<int>(logits_dtype);
+    a.sigmoid = r->score == MOE_SCORE_SIGMOID;
+    a.n_groups = static_cast<int>(r->n_groups);
+    a.topk_groups = static_cast<int>(r->topk_groups);
+    a.group_top = static_cast<int>(r->group_top);
+    a.renormalise = r->renormalise != 0;
+    a.scale = r->scale;
+    MOE_CUDA(moe::launch_route_scored(a, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
 }
 
 MOE_API int moe_w4a8_debug_routing(const moe_dims_t* d, const void* workspace, size_t workspace_bytes,

@@ -1,0 +1,365 @@
+// Routing by scores: softmax or sigmoid of the router's logits, a bias that moves
+// the choice but not the weights, groups of experts of which some are kept,
+// and the k best experts.
+//
+// Per token: s_e = softmax_e(x) or 1 / (1 + e^-x); r_e = s_e + bias_e, or x_e itself without a bias
+// (s grows with x, so the order is the same); a group's value is its largest r, or the sum of its two
+// largest (of s where there is no bias); of the groups the best, of their experts the k best by (r desc,
+// index asc); w = s of those, divided by their sum if asked for, times the scale.
+//
+// Which experts are chosen is decided as in exact arithmetic on the given logits and fp32 biases: the
+// choice is made in fp32, and where two candidates whose order matters lie closer together than the error
+// bounds below, the token is taken again in fp64 (one in some hundred to a thousand tokens with a bias;
+// without one the logits themselves are compared).
+//
+// Bound: HBM for many tokens (the logits, read once), in fact the instructions of a warp per token.  A lane
+// holds J consecutive experts of one group (32 / groups lanes a group), so lane order is expert order.  It
+// sorts them once, by a network on 32-bit keys whose low bits are the expert's place in the lane; the k best
+// of the warp are then k rounds of a warp-wide maximum and one ballot, in which the winner moves its list up.
+//
+// Errors.  2^x and the quotient are the fast ones: s is off by at most s (2e-6 + 1.2e-7 |x - c|), c the largest
+// logit for softmax and 0 for the sigmoid (two units in 2^22 of the exponential, the argument's rounding, the
+// sum's and the quotient's), which is below 2.2e-6 times the largest score whatever x is: s |x - c| is at most
+// 0.37 of it (of a sigmoid above one half, only 1 - s is off by that factor).  For the experts on the list s is
+// computed anew with expf and a correctly rounded quotient, off by 4e-7 s.
+#include <algorithm>
+
+#include "attention_common.cuh"
+#include "route_scored.h"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 4;  // tokens of a block
+
+// An order-preserving key: absent 0, then NaN, then the numbers (-0 and 0 the same).
+template <int MAXJ>
+__device__ __forceinline__ uint32_t key_of(float v) {
+    if (v != v) return 2 * MAXJ;
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_number(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
+__device__ __forceinline__ unsigned long long key_of(double v) {
+    if (v != v) return 1;
+    const unsigned long long u = __double_as_longlong(v + 0.0);
+    return (u >> 63) ? ~u : (u | 1ull << 63);
+}
+
+__device__ __forceinline__ float widen(uint32_t h, int dtype) { return dtype == 1 ? __uint_as_float(h << 16) : Elem<__half>::unpack(h).x; }
+__device__ __forceinline__ float logit(const RouteScoredArgs& a, int64_t at) {
+    if (a.dtype == 0) return __ldg(static_cast<const float*>(a.logits) + at);
+    return widen(__ldg(static_cast<const unsigned short*>(a.logits) + at), a.dtype);
+}
+
+// The place of a lane: its group, its first expert and how many it has.
+struct Lane {
+    int group, first, n;
+    __device__ __forceinline__ Lane(const RouteScoredArgs& a) {
+        const int lane = threadIdx.x & 31, sub = lane & ((1 << a.lanes_log2) - 1);
+        group = lane >> a.lanes_log2;
+        first = group * a.group_size + sub * a.per_lane;
+        n = min(max(a.group_size - sub * a.per_lane, 0), a.per_lane);
+    }
+};
+
+// The choice in fp64: expert of rank `lane` (lane < k).
+template <int MAXJ>
+__device__ __noinline__ int choose_exactly(const RouteScoredArgs& a, int64_t row) {
+    const int lane = threadIdx.x & 31, lanes = 1 << a.lanes_log2;
+    const Lane me(a);
+    const bool softmax = a.sigmoid == 0, groups = a.topk_groups < a.n_groups;
+    double top = -INFINITY, sum = 0.0;
+    if (softmax) {
+        float m = -INFINITY;
+        for (int i = 0; i < me.n; ++i) m = fmaxf(m, logit(a, row + me.first + i));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        top = m;
+        for (int i = 0; i < me.n; ++i) {
+            const double x = logit(a, row + me.first + i);
+            if (x == x) sum += exp(x - top);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    }
+    unsigned long long key[MAXJ];
+    double b1 = -INFINITY, b2 = -INFINITY;  // the two largest
+#pragma unroll
+    for (int i = 0; i < MAXJ; ++i) {
+        key[i] = 0;
+        if (i >= me.n) continue;
+        const double x = logit(a, row + me.first + i);
+        double r = x, g = x;
+        if (a.bias || (groups && a.group_top == 2)) {
+            const double s = softmax ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x));
+            g = a.bias ? s + static_cast<double>(__ldg(a.bias + me.first + i)) : s;
+            if (a.bias) r = g;
+        }
+        key[i] = key_of(r);
+        if (g > b1) b2 = b1, b1 = g;
+        else if (g > b2) b2 = g;
+    }
+    if (groups) {
+        for (int o = 1; o < lanes; o <<= 1) {
+            const double o1 = __shfl_xor_sync(~0u, b1, o), o2 = __shfl_xor_sync(~0u, b2, o);
+            b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+            b1 = fmax(b1, o1);
+        }
+        const unsigned long long g = key_of(a.group_top == 2 ? b1 + b2 : b1);
+        int better = 0;
+        for (int i = 0; i < a.n_groups; ++i) {
+            const unsigned long long o = __shfl_sync(~0u, g, i * lanes);
+            better += o > g || (o == g && i < me.group);
+        }
+        if (better >= a.topk_groups)
+#pragma unroll
+            for (int i = 0; i < MAXJ; ++i) key[i] = 0;
+    }
+    int mine = 0;
+    for (int r = 0; r < a.k; ++r) {
+        unsigned long long best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < MAXJ; ++i)
+            if (key[i] > best) best = key[i], at = i;
+        unsigned long long m = best;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
+        const int win = __ffs(__ballot_sync(~0u, best == m)) - 1;
+        const int e = __shfl_sync(~0u, me.first + at, win);
+        if (lane == r) mine = e;
+        if (lane == win)
+#pragma unroll
+            for (int i = 0; i < MAXJ; ++i)
+                if (i == at) key[i] = 0;
+    }
+    return mine;
+}
+
+__device__ __forceinline__ float sigmoid_of(float x) {
+    const float t = expf(-fabsf(x));
+    return __fdiv_rn(x >= 0.f ? 1.f : t, 1.f + t);  // (NaN of a NaN, by t)
+}
+
+template <int MAXJ>
+__global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const RouteScoredArgs a) {
+    constexpr int kBits = MAXJ == 1 ? 0 : MAXJ == 2 ? 1 : MAXJ == 4 ? 2 : MAXJ == 8 ? 3 : MAXJ == 16 ? 4 : 5;
+    const int lane = threadIdx.x & 31, lanes = 1 << a.lanes_log2;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    wait_for_stream();
+    if (t >= a.T) return;
+    const int64_t row = t * a.stride;
+    const Lane me(a);
+    const bool softmax = a.sigmoid == 0, groups = a.topk_groups < a.n_groups;
+    float x[MAXJ];
+    if (MAXJ >= 4 && a.vec) {
+        if (a.dtype == 0) {
+#pragma unroll
+            for (int i = 0; i + 3 < MAXJ; i += 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row + me.first + i));
+                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i + 3 < MAXJ; i += 4) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(a.logits) + row + me.first + i));
+                x[i] = widen(v.x & 0xFFFFu, a.dtype), x[i + 1] = widen(v.x >> 16, a.dtype);
+                x[i + 2] = widen(v.y & 0xFFFFu, a.dtype), x[i + 3] = widen(v.y >> 16, a.dtype);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < MAXJ; ++i) x[i] = i < me.n ? logit(a, row + me.first + i) : -INFINITY;
+    }
+    // what the choice is made by: r (with a bias or for sums), else x
+    const bool scores = a.bias || (groups && a.group_top == 2) || (softmax && !a.renormalise);
+    float r[MAXJ], m = 0.f, sum = 1.f, big = 1.f;  // big: no score is larger
+    if (softmax) {
+        m = x[0];
+#pragma unroll
+        for (int i = 1; i < MAXJ; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    }
+    if (scores) {
+        if (softmax) {
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < MAXJ; ++i) {
+                r[i] = exp2_fast((x[i] - m) * kLog2e);
+                sum += i < me.n && x[i] == x[i] ? r[i] : 0.f;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            big = __fdividef(1.f, sum);
+#pragma unroll
+            for (int i = 0; i < MAXJ; ++i) r[i] *= big;
+        } else {
+#pragma unroll
+            for (int i = 0; i < MAXJ; ++i) {
+                const float e = exp2_fast(-fabsf(x[i]) * kLog2e);
+                r[i] = __fdividef(x[i] >= 0.f ? 1.f : e, 1.f + e);
+            }
+        }
+        if (a.bias) {
+            if (MAXJ >= 4 && a.vec) {
+#pragma unroll
+                for (int i = 0; i + 3 < MAXJ; i += 4) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(a.bias + me.first + i));
+                    r[i] += v.x, r[i + 1] += v.y, r[i + 2] += v.z, r[i + 3] += v.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < MAXJ; ++i)
+                    if (i < me.n) r[i] += __ldg(a.bias + me.first + i);
+            }
+        }
+    }
+    bool doubt = false, kept = true;
+    if (groups) {
+        const bool by_r = a.bias || a.group_top == 2;
+        float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < MAXJ; ++i) {
+            const float g = i < me.n ? (by_r ? r[i] : x[i]) : -INFINITY;
+            b2 = fmaxf(b2, fminf(b1, g));
+            b1 = fmaxf(b1, g);
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+            const float o1 = __shfl_xor_sync(~0u, b1, o), o2 = __shfl_xor_sync(~0u, b2, o);
+            b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+            b1 = fmaxf(b1, o1);
+        }
+        const uint32_t g = key_of<MAXJ>(a.group_top == 2 ? b1 + b2 : b1);
+        int better = 0;
+        for (int i = 0; i < a.n_groups; ++i) {
+            const uint32_t o = __shfl_sync(~0u, g, i * lanes);
+            better += o > g || (o == g && i < me.group);
+        }
+        kept = better < a.topk_groups;
+        if (by_r) {
+            const float in = key_number(__reduce_min_sync(~0u, kept ? g : ~0u)), out = key_number(__reduce_max_sync(~0u, kept ? 0u : g));
+            const float size = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(fabsf(b1) + fabsf(b2))));
+            doubt = !(in - out > 1e-5f * big + 5e-7f * size);
+        }
+    }
+    uint32_t s[MAXJ];
+#pragma unroll
+    for (int i = 0; i < MAXJ; ++i) s[i] = i < me.n && kept ? (key_of<MAXJ>(a.bias ? r[i] : x[i]) & ~(MAXJ - 1u)) | (MAXJ - 1 - i) : 0u;
+    // sorted, the largest first (odd-even merges)
+#pragma unroll
+    for (int p = 1; p < MAXJ; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < MAXJ; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < MAXJ && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t lo = min(s[i + j], s[i + j + k]);
+                        s[i + j] = max(s[i + j], s[i + j + k]);
+                        s[i + j + k] = lo;
+                    }
+    int e = -1;           // of rank `lane`, and of the one behind the last
+    uint32_t bucket = 0;  // of its key
+    const int places = min(a.k + 1, 32);
+    for (int q = 0; q < places; ++q) {
+        const uint32_t own = s[0] >> kBits, best = __reduce_max_sync(~0u, own);
+        const int win = __ffs(__ballot_sync(~0u, own == best)) - 1;
+        const int we = __shfl_sync(~0u, me.first + (MAXJ - 1 - static_cast<int>(s[0] & (MAXJ - 1u))), win);
+        if (lane == q) {
+            e = best ? we : -1;
+            bucket = best;
+        }
+        if (lane == win) {
+#pragma unroll
+            for (int i = 0; i + 1 < MAXJ; ++i) s[i] = s[i + 1];
+            s[MAXJ - 1] = 0;
+        }
+    }
+    // (with k = 32 the best of the rest has no lane)
+    const uint32_t rest = a.k == 32 ? __reduce_max_sync(~0u, s[0] >> kBits) : 0u;
+
+    float xe = -INFINITY, be = 0.f, se = 0.f;
+    auto score = [&]() {
+        xe = -INFINITY, be = 0.f, se = 0.f;
+        if (e < 0) return;
+        xe = logit(a, row + e);
+        if (a.bias) be = __ldg(a.bias + e);
+        se = softmax ? __fdiv_rn(expf(xe - m), sum) : sigmoid_of(xe);
+    };
+    score();
+    const int next_e = __shfl_down_sync(~0u, e, 1);
+    const bool last = lane == a.k - 1;
+    if (a.bias) {
+        // Each place against the next: what stands in the wrong order is close to its neighbour; what should be on the list and
+        // is not has a key no better than the first one's behind it.
+        constexpr float kCut = MAXJ * 1.2e-7f;  // the keys' low bits
+        const float re = se + be, err = 4e-7f * se + 1.2e-7f * fabsf(re);
+        const float loose = 2.2e-6f * big + se * (2e-6f + 1.2e-7f * fabsf(xe - m)) + kCut * fabsf(re);
+        float up = __shfl_down_sync(~0u, re + (lane == a.k ? loose : err), 1);
+        const float next_x = __shfl_down_sync(~0u, xe, 1), next_b = __shfl_down_sync(~0u, be, 1);
+        bool there = next_e >= 0;
+        if (lane == 31) {
+            there = rest != 0;
+            up = key_number((rest + 1) << kBits) + 2.2e-6f * big;
+        }
+        const bool same = !last && next_x == xe && next_b == be && next_e > e;
+        doubt |= lane < a.k && there && !same && !(re - err > up);
+    } else if (a.dtype == 0) {
+        // (16-bit logits in one bucket are the same)
+        const uint32_t next = __shfl_down_sync(~0u, bucket, 1);
+        const float next_x = __shfl_down_sync(~0u, xe, 1);
+        const bool one = bucket == (lane == 31 ? rest : next) && bucket != 0;
+        doubt |= lane < a.k && one && (last || !(xe > next_x || (xe == next_x && next_e > e)));
+    }
+    if (__any_sync(~0u, doubt)) {
+        e = lane < a.k ? 0 : -1;
+        const int got = choose_exactly<MAXJ>(a, row);
+        if (lane < a.k) e = got;
+        score();
+    }
+
+    if (lane >= a.k) xe = -INFINITY, se = 0.f;
+    float w = se;
+    if (a.renormalise) {
+        float top = xe;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        // relative to the largest logit where the scores themselves could vanish (a sigmoid far below zero is an exponential)
+        if (softmax || top < -60.f) w = lane < a.k ? expf(xe - top) : 0.f;
+        float all = w;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+        w = __fdiv_rn(w, all);
+    }
+    if (lane < a.k) {
+        a.ids[t * a.k + lane] = e;
+        a.wts[t * a.k + lane] = w * a.scale;
+    }
+}
+
+template <int MAXJ>
+cudaError_t launch_j(RouteScoredArgs a, cudaStream_t st) {
+    // four at a time where every lane is full and begins on a multiple of four
+    a.vec = a.per_lane == MAXJ && a.group_size == MAXJ << a.lanes_log2 && a.stride % 4 == 0;
+    return launch_in_stream(route_scored_kernel<MAXJ>, dim3(static_cast<unsigned>((a.T + kWarps - 1) / kWarps)), 32 * kWarps, 0, 1, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_route_scored(RouteScoredArgs a, cudaStream_t st) {
+    a.lanes_log2 = 5;
+    while ((a.n_groups << a.lanes_log2) > 32) --a.lanes_log2;
+    a.group_size = static_cast<int>(a.E) / a.n_groups;
+    a.per_lane = (a.group_size + (1 << a.lanes_log2) - 1) >> a.lanes_log2;
+    if (a.per_lane <= 1) return launch_j<1>(a, st);
+    if (a.per_lane <= 2) return launch_j<2>(a, st);
+    if (a.per_lane <= 4) return launch_j<4>(a, st);
+    if (a.per_lane <= 8) return launch_j<8>(a, st);
+    if (a.per_lane <= 16) return launch_j<16>(a, st);
+    return launch_j<32>(a, st);
+}
+
+}  // namespace moe

@@ -158,6 +158,54 @@ int moe_w4a8_route(const float* router_logits, const moe_dims_t* d,
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Routing by scores: the choice of experts of layers whose router is not the
+ * softmax over the picked logits that moe_w4a8_route has.  Per token, from its
+ * logits x_e:
+ *
+ *   s_e = softmax_e(x), or 1 / (1 + exp(-x_e)) with MOE_SCORE_SIGMOID;
+ *   r_e = s_e + bias_e (s_e alone where bias is null): what the choice goes by;
+ *   groups: the experts are n_groups runs of equal length; a group's value is
+ *           its largest r_e, or the sum of its two largest (group_top 2), and
+ *           the topk_groups best groups are kept (equal values: the lower);
+ *   ids  = the top_k best experts of the kept groups by r, descending (equal:
+ *           the lower index); an expert whose logit is a NaN has a NaN for its
+ *           score, stands behind all numbers and is left out of the others' sums;
+ *   w    = s of those; with renormalise divided by their sum; times scale.
+ *
+ * The choice is that of exact arithmetic on the given logits and biases, where
+ * fp64 tells the candidates apart; weights are fp32.  The results are what
+ * moe_w4a8_forward_routed and moe_w4a8_forward_bf16_routed take.
+ *
+ * router_logits: [T] rows of n_experts values of logits_dtype (MOE_LOGITS_*),
+ * logits_stride elements apart.  bias: float [n_experts] or null.  topk_ids:
+ * int32 [T][top_k], topk_w: float [T][top_k].  All are 16-byte-aligned device
+ * arrays.  One kernel, no workspace.  MOE_ERR_INVALID_ARG: a null or misaligned
+ * pointer, sizes below one (T below zero), top_k above n_experts or above what
+ * the kept groups hold, n_experts not a multiple of n_groups, topk_groups above
+ * n_groups, group_top not 1 or 2 (2: groups of two experts at least), an unknown
+ * score or dtype, a stride below n_experts, a scale that is not finite.
+ * MOE_ERR_UNSUPPORTED: n_experts > 1024, top_k > 32, n_groups not a power of two
+ * or above 32, T > 2^24.  T = 0 enqueues nothing.
+ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_LOGITS_FP32 0
+#define MOE_LOGITS_BF16 1
+#define MOE_LOGITS_FP16 2
+
+typedef struct {
+    int64_t n_experts, top_k;
+    int64_t score;  /* MOE_SCORE_* */
+    int64_t n_groups, topk_groups; /* 1, 1: no groups */
+    int64_t group_top;             /* 1 or 2 */
+    int64_t renormalise;
+    float scale;
+} moe_route_rule_t;
+
+int moe_w4a8_route_scored(const moe_route_rule_t* rule, int64_t n_tokens, const void* router_logits, int64_t logits_stride,
+                          int64_t logits_dtype, const float* bias, int32_t* topk_ids, float* topk_w, void* stream);
+
+/*
  * The layer with its intermediates exposed, for checking: with engine =
  * MOE_ENGINE_AUTO it runs exactly the kernels of moe_w4a8_forward (another
  * engine value forces that engine; MOE_ERR_UNSUPPORTED if the sizes do not
@@ -353,6 +401,18 @@ int moe_w4a8_forward_bf16(const uint16_t* x_bf16, const float* router_logits,
                           const uint8_t* w2_packed, const float* w2_scale,
                           const moe_dims_t* d, float* out,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_w4a8_forward_bf16 with the routing supplied by the caller (see
+ * moe_w4a8_forward_routed for topk_ids and topk_w): the step of a layer whose
+ * router is moe_w4a8_route_scored.  Workspace, other arguments and errors as for
+ * moe_w4a8_forward_bf16.
+ */
+int moe_w4a8_forward_bf16_routed(const uint16_t* x_bf16, const int32_t* topk_ids, const float* topk_w,
+                                 const uint8_t* w13_packed, const float* w13_scale,
+                                 const uint8_t* w2_packed, const float* w2_scale,
+                                 const moe_dims_t* d, float* out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * The layer on a mixed 2/4-bit bank (the page's mixed W2/W4 expert
