@@ -23,8 +23,8 @@
 // that are not there and rows past the last visible one read zeros, and rows behind it inside a box are cleared by hand.  Work
 // is dealt in equal shares of 64-key units; the pieces of a cut tile go through the workspace and the join.
 //
-// Warps: 0 MMA issue (one lane) and the tensor-memory allocation, 1 the keys, 2 and 3 the queries, 4 to 7 softmax and
-// output.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
+// Warps: 0 the products S and the tensor-memory allocation, 3 the products O, each issued by one lane, so that neither waits
+// for what the other needs; 1 the keys, 2 the queries, 4 to 7 softmax and output.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
 // its own copies in flight.  The softmax warps meet at a barrier once per tile, whatever became of their waits, and leave
 // together.
 #include <algorithm>
@@ -56,7 +56,7 @@ struct LatCfg {
     static constexpr int kOffPairs = kOffP + kP;
     static constexpr int kOffTails = kOffPairs + kPairs * kPair;
     static constexpr int kOffBars = kOffTails + kTails * kBlock;
-    static constexpr int kBars = 2 * kPairs + 2 * kTails + 9;
+    static constexpr int kBars = 2 * kPairs + 2 * kTails + 12;
     static constexpr int kOffAt = (kOffBars + 8 * kBars + 15) & ~15;   // [ROWS] where an output row begins
     static constexpr int kOffFactor = kOffAt + 8 * ROWS;               // [ROWS] what O's rows are multiplied by
     static constexpr int kOffMisc = kOffFactor + 4 * ROWS;
@@ -130,7 +130,7 @@ __device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int warp
 
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
-    attend_latent_kernel(const LatentArgs a, int box_rows, const __grid_constant__ CUtensorMap map) {
+    attend_latent_kernel(const LatentArgs a, int box_rows, int q_rows, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
     using C = LatCfg<ROWS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* full_p = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [pairs] the bytes have landed
@@ -138,13 +138,14 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
     uint64_t* full_t = empty_p + C::kPairs;  // [tails]
     uint64_t* empty_t = full_t + C::kTails;  // [tails]
     uint64_t* s_full = empty_t + C::kTails;  // [2] MMA commit: S is there
-    uint64_t* p_full = s_full + 2;           // the softmax warps: P is there, S is read
+    uint64_t* s_free = s_full + 2;           // [2] the softmax warps: S is read
+    uint64_t* p_full = s_free + 2;           // the softmax warps: P is there, O rescaled
     uint64_t* o_done = p_full + 1;           // MMA commit: the tile's O is added, P is read
     uint64_t* o_free = o_done + 1;           // the softmax warps: the piece's O is read
-    uint64_t* q_full = o_free + 1;           // the two warps of the queries
+    uint64_t* q_full = o_free + 1;           // the queries are there
     uint64_t* q_free = q_full + 1;           // MMA commit: the piece's last S is there
     uint64_t* cut_in = q_free + 1;           // the bytes of a tile that is cleared by hand
-    uint64_t* done = cut_in + 1;             // MMA commit: everything issued has finished
+    uint64_t* done = cut_in + 1;             // [2] MMA commit: everything that S's, O's warp issued has finished
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
     int* odd = abort_flag + 1;               // some row of a whole tile ended with a NaN
@@ -167,15 +168,17 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
             mbar_init(full_t + i, 1);
             mbar_init(empty_t + i, 1);
         }
-        mbar_init(s_full, 1);
-        mbar_init(s_full + 1, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(s_free + i, 4);
+            mbar_init(done + i, 1);
+        }
         mbar_init(p_full, 4);
         mbar_init(o_done, 1);
         mbar_init(o_free, 4);
-        mbar_init(q_full, 2);
+        mbar_init(q_full, 1);
         mbar_init(q_free, 1);
         mbar_init(cut_in, 1);
-        mbar_init(done, 1);
         *abort_flag = *odd = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -190,91 +193,94 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
     fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = __shfl_sync(~0u, *tmem_holder, 0);
     const int pairs = (kv.d + 127) / 128;        // of a key: 128 components each, the latent part's last one may reach behind it
     const bool tail = a.dk > 128 * pairs;        // components behind the pairs
     bool ok = true;
 
+    auto wait = [&](uint64_t* bar, uint32_t phase) { return ok = __all_sync(~0u, ok && wait_bar(bar, phase, ctl)); };
+
     if (warp == 0) {
-        if (elect_one()) {
-            // ------------------------------------------------------------ MMA issue, by one lane
-            const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(smem_u32(smem + C::kOffPairs)), td = sdesc(smem_u32(smem + C::kOffTails));
-            const uint64_t vd = sdesc_mn(smem_u32(smem + C::kOffPairs), C::kBlock), pd = sdesc(smem_u32(smem + C::kOffP));
-            Place<C::kPairs> sp, vp;             // the next pair of S, of O
-            Place<C::kTails> st;
-            uint32_t ts = 0, to = 0, items = 0;  // tiles so far whose S, whose O is issued; pieces
-            while (ok && c.u < c.end) {
-                const int n = c.take;
-                int js = 0, part = 0, jo = 0;    // the tile whose S is next and its next part; the one whose O is next
-                uint64_t t0 = 0;
-                for (uint32_t idle = 0; jo < n;) {
-                    bool did = false;
-                    if (jo < js && mbar_test(p_full, to & 1) && (jo > 0 || mbar_test(o_free, (items & 1) ^ 1))) {
-                        tc_fence_after();
-                        for (int x = 0; x < pairs; ++x) {
+        // ---------------------------------------------------------------- S = Q X^T, part by part as the key's parts arrive
+        const bool leader = elect_one();
+        const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(smem_u32(smem + C::kOffPairs)), td = sdesc(smem_u32(smem + C::kOffTails));
+        Place<C::kPairs> kp;
+        Place<C::kTails> tp;
+        uint32_t t = 0, items = 0;           // tiles and pieces so far
+        while (ok && c.u < c.end) {
+            const int n = c.take;
+            if (!wait(q_full, items & 1)) break;
+            for (int j = 0; j < n; ++j, ++t) {
+                const uint32_t buf = t & 1, s_col = tmem + C::kSCol + kLatKeys * buf;
+                if (!wait(s_free + buf, (t >> 1 & 1) ^ 1)) break;
+                for (int x = 0; x < pairs; ++x) {
+                    if (!wait(full_p + kp.slot, kp.phase)) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t q = qd + ((2 * x * C::kQBlock) >> 4), k = kd + ((kp.slot * C::kPair) >> 4);
 #pragma unroll
-                            for (int k = 0; k < kLatKeys / 16; ++k)
-                                mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, vd + ((vp.slot * C::kPair + k * 2048) >> 4), pd + ((k * 32) >> 4),
-                                              idesc16<T>(128, ROWS, false, true), jo > 0 || k > 0);
-                            mma_commit<1>(empty_p + vp.slot);
-                            vp.next();
-                        }
-                        mma_commit<1>(o_done);
-                        ++jo;
-                        ++to;
-                        did = true;
-                    } else if (js < n && js <= jo + 1 && (js > 0 || part > 0 || mbar_test(q_full, items & 1)) &&
-                               mbar_test(part < pairs ? full_p + sp.slot : full_t + st.slot, part < pairs ? sp.phase : st.phase)) {
-                        // (S of tile js goes where S of tile js - 2 was, which is read when that one's P is there)
-                        tc_fence_after();
-                        const uint64_t qp = qd + ((2 * part * C::kQBlock) >> 4);
-                        const uint64_t kp = part < pairs ? kd + ((sp.slot * C::kPair) >> 4) : td + ((st.slot * C::kBlock) >> 4);
-                        const uint32_t s_col = tmem + C::kSCol + kLatKeys * (ts & 1);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_f16_ss<1>(s_col, qp + k * 2, kp + k * 2, idesc16<T>(64, kLatKeys, false), part > 0 || k > 0);
-                        if (part < pairs) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f16_ss<1>(s_col, qp + (C::kQBlock >> 4) + k * 2, kp + (C::kBlock >> 4) + k * 2, idesc16<T>(64, kLatKeys, false), 1);
-                            sp.next();
-                        } else {
-                            mma_commit<1>(empty_t + st.slot);
-                            st.next();
-                        }
-                        if (++part == pairs + tail) {
-                            mma_commit<1>(s_full + (ts & 1));
-                            part = 0;
-                            ++ts;
-                            if (++js == n) mma_commit<1>(q_free);
-                        }
-                        did = true;
+                        for (int i = 0; i < 8; ++i)
+                            mma_f16_ss<1>(s_col, q + (i / 4 * C::kQBlock >> 4) + i % 4 * 2, k + (i / 4 * C::kBlock >> 4) + i % 4 * 2,
+                                          idesc16<T>(64, kLatKeys, false), x > 0 || i > 0);
                     }
-                    if (did) {
-                        idle = 0;
-                        t0 = 0;
-                    } else if (++idle % 64 == 0) {
-                        if (*ctl.abort) {
-                            ok = false;
-                            break;
-                        }
-                        const uint64_t now = global_ns();
-                        if (t0 == 0) {
-                            t0 = now;
-                        } else if (now - t0 > kWaitNs) {
-                            *ctl.abort = 1;
-                            atomicOr(&ctl.hdr->status, kDevTimeout);
-                            ok = false;
-                            break;
-                        }
-                    }
+                    __syncwarp();
+                    kp.next();
                 }
-                ++items;
-                deal_next<ROWS, kLatKeys>(a, c);
+                if (ok && tail && wait(full_t + tp.slot, tp.phase)) {
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t q = qd + ((2 * pairs * C::kQBlock) >> 4), k = td + ((tp.slot * C::kBlock) >> 4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_f16_ss<1>(s_col, q + i * 2, k + i * 2, idesc16<T>(64, kLatKeys, false), 1);
+                        mma_commit<1>(empty_t + tp.slot);
+                    }
+                    __syncwarp();
+                    tp.next();
+                }
+                if (!ok) break;
+                if (leader) {
+                    mma_commit<1>(s_full + buf);
+                    if (j + 1 == n) mma_commit<1>(q_free);
+                }
+                __syncwarp();
             }
-            mma_commit<1>(done);
-            drain_bar(done, 0, global_ns() + kWaitNs);
+            ++items;
+            deal_next<ROWS, kLatKeys>(a, c);
         }
+        if (leader) mma_commit<1>(done);
         __syncwarp();
+        drain_bar(done, 0, global_ns() + kWaitNs);
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- O^T += X^T P^T
+        const bool leader = elect_one();
+        const uint64_t vd = sdesc_mn(smem_u32(smem + C::kOffPairs), C::kBlock), pd = sdesc(smem_u32(smem + C::kOffP));
+        Place<C::kPairs> vp;
+        uint32_t t = 0, items = 0;
+        while (ok && c.u < c.end) {
+            const int n = c.take;
+            for (int j = 0; j < n; ++j, ++t) {
+                if (!wait(p_full, t & 1) || (j == 0 && !wait(o_free, (items & 1) ^ 1))) break;
+                tc_fence_after();
+                for (int x = 0; x < pairs; ++x) {
+                    if (leader) {
+                        const uint64_t v = vd + ((vp.slot * C::kPair) >> 4);
+#pragma unroll
+                        for (int k = 0; k < kLatKeys / 16; ++k)
+                            mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, v + (k * 2048 >> 4), pd + (k * 32 >> 4), idesc16<T>(128, ROWS, false, true), j > 0 || k > 0);
+                        mma_commit<1>(empty_p + vp.slot);
+                    }
+                    __syncwarp();
+                    vp.next();
+                }
+                if (leader) mma_commit<1>(o_done);
+                __syncwarp();
+            }
+            ++items;
+            deal_next<ROWS, kLatKeys>(a, c);
+        }
+        if (leader) mma_commit<1>(done + 1);
+        __syncwarp();
+        drain_bar(done + 1, 0, global_ns() + kWaitNs);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- the keys
         Place<C::kPairs> pp;
@@ -361,23 +367,41 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
             drain_bar(full_t + u % C::kTails, (u / C::kTails) & 1, end);
             drain_bar(empty_t + u % C::kTails, (u / C::kTails) & 1, end);
         }
-    } else if (warp < 4) {
-        // ---------------------------------------------------------------- the queries, half of the rows each
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- the queries
         uint32_t items = 0;
-        const int chunks = (2 * pairs + tail) * 8;  // of a row, zeros past its components
+        const int blocks = 2 * pairs + tail;        // of 64 components, zeros past the row's
         while (ok && c.u < c.end) {
-            ok = __all_sync(~0u, wait_bar(q_free, (items & 1) ^ 1, ctl));
-            if (!ok) break;
+            if (!wait(q_free, (items & 1) ^ 1)) break;
             ++items;
             const int r0 = c.rt * ROWS, rows = min(c.s.q_len * kv.group - r0, ROWS);
-            for (int r = (warp - 2) * (ROWS / 2); r < (warp - 1) * (ROWS / 2); ++r) {
+            if (q_rows) {  // a box of ROWS rows for each block; rows past the sequence's are whatever follows
+                if (lane == 0) {
+                    int tok, head;
+                    row_of(kv, r0, tok, head);
+                    mbar_expect_tx(own_bar(q_full), blocks * C::kQBlock);
+                    const int y = q_rows == 1 ? (c.s.q0 + tok) * kv.group + head : head, z = q_rows == 1 ? 0 : c.s.q0 + tok;
+                    for (int x = 0; x < blocks; ++x) tma_tile3d<1>(smem_u32(smem + C::kOffQ) + x * C::kQBlock, &qmap, 64 * x, y, z, own_bar(q_full));
+                }
+                __syncwarp();
+                deal_next<ROWS, kLatKeys>(a, c);
+                continue;
+            }
+            // where the rows begin: each lane finds its rows' places once, then passes them round
+            for (int g = 0; g < ROWS; g += 32) {
                 int tok, head;
-                row_of(kv, r0 + min(r, rows - 1), tok, head);
-                const T* src = static_cast<const T*>(a.q) + (c.s.q0 + tok) * a.q_ts + head * a.q_hs;
-                uint8_t* dst = smem + C::kOffQ + r * 128;
-                for (int x = lane; x < chunks; x += 32) {
-                    const bool in = r < rows && x * 8 < a.dk;
-                    cp_async16(dst + (x / 8) * C::kQBlock + (((x & 7) ^ (r & 7)) << 4), src + (in ? x * 8 : 0), in ? 16 : 0);
+                row_of(kv, r0 + max(min(g + lane, rows - 1), 0), tok, head);
+                const int64_t at = static_cast<int64_t>(c.s.q0 + tok) * a.q_ts + head * a.q_hs;
+#pragma unroll 1
+                for (int i = 0; i < min(ROWS - g, 32); i += 4) {  // 8 lanes a row, the blocks one after another
+                    const int64_t from = __shfl_sync(~0u, at, i + lane / 8);
+                    const int r = g + i + lane / 8, x = lane & 7;
+                    uint8_t* dst = smem + C::kOffQ + r * 128 + ((x ^ (r & 7)) << 4);
+#pragma unroll 3
+                    for (int y = 0; y < blocks; ++y) {
+                        const bool in = r < rows && y * 64 + x * 8 < a.dk;
+                        cp_async16(dst + y * C::kQBlock, static_cast<const T*>(a.q) + (in ? from + y * 64 + x * 8 : 0), in ? 16 : 0);
+                    }
                 }
             }
             cp_async_commit();
@@ -387,7 +411,10 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
             if (lane == 0) mbar_arrive(own_bar(q_full));
             deal_next<ROWS, kLatKeys>(a, c);
         }
-        if (items) drain_bar(q_free, (items - 1) & 1, global_ns() + kWaitNs);  // (its arrival, too, has come)
+        if (items) {  // (its arrival, too, has come; after a timeout the queries may still be on their way)
+            drain_bar(q_full, (items - 1) & 1, global_ns() + kWaitNs);
+            drain_bar(q_free, (items - 1) & 1, global_ns() + kWaitNs);
+        }
     } else {
         // ---------------------------------------------------------------- softmax and output
         const int w = warp - 4;                   // S: rows 16 w ..; O^T: components 32 w .. of each 128
@@ -419,6 +446,11 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                     tmem_ld_frag(tmem + lane_base + C::kSCol + kLatKeys * (t & 1), v);
                     tmem_ld_wait();
                     tmem_tie<32>(v);
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(own_bar(s_free + (t & 1)));
+                if (ok && live) {
                     const int key0 = (c.first + c.off + j) * kLatKeys;
                     if (key0 + kLatKeys - 1 > all) {
 #pragma unroll
@@ -522,8 +554,9 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
             bool bad = false;
             for (int x = 0; x < pairs; ++x) {
                 const int e = 128 * x + 32 * w + lane;    // this thread's component
+                float* dst = a.part_o + part * ROWS * (128 * pairs) + e;
 #pragma unroll 1
-                for (int y = 0; y < rows; y += 16) {
+                for (int y = 0; y < rows; y += 16, dst += 16 * 128 * pairs) {
                     uint32_t o[16];
                     tmem_ld16(tmem + lane_base + C::kOCol + ROWS * x + y, o);
                     tmem_ld_wait();
@@ -532,9 +565,9 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
 #pragma unroll
                         for (int r = 0; r < 16; r += 2) {
                             // two rows: the even lane of a pair writes both lanes' components of the first, the odd lane of the second
-                            if (y + r >= rows) break;
-                            const float f0 = __uint_as_float(o[r]) * factor[y + r], f1 = __uint_as_float(o[r + 1]) * factor[min(y + r + 1, rows - 1)];
-                            bad |= f0 != f0 || (f1 != f1 && y + r + 1 < rows);
+                            const float2 f = *reinterpret_cast<const float2*>(factor + y + r);
+                            const float f0 = __uint_as_float(o[r]) * f.x, f1 = __uint_as_float(o[r + 1]) * f.y;
+                            bad |= (f0 != f0 && y + r < rows) || (f1 != f1 && y + r + 1 < rows);
                             const float got = __shfl_xor_sync(~0u, lane & 1 ? f0 : f1, 1);
                             const int rr = y + r + (lane & 1);
                             if (rr < rows && (e & ~1) < kv.d)
@@ -542,9 +575,10 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                                     lane & 1 ? Elem<T>::pack(got, f1) : Elem<T>::pack(f0, got);
                         }
                     } else {
+                        float* to = dst;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (y + r < rows) a.part_o[(part * ROWS + y + r) * (128 * pairs) + e] = __uint_as_float(o[r]);
+                        for (int r = 0; r < 16; ++r, to += 128 * pairs)  // (rows past the tile's are written, too, and never read)
+                            *to = __uint_as_float(o[r]);
                     }
                 }
             }
@@ -585,7 +619,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
     auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
     const int step = c1 - c0;
-    for (int k = 0; cta - (c0 + 1) + k * step < rows * pairs; k += kJoinWarps / share) {
+    const int each = kJoinWarps / share;  // items of a block at a time; the blocks of a boundary take turns
+    for (int k = blockIdx.y * each; cta - (c0 + 1) + k * step < rows * pairs; k += gridDim.y * each) {
         const int item = cta - (c0 + 1) + (k + (share > 1 ? 0 : warp)) * step;
         const int r = item / pairs, col = item % pairs * 128;
         float mm = kNegInf, ll = 0.f;
@@ -669,17 +704,48 @@ cudaError_t make_map(const LatentArgs& a, int dtype, int box, CUtensorMap* map) 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The queries as a 3-D map (component, head, token), boxes of 64 components x `rows` (token, head) rows: by rows of uniform
+// stride where there is one (returns 1: second coordinate token * heads + head), else where whole heads of a token or whole
+// tokens make a tile (returns 2).  0: no map.
+template <int ROWS>
+int make_qmap(const LatentArgs& a, int dtype, CUtensorMap* map, cudaError_t* err) {
+    const KvArgs& kv = a.kv;
+    const int64_t most = int64_t(1) << 39;
+    const bool heads = kv.hq > 1, tokens = kv.n_tokens > 1;
+    if ((heads && (a.q_hs <= 0 || a.q_hs >= most)) || (tokens && (a.q_ts <= 0 || a.q_ts >= most))) return 0;
+    const bool uniform = !heads || !tokens || a.q_ts == a.q_hs * kv.hq;
+    const int bh = std::min(kv.hq, ROWS);
+    if (!uniform && (ROWS % bh != 0 || kv.hq % bh != 0)) return 0;
+    Encode encode = nullptr;
+    if ((*err = get_encode(&encode)) != cudaSuccess) return 0;
+    const int64_t step = 2 * (heads ? a.q_hs : tokens ? a.q_ts : 8);
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.dk), static_cast<cuuint64_t>(uniform ? int64_t(kv.hq) * kv.n_tokens : kv.hq),
+                                static_cast<cuuint64_t>(uniform ? 1 : kv.n_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(step), static_cast<cuuint64_t>(uniform ? 16 : 2 * a.q_ts)};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(uniform ? ROWS : bh), static_cast<cuuint32_t>(uniform ? 1 : ROWS / bh)};
+    const CUresult r = encode(map, dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(a.q), dims,
+                              strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    *err = r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return uniform ? 1 : 2;
+}
+
 template <typename T, int ROWS>
 cudaError_t launch_r(const LatentArgs& a, int dtype, int n_ctas, cudaStream_t st) {
     using C = LatCfg<ROWS>;
     const int box = std::min(a.kv.page & -a.kv.page, kLatKeys);
     CUtensorMap map;
     if (cudaError_t e = make_map(a, dtype, box, &map); e != cudaSuccess) return e;
-    cudaError_t e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    CUtensorMap qmap = map;
+    cudaError_t e = cudaSuccess;
+    const int q_rows = make_qmap<ROWS>(a, dtype, &qmap, &e);
     if (e != cudaSuccess) return e;
-    e = launch_in_stream(attend_latent_kernel<T, ROWS>, dim3(n_ctas), C::kThreads, C::kSmem, 1, st, a, box, map);
+    e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_in_stream(attend_latent_kernel<T, ROWS>, dim3(n_ctas), C::kThreads, C::kSmem, 1, st, a, box, q_rows, map, qmap);
     if (e != cudaSuccess || !a.split || n_ctas < 2) return e;
-    return launch_in_stream(latent_join_kernel<T, ROWS>, dim3(n_ctas - 1), kJoinWarps * 32, 0, 1, st, a);
+    return launch_in_stream(latent_join_kernel<T, ROWS>, dim3(n_ctas - 1, ROWS / 4), kJoinWarps * 32, 0, 1, st, a);
 }
 
 template <typename T>
