@@ -18,10 +18,14 @@
 // A softmax thread has the matrix-fragment places of S (two rows, 16 keys each), four lanes a row.  P goes to shared memory in
 // 16 bits.  The reference m is raised, and O rescaled, only when a row's maximum has grown by more than 2^8 over it.
 //
-// The keys' tile is a ring of pairs of 64-component blocks (a pair is what one product of 128 components reads) and a
-// ring of tail blocks (the components behind the last pair); a pair is free as soon as its part of O^T is issued.  Pages
-// that are not there and rows past the last visible one read zeros, and rows behind it inside a box are cleared by hand.  Work
-// is dealt in equal shares of 64-key units; the pieces of a cut tile go through the workspace and the join.
+// The keys come eight rows at a time with all their components, 9 KB that lie side by side in the cache, so that what DRAM opens
+// is read at once (boxes of 64 components x 64 rows stream at 3.3 TB/s, these at 5.6).  In shared memory such a group is
+// [block of 64 components][row], a swizzle atom each, so a product finds its next eight keys a group further, its next 64
+// components a KB further.  The ring has two units, free again in slots of 16 keys as O's products pass them.  From
+// 65 rows on two CTAs with 64 rows each share the units: each brings half of a unit into both (TMA multicast).
+// Pages that are not there and rows past the last visible one read zeros, and rows behind it inside a group are
+// cleared by hand.  Work is dealt in equal shares of 64-key units; the pieces of a cut tile go through the workspace and the
+// join.
 //
 // Warps: 0 the products S and the tensor-memory allocation, 3 the products O, each issued by one lane, so that neither waits
 // for what the other needs; 1 the keys, 2 the queries, 4 to 7 softmax and output.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
@@ -35,28 +39,31 @@
 namespace moe {
 namespace {
 
-constexpr int kLatKeys = 64;  // keys of a unit
-constexpr int kMinShare = 2;  // units of a CTA at least, where there are few
-constexpr int kExtra = 2;     // units that a tile's beginning and end count for
+constexpr int kLatKeys = 64;   // keys of a unit
+constexpr int kSlotKeys = 16;  // keys of a slot of the ring, which holds two units
+constexpr int kSlots = 2 * kLatKeys / kSlotKeys;
+constexpr int kMinShare = 2;   // units of a CTA at least, where there are few
+constexpr int kExtra = 2;      // units that a tile's beginning and end count for
 constexpr int kJoinWarps = 8;
 
-template <int ROWS>
+// ROWS rows of a CTA, CL CTAs that share a tile of keys.
+template <int ROWS, int CL>
 struct LatCfg {
-    static constexpr int kBlock = kLatKeys * 128, kPair = 2 * kBlock;  // bytes
-    static constexpr int kQBlock = ROWS * 128;                         // ROWS queries of 64 components
-    static constexpr int kQ = (2 * kMaxLatent / 128 + 1) * kQBlock;
+    static constexpr int kTile = ROWS * CL;                      // rows of a tile
+    static constexpr int kBlocks = (kMaxLatent + kMaxLatentRot) / 64;
+    static constexpr int kQBlock = ROWS * 128;                   // bytes: ROWS queries of 64 components
+    static constexpr int kQ = kBlocks * kQBlock;
     static constexpr int kP = ROWS * 128;
-    static constexpr int kPairs = ROWS == 64 ? 8 : ROWS == 32 ? 10 : 11, kTails = ROWS == 64 ? 2 : 3;
+    static constexpr int kRing = kSlots * kSlotKeys * kBlocks * 128;
     static constexpr int kThreads = 256;
     static constexpr int kOCol = 0, kSCol = 4 * ROWS, kCols = 512;
     static constexpr int kOffQ = 0;
     // (S is of 64 rows of Q: where ROWS is less, the MMA reads what lies behind them, at most 6 KB behind Q's end, into
     // rows of S that are never looked at)
     static constexpr int kOffP = kQ;
-    static constexpr int kOffPairs = kOffP + kP;
-    static constexpr int kOffTails = kOffPairs + kPairs * kPair;
-    static constexpr int kOffBars = kOffTails + kTails * kBlock;
-    static constexpr int kBars = 2 * kPairs + 2 * kTails + 12;
+    static constexpr int kOffRing = kOffP + kP;
+    static constexpr int kOffBars = kOffRing + kRing;
+    static constexpr int kBars = kSlots + 15;
     static constexpr int kOffAt = (kOffBars + 8 * kBars + 15) & ~15;   // [ROWS] where an output row begins
     static constexpr int kOffFactor = kOffAt + 8 * ROWS;               // [ROWS] what O's rows are multiplied by
     static constexpr int kOffMisc = kOffFactor + 4 * ROWS;
@@ -64,7 +71,6 @@ struct LatCfg {
     static constexpr int kSmem = kOffStart + sizeof(Cursor);
     static_assert(kSCol + 2 * kLatKeys <= kCols, "tensor-memory columns");
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert(kPairs >= kMaxLatent / 128, "a tile of keys fits the ring");
 };
 
 // 16 lanes x 64 columns of 32 bits, as the accumulator fragments of eight 16 x 8 matrices (no wait).
@@ -92,22 +98,63 @@ __device__ __forceinline__ bool softmax_any(bool x) {
     return r != 0;
 }
 
-// A place in a ring of N slots, and the phase of its barrier.
-template <int N>
-struct Place {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == N) slot = 0, phase ^= 1;
+// Shared-memory matrix descriptor, 128-byte swizzle: 8-row groups `group` bytes apart; across (an operand that is read across its
+// rows): the next 64 values `across` bytes on.
+__device__ __forceinline__ uint64_t sdesc_groups(uint32_t saddr, uint32_t group, uint32_t across = 16) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | static_cast<uint64_t>(across >> 4) << 16 | static_cast<uint64_t>(group >> 4) << 32 |
+           static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
+// Arrivals on the CTA's own barriers.
+__device__ __forceinline__ void arrive_own(uint64_t* bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory"); }
+__device__ __forceinline__ void arrive_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// Bytes to come, without an arrival.
+__device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// One arrival on `bar` of both CTAs of a pair when every MMA issued so far has finished (CL = 1: on the CTA's own).
+template <int CL>
+__device__ __forceinline__ void commit_all(uint64_t* bar) {
+    if constexpr (CL == 1) mma_commit<1>(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(smem_u32(bar)),
+                     "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
+// Eight rows of the cache, all their 64-component blocks, [block][row] -> shared memory; counted on `bar`.  WIDE: a box
+// has all blocks (rows of whole blocks), else one box each.  BOTH: into both CTAs of a pair, counted on each one's barrier.
+template <bool BOTH>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, bool wide, int blocks, int row, int page, uint32_t bar) {
+    const uint64_t m = reinterpret_cast<uint64_t>(map);
+    if (wide) {
+        if constexpr (BOTH)
+            asm volatile(
+                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, %4, %5}], [%6], "
+                "%7;\n" ::"r"(dst), "l"(m), "r"(0), "r"(row), "r"(0), "r"(page), "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+        else
+            tma_tile4d<1>(dst, map, 0, row, 0, page, bar);
+        return;
     }
-};
+    for (int b = 0; b < blocks; ++b) {
+        if constexpr (BOTH)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], "
+                "%6;\n" ::"r"(dst + b * 1024), "l"(m), "r"(64 * b), "r"(row), "r"(page), "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+        else
+            tma_tile3d<1>(dst + b * 1024, map, 64 * b, row, page, bar);
+    }
+}
 
 // The rows of the CTA's whole tiles that ended with a NaN, taken again one by one by the softmax warps.
-template <typename T, int ROWS>
-__device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int warp) {
+template <typename T, int ROWS, int CL>
+__device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int rank, int warp) {
+    constexpr int kTile = ROWS * CL;
     const int lane = threadIdx.x & 31;
     while (c.u < c.end) {
-        const int r0 = c.rt * ROWS;
+        const int r0 = c.rt * kTile + ROWS * rank;
         const int rows = c.whole() ? min(c.s.q_len * a.kv.group - r0, ROWS) : 0;
         for (int r = warp; r < rows; r += 4) {
             int tok, head;
@@ -124,27 +171,25 @@ __device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int warp
             }
             if (__any_sync(~0u, odd)) latent_row<T>(a, c.b, c.s.q0 + tok, head, c.s.pos0 + tok);
         }
-        deal_next<ROWS, kLatKeys>(a, c);
+        deal_next<kTile, kLatKeys>(a, c);
     }
 }
 
-template <typename T, int ROWS>
-__global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
-    attend_latent_kernel(const LatentArgs a, int box_rows, int q_rows, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
-    using C = LatCfg<ROWS>;
+template <typename T, int ROWS, int CL>
+__global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
+    attend_latent_kernel(const LatentArgs a, int wide, int q_rows, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
+    using C = LatCfg<ROWS, CL>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t* full_p = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [pairs] the bytes have landed
-    uint64_t* empty_p = full_p + C::kPairs;  // [pairs] MMA commit: the pair is read
-    uint64_t* full_t = empty_p + C::kPairs;  // [tails]
-    uint64_t* empty_t = full_t + C::kTails;  // [tails]
-    uint64_t* s_full = empty_t + C::kTails;  // [2] MMA commit: S is there
+    uint64_t* empty = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [slots] MMA commit of each CTA: the slot is read
+    uint64_t* full = empty + kSlots;         // [2] the unit's bytes have landed
+    uint64_t* s_full = full + 2;             // [2] MMA commit: S is there
     uint64_t* s_free = s_full + 2;           // [2] the softmax warps: S is read
     uint64_t* p_full = s_free + 2;           // the softmax warps: P is there, O rescaled
-    uint64_t* o_done = p_full + 1;           // MMA commit: the tile's O is added, P is read
+    uint64_t* o_done = p_full + 1;           // MMA commit: the unit's O is added, P is read
     uint64_t* o_free = o_done + 1;           // the softmax warps: the piece's O is read
     uint64_t* q_full = o_free + 1;           // the queries are there
     uint64_t* q_free = q_full + 1;           // MMA commit: the piece's last S is there
-    uint64_t* cut_in = q_free + 1;           // the bytes of a tile that is cleared by hand
+    uint64_t* cut_in = q_free + 1;           // the bytes of eight rows that are cleared by hand
     uint64_t* done = cut_in + 1;             // [2] MMA commit: everything that S's, O's warp issued has finished
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
@@ -160,15 +205,9 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < C::kPairs; ++i) {
-            mbar_init(full_p + i, 1);
-            mbar_init(empty_p + i, 1);
-        }
-        for (int i = 0; i < C::kTails; ++i) {
-            mbar_init(full_t + i, 1);
-            mbar_init(empty_t + i, 1);
-        }
+        for (int i = 0; i < kSlots; ++i) mbar_init(empty + i, CL);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(full + i, 1);
             mbar_init(s_full + i, 1);
             mbar_init(s_free + i, 4);
             mbar_init(done + i, 1);
@@ -185,67 +224,48 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
     if (warp == 0) tmem_alloc<1>(tmem_holder, C::kCols);
     wait_for_stream();
     if (blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
+    const int rank = CL == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CL;
     Cursor c;
-    deal_begin<ROWS, kLatKeys>(a, reinterpret_cast<long long*>(smem + C::kOffPairs), kMinShare, kExtra, blockIdx.x, gridDim.x, c);  // (scratch: the ring)
+    deal_begin<C::kTile, kLatKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), kMinShare, kExtra, me, gridDim.x / CL, c);  // (scratch: the ring)
     if (tid == 0) *reinterpret_cast<Cursor*>(smem + C::kOffStart) = c;
     clear_stray_rows<T>(a);  // (kv.d is what the outputs have)
     tc_fence_before();
     fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
     __syncthreads();
+    if constexpr (CL == 2) cluster_sync();  // the peer's barriers are there
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(~0u, *tmem_holder, 0);
-    const int pairs = (kv.d + 127) / 128;        // of a key: 128 components each, the latent part's last one may reach behind it
-    const bool tail = a.dk > 128 * pairs;        // components behind the pairs
+    const int blocks = (a.dk + 63) / 64;         // of a row of the cache, 64 components each
+    const int parts = (kv.d + 127) / 128;        // of the latent part: 128 components each, the last may reach behind it
+    const uint32_t group = blocks * 1024, slot = 2 * group;  // bytes of eight rows, of a slot of the ring
     bool ok = true;
-
     auto wait = [&](uint64_t* bar, uint32_t phase) { return ok = __all_sync(~0u, ok && wait_bar(bar, phase, ctl)); };
 
     if (warp == 0) {
-        // ---------------------------------------------------------------- S = Q X^T, part by part as the key's parts arrive
+        // ---------------------------------------------------------------- S = Q X^T
         const bool leader = elect_one();
-        const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc(smem_u32(smem + C::kOffPairs)), td = sdesc(smem_u32(smem + C::kOffTails));
-        Place<C::kPairs> kp;
-        Place<C::kTails> tp;
-        uint32_t t = 0, items = 0;           // tiles and pieces so far
+        const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc_groups(smem_u32(smem + C::kOffRing), group);
+        uint32_t t = 0, items = 0;           // units and pieces so far
         while (ok && c.u < c.end) {
             const int n = c.take;
             if (!wait(q_full, items & 1)) break;
             for (int j = 0; j < n; ++j, ++t) {
                 const uint32_t buf = t & 1, s_col = tmem + C::kSCol + kLatKeys * buf;
-                if (!wait(s_free + buf, (t >> 1 & 1) ^ 1)) break;
-                for (int x = 0; x < pairs; ++x) {
-                    if (!wait(full_p + kp.slot, kp.phase)) break;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint64_t q = qd + ((2 * x * C::kQBlock) >> 4), k = kd + ((kp.slot * C::kPair) >> 4);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            mma_f16_ss<1>(s_col, q + (i / 4 * C::kQBlock >> 4) + i % 4 * 2, k + (i / 4 * C::kBlock >> 4) + i % 4 * 2,
-                                          idesc16<T>(64, kLatKeys, false), x > 0 || i > 0);
-                    }
-                    __syncwarp();
-                    kp.next();
-                }
-                if (ok && tail && wait(full_t + tp.slot, tp.phase)) {
-                    tc_fence_after();
-                    if (leader) {
-                        const uint64_t q = qd + ((2 * pairs * C::kQBlock) >> 4), k = td + ((tp.slot * C::kBlock) >> 4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f16_ss<1>(s_col, q + i * 2, k + i * 2, idesc16<T>(64, kLatKeys, false), 1);
-                        mma_commit<1>(empty_t + tp.slot);
-                    }
-                    __syncwarp();
-                    tp.next();
-                }
-                if (!ok) break;
+                if (!wait(s_free + buf, (t >> 1 & 1) ^ 1) || !wait(full + buf, t >> 1 & 1)) break;
+                tc_fence_after();
                 if (leader) {
+                    uint64_t q = qd, k = kd + ((4 * buf * slot) >> 4);
+                    for (int x = 0; x < blocks; ++x, q += C::kQBlock >> 4, k += 1024 >> 4) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_f16_ss<1>(s_col, q + 2 * i, k + 2 * i, idesc16<T>(64, kLatKeys, false), x > 0 || i > 0);
+                    }
                     mma_commit<1>(s_full + buf);
                     if (j + 1 == n) mma_commit<1>(q_free);
                 }
                 __syncwarp();
             }
             ++items;
-            deal_next<ROWS, kLatKeys>(a, c);
+            deal_next<C::kTile, kLatKeys>(a, c);
         }
         if (leader) mma_commit<1>(done);
         __syncwarp();
@@ -253,138 +273,114 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
     } else if (warp == 3) {
         // ---------------------------------------------------------------- O^T += X^T P^T
         const bool leader = elect_one();
-        const uint64_t vd = sdesc_mn(smem_u32(smem + C::kOffPairs), C::kBlock), pd = sdesc(smem_u32(smem + C::kOffP));
-        Place<C::kPairs> vp;
+        const uint64_t vd = sdesc_groups(smem_u32(smem + C::kOffRing), group, 1024), pd = sdesc(smem_u32(smem + C::kOffP));
         uint32_t t = 0, items = 0;
         while (ok && c.u < c.end) {
             const int n = c.take;
             for (int j = 0; j < n; ++j, ++t) {
                 if (!wait(p_full, t & 1) || (j == 0 && !wait(o_free, (items & 1) ^ 1))) break;
                 tc_fence_after();
-                for (int x = 0; x < pairs; ++x) {
-                    if (leader) {
-                        const uint64_t v = vd + ((vp.slot * C::kPair) >> 4);
+                if (leader) {
+                    uint64_t v = vd + ((4 * (t & 1) * slot) >> 4);
 #pragma unroll
-                        for (int k = 0; k < kLatKeys / 16; ++k)
-                            mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, v + (k * 2048 >> 4), pd + (k * 32 >> 4), idesc16<T>(128, ROWS, false, true), j > 0 || k > 0);
-                        mma_commit<1>(empty_p + vp.slot);
+                    for (int k = 0; k < kLatKeys / kSlotKeys; ++k, v += slot >> 4) {  // 16 keys, 128 components at a time
+                        for (int x = 0; x < parts; ++x)
+                            mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, v + (x * 2048 >> 4), pd + (k * 32 >> 4), idesc16<T>(128, ROWS, false, true), j > 0 || k > 0);
+                        commit_all<CL>(empty + 4 * (t & 1) + k);
                     }
-                    __syncwarp();
-                    vp.next();
+                    mma_commit<1>(o_done);
                 }
-                if (leader) mma_commit<1>(o_done);
                 __syncwarp();
             }
             ++items;
-            deal_next<ROWS, kLatKeys>(a, c);
+            deal_next<C::kTile, kLatKeys>(a, c);
         }
         if (leader) mma_commit<1>(done + 1);
         __syncwarp();
         drain_bar(done + 1, 0, global_ns() + kWaitNs);
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- the keys
-        Place<C::kPairs> pp;
-        Place<C::kTails> tp;
-        int uses_p = 0, uses_t = 0;  // slots filled so far
-        uint32_t cuts = 0;
-        const uint32_t ring = smem_u32(smem + C::kOffPairs), tring = smem_u32(smem + C::kOffTails);
-        const int boxes = kLatKeys / box_rows;    // of a block, 8 at most
-        const int bx = lane % boxes, blk = lane / boxes;
-        auto claim = [&](uint64_t* empty, uint32_t phase) { return ok = __all_sync(~0u, wait_bar(empty, phase ^ 1, ctl)); };
+        // ---------------------------------------------------------------- the keys: lane i has rows 8 i .. of a unit
+        uint32_t t = 0, cuts = 0;
+        const uint32_t ring = smem_u32(smem + C::kOffRing);
         while (ok && c.u < c.end) {
             int lo, hi;
-            const int r0 = c.rt * ROWS;
-            key_range(kv, 0, c.s, r0, min(r0 + ROWS, c.s.q_len * kv.group), lo, hi);
-            for (int j = 0; j < c.take && ok; ++j) {
-                const int key0 = (c.first + c.off + j) * kLatKeys, key = key0 + bx * box_rows;
+            const int r0 = c.rt * C::kTile;
+            key_range(kv, 0, c.s, r0, min(r0 + C::kTile, c.s.q_len * kv.group), lo, hi);
+            for (int j = 0; j < c.take && ok; ++j, ++t) {
+                const int key0 = (c.first + c.off + j) * kLatKeys, key = key0 + 8 * lane;
                 int page = kv.n_pages, row = 0;   // outside the map: zeros
-                if (key < hi) {
+                if (lane < 8 && key < hi) {
                     const int p = div_by(key, kv.by_page), id = page_id(kv, c.b, p);
                     row = key - p * kv.page;
                     if (id >= 0) page = id;
                 }
                 const int last = hi - key0;       // rows that some row of the tile sees
-                const bool cut = last > 0 && last < kLatKeys && last % box_rows != 0;
-                auto copy = [&](int x, uint32_t dst, int blocks, uint64_t* bar) {
-                    if (lane == 0) mbar_expect_tx(own_bar(bar), blocks * C::kBlock);
-                    __syncwarp();
-                    if (blk < blocks) tma_tile3d<1>(dst + blk * C::kBlock + bx * box_rows * 128, &map, x + 64 * blk, row, page, own_bar(bar));
-                };
-                if (!cut) {
-                    for (int x = 0; x < pairs && claim(empty_p + pp.slot, pp.phase); ++x) {
-                        copy(128 * x, ring + pp.slot * C::kPair, 2, full_p + pp.slot);
-                        pp.next();
-                        ++uses_p;
+                // eight rows of which some are seen: those behind are cleared before the products may read them; in a
+                // pair each CTA brings these for itself
+                const int cut = last > 0 && last < kLatKeys && last % 8 != 0 ? last / 8 : -1;
+                uint64_t* there = full + (t & 1);
+                const uint32_t unit = ring + 4 * (t & 1) * slot;
+                for (int x = 0; x < kLatKeys / kSlotKeys && wait(empty + 4 * (t & 1) + x, (t >> 1 & 1) ^ 1); ++x) {
+                    if (lane == 0) {
+                        if (x > 0) {
+                        } else if (cut < 0) {
+                            arrive_expect(there, 8 * group);
+                        } else {
+                            expect(there, 7 * group);
+                            arrive_expect(cut_in, group);
+                        }
                     }
-                } else {  // the boxes' rows behind the last visible one are cleared before the products may read them
-                    auto q = pp;
-                    for (int x = 0; x < pairs && claim(empty_p + q.slot, q.phase); ++x) q.next();
-                    if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(own_bar(cut_in), pairs * C::kPair);
                     __syncwarp();
-                    q = pp;
-                    for (int x = 0; x < pairs; ++x) {
-                        if (blk < 2)
-                            tma_tile3d<1>(ring + q.slot * C::kPair + blk * C::kBlock + bx * box_rows * 128, &map, 128 * x + 64 * blk, row, page, own_bar(cut_in));
-                        q.next();
+                    if (lane / 2 == x) {
+                        const uint32_t dst = unit + lane * group;
+                        if (lane == cut) load_rows<false>(dst, &map, wide, blocks, row, page, own_bar(cut_in));
+                        else if (CL == 1) load_rows<false>(dst, &map, wide, blocks, row, page, own_bar(there));
+                        else if ((lane & 1) == rank) load_rows<CL == 2>(dst, &map, wide, blocks, row, page, smem_u32(there));
                     }
+                    __syncwarp();
                 }
-                if (ok && tail && claim(empty_t + tp.slot, tp.phase)) {
-                    copy(128 * pairs, tring + tp.slot * C::kBlock, 1, full_t + tp.slot);
-                    tp.next();
-                    ++uses_t;
-                }
-                if (cut) {
-                    // (also when the tail was not to be had: these copies are under way)
+                if (cut >= 0) {
+                    // (also when a slot was not to be had: the copy may be under way)
                     const bool in = __all_sync(~0u, wait_bar(cut_in, cuts & 1, ctl));
                     if (!in) drain_bar(cut_in, cuts & 1, global_ns() + kWaitNs);
+                    ++cuts;
                     ok = ok && in;
                     if (!ok) break;
-                    ++cuts;
-                    const int end = (last + box_rows - 1) / box_rows * box_rows, per = (end - last) * 8;
-                    for (int x = 0; x < pairs; ++x) {
-                        uint8_t* at = smem + C::kOffPairs + pp.slot * C::kPair + last * 128;
-                        for (int y = lane; y < 2 * per; y += 32)
-                            *reinterpret_cast<uint4*>(at + (y >= per ? C::kBlock + (y - per) * 16 : y * 16)) = make_uint4(0, 0, 0, 0);
-                        fence_async_proxy();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(own_bar(full_p + pp.slot));
-                        pp.next();
-                        ++uses_p;
-                    }
+                    const int first = last % 8, per = (8 - first) * 8;
+                    uint8_t* at = smem + C::kOffRing + 4 * (t & 1) * slot + cut * group + first * 128;
+                    for (int x = lane; x < per * blocks; x += 32) *reinterpret_cast<uint4*>(at + x / per * 1024 + x % per * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) arrive_own(there);
                 }
             }
-            deal_next<ROWS, kLatKeys>(a, c);
+            deal_next<C::kTile, kLatKeys>(a, c);
         }
-        // Nothing is on its way to this CTA's memory when it leaves: every slot's last use has landed and been read (or,
-        // after a timeout, the limit has passed).
+        // Nothing is on its way to this CTA's memory when it leaves: the last units have landed and been read (or, after a
+        // timeout, the limit has passed).
         const uint64_t end = global_ns() + kWaitNs;
-        for (int u = max(uses_p - C::kPairs, 0); u < uses_p; ++u) {
-            drain_bar(full_p + u % C::kPairs, (u / C::kPairs) & 1, end);
-            drain_bar(empty_p + u % C::kPairs, (u / C::kPairs) & 1, end);
-        }
-        for (int u = max(uses_t - C::kTails, 0); u < uses_t; ++u) {
-            drain_bar(full_t + u % C::kTails, (u / C::kTails) & 1, end);
-            drain_bar(empty_t + u % C::kTails, (u / C::kTails) & 1, end);
+        const uint32_t units = t + (ok ? 0 : 1);
+        for (uint32_t u = units > 2 ? units - 2 : 0; u < units; ++u) {
+            drain_bar(full + (u & 1), u >> 1 & 1, end);
+            for (int x = 0; x < 4; ++x) drain_bar(empty + 4 * (u & 1) + x, u >> 1 & 1, end);
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------- the queries
         uint32_t items = 0;
-        const int blocks = 2 * pairs + tail;        // of 64 components, zeros past the row's
         while (ok && c.u < c.end) {
             if (!wait(q_free, (items & 1) ^ 1)) break;
             ++items;
-            const int r0 = c.rt * ROWS, rows = min(c.s.q_len * kv.group - r0, ROWS);
+            const int r0 = c.rt * C::kTile + ROWS * rank, rows = min(c.s.q_len * kv.group - r0, ROWS);  // (a pair's second CTA may have none)
             if (q_rows) {  // a box of ROWS rows for each block; rows past the sequence's are whatever follows
                 if (lane == 0) {
                     int tok, head;
                     row_of(kv, r0, tok, head);
-                    mbar_expect_tx(own_bar(q_full), blocks * C::kQBlock);
+                    arrive_expect(q_full, blocks * C::kQBlock);
                     const int y = q_rows == 1 ? (c.s.q0 + tok) * kv.group + head : head, z = q_rows == 1 ? 0 : c.s.q0 + tok;
                     for (int x = 0; x < blocks; ++x) tma_tile3d<1>(smem_u32(smem + C::kOffQ) + x * C::kQBlock, &qmap, 64 * x, y, z, own_bar(q_full));
                 }
                 __syncwarp();
-                deal_next<ROWS, kLatKeys>(a, c);
+                deal_next<C::kTile, kLatKeys>(a, c);
                 continue;
             }
             // where the rows begin: each lane finds its rows' places once, then passes them round
@@ -408,8 +404,8 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
             cp_async_wait<0>();
             fence_async_proxy();
             __syncwarp();
-            if (lane == 0) mbar_arrive(own_bar(q_full));
-            deal_next<ROWS, kLatKeys>(a, c);
+            if (lane == 0) arrive_own(q_full);
+            deal_next<C::kTile, kLatKeys>(a, c);
         }
         if (items) {  // (its arrival, too, has come; after a timeout the queries may still be on their way)
             drain_bar(q_full, (items - 1) & 1, global_ns() + kWaitNs);
@@ -423,12 +419,12 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
         uint32_t t = 0;                           // tiles so far
         while (ok && c.u < c.end) {
             const int n = c.take;
-            const int r0 = c.rt * ROWS, rows = min(c.s.q_len * kv.group - r0, ROWS);
+            const int r0 = c.rt * C::kTile + ROWS * rank, rows = min(c.s.q_len * kv.group - r0, ROWS);  // (a pair's second CTA may have none)
             const bool live = 16 * w < rows;
             int pos[2];                           // of this thread's rows: 16 w + lane / 4, and 8 on
 #pragma unroll
-            for (int x = 0; x < 2; ++x) pos[x] = min(c.s.pos0 + div_by(r0 + min(16 * w + lane / 4 + 8 * x, rows - 1), kv.by_group), kv.cap - 1);
-            const int all = min(c.s.pos0 + div_by(r0 + min(16 * w, rows - 1), kv.by_group), kv.cap - 1);  // every row of the warp sees keys <= all
+            for (int x = 0; x < 2; ++x) pos[x] = min(c.s.pos0 + div_by(r0 + max(min(16 * w + lane / 4 + 8 * x, rows - 1), 0), kv.by_group), kv.cap - 1);
+            const int all = min(c.s.pos0 + div_by(r0 + max(min(16 * w, rows - 1), 0), kv.by_group), kv.cap - 1);  // every row of the warp sees keys <= all
             if (tid - 128 < rows) {
                 int tok, head;
                 row_of(kv, r0 + tid - 128, tok, head);
@@ -449,7 +445,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(own_bar(s_free + (t & 1)));
+                if (ok && lane == 0) arrive_own(s_free + (t & 1));
                 if (ok && live) {
                     const int key0 = (c.first + c.off + j) * kLatKeys;
                     if (key0 + kLatKeys - 1 > all) {
@@ -487,7 +483,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                         if (ok) {
                             tc_fence_after();
 #pragma unroll 1
-                            for (int x = 0; x < pairs * ROWS; x += 16) {
+                            for (int x = 0; x < parts * ROWS; x += 16) {
                                 uint32_t o[16];
                                 tmem_ld16(tmem + lane_base + C::kOCol + x, o);
                                 tmem_ld_wait();
@@ -521,7 +517,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(own_bar(p_full));
+                if (ok && lane == 0) arrive_own(p_full);
             }
             if (ok) ok = __all_sync(~0u, wait_bar(o_done, (t & 1) ^ 1, ctl));
             if (softmax_any(!ok)) {
@@ -531,7 +527,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
             // ------------------------------------------------------------ the tile's output
             tc_fence_after();
             const bool whole = c.whole();
-            const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (c.u == c.begin ? 0 : 1);
+            const int64_t part0 = (2 * static_cast<int64_t>(me) + (c.u == c.begin ? 0 : 1)) * C::kTile + ROWS * rank;  // its first row among the pieces'
             if (live) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -542,7 +538,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                     factor[r] = l[x] == 0.f ? 0.f : 1.f / l[x];
                     if (l[x] != l[x]) *odd = 1;
                     if (!whole) {
-                        a.part_ml[part * ROWS + r] = make_float2(m[x] == kNegInf ? kNegInf : m[x] * sc, l[x]);
+                        a.part_ml[part0 + r] = make_float2(m[x] == kNegInf ? kNegInf : m[x] * sc, l[x]);
                     } else if (a.lse) {
                         int tok, head;
                         row_of(kv, r0 + r, tok, head);
@@ -552,11 +548,11 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
             }
             softmax_sync();
             bool bad = false;
-            for (int x = 0; x < pairs; ++x) {
+            for (int x = 0; x < parts; ++x) {
                 const int e = 128 * x + 32 * w + lane;    // this thread's component
-                float* dst = a.part_o + part * ROWS * (128 * pairs) + e;
+                float* dst = a.part_o + part0 * (128 * parts) + e;
 #pragma unroll 1
-                for (int y = 0; y < rows; y += 16, dst += 16 * 128 * pairs) {
+                for (int y = 0; y < rows; y += 16, dst += 16 * 128 * parts) {
                     uint32_t o[16];
                     tmem_ld16(tmem + lane_base + C::kOCol + ROWS * x + y, o);
                     tmem_ld_wait();
@@ -567,7 +563,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                             // two rows: the even lane of a pair writes both lanes' components of the first, the odd lane of the second
                             const float2 f = *reinterpret_cast<const float2*>(factor + y + r);
                             const float f0 = __uint_as_float(o[r]) * f.x, f1 = __uint_as_float(o[r + 1]) * f.y;
-                            bad |= (f0 != f0 && y + r < rows) || (f1 != f1 && y + r + 1 < rows);
+                            bad |= e < kv.d && ((f0 != f0 && y + r < rows) || (f1 != f1 && y + r + 1 < rows));
                             const float got = __shfl_xor_sync(~0u, lane & 1 ? f0 : f1, 1);
                             const int rr = y + r + (lane & 1);
                             if (rr < rows && (e & ~1) < kv.d)
@@ -577,7 +573,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                     } else {
                         float* to = dst;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r, to += 128 * pairs)  // (rows past the tile's are written, too, and never read)
+                        for (int r = 0; r < 16; ++r, to += 128 * parts)  // (rows past the tile's are written, too, and never read)
                             *to = __uint_as_float(o[r]);
                     }
                 }
@@ -585,14 +581,15 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
             tc_fence_before();
             if (bad) *odd = 1;
             softmax_sync();                           // (`factor` and `row_at` are read)
-            if (lane == 0) mbar_arrive(own_bar(o_free));
-            deal_next<ROWS, kLatKeys>(a, c);
+            if (lane == 0) arrive_own(o_free);
+            deal_next<C::kTile, kLatKeys>(a, c);
         }
-        if (ok && *odd) retake_rows<T, ROWS>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), w);
+        if (ok && *odd) retake_rows<T, ROWS, CL>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w);
     }
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (CL == 2) cluster_sync();  // nothing of the peer's comes any more
     if (warp == 0) {
         tc_fence_after();
         tmem_free<1>(tmem, C::kCols);
@@ -675,7 +672,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
         int i, head;
         row_of(kv, r0 + r, i, head);
         const int tok = rec.q0 + i;
-        const bool bad = ll != ll || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w;
+        // (what lies behind the latent part may be anything)
+        const bool bad = ll != ll || (col + 4 * lane < kv.d && (acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w));
         if (__any_sync(~0u, bad)) {
             latent_row<T>(a, rec.b, tok, head, rec.pos0 + i, col, col + 128);
             continue;
@@ -688,19 +686,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     }
 }
 
-// The cache [pages][page_size][Dc + R] as a 3-D map (component, row, page), boxes of 64 components x `box` rows in
-// 128-byte-swizzled rows.  Anything outside reads zeros: components past the row's, the page past the last.
-cudaError_t make_map(const LatentArgs& a, int dtype, int box, CUtensorMap* map) {
+// The cache [pages][page_size][Dc + R], eight rows at a time in 128-byte-swizzled rows of 64 components.  Rows of whole blocks of
+// 64: a 4-D map (component, row, block, page), a box has the rows' every block; else a 3-D map (component, row, page) and a box a
+// block, which leaves out what lies behind a row's end.  The page past the last reads zeros.
+cudaError_t make_map(const LatentArgs& a, int dtype, bool wide, CUtensorMap* map) {
     Encode encode = nullptr;
     if (cudaError_t e = get_encode(&encode); e != cudaSuccess) return e;
     const KvArgs& kv = a.kv;
-    const cuuint32_t elem[3] = {1, 1, 1};
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.dk), static_cast<cuuint64_t>(kv.page), static_cast<cuuint64_t>(kv.n_pages)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * kv.k_rs), static_cast<cuuint64_t>(kv.n_pages > 1 ? 2 * kv.k_ps : 16)};
-    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 1};
-    const CUresult r = encode(map, dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, kv.k, dims, strides, boxes, elem,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t row = 2 * kv.k_rs, page = kv.n_pages > 1 ? 2 * kv.k_ps : 16, n_rows = kv.page, n_pages = kv.n_pages, blocks = a.dk / 64;
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    const cuuint64_t dims4[4] = {64, n_rows, blocks, n_pages}, strides4[3] = {row, 128, page};
+    const cuuint32_t boxes4[4] = {64, 8, static_cast<cuuint32_t>(blocks), 1};
+    const cuuint64_t dims3[3] = {static_cast<cuuint64_t>(a.dk), n_rows, n_pages}, strides3[2] = {row, page};
+    const cuuint32_t boxes3[3] = {64, 8, 1};
+    const CUresult r = encode(map, dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wide ? 4 : 3, kv.k, wide ? dims4 : dims3,
+                              wide ? strides4 : strides3, wide ? boxes4 : boxes3, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -731,28 +732,30 @@ int make_qmap(const LatentArgs& a, int dtype, CUtensorMap* map, cudaError_t* err
     return uniform ? 1 : 2;
 }
 
-template <typename T, int ROWS>
+template <typename T, int ROWS, int CL>
 cudaError_t launch_r(const LatentArgs& a, int dtype, int n_ctas, cudaStream_t st) {
-    using C = LatCfg<ROWS>;
-    const int box = std::min(a.kv.page & -a.kv.page, kLatKeys);
+    using C = LatCfg<ROWS, CL>;
+    const bool wide = a.dk % 64 == 0;
     CUtensorMap map;
-    if (cudaError_t e = make_map(a, dtype, box, &map); e != cudaSuccess) return e;
+    if (cudaError_t e = make_map(a, dtype, wide, &map); e != cudaSuccess) return e;
     CUtensorMap qmap = map;
     cudaError_t e = cudaSuccess;
     const int q_rows = make_qmap<ROWS>(a, dtype, &qmap, &e);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_in_stream(attend_latent_kernel<T, ROWS>, dim3(n_ctas), C::kThreads, C::kSmem, 1, st, a, box, q_rows, map, qmap);
-    if (e != cudaSuccess || !a.split || n_ctas < 2) return e;
-    return launch_in_stream(latent_join_kernel<T, ROWS>, dim3(n_ctas - 1, ROWS / 4), kJoinWarps * 32, 0, 1, st, a);
+    const int groups = n_ctas / CL;
+    e = launch_in_stream(attend_latent_kernel<T, ROWS, CL>, dim3(groups * CL), C::kThreads, C::kSmem, CL, st, a, wide ? 1 : 0, q_rows, map, qmap);
+    if (e != cudaSuccess || !a.split || groups < 2) return e;
+    return launch_in_stream(latent_join_kernel<T, C::kTile>, dim3(groups - 1, C::kTile / 4), kJoinWarps * 32, 0, 1, st, a);
 }
 
 template <typename T>
 cudaError_t launch_t(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
-    if (rows <= 16) return launch_r<T, 16>(a, dtype, n_ctas, st);
-    if (rows <= 32) return launch_r<T, 32>(a, dtype, n_ctas, st);
-    return launch_r<T, 64>(a, dtype, n_ctas, st);
+    if (rows <= 16) return launch_r<T, 16, 1>(a, dtype, n_ctas, st);
+    if (rows <= 32) return launch_r<T, 32, 1>(a, dtype, n_ctas, st);
+    if (rows <= 64 || n_ctas < 2) return launch_r<T, 64, 1>(a, dtype, n_ctas, st);
+    return launch_r<T, 64, 2>(a, dtype, n_ctas, st);
 }
 
 }  // namespace
