@@ -39,22 +39,24 @@
 namespace moe {
 namespace {
 
-constexpr int kLatKeys = 64;   // keys of a unit
-constexpr int kSlotKeys = 16;  // keys of a slot of the ring, which holds two units
-constexpr int kSlots = 2 * kLatKeys / kSlotKeys;
-constexpr int kMinShare = 2;   // units of a CTA at least, where there are few
-constexpr int kExtra = 2;      // units that a tile's beginning and end count for
+constexpr int kSlotKeys = 32;  // keys of a slot of the ring
+constexpr int kMinShare = 128; // keys of a CTA at least, where there are few
+constexpr int kExtra = 128;    // keys that a tile's beginning and end count for
 constexpr int kJoinWarps = 8;
 
-// ROWS rows of a CTA, CL CTAs that share a tile of keys.
-template <int ROWS, int CL>
+// ROWS rows of a CTA, CL CTAs that share a tile of keys, which come in units of KEYS.
+template <int ROWS, int CL, int KEYS>
 struct LatCfg {
     static constexpr int kTile = ROWS * CL;                      // rows of a tile
     static constexpr int kBlocks = (kMaxLatent + kMaxLatentRot) / 64;
+    static constexpr int kSlots = KEYS / kSlotKeys;              // of a unit
+    static constexpr int kUnits = (ROWS == 64 ? 4 : 5) / kSlots; // of the ring
+    static constexpr int kS = 128 / KEYS;                        // buffers of S: units that S may be ahead
+    static constexpr int kPs = 64 / KEYS;                        // buffers of P, side by side in rows of 128 bytes
     static constexpr int kQBlock = ROWS * 128;                   // bytes: ROWS queries of 64 components
     static constexpr int kQ = kBlocks * kQBlock;
     static constexpr int kP = ROWS * 128;
-    static constexpr int kRing = kSlots * kSlotKeys * kBlocks * 128;
+    static constexpr int kRing = kUnits * KEYS * kBlocks * 128;
     static constexpr int kThreads = 256;
     static constexpr int kOCol = 0, kSCol = 4 * ROWS, kCols = 512;
     static constexpr int kOffQ = 0;
@@ -63,26 +65,34 @@ struct LatCfg {
     static constexpr int kOffP = kQ;
     static constexpr int kOffRing = kOffP + kP;
     static constexpr int kOffBars = kOffRing + kRing;
-    static constexpr int kBars = kSlots + 15;
+    static constexpr int kBars = kUnits * (kSlots + 1) + 2 * kS + 2 * kPs + 6;
     static constexpr int kOffAt = (kOffBars + 8 * kBars + 15) & ~15;   // [ROWS] where an output row begins
     static constexpr int kOffFactor = kOffAt + 8 * ROWS;               // [ROWS] what O's rows are multiplied by
     static constexpr int kOffMisc = kOffFactor + 4 * ROWS;
     static constexpr int kOffStart = kOffMisc + 16;                    // the cursor at the share's beginning
     static constexpr int kSmem = kOffStart + sizeof(Cursor);
-    static_assert(kSCol + 2 * kLatKeys <= kCols, "tensor-memory columns");
+    static_assert(kSCol + kS * KEYS <= kCols, "tensor-memory columns");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// 16 lanes x 64 columns of 32 bits, as the accumulator fragments of eight 16 x 8 matrices (no wait).
+// 16 lanes x KEYS columns of 32 bits, as the accumulator fragments of 16 x 8 matrices (no wait).
+template <int KEYS>
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr));
+    if constexpr (KEYS == 64)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+            "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+              "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+              "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+              "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+            : "r"(taddr));
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+              "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+            : "r"(taddr));
 }
 
 // Barrier 1 of the 128 softmax threads: plain, or with the OR of a predicate.
@@ -97,6 +107,16 @@ __device__ __forceinline__ bool softmax_any(bool x) {
                  : "=r"(r) : "r"(static_cast<uint32_t>(x)) : "memory");
     return r != 0;
 }
+
+// A place in a ring of N, and the phase of its barrier.
+template <int N>
+struct Place {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) slot = 0, phase ^= 1;
+    }
+};
 
 // Shared-memory matrix descriptor, 128-byte swizzle: 8-row groups `group` bytes apart; across (an operand that is read across its
 // rows): the next 64 values `across` bytes on.
@@ -149,7 +169,7 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, 
 }
 
 // The rows of the CTA's whole tiles that ended with a NaN, taken again one by one by the softmax warps.
-template <typename T, int ROWS, int CL>
+template <typename T, int ROWS, int CL, int KEYS>
 __device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int rank, int warp) {
     constexpr int kTile = ROWS * CL;
     const int lane = threadIdx.x & 31;
@@ -171,22 +191,22 @@ __device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int rank
             }
             if (__any_sync(~0u, odd)) latent_row<T>(a, c.b, c.s.q0 + tok, head, c.s.pos0 + tok);
         }
-        deal_next<kTile, kLatKeys>(a, c);
+        deal_next<kTile, KEYS>(a, c);
     }
 }
 
-template <typename T, int ROWS, int CL>
-__global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
+template <typename T, int ROWS, int CL, int KEYS>
+__global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
     attend_latent_kernel(const LatentArgs a, int wide, int q_rows, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
-    using C = LatCfg<ROWS, CL>;
+    using C = LatCfg<ROWS, CL, KEYS>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t* empty = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [slots] MMA commit of each CTA: the slot is read
-    uint64_t* full = empty + kSlots;         // [2] the unit's bytes have landed
-    uint64_t* s_full = full + 2;             // [2] MMA commit: S is there
-    uint64_t* s_free = s_full + 2;           // [2] the softmax warps: S is read
-    uint64_t* p_full = s_free + 2;           // the softmax warps: P is there, O rescaled
-    uint64_t* o_done = p_full + 1;           // MMA commit: the unit's O is added, P is read
-    uint64_t* o_free = o_done + 1;           // the softmax warps: the piece's O is read
+    uint64_t* empty = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [slots of the ring] MMA commit of each CTA: the slot is read
+    uint64_t* full = empty + C::kUnits * C::kSlots;  // [units of the ring] the unit's bytes have landed
+    uint64_t* s_full = full + C::kUnits;     // [kS] MMA commit: S is there
+    uint64_t* s_free = s_full + C::kS;       // [kS] the softmax warps: S is read
+    uint64_t* p_full = s_free + C::kS;       // [kPs] the softmax warps: P is there, O rescaled
+    uint64_t* o_done = p_full + C::kPs;      // [kPs] MMA commit: the unit's O is added, P is read
+    uint64_t* o_free = o_done + C::kPs;      // the softmax warps: the piece's O is read
     uint64_t* q_full = o_free + 1;           // the queries are there
     uint64_t* q_free = q_full + 1;           // MMA commit: the piece's last S is there
     uint64_t* cut_in = q_free + 1;           // the bytes of eight rows that are cleared by hand
@@ -205,19 +225,22 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) mbar_init(empty + i, CL);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(full + i, 1);
+        for (int i = 0; i < C::kUnits * C::kSlots; ++i) mbar_init(empty + i, CL);
+        for (int i = 0; i < C::kUnits; ++i) mbar_init(full + i, 1);
+        for (int i = 0; i < C::kS; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(s_free + i, 4);
-            mbar_init(done + i, 1);
         }
-        mbar_init(p_full, 4);
-        mbar_init(o_done, 1);
+        for (int i = 0; i < C::kPs; ++i) {
+            mbar_init(p_full + i, 4);
+            mbar_init(o_done + i, 1);
+        }
         mbar_init(o_free, 4);
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
         mbar_init(cut_in, 1);
+        mbar_init(done, 1);
+        mbar_init(done + 1, 1);
         *abort_flag = *odd = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -226,7 +249,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
     if (blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
     const int rank = CL == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CL;
     Cursor c;
-    deal_begin<C::kTile, kLatKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), kMinShare, kExtra, me, gridDim.x / CL, c);  // (scratch: the ring)
+    deal_begin<C::kTile, KEYS>(a, reinterpret_cast<long long*>(smem + C::kOffRing), kMinShare / KEYS, kExtra / KEYS, me, gridDim.x / CL, c);  // (scratch: the ring)
     if (tid == 0) *reinterpret_cast<Cursor*>(smem + C::kOffStart) = c;
     clear_stray_rows<T>(a);  // (kv.d is what the outputs have)
     tc_fence_before();
@@ -237,7 +260,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
     const uint32_t tmem = __shfl_sync(~0u, *tmem_holder, 0);
     const int blocks = (a.dk + 63) / 64;         // of a row of the cache, 64 components each
     const int parts = (kv.d + 127) / 128;        // of the latent part: 128 components each, the last may reach behind it
-    const uint32_t group = blocks * 1024, slot = 2 * group;  // bytes of eight rows, of a slot of the ring
+    const uint32_t group = blocks * 1024, unit = KEYS / 8 * group;  // bytes of eight rows, of a unit
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase) { return ok = __all_sync(~0u, ok && wait_bar(bar, phase, ctl)); };
 
@@ -245,27 +268,31 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
         // ---------------------------------------------------------------- S = Q X^T
         const bool leader = elect_one();
         const uint64_t qd = sdesc(smem_u32(smem + C::kOffQ)), kd = sdesc_groups(smem_u32(smem + C::kOffRing), group);
-        uint32_t t = 0, items = 0;           // units and pieces so far
+        Place<C::kUnits> in;
+        Place<C::kS> s;
+        uint32_t items = 0;                  // pieces so far
         while (ok && c.u < c.end) {
             const int n = c.take;
             if (!wait(q_full, items & 1)) break;
-            for (int j = 0; j < n; ++j, ++t) {
-                const uint32_t buf = t & 1, s_col = tmem + C::kSCol + kLatKeys * buf;
-                if (!wait(s_free + buf, (t >> 1 & 1) ^ 1) || !wait(full + buf, t >> 1 & 1)) break;
+            for (int j = 0; j < n; ++j) {
+                if (!wait(s_free + s.slot, s.phase ^ 1) || !wait(full + in.slot, in.phase)) break;
                 tc_fence_after();
                 if (leader) {
-                    uint64_t q = qd, k = kd + ((4 * buf * slot) >> 4);
+                    const uint32_t s_col = tmem + C::kSCol + KEYS * s.slot;
+                    uint64_t q = qd, k = kd + ((in.slot * unit) >> 4);
                     for (int x = 0; x < blocks; ++x, q += C::kQBlock >> 4, k += 1024 >> 4) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f16_ss<1>(s_col, q + 2 * i, k + 2 * i, idesc16<T>(64, kLatKeys, false), x > 0 || i > 0);
+                        for (int i = 0; i < 4; ++i) mma_f16_ss<1>(s_col, q + 2 * i, k + 2 * i, idesc16<T>(64, KEYS, false), x > 0 || i > 0);
                     }
-                    mma_commit<1>(s_full + buf);
+                    mma_commit<1>(s_full + s.slot);
                     if (j + 1 == n) mma_commit<1>(q_free);
                 }
                 __syncwarp();
+                in.next();
+                s.next();
             }
             ++items;
-            deal_next<C::kTile, kLatKeys>(a, c);
+            deal_next<C::kTile, KEYS>(a, c);
         }
         if (leader) mma_commit<1>(done);
         __syncwarp();
@@ -274,95 +301,100 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
         // ---------------------------------------------------------------- O^T += X^T P^T
         const bool leader = elect_one();
         const uint64_t vd = sdesc_groups(smem_u32(smem + C::kOffRing), group, 1024), pd = sdesc(smem_u32(smem + C::kOffP));
-        uint32_t t = 0, items = 0;
+        Place<C::kUnits> in;
+        Place<C::kPs> p;
+        uint32_t items = 0;
         while (ok && c.u < c.end) {
             const int n = c.take;
-            for (int j = 0; j < n; ++j, ++t) {
-                if (!wait(p_full, t & 1) || (j == 0 && !wait(o_free, (items & 1) ^ 1))) break;
+            for (int j = 0; j < n; ++j) {
+                if (!wait(p_full + p.slot, p.phase) || (j == 0 && !wait(o_free, (items & 1) ^ 1))) break;
                 tc_fence_after();
                 if (leader) {
-                    uint64_t v = vd + ((4 * (t & 1) * slot) >> 4);
+                    uint64_t v = vd + ((in.slot * unit) >> 4);
 #pragma unroll
-                    for (int k = 0; k < kLatKeys / kSlotKeys; ++k, v += slot >> 4) {  // 16 keys, 128 components at a time
+                    for (int k = 0; k < KEYS / 16; ++k, v += 2 * group >> 4) {  // 16 keys, 128 components at a time
                         for (int x = 0; x < parts; ++x)
-                            mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, v + (x * 2048 >> 4), pd + (k * 32 >> 4), idesc16<T>(128, ROWS, false, true), j > 0 || k > 0);
-                        commit_all<CL>(empty + 4 * (t & 1) + k);
+                            mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, v + (x * 2048 >> 4), pd + ((p.slot * 64 + k * 32) >> 4), idesc16<T>(128, ROWS, false, true),
+                                          j > 0 || k > 0);
+                        if (k & 1) commit_all<CL>(empty + in.slot * C::kSlots + k / 2);
                     }
-                    mma_commit<1>(o_done);
+                    mma_commit<1>(o_done + p.slot);
                 }
                 __syncwarp();
+                in.next();
+                p.next();
             }
             ++items;
-            deal_next<C::kTile, kLatKeys>(a, c);
+            deal_next<C::kTile, KEYS>(a, c);
         }
         if (leader) mma_commit<1>(done + 1);
         __syncwarp();
         drain_bar(done + 1, 0, global_ns() + kWaitNs);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- the keys: lane i has rows 8 i .. of a unit
-        uint32_t t = 0, cuts = 0;
+        Place<C::kUnits> in;
+        uint32_t uses = 0, cuts = 0;         // units begun so far, those cut
         const uint32_t ring = smem_u32(smem + C::kOffRing);
         while (ok && c.u < c.end) {
             int lo, hi;
             const int r0 = c.rt * C::kTile;
             key_range(kv, 0, c.s, r0, min(r0 + C::kTile, c.s.q_len * kv.group), lo, hi);
-            for (int j = 0; j < c.take && ok; ++j, ++t) {
-                const int key0 = (c.first + c.off + j) * kLatKeys, key = key0 + 8 * lane;
-                int page = kv.n_pages, row = 0;   // outside the map: zeros
-                if (lane < 8 && key < hi) {
-                    const int p = div_by(key, kv.by_page), id = page_id(kv, c.b, p);
-                    row = key - p * kv.page;
-                    if (id >= 0) page = id;
-                }
+            for (int j = 0; j < c.take && ok; ++j) {
+                const int key0 = (c.first + c.off + j) * KEYS, key = key0 + 8 * lane;
+                const int p = div_by(max(key, 0), kv.by_page), row = key - p * kv.page;
+                const bool seen = lane < KEYS / 8 && key < hi && p < kv.width;
+                // (looked at when the slot is free)
+                const int id = seen ? __ldg(kv.table + static_cast<int64_t>(c.b) * kv.width + p) : -1;
                 const int last = hi - key0;       // rows that some row of the tile sees
                 // eight rows of which some are seen: those behind are cleared before the products may read them; in a
                 // pair each CTA brings these for itself
-                const int cut = last > 0 && last < kLatKeys && last % 8 != 0 ? last / 8 : -1;
-                uint64_t* there = full + (t & 1);
-                const uint32_t unit = ring + 4 * (t & 1) * slot;
-                for (int x = 0; x < kLatKeys / kSlotKeys && wait(empty + 4 * (t & 1) + x, (t >> 1 & 1) ^ 1); ++x) {
-                    if (lane == 0) {
-                        if (x > 0) {
-                        } else if (cut < 0) {
-                            arrive_expect(there, 8 * group);
+                const int cut = last > 0 && last < KEYS && last % 8 != 0 ? last / 8 : -1;
+                uint64_t* there = full + in.slot;
+                const uint32_t dst = ring + in.slot * unit + lane * group;
+                ++uses;
+#pragma unroll
+                for (int x = 0; x < C::kSlots; ++x) {
+                    if (!wait(empty + in.slot * C::kSlots + x, in.phase ^ 1)) break;
+                    if (x == 0 && lane == 0) {
+                        if (cut < 0) {
+                            arrive_expect(there, unit);
                         } else {
-                            expect(there, 7 * group);
+                            expect(there, unit - group);
                             arrive_expect(cut_in, group);
                         }
                     }
                     __syncwarp();
-                    if (lane / 2 == x) {
-                        const uint32_t dst = unit + lane * group;
-                        if (lane == cut) load_rows<false>(dst, &map, wide, blocks, row, page, own_bar(cut_in));
-                        else if (CL == 1) load_rows<false>(dst, &map, wide, blocks, row, page, own_bar(there));
-                        else if ((lane & 1) == rank) load_rows<CL == 2>(dst, &map, wide, blocks, row, page, smem_u32(there));
+                    if (lane / 4 == x) {          // outside the map: zeros
+                        const int page = static_cast<unsigned>(id) < static_cast<unsigned>(kv.n_pages) ? id : kv.n_pages, y = seen ? row : 0;
+                        if (lane == cut) load_rows<false>(dst, &map, wide, blocks, y, page, smem_u32(cut_in));
+                        else if (CL == 1 || (lane & 1) == rank) load_rows<CL == 2>(dst, &map, wide, blocks, y, page, smem_u32(there));
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
                 if (cut >= 0) {
                     // (also when a slot was not to be had: the copy may be under way)
-                    const bool in = __all_sync(~0u, wait_bar(cut_in, cuts & 1, ctl));
-                    if (!in) drain_bar(cut_in, cuts & 1, global_ns() + kWaitNs);
+                    const bool got = __all_sync(~0u, wait_bar(cut_in, cuts & 1, ctl));
+                    if (!got) drain_bar(cut_in, cuts & 1, global_ns() + kWaitNs);
                     ++cuts;
-                    ok = ok && in;
+                    ok = ok && got;
                     if (!ok) break;
                     const int first = last % 8, per = (8 - first) * 8;
-                    uint8_t* at = smem + C::kOffRing + 4 * (t & 1) * slot + cut * group + first * 128;
+                    uint8_t* at = smem + C::kOffRing + in.slot * unit + cut * group + first * 128;
                     for (int x = lane; x < per * blocks; x += 32) *reinterpret_cast<uint4*>(at + x / per * 1024 + x % per * 16) = make_uint4(0, 0, 0, 0);
                     fence_async_proxy();
                     __syncwarp();
                     if (lane == 0) arrive_own(there);
                 }
+                in.next();
             }
-            deal_next<C::kTile, kLatKeys>(a, c);
+            deal_next<C::kTile, KEYS>(a, c);
         }
-        // Nothing is on its way to this CTA's memory when it leaves: the last units have landed and been read (or, after a
-        // timeout, the limit has passed).
+        // Nothing is on its way to this CTA's memory when it leaves: the ring's last units have landed and been read (or, after
+        // a timeout, the limit has passed).
         const uint64_t end = global_ns() + kWaitNs;
-        const uint32_t units = t + (ok ? 0 : 1);
-        for (uint32_t u = units > 2 ? units - 2 : 0; u < units; ++u) {
-            drain_bar(full + (u & 1), u >> 1 & 1, end);
-            for (int x = 0; x < 4; ++x) drain_bar(empty + 4 * (u & 1) + x, u >> 1 & 1, end);
+        for (uint32_t u = uses > C::kUnits ? uses - C::kUnits : 0; u < uses; ++u) {
+            drain_bar(full + u % C::kUnits, u / C::kUnits & 1, end);
+            for (int x = 0; x < C::kSlots; ++x) drain_bar(empty + u % C::kUnits * C::kSlots + x, u / C::kUnits & 1, end);
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------- the queries
@@ -380,7 +412,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
                     for (int x = 0; x < blocks; ++x) tma_tile3d<1>(smem_u32(smem + C::kOffQ) + x * C::kQBlock, &qmap, 64 * x, y, z, own_bar(q_full));
                 }
                 __syncwarp();
-                deal_next<C::kTile, kLatKeys>(a, c);
+                deal_next<C::kTile, KEYS>(a, c);
                 continue;
             }
             // where the rows begin: each lane finds its rows' places once, then passes them round
@@ -405,7 +437,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) arrive_own(q_full);
-            deal_next<C::kTile, kLatKeys>(a, c);
+            deal_next<C::kTile, KEYS>(a, c);
         }
         if (items) {  // (its arrival, too, has come; after a timeout the queries may still be on their way)
             drain_bar(q_full, (items - 1) & 1, global_ns() + kWaitNs);
@@ -416,14 +448,16 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
         const int w = warp - 4;                   // S: rows 16 w ..; O^T: components 32 w .. of each 128
         const uint32_t lane_base = static_cast<uint32_t>(32 * w) << 16;
         const float sc = a.scale * kLog2e;
-        uint32_t t = 0;                           // tiles so far
+        Place<C::kS> sb;
+        Place<C::kPs> pb, before;                 // P's place, and that of the unit before
         while (ok && c.u < c.end) {
             const int n = c.take;
             const int r0 = c.rt * C::kTile + ROWS * rank, rows = min(c.s.q_len * kv.group - r0, ROWS);  // (a pair's second CTA may have none)
             const bool live = 16 * w < rows;
             int pos[2];                           // of this thread's rows: 16 w + lane / 4, and 8 on
 #pragma unroll
-            for (int x = 0; x < 2; ++x) pos[x] = min(c.s.pos0 + div_by(r0 + max(min(16 * w + lane / 4 + 8 * x, rows - 1), 0), kv.by_group), kv.cap - 1);
+            for (int x = 0; x < 2; ++x)
+                pos[x] = min(c.s.pos0 + div_by(r0 + max(min(16 * w + lane / 4 + 8 * x, rows - 1), 0), kv.by_group), kv.cap - 1);
             const int all = min(c.s.pos0 + div_by(r0 + max(min(16 * w, rows - 1), 0), kv.by_group), kv.cap - 1);  // every row of the warp sees keys <= all
             if (tid - 128 < rows) {
                 int tok, head;
@@ -432,29 +466,30 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
             }
             float m[2] = {kNegInf, kNegInf};      // the references, in units of S
             float l[2] = {0.f, 0.f};              // this thread's part of the sums
-            for (int j = 0; j < n; ++j, ++t) {
-                if (ok) ok = __all_sync(~0u, wait_bar(s_full + (t & 1), t >> 1 & 1, ctl));
-                uint32_t v[32];
+            for (int j = 0; j < n; ++j) {
+                wait(s_full + sb.slot, sb.phase);
+                uint32_t v[KEYS / 2];
                 float top[2] = {kNegInf, kNegInf};
                 bool grew = false;
                 if (ok && live) {
                     tc_fence_after();
-                    tmem_ld_frag(tmem + lane_base + C::kSCol + kLatKeys * (t & 1), v);
+                    tmem_ld_frag<KEYS>(tmem + lane_base + C::kSCol + KEYS * sb.slot, v);
                     tmem_ld_wait();
-                    tmem_tie<32>(v);
+                    tmem_tie<KEYS / 2>(v);
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (ok && lane == 0) arrive_own(s_free + (t & 1));
+                if (ok && lane == 0) arrive_own(s_free + sb.slot);
+                sb.next();
                 if (ok && live) {
-                    const int key0 = (c.first + c.off + j) * kLatKeys;
-                    if (key0 + kLatKeys - 1 > all) {
+                    const int key0 = (c.first + c.off + j) * KEYS;
+                    if (key0 + KEYS - 1 > all) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < KEYS / 2; ++i)
                             if (key0 + 8 * (i / 4) + 2 * (lane & 3) + (i & 1) > pos[i >> 1 & 1]) v[i] = __float_as_uint(kNegInf);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) top[i >> 1 & 1] = fmaxf(top[i >> 1 & 1], __uint_as_float(v[i]));
+                    for (int i = 0; i < KEYS / 2; ++i) top[i >> 1 & 1] = fmaxf(top[i >> 1 & 1], __uint_as_float(v[i]));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 1));
@@ -479,8 +514,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
                     }
                     if (j > 0) {  // O is rescaled between the products: the one before has to be there
                         softmax_sync();
-                        ok = __all_sync(~0u, wait_bar(o_done, (t & 1) ^ 1, ctl));
-                        if (ok) {
+                        if (wait(o_done + before.slot, before.phase)) {
                             tc_fence_after();
 #pragma unroll 1
                             for (int x = 0; x < parts * ROWS; x += 16) {
@@ -497,7 +531,8 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
                         }
                     }
                 }
-                if (ok && j > 0) ok = __all_sync(~0u, wait_bar(o_done, (t & 1) ^ 1, ctl));  // P before is read
+                // what P's place held before is read (with one place: the unit before's; with two, across pieces, it is known)
+                if (j >= C::kPs) wait(o_done + pb.slot, pb.phase ^ 1);
                 if (ok && live) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -505,21 +540,23 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
                         const int r = 16 * w + lane / 4 + 8 * x;
                         uint8_t* at = smem + C::kOffP + r * 128 + (lane & 3) * 4;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < KEYS / 8; ++i) {
                             const float p0 = exp2_fast(fmaf(__uint_as_float(v[4 * i + 2 * x]), sc, -base));
                             const float p1 = exp2_fast(fmaf(__uint_as_float(v[4 * i + 2 * x + 1]), sc, -base));
                             l[x] += p0 + p1;
                             // the product's operand: 16 bits; the sum l is of the fp32 values
-                            *reinterpret_cast<uint32_t*>(at + ((i ^ (r & 7)) << 4)) = Elem<T>::pack(p0, p1);
+                            *reinterpret_cast<uint32_t*>(at + (((4 * pb.slot + i) ^ (r & 7)) << 4)) = Elem<T>::pack(p0, p1);
                         }
                     }
                     fence_async_proxy();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (ok && lane == 0) arrive_own(p_full);
+                if (ok && lane == 0) arrive_own(p_full + pb.slot);
+                before = pb;
+                pb.next();
             }
-            if (ok) ok = __all_sync(~0u, wait_bar(o_done, (t & 1) ^ 1, ctl));
+            if (ok) wait(o_done + before.slot, before.phase);
             if (softmax_any(!ok)) {
                 ok = false;
                 break;
@@ -582,9 +619,9 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL>::kThreads, 1)
             if (bad) *odd = 1;
             softmax_sync();                           // (`factor` and `row_at` are read)
             if (lane == 0) arrive_own(o_free);
-            deal_next<C::kTile, kLatKeys>(a, c);
+            deal_next<C::kTile, KEYS>(a, c);
         }
-        if (ok && *odd) retake_rows<T, ROWS, CL>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w);
+        if (ok && *odd) retake_rows<T, ROWS, CL, KEYS>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w);
     }
 
     tc_fence_before();
@@ -732,9 +769,9 @@ int make_qmap(const LatentArgs& a, int dtype, CUtensorMap* map, cudaError_t* err
     return uniform ? 1 : 2;
 }
 
-template <typename T, int ROWS, int CL>
+template <typename T, int ROWS, int CL, int KEYS>
 cudaError_t launch_r(const LatentArgs& a, int dtype, int n_ctas, cudaStream_t st) {
-    using C = LatCfg<ROWS, CL>;
+    using C = LatCfg<ROWS, CL, KEYS>;
     const bool wide = a.dk % 64 == 0;
     CUtensorMap map;
     if (cudaError_t e = make_map(a, dtype, wide, &map); e != cudaSuccess) return e;
@@ -742,20 +779,20 @@ cudaError_t launch_r(const LatentArgs& a, int dtype, int n_ctas, cudaStream_t st
     cudaError_t e = cudaSuccess;
     const int q_rows = make_qmap<ROWS>(a, dtype, &qmap, &e);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS, CL, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int groups = n_ctas / CL;
-    e = launch_in_stream(attend_latent_kernel<T, ROWS, CL>, dim3(groups * CL), C::kThreads, C::kSmem, CL, st, a, wide ? 1 : 0, q_rows, map, qmap);
+    e = launch_in_stream(attend_latent_kernel<T, ROWS, CL, KEYS>, dim3(groups * CL), C::kThreads, C::kSmem, CL, st, a, wide ? 1 : 0, q_rows, map, qmap);
     if (e != cudaSuccess || !a.split || groups < 2) return e;
     return launch_in_stream(latent_join_kernel<T, C::kTile>, dim3(groups - 1, C::kTile / 4), kJoinWarps * 32, 0, 1, st, a);
 }
 
 template <typename T>
 cudaError_t launch_t(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
-    if (rows <= 16) return launch_r<T, 16, 1>(a, dtype, n_ctas, st);
-    if (rows <= 32) return launch_r<T, 32, 1>(a, dtype, n_ctas, st);
-    if (rows <= 64 || n_ctas < 2) return launch_r<T, 64, 1>(a, dtype, n_ctas, st);
-    return launch_r<T, 64, 2>(a, dtype, n_ctas, st);
+    if (rows <= 16) return launch_r<T, 16, 1, 32>(a, dtype, n_ctas, st);
+    if (rows <= 32) return launch_r<T, 32, 1, 32>(a, dtype, n_ctas, st);
+    if (rows <= 64 || n_ctas < 2) return launch_r<T, 64, 1, 32>(a, dtype, n_ctas, st);
+    return launch_r<T, 64, 2, 64>(a, dtype, n_ctas, st);
 }
 
 }  // namespace
