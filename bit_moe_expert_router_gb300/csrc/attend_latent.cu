@@ -28,7 +28,8 @@
 // join.
 //
 // Warps: 0 the products S and the tensor-memory allocation, 3 the products O, each issued by one lane, so that neither waits
-// for what the other needs; 1 the keys, 2 the queries, 4 to 7 softmax and output.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
+// for what the other needs; 1 the keys, 2 the queries, 4 to 7 softmax and output, 8 what brings
+// the keys to come into L2.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
 // its own copies in flight.  The softmax warps meet at a barrier once per tile, whatever became of their waits, and leave
 // together.
 #include <algorithm>
@@ -57,7 +58,9 @@ struct LatCfg {
     static constexpr int kQ = kBlocks * kQBlock;
     static constexpr int kP = ROWS * 128;
     static constexpr int kRing = kUnits * KEYS * kBlocks * 128;
-    static constexpr int kThreads = 256;
+    static constexpr bool kPrefetch = CL == 2;
+    static constexpr int kThreads = kPrefetch ? 288 : 256;
+    static constexpr int kAhead = 256 / KEYS;                    // units between the copies and their prefetch into L2
     static constexpr int kOCol = 0, kSCol = 4 * ROWS, kCols = 512;
     static constexpr int kOffQ = 0;
     // (S is of 64 rows of Q: where ROWS is less, the MMA reads what lies behind them, at most 6 KB behind Q's end, into
@@ -144,6 +147,17 @@ __device__ __forceinline__ void commit_all(uint64_t* bar) {
                      "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
+// Eight rows of the cache into L2.
+__device__ __forceinline__ void prefetch_rows(const CUtensorMap* map, bool wide, int blocks, int row, int page) {
+    const uint64_t m = reinterpret_cast<uint64_t>(map);
+    if (wide) {
+        asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n" ::"l"(m), "r"(0), "r"(row), "r"(0), "r"(page) : "memory");
+        return;
+    }
+    for (int b = 0; b < blocks; ++b)
+        asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n" ::"l"(m), "r"(64 * b), "r"(row), "r"(page) : "memory");
+}
+
 // Eight rows of the cache, all their 64-component blocks, [block][row] -> shared memory; counted on `bar`.  WIDE: a box
 // has all blocks (rows of whole blocks), else one box each.  BOTH: into both CTAs of a pair, counted on each one's barrier.
 template <bool BOTH>
@@ -214,6 +228,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
     int* odd = abort_flag + 1;               // some row of a whole tile ended with a NaN
+    volatile uint32_t* begun = reinterpret_cast<uint32_t*>(odd + 1);  // units whose copies are begun
     int64_t* row_at = reinterpret_cast<int64_t*>(smem + C::kOffAt);
     float* factor = reinterpret_cast<float*>(smem + C::kOffFactor);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -242,6 +257,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         mbar_init(done, 1);
         mbar_init(done + 1, 1);
         *abort_flag = *odd = 0;
+        *begun = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 0) tmem_alloc<1>(tmem_holder, C::kCols);
@@ -352,6 +368,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 uint64_t* there = full + in.slot;
                 const uint32_t dst = ring + in.slot * unit + lane * group;
                 ++uses;
+                if (C::kPrefetch && lane == 0) *begun = uses;
 #pragma unroll
                 for (int x = 0; x < C::kSlots; ++x) {
                     if (!wait(empty + in.slot * C::kSlots + x, in.phase ^ 1)) break;
@@ -442,6 +459,27 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         if (items) {  // (its arrival, too, has come; after a timeout the queries may still be on their way)
             drain_bar(q_full, (items - 1) & 1, global_ns() + kWaitNs);
             drain_bar(q_free, (items - 1) & 1, global_ns() + kWaitNs);
+        }
+    } else if (C::kPrefetch && warp == 8) {
+        // ---------------------------------------------------------------- the keys to come, into L2: the ring is too short for DRAM's way
+        uint32_t u = 0;
+        while (c.u < c.end) {
+            int lo, hi;
+            const int r0 = c.rt * C::kTile;
+            key_range(kv, 0, c.s, r0, min(r0 + C::kTile, c.s.q_len * kv.group), lo, hi);
+            for (int j = 0; j < c.take; ++j, ++u) {
+                const int key = (c.first + c.off + j) * KEYS + 8 * lane;
+                const int p = div_by(max(key, 0), kv.by_page);
+                const bool mine = lane < KEYS / 8 && key < hi && p < kv.width && (CL == 1 || (lane & 1) == rank);
+                const int id = mine ? __ldg(kv.table + static_cast<int64_t>(c.b) * kv.width + p) : -1;
+                uint32_t now;
+                while ((now = *begun) + C::kAhead <= u && !*ctl.abort) __nanosleep(50);  // (ends: the loader's waits do)
+                if (*ctl.abort) break;
+                if (now <= u && static_cast<unsigned>(id) < static_cast<unsigned>(kv.n_pages)) prefetch_rows(&map, wide, blocks, key - p * kv.page, id);
+                __syncwarp();
+            }
+            if (*ctl.abort) break;
+            deal_next<C::kTile, KEYS>(a, c);
         }
     } else {
         // ---------------------------------------------------------------- softmax and output
@@ -633,12 +671,14 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
     }
 }
 
-// The join of the pieces of a cut tile.  Block c stands for the boundary before CTA c + 1; the (row, 128 components) items of a
-// tile that several boundaries cut are dealt over their blocks, a warp for an item, or eight that share its pieces where
-// they are many.  The sums' order is that of the pieces' CTAs, so two runs give the same bits.
+// The join of the pieces of a cut tile.  Block (c, y) stands for the boundary before CTA c + 1; the rows of a tile that several
+// boundaries cut are dealt over their blocks.  A warp takes a row, all its components, its pieces' loads two at a time; where the
+// pieces are many, eight warps share those of 128 components of a row.  The sums' order is that of the pieces' CTAs, so two runs
+// give the same bits.
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const LatentArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) latent_join_kernel(const LatentArgs a) {
     wait_for_stream();
+    constexpr int kVec = kMaxLatent / 128;  // fours of components of a lane
     __shared__ float4 part[kJoinWarps][32];
     __shared__ float part_l[kJoinWarps];
     const int cta = blockIdx.x + 1;
@@ -646,80 +686,106 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     if (!rec.cut) return;
     const KvArgs& kv = a.kv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int pairs = (kv.d + 127) / 128;
+    const int parts = (kv.d + 127) / 128;
     const int c0 = static_cast<int>(div_line(rec.begin, rec.per)), c1 = static_cast<int>(div_line(rec.begin + rec.n - 1, rec.per));
-    const int share = c1 - c0 + 1 > 8 ? kJoinWarps : 1;  // warps of an item
-    const int wi = share > 1 ? warp : 0;
     const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
     auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
-    const int step = c1 - c0;
-    const int each = kJoinWarps / share;  // items of a block at a time; the blocks of a boundary take turns
-    for (int k = blockIdx.y * each; cta - (c0 + 1) + k * step < rows * pairs; k += gridDim.y * each) {
-        const int item = cta - (c0 + 1) + (k + (share > 1 ? 0 : warp)) * step;
-        const int r = item / pairs, col = item % pairs * 128;
-        float mm = kNegInf, ll = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-            for (int p = c0 + lane; p <= c1; p += 32) mm = fmaxf(mm, a.part_ml[slot_of(p) * ROWS + r].x);
-            constexpr int kAhead = 8;
-            for (int p0 = c0 + wi; p0 <= c1; p0 += kAhead * share) {
-                float2 v[kAhead];
-                float4 o[kAhead];
-#pragma unroll
-                for (int y = 0; y < kAhead; ++y) {
-                    const int64_t at = slot_of(min(p0 + y * share, c1)) * ROWS + r;
-                    v[y] = a.part_ml[at];
-                    o[y] = reinterpret_cast<const float4*>(a.part_o + at * (128 * pairs) + col)[lane];
-                }
-                if (p0 == c0 + wi) {
-#pragma unroll
-                    for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
-                }
-                const float base = mm == kNegInf ? 0.f : mm;
-#pragma unroll
-                for (int y = 0; y < kAhead; ++y) {
-                    if (p0 + y * share > c1) break;
-                    const float f = exp2_fast(v[y].x - base);
-                    ll += v[y].y * f;
-                    acc.x += o[y].x * f;
-                    acc.y += o[y].y * f;
-                    acc.z += o[y].z * f;
-                    acc.w += o[y].w * f;
-                }
-            }
-        }
-        if (share > 1) {  // (every warp of the block has the same item)
-            __syncthreads();
-            part[warp][lane] = acc;
-            if (lane == 0) part_l[warp] = ll;
-            __syncthreads();
-            if (warp == 0) {
-#pragma unroll
-                for (int w = 1; w < kJoinWarps; ++w) {
-                    const float4 v = part[w][lane];
-                    ll += part_l[w];
-                    acc.x += v.x;
-                    acc.y += v.y;
-                    acc.z += v.z;
-                    acc.w += v.w;
-                }
-            }
-        }
-        if (wi != 0 || r >= rows) continue;
+    const int step = c1 - c0, turn = cta - (c0 + 1);  // boundaries of the tile, and which of them this is
+    auto add = [](float4& to, const float4& x, float f) {
+        to.x += x.x * f;
+        to.y += x.y * f;
+        to.z += x.z * f;
+        to.w += x.w * f;
+    };
+    // Writes a row's components from `col` on, 128 at a time, and with component 0 its lse.
+    auto finish = [&](int r, const float4* acc, int n, int col, float mm, float ll) {
         int i, head;
         row_of(kv, r0 + r, i, head);
         const int tok = rec.q0 + i;
-        // (what lies behind the latent part may be anything)
-        const bool bad = ll != ll || (col + 4 * lane < kv.d && (acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w));
+        bool bad = ll != ll;
+        for (int x = 0; x < n; ++x)  // (what lies behind the latent part may be anything)
+            bad |= col + 128 * x + 4 * lane < kv.d && (acc[x].x != acc[x].x || acc[x].y != acc[x].y || acc[x].z != acc[x].z || acc[x].w != acc[x].w);
         if (__any_sync(~0u, bad)) {
-            latent_row<T>(a, rec.b, tok, head, rec.pos0 + i, col, col + 128);
-            continue;
+            latent_row<T>(a, rec.b, tok, head, rec.pos0 + i, col, col + 128 * n);
+            return;
         }
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        if (col + 4 * lane < kv.d)
-            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col + 4 * lane) =
-                make_uint2(Elem<T>::pack(acc.x * inv, acc.y * inv), Elem<T>::pack(acc.z * inv, acc.w * inv));
+        T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col + 4 * lane;
+        for (int x = 0; x < n; ++x)
+            if (col + 128 * x + 4 * lane < kv.d)
+                *reinterpret_cast<uint2*>(dst + 128 * x) = make_uint2(Elem<T>::pack(acc[x].x * inv, acc[x].y * inv), Elem<T>::pack(acc[x].z * inv, acc[x].w * inv));
         if (lane == 0 && col == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
+    };
+    if (step < 8) {
+        for (int r = turn + step * (blockIdx.y * kJoinWarps + warp); r < rows; r += step * gridDim.y * kJoinWarps) {
+            float mm = kNegInf, ll = 0.f;
+            float4 acc[kVec];
+#pragma unroll
+            for (int x = 0; x < kVec; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = c0; p <= c1; p += 2) {
+                const int64_t at0 = slot_of(p) * ROWS + r, at1 = slot_of(min(p + 1, c1)) * ROWS + r;
+                const bool two = p < c1;
+                float4 o0[kVec], o1[kVec];
+#pragma unroll
+                for (int x = 0; x < kVec; ++x) {
+                    o0[x] = o1[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (x < parts) o0[x] = reinterpret_cast<const float4*>(a.part_o + at0 * (128 * parts) + 128 * x)[lane];
+                    if (x < parts && two) o1[x] = reinterpret_cast<const float4*>(a.part_o + at1 * (128 * parts) + 128 * x)[lane];
+                }
+                const float2 v0 = a.part_ml[at0], v1 = two ? a.part_ml[at1] : make_float2(kNegInf, 0.f);
+                const float top = fmaxf(mm, fmaxf(v0.x, v1.x)), base = top == kNegInf ? 0.f : top;
+                const float f = exp2_fast(mm - base), f0 = exp2_fast(v0.x - base), f1 = exp2_fast(v1.x - base);
+                mm = top;
+                ll = ll * f + v0.y * f0 + v1.y * f1;
+#pragma unroll
+                for (int x = 0; x < kVec; ++x) {
+                    acc[x] = make_float4(acc[x].x * f, acc[x].y * f, acc[x].z * f, acc[x].w * f);
+                    add(acc[x], o0[x], f0);
+                    if (two) add(acc[x], o1[x], f1);
+                }
+            }
+            finish(r, acc, parts, 0, mm, ll);
+        }
+        return;
+    }
+    for (int k = blockIdx.y; turn + k * step < rows * parts; k += gridDim.y) {  // (every warp of the block has the same item)
+        const int item = turn + k * step, r = item / parts, col = item % parts * 128;
+        float mm = kNegInf, ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = c0 + lane; p <= c1; p += 32) mm = fmaxf(mm, a.part_ml[slot_of(p) * ROWS + r].x);
+        constexpr int kNext = 4;
+        for (int p0 = c0 + warp; p0 <= c1; p0 += kNext * kJoinWarps) {
+            float2 v[kNext];
+            float4 o[kNext];
+#pragma unroll
+            for (int y = 0; y < kNext; ++y) {
+                const int64_t at = slot_of(min(p0 + y * kJoinWarps, c1)) * ROWS + r;
+                v[y] = a.part_ml[at];
+                o[y] = reinterpret_cast<const float4*>(a.part_o + at * (128 * parts) + col)[lane];
+            }
+            if (p0 == c0 + warp) {
+#pragma unroll
+                for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
+            }
+            const float base = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+            for (int y = 0; y < kNext; ++y) {
+                if (p0 + y * kJoinWarps > c1) break;
+                const float f = exp2_fast(v[y].x - base);
+                ll += v[y].y * f;
+                add(acc, o[y], f);
+            }
+        }
+        __syncthreads();
+        part[warp][lane] = acc;
+        if (lane == 0) part_l[warp] = ll;
+        __syncthreads();
+        if (warp != 0) continue;
+        for (int w = 1; w < kJoinWarps; ++w) {
+            add(acc, part[w][lane], 1.f);
+            ll += part_l[w];
+        }
+        finish(r, &acc, 1, col, mm, ll);
     }
 }
 
@@ -784,7 +850,7 @@ cudaError_t launch_r(const LatentArgs& a, int dtype, int n_ctas, cudaStream_t st
     const int groups = n_ctas / CL;
     e = launch_in_stream(attend_latent_kernel<T, ROWS, CL, KEYS>, dim3(groups * CL), C::kThreads, C::kSmem, CL, st, a, wide ? 1 : 0, q_rows, map, qmap);
     if (e != cudaSuccess || !a.split || groups < 2) return e;
-    return launch_in_stream(latent_join_kernel<T, C::kTile>, dim3(groups - 1, C::kTile / 4), kJoinWarps * 32, 0, 1, st, a);
+    return launch_in_stream(latent_join_kernel<T, C::kTile>, dim3(groups - 1, C::kTile / kJoinWarps), kJoinWarps * 32, 0, 1, st, a);
 }
 
 template <typename T>
