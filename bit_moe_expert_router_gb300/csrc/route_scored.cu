@@ -63,25 +63,40 @@ struct Lane {
     }
 };
 
-// The choice in fp64: expert of rank `lane` (lane < k).
+// What one expert's choice goes by in fp64: s with its bias if there is one; top, sum: of the softmax (sum 1 where the scores are
+// only compared with one another).
+__device__ __forceinline__ double exact_score(const RouteScoredArgs& a, int64_t row, int e, double top, double sum) {
+    const double x = logit(a, row + e);
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : a.bias ? exp(x - top) / sum : exp(x - top);
+    return a.bias ? s + static_cast<double>(__ldg(a.bias + e)) : s;
+}
+__device__ __noinline__ double exact_sum(const RouteScoredArgs& a, int64_t row, const Lane& me, double top) {
+    double sum = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < me.n; ++i) {
+        const double x = logit(a, row + me.first + i);
+        if (x == x) sum += exp(x - top);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    return sum;
+}
+
+// The whole choice in fp64 (of which a warp does little at a time: about 10 us for 8 experts a lane), where the kernel's shorter
+// ways do not settle it: expert of rank `lane` (lane < k).
 template <int MAXJ>
 __device__ __noinline__ int choose_exactly(const RouteScoredArgs& a, int64_t row) {
     const int lane = threadIdx.x & 31, lanes = 1 << a.lanes_log2;
     const Lane me(a);
     const bool softmax = a.sigmoid == 0, groups = a.topk_groups < a.n_groups;
-    double top = -INFINITY, sum = 0.0;
+    double top = -INFINITY, sum = 1.0;
     if (softmax) {
         float m = -INFINITY;
         for (int i = 0; i < me.n; ++i) m = fmaxf(m, logit(a, row + me.first + i));
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
         top = m;
-        for (int i = 0; i < me.n; ++i) {
-            const double x = logit(a, row + me.first + i);
-            if (x == x) sum += exp(x - top);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (a.bias) sum = exact_sum(a, row, me, top);
     }
     unsigned long long key[MAXJ];
     double b1 = -INFINITY, b2 = -INFINITY;  // the two largest
@@ -92,8 +107,7 @@ __device__ __noinline__ int choose_exactly(const RouteScoredArgs& a, int64_t row
         const double x = logit(a, row + me.first + i);
         double r = x, g = x;
         if (a.bias || (groups && a.group_top == 2)) {
-            const double s = softmax ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x));
-            g = a.bias ? s + static_cast<double>(__ldg(a.bias + me.first + i)) : s;
+            g = exact_score(a, row, me.first + i, top, sum);
             if (a.bias) r = g;
         }
         key[i] = key_of(r);
@@ -143,7 +157,7 @@ __device__ __forceinline__ float sigmoid_of(float x) {
 }
 
 template <int MAXJ>
-__global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const RouteScoredArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, MAXJ <= 8 ? 8 : MAXJ == 16 ? 7 : 4) route_scored_kernel(const __grid_constant__ RouteScoredArgs a) {
     constexpr int kBits = MAXJ == 1 ? 0 : MAXJ == 2 ? 1 : MAXJ == 4 ? 2 : MAXJ == 8 ? 3 : MAXJ == 16 ? 4 : 5;
     const int lane = threadIdx.x & 31, lanes = 1 << a.lanes_log2;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -216,7 +230,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const RouteSc
             }
         }
     }
-    bool doubt = false, kept = true;
+    bool doubt = false, kept = true, settled = true;  // settled: the groups are
+    double esum = 0.0;                                // the softmax's sum in fp64, once it is needed
     if (groups) {
         const bool by_r = a.bias || a.group_top == 2;
         float b1 = -INFINITY, b2 = -INFINITY;
@@ -241,7 +256,49 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const RouteSc
         if (by_r) {
             const float in = key_number(__reduce_min_sync(~0u, kept ? g : ~0u)), out = key_number(__reduce_max_sync(~0u, kept ? 0u : g));
             const float size = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(fabsf(b1) + fabsf(b2))));
-            doubt = !(in - out > 1e-5f * big + 5e-7f * size);
+            const float near = 1e-5f * big + 5e-7f * size;
+            if (!(in - out > near)) {
+                // The groups' values in fp64, of the experts that make them: the largest, and the largest of the others.  Where the next
+                // one is too close to the last of these in a group at the border, the long way.
+                auto largest = [&](int but, float& v) {  // of the group but expert `but`: the first
+                    int e = 1 << 30;
+                    v = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < MAXJ; ++i)
+                        if (i < me.n && me.first + i != but && r[i] > v) v = r[i], e = me.first + i;
+                    for (int o = 1; o < lanes; o <<= 1) {
+                        const float ov = __shfl_xor_sync(~0u, v, o);
+                        const int oe = __shfl_xor_sync(~0u, e, o);
+                        if (ov > v || (ov == v && oe < e)) v = ov, e = oe;
+                    }
+                    return e;
+                };
+                float v1, v2, v3 = -INFINITY;
+                const int e1 = largest(-1, v1), e2 = largest(e1, v2);
+                if (a.group_top == 2) {  // (the third: whatever is below the second and not it)
+#pragma unroll
+                    for (int i = 0; i < MAXJ; ++i)
+                        if (i < me.n && me.first + i != e1 && me.first + i != e2) v3 = fmaxf(v3, r[i]);
+                    for (int o = 1; o < lanes; o <<= 1) v3 = fmaxf(v3, __shfl_xor_sync(~0u, v3, o));
+                }
+                const float value = key_number(g);
+                const bool border = !(value - out > 4.f * near) && !(in - value > 4.f * near);
+                settled = lanes >= a.group_top && !__any_sync(~0u, border && !((a.group_top == 2 ? v2 - v3 : v1 - v2) > near));
+                if (settled) {
+                    if (softmax && a.bias) esum = exact_sum(a, row, me, m);
+                    const int sub = lane & (lanes - 1), e = sub == 0 ? e1 : e2;
+                    double x = -INFINITY;
+                    if (sub < a.group_top && e < (1 << 30)) x = exact_score(a, row, e, m, esum);
+                    if (a.group_top == 2) x += __shfl_xor_sync(~0u, x, 1);
+                    const unsigned long long own = __shfl_sync(~0u, key_of(x), lane - sub);
+                    better = 0;
+                    for (int i = 0; i < a.n_groups; ++i) {
+                        const unsigned long long o = __shfl_sync(~0u, own, i * lanes);
+                        better += o > own || (o == own && i < me.group);
+                    }
+                    kept = better < a.topk_groups;
+                }
+            }
         }
     }
     uint32_t s[MAXJ];
@@ -314,10 +371,46 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const RouteSc
         const bool one = bucket == (lane == 31 ? rest : next) && bucket != 0;
         doubt |= lane < a.k && one && (last || !(xe > next_x || (xe == next_x && next_e > e)));
     }
-    if (__any_sync(~0u, doubt)) {
-        e = lane < a.k ? 0 : -1;
-        const int got = choose_exactly<MAXJ>(a, row);
-        if (lane < a.k) e = got;
+    if (__any_sync(~0u, doubt || !settled)) {
+        // What could be on the list goes to a lane each, is taken in fp64 and put in order.
+        int n = 32;
+        if (settled && a.k < 24) {
+            const float low = __shfl_sync(~0u, a.bias ? se + be : xe, a.k - 1);
+            // (nothing with a key below it can be among the best)
+            const float limit = a.bias ? low - (1e-5f * big + 4.f * MAXJ * 1.2e-7f * fabsf(low)) : low;
+            for (n = a.k + 1; n < 32; ++n) {  // the lanes' lists go on
+                const uint32_t own = s[0] >> kBits, best = __reduce_max_sync(~0u, own);
+                if (best == 0 || !(key_number((best << kBits) + (MAXJ - 1)) >= limit)) break;
+                const int win = __ffs(__ballot_sync(~0u, own == best)) - 1;
+                const int we = __shfl_sync(~0u, me.first + (MAXJ - 1 - static_cast<int>(s[0] & (MAXJ - 1u))), win);
+                if (lane == n) e = we;
+                if (lane == win) {
+#pragma unroll
+                    for (int i = 0; i + 1 < MAXJ; ++i) s[i] = s[i + 1];
+                    s[MAXJ - 1] = 0;
+                }
+            }
+        }
+        int got;
+        if (n < 32) {
+            if (softmax && a.bias && esum == 0.0) esum = exact_sum(a, row, me, m);
+            unsigned long long key = 0;
+            if (e >= 0) key = key_of(a.bias ? exact_score(a, row, e, m, esum) : static_cast<double>(logit(a, row + e)));
+            int rank = 0;
+            for (int i = 0; i < n; ++i) {
+                const unsigned long long o = __shfl_sync(~0u, key, i);
+                const int oe = __shfl_sync(~0u, e, i);
+                rank += o > key || (o == key && oe < e);
+            }
+            __shared__ int places[kWarps][32];
+            int* place = places[threadIdx.x >> 5];
+            if (lane < n && e >= 0) place[rank] = e;
+            __syncwarp();
+            got = lane < a.k ? place[lane] : -1;
+        } else {
+            got = choose_exactly<MAXJ>(a, row);
+        }
+        e = lane < a.k ? got : -1;
         score();
     }
 
