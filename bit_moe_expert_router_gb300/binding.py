@@ -445,34 +445,44 @@ def moe_w4a8_route_scored(router_logits, rule: RouteRule, topk_ids, topk_w, bias
     router_logits [tokens, n_experts] float32, bfloat16 or float16, any token stride; bias [n_experts] float32, added to the
     scores for the choice alone, or None; topk_ids [tokens, top_k] int32, topk_w [tokens, top_k] float32.
     """
+    n, index, k = router_logits.shape[0], router_logits.get_device(), rule.top_k
     dtype = _LOGITS.get(router_logits.dtype)
-    if dtype is None:
+    # (one test on the way of every call; what was wrong is found out in _refuse_route)
+    if not (dtype is not None and index >= 0 and router_logits.shape == (n, rule.n_experts) and router_logits.stride(1) == 1
+            and topk_ids is not None and topk_ids.dtype is torch.int32 and topk_ids.shape == (n, k) and topk_ids.get_device() == index
+            and topk_ids.is_contiguous() and topk_w is not None and topk_w.dtype is torch.float32 and topk_w.shape == (n, k)
+            and topk_w.get_device() == index and topk_w.is_contiguous()
+            and (bias is None or (bias.dtype is torch.float32 and bias.shape == (rule.n_experts,) and bias.get_device() == index and bias.is_contiguous()))):
+        _refuse_route(router_logits, rule, topk_ids, topk_w, bias)
+    stride = router_logits.stride(0)
+    args = (rule._p, n, router_logits.data_ptr(), stride if n > 1 else max(stride, rule.n_experts), dtype,
+            None if bias is None else bias.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr())
+    if torch._C._cuda_getDevice() == index:
+        status = _lib.moe_w4a8_route_scored(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = _lib.moe_w4a8_route_scored(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        raise MoeError("moe_w4a8_route_scored", status)
+
+
+def _refuse_route(router_logits, rule, topk_ids, topk_w, bias):
+    if router_logits.dtype not in _LOGITS:
         raise TypeError(f"router_logits: dtype {router_logits.dtype}, expected one of {list(_LOGITS)}")
     if not router_logits.is_cuda:
         raise ValueError("router_logits must be a CUDA tensor")
-    if router_logits.dim() != 2 or router_logits.shape[1] != rule.n_experts:
-        raise ValueError(f"router_logits: shape {tuple(router_logits.shape)}, expected [tokens, {rule.n_experts}]")
     n = router_logits.shape[0]
-    stride, last = router_logits.stride()
-    if last != 1 and rule.n_experts > 1:
+    if router_logits.shape != (n, rule.n_experts):
+        raise ValueError(f"router_logits: shape {tuple(router_logits.shape)}, expected [tokens, {rule.n_experts}]")
+    if router_logits.stride(1) != 1:
         raise ValueError("router_logits: a token's logits must be contiguous")
-    index = router_logits.get_device()
     for t, name, want, shape in ((topk_ids, "topk_ids", torch.int32, (n, rule.top_k)), (topk_w, "topk_w", torch.float32, (n, rule.top_k)),
                                  (bias, "bias", torch.float32, (rule.n_experts,))):
         if t is None and name == "bias":
             continue
-        if t is None or t.dtype is not want or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-            _need(t, name, want, shape)
+        _need(t, name, want, shape)
+        if t.device != router_logits.device:
             raise ValueError(f"{name} is on {t.device}, router_logits on {router_logits.device}")
-    args = (rule._p, n, router_logits.data_ptr(), stride if n > 1 else max(stride, rule.n_experts), dtype,
-            None if bias is None else bias.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr())
-    if torch._C._cuda_getDevice() == index:
-        status = _load().moe_w4a8_route_scored(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            status = _load().moe_w4a8_route_scored(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status:
-        raise MoeError("moe_w4a8_route_scored", status)
 
 
 def moe_w4a8_forward_routed(x_q, x_scale, topk_ids, topk_w, w13_packed, w13_scale, w2_packed, w2_scale, d: Dims,

@@ -15,7 +15,7 @@
 //   O^T += X^T P^T  turned over: 128 components of the latent part x ROWS rows, four times, A = X along the keys' other
 //                   direction (no transposition is needed), B = P.  The accumulator takes 4 ROWS columns of tensor memory,
 //                   where O of 128 rows x 512 components alone would fill all of it.
-// A softmax thread has the matrix-fragment places of S (two rows, 16 keys each), four lanes a row.  P goes to shared memory in
+// A softmax thread has the matrix-fragment places of S (two rows, KEYS / 8 keys each), four lanes and two warps a row.  P goes to shared memory in
 // 16 bits.  The reference m is raised, and O rescaled, only when a row's maximum has grown by more than 2^8 over it.
 //
 // The keys come eight rows at a time with all their components, 9 KB that lie side by side in the cache, so that what DRAM opens
@@ -28,8 +28,8 @@
 // join.
 //
 // Warps: 0 the products S and the tensor-memory allocation, 3 the products O, each issued by one lane, so that neither waits
-// for what the other needs; 1 the keys, 2 the queries, 4 to 7 softmax and output, 8 what brings
-// the keys to come into L2.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
+// for what the other needs; 1 the keys, 2 the queries, 4 to 11 softmax and output, a warp for half of
+// the keys of 16 rows, 12 what brings the keys to come into L2.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
 // its own copies in flight.  The softmax warps meet at a barrier once per tile, whatever became of their waits, and leave
 // together.
 #include <algorithm>
@@ -59,7 +59,7 @@ struct LatCfg {
     static constexpr int kP = ROWS * 128;
     static constexpr int kRing = kUnits * KEYS * kBlocks * 128;
     static constexpr bool kPrefetch = CL == 2;
-    static constexpr int kThreads = kPrefetch ? 288 : 256;
+    static constexpr int kThreads = kPrefetch ? 416 : 384;
     static constexpr int kAhead = 256 / KEYS;                    // units between the copies and their prefetch into L2
     static constexpr int kOCol = 0, kSCol = 4 * ROWS, kCols = 512;
     static constexpr int kOffQ = 0;
@@ -71,42 +71,39 @@ struct LatCfg {
     static constexpr int kBars = kUnits * (kSlots + 1) + 2 * kS + 2 * kPs + 6;
     static constexpr int kOffAt = (kOffBars + 8 * kBars + 15) & ~15;   // [ROWS] where an output row begins
     static constexpr int kOffFactor = kOffAt + 8 * ROWS;               // [ROWS] what O's rows are multiplied by
-    static constexpr int kOffMisc = kOffFactor + 4 * ROWS;
+    static constexpr int kOffEx = kOffFactor + 4 * ROWS;               // [2][ROWS] what the halves of a row tell one another
+    static constexpr int kOffMisc = kOffEx + 8 * ROWS;
     static constexpr int kOffStart = kOffMisc + 16;                    // the cursor at the share's beginning
     static constexpr int kSmem = kOffStart + sizeof(Cursor);
     static_assert(kSCol + kS * KEYS <= kCols, "tensor-memory columns");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// 16 lanes x KEYS columns of 32 bits, as the accumulator fragments of 16 x 8 matrices (no wait).
-template <int KEYS>
+// 16 lanes x COLS columns of 32 bits, as the accumulator fragments of 16 x 8 matrices (no wait).
+template <int COLS>
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* v) {
-    if constexpr (KEYS == 64)
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-            "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-              "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-              "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-              "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-            : "r"(taddr));
-    else
+    static_assert(COLS == 16 || COLS == 32, "of a warp");
+    if constexpr (COLS == 32)
         asm volatile(
             "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
               "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
             : "r"(taddr));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "r"(taddr));
 }
 
-// Barrier 1 of the 128 softmax threads: plain, or with the OR of a predicate.
+// Barrier 1 of the 256 softmax threads: plain, or with the OR of a predicate.
 __device__ __forceinline__ void softmax_sync() {
     __syncwarp();
-    asm volatile("bar.sync 1, 128;\n" ::: "memory");
+    asm volatile("bar.sync 1, 256;\n" ::: "memory");
 }
 __device__ __forceinline__ bool softmax_any(bool x) {
     uint32_t r;
     __syncwarp();
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
                  : "=r"(r) : "r"(static_cast<uint32_t>(x)) : "memory");
     return r != 0;
 }
@@ -190,7 +187,7 @@ __device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int rank
     while (c.u < c.end) {
         const int r0 = c.rt * kTile + ROWS * rank;
         const int rows = c.whole() ? min(c.s.q_len * a.kv.group - r0, ROWS) : 0;
-        for (int r = warp; r < rows; r += 4) {
+        for (int r = warp; r < rows; r += 8) {
             int tok, head;
             row_of(a.kv, r0 + r, tok, head);
             bool odd = false;
@@ -231,6 +228,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
     volatile uint32_t* begun = reinterpret_cast<uint32_t*>(odd + 1);  // units whose copies are begun
     int64_t* row_at = reinterpret_cast<int64_t*>(smem + C::kOffAt);
     float* factor = reinterpret_cast<float*>(smem + C::kOffFactor);
+    float* ex = reinterpret_cast<float*>(smem + C::kOffEx);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const KvArgs& kv = a.kv;
     const Ctl ctl{abort_flag, a.hdr};
@@ -244,13 +242,13 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         for (int i = 0; i < C::kUnits; ++i) mbar_init(full + i, 1);
         for (int i = 0; i < C::kS; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(s_free + i, 4);
+            mbar_init(s_free + i, 8);
         }
         for (int i = 0; i < C::kPs; ++i) {
-            mbar_init(p_full + i, 4);
+            mbar_init(p_full + i, 8);
             mbar_init(o_done + i, 1);
         }
-        mbar_init(o_free, 4);
+        mbar_init(o_free, 8);
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
         mbar_init(cut_in, 1);
@@ -460,7 +458,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             drain_bar(q_full, (items - 1) & 1, global_ns() + kWaitNs);
             drain_bar(q_free, (items - 1) & 1, global_ns() + kWaitNs);
         }
-    } else if (C::kPrefetch && warp == 8) {
+    } else if (C::kPrefetch && warp == 12) {
         // ---------------------------------------------------------------- the keys to come, into L2: the ring is too short for DRAM's way
         uint32_t u = 0;
         while (c.u < c.end) {
@@ -483,7 +481,9 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         }
     } else {
         // ---------------------------------------------------------------- softmax and output
-        const int w = warp - 4;                   // S: rows 16 w ..; O^T: components 32 w .. of each 128
+        const int w = warp & 3;                   // S: rows 16 w ..; O^T: components 32 w .. of each 128
+        const int half = warp / 4 - 1;            // S: keys KEYS / 2 half ..; O^T: every second 128 components
+        constexpr int kN = KEYS / 4;              // values of S of a thread
         const uint32_t lane_base = static_cast<uint32_t>(32 * w) << 16;
         const float sc = a.scale * kLog2e;
         Place<C::kS> sb;
@@ -506,48 +506,55 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             float l[2] = {0.f, 0.f};              // this thread's part of the sums
             for (int j = 0; j < n; ++j) {
                 wait(s_full + sb.slot, sb.phase);
-                uint32_t v[KEYS / 2];
+                uint32_t v[kN];
                 float top[2] = {kNegInf, kNegInf};
                 bool grew = false;
                 if (ok && live) {
                     tc_fence_after();
-                    tmem_ld_frag<KEYS>(tmem + lane_base + C::kSCol + KEYS * sb.slot, v);
+                    tmem_ld_frag<KEYS / 2>(tmem + lane_base + C::kSCol + KEYS * sb.slot + KEYS / 2 * half, v);
                     tmem_ld_wait();
-                    tmem_tie<KEYS / 2>(v);
+                    tmem_tie<kN>(v);
                     tc_fence_before();
                 }
                 __syncwarp();
                 if (ok && lane == 0) arrive_own(s_free + sb.slot);
                 sb.next();
                 if (ok && live) {
-                    const int key0 = (c.first + c.off + j) * KEYS;
-                    if (key0 + KEYS - 1 > all) {
+                    const int key0 = (c.first + c.off + j) * KEYS + KEYS / 2 * half;
+                    if (key0 + KEYS / 2 - 1 > all) {
 #pragma unroll
-                        for (int i = 0; i < KEYS / 2; ++i)
+                        for (int i = 0; i < kN; ++i)
                             if (key0 + 8 * (i / 4) + 2 * (lane & 3) + (i & 1) > pos[i >> 1 & 1]) v[i] = __float_as_uint(kNegInf);
                     }
 #pragma unroll
-                    for (int i = 0; i < KEYS / 2; ++i) top[i >> 1 & 1] = fmaxf(top[i >> 1 & 1], __uint_as_float(v[i]));
-#pragma unroll
                     for (int x = 0; x < 2; ++x) {
+                        float even = __uint_as_float(v[2 * x]), uneven = __uint_as_float(v[2 * x + 1]);
+#pragma unroll
+                        for (int i = 4; i < kN; i += 4) even = fmaxf(even, __uint_as_float(v[i + 2 * x])), uneven = fmaxf(uneven, __uint_as_float(v[i + 2 * x + 1]));
+                        top[x] = fmaxf(even, uneven);
                         top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 1));
                         top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 2));
                         grew |= (top[x] - m[x]) * sc > 8.f;  // (m = -inf: inf, or NaN if the row has seen nothing yet)
                     }
                 }
-                if (softmax_any(grew || !ok)) {
+                if (softmax_any(grew || !ok)) {  // (of either half of a row: the same for both)
+                    if (live && (lane & 3) == 0) {
+                        ex[ROWS * half + 16 * w + lane / 4] = top[0];
+                        ex[ROWS * half + 16 * w + lane / 4 + 8] = top[1];
+                    }
                     ok = !softmax_any(!ok);
                     if (!ok) break;
                     if (live) {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
+                            top[x] = fmaxf(top[x], ex[ROWS * (half ^ 1) + 16 * w + lane / 4 + 8 * x]);
                             float f = 1.f;
                             if ((top[x] - m[x]) * sc > 8.f) {
                                 f = m[x] == kNegInf ? 0.f : exp2_fast((m[x] - top[x]) * sc);
                                 m[x] = top[x];
                             }
                             l[x] *= f;
-                            if ((lane & 3) == 0) factor[16 * w + lane / 4 + 8 * x] = f;
+                            if ((lane & 3) == 0 && half == 0) factor[16 * w + lane / 4 + 8 * x] = f;
                         }
                     }
                     if (j > 0) {  // O is rescaled between the products: the one before has to be there
@@ -555,7 +562,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                         if (wait(o_done + before.slot, before.phase)) {
                             tc_fence_after();
 #pragma unroll 1
-                            for (int x = 0; x < parts * ROWS; x += 16) {
+                            for (int x = 16 * half; x < parts * ROWS; x += 32) {
                                 uint32_t o[16];
                                 tmem_ld16(tmem + lane_base + C::kOCol + x, o);
                                 tmem_ld_wait();
@@ -578,12 +585,12 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                         const int r = 16 * w + lane / 4 + 8 * x;
                         uint8_t* at = smem + C::kOffP + r * 128 + (lane & 3) * 4;
 #pragma unroll
-                        for (int i = 0; i < KEYS / 8; ++i) {
+                        for (int i = 0; i < KEYS / 16; ++i) {
                             const float p0 = exp2_fast(fmaf(__uint_as_float(v[4 * i + 2 * x]), sc, -base));
                             const float p1 = exp2_fast(fmaf(__uint_as_float(v[4 * i + 2 * x + 1]), sc, -base));
                             l[x] += p0 + p1;
                             // the product's operand: 16 bits; the sum l is of the fp32 values
-                            *reinterpret_cast<uint32_t*>(at + (((4 * pb.slot + i) ^ (r & 7)) << 4)) = Elem<T>::pack(p0, p1);
+                            *reinterpret_cast<uint32_t*>(at + (((4 * pb.slot + KEYS / 16 * half + i) ^ (r & 7)) << 4)) = Elem<T>::pack(p0, p1);
                         }
                     }
                     fence_async_proxy();
@@ -608,22 +615,30 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     l[x] += __shfl_xor_sync(~0u, l[x], 1);
                     l[x] += __shfl_xor_sync(~0u, l[x], 2);
+                    if (half == 1 && (lane & 3) == 0) ex[ROWS + 16 * w + lane / 4 + 8 * x] = l[x];
+                }
+            }
+            softmax_sync();
+            if (live && half == 0 && (lane & 3) == 0) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
                     const int r = 16 * w + lane / 4 + 8 * x;
-                    if ((lane & 3) != 0 || r >= rows) continue;
-                    factor[r] = l[x] == 0.f ? 0.f : 1.f / l[x];
-                    if (l[x] != l[x]) *odd = 1;
+                    if (r >= rows) continue;
+                    const float sum = l[x] + ex[ROWS + r];
+                    factor[r] = sum == 0.f ? 0.f : 1.f / sum;
+                    if (sum != sum) *odd = 1;
                     if (!whole) {
-                        a.part_ml[part0 + r] = make_float2(m[x] == kNegInf ? kNegInf : m[x] * sc, l[x]);
+                        a.part_ml[part0 + r] = make_float2(m[x] == kNegInf ? kNegInf : m[x] * sc, sum);
                     } else if (a.lse) {
                         int tok, head;
                         row_of(kv, r0 + r, tok, head);
-                        a.lse[static_cast<int64_t>(c.s.q0 + tok) * kv.hq + head] = l[x] == 0.f ? kNegInf : (m[x] * sc + log2f(l[x])) * kLn2;
+                        a.lse[static_cast<int64_t>(c.s.q0 + tok) * kv.hq + head] = sum == 0.f ? kNegInf : (m[x] * sc + log2f(sum)) * kLn2;
                     }
                 }
             }
             softmax_sync();
             bool bad = false;
-            for (int x = 0; x < parts; ++x) {
+            for (int x = half; x < parts; x += 2) {
                 const int e = 128 * x + 32 * w + lane;    // this thread's component
                 float* dst = a.part_o + part0 * (128 * parts) + e;
 #pragma unroll 1
@@ -659,7 +674,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             if (lane == 0) arrive_own(o_free);
             deal_next<C::kTile, KEYS>(a, c);
         }
-        if (ok && *odd) retake_rows<T, ROWS, CL, KEYS>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, w);
+        if (ok && *odd) retake_rows<T, ROWS, CL, KEYS>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, warp - 4);
     }
 
     tc_fence_before();

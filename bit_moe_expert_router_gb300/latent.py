@@ -83,6 +83,7 @@ class LatentBatch:
         self._c = _LatentBatch(seqs, n_heads, latent_dim, self.rot_dim, page, pages, width, max_q_len, max_kv_len, _DTYPES[self.dtype],
                                page_stride, row_stride, cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr())
         self._p = ctypes.addressof(self._c)
+        self._prep = None  # the HeadPrep that was found to fit
         lib = _load()
         if _device() == self._index:
             self._workspace = lib.moe_w4a8_latent_attention_workspace_size(self._p)
@@ -110,13 +111,10 @@ class LatentBatch:
     def alloc_workspace(self) -> torch.Tensor:
         return alloc_workspace(self.workspace_size(), self.device)
 
-    def _rows(self, t, name, shape):
-        """(address, strides but the last) of a tensor of this batch."""
-        # (one test on the way of every call; what was wrong is found out below)
-        if t.shape == shape and t.dtype is self.dtype and t.get_device() == self._index:
-            *strides, last = t.stride()
-            if last == 1:
-                return t.data_ptr(), *strides
+    def _refuse(self, t, name, shape):
+        """Why `t` is not a tensor of this batch of that shape."""
+        if t is None:
+            raise ValueError(f"{name} is required")
         if t.dtype is not self.dtype:
             raise TypeError(f"{name}: dtype {t.dtype}, expected {self.dtype}")
         if t.device != self.device:
@@ -125,16 +123,43 @@ class LatentBatch:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
         raise ValueError(f"{name}: its last dimension must be contiguous")
 
+    def _rows2(self, t, name, shape):
+        """(address, token stride) of a tensor of this batch."""
+        # (one test on the way of every call; what was wrong is found out in _refuse)
+        if t is not None and t.shape == shape and t.dtype is self.dtype and t.get_device() == self._index:
+            ts, es = t.stride()
+            if es == 1:
+                return t.data_ptr(), ts
+        self._refuse(t, name, shape)
 
-def _call(fn: str, index: int, *args):
+    def _rows3(self, t, name, shape):
+        """(address, token stride, head stride) of a tensor of this batch."""
+        if t is not None and t.shape == shape and t.dtype is self.dtype and t.get_device() == self._index:
+            ts, hs, es = t.stride()
+            if es == 1:
+                return t.data_ptr(), ts, hs
+        self._refuse(t, name, shape)
+
+
+def _enqueue(fn: str, index: int, *args):
     """Calls `fn` with `args` and the current stream of device `index`, with that device current."""
-    if _device() == index:
+    with torch.cuda.device(index):
         status = getattr(_load(), fn)(*args, _stream(index))
-    else:
-        with torch.cuda.device(index):
-            status = getattr(_load(), fn)(*args, _stream(index))
     if status != 0:
         raise MoeError(fn, status)
+
+
+def _fit(batch: LatentBatch, prep: HeadPrep):
+    """Whether a HeadPrep goes with a batch, looked at once for the two."""
+    if prep._index >= 0 and prep._index != batch._index:
+        raise ValueError(f"HeadPrep is on {prep.device}, the cache on {batch.device}")
+    if prep.q_weight is not None:
+        raise ValueError("latent queries have no norm of their own: q_weight must be None")
+    if prep.k_weight is not None and prep.k_weight.numel() != batch.latent_dim:
+        raise ValueError(f"a norm weight of {prep.k_weight.numel()} components, latent vectors of {batch.latent_dim}")
+    if (0 if prep.cos_sin is None else prep.cos_sin.shape[1]) != batch.rot_dim:
+        raise ValueError(f"the table of HeadPrep has to be as wide as the key part, {batch.rot_dim}")
+    batch._prep = prep
 
 
 def moe_w4a8_latent_append(batch: LatentBatch, prep: HeadPrep, latent, k_rot=None, q_rot=None, q_rot_out=None):
@@ -146,28 +171,23 @@ def moe_w4a8_latent_append(batch: LatentBatch, prep: HeadPrep, latent, k_rot=Non
     without a key part (rot_dim 0) takes latent alone.
     """
     n, rot = latent.shape[0], batch.rot_dim
-    if prep._index >= 0 and prep._index != batch._index:
-        raise ValueError(f"HeadPrep is on {prep.device}, the cache on {batch.device}")
-    if prep.q_weight is not None:
-        raise ValueError("latent queries have no norm of their own: q_weight must be None")
-    if prep.k_weight is not None and prep.k_weight.numel() != batch.latent_dim:
-        raise ValueError(f"a norm weight of {prep.k_weight.numel()} components, latent vectors of {batch.latent_dim}")
-    if (0 if prep.cos_sin is None else prep.cos_sin.shape[1]) != rot:
-        raise ValueError(f"the table of HeadPrep has to be as wide as the key part, {rot}")
+    if batch._prep is not prep:
+        _fit(batch, prep)
     if prep.positions is not None and prep.positions.shape != (n,):
         raise ValueError(f"positions: shape {tuple(prep.positions.shape)}, expected {(n,)}")
-    args = batch._rows(latent, "latent", (n, batch.latent_dim))
+    row = batch._rows2(latent, "latent", (n, batch.latent_dim))
     if rot:
-        for t, name in ((k_rot, "k_rot"), (q_rot, "q_rot"), (q_rot_out, "q_rot_out")):
-            if t is None:
-                raise ValueError(f"{name} is required")
         heads = (n, batch.n_heads, rot)
-        args += batch._rows(k_rot, "k_rot", (n, rot)) + batch._rows(q_rot, "q_rot", heads) + batch._rows(q_rot_out, "q_rot_out", heads)
+        args = (batch._p, prep._p, n, *row, *batch._rows2(k_rot, "k_rot", (n, rot)), *batch._rows3(q_rot, "q_rot", heads),
+                *batch._rows3(q_rot_out, "q_rot_out", heads))
     else:
         if not (k_rot is None and q_rot is None and q_rot_out is None):
             raise ValueError("rows without a key part: k_rot, q_rot and q_rot_out must be None")
-        args += (None, 0, None, 0, 0, None, 0, 0)
-    _call("moe_w4a8_latent_append", batch._index, batch._p, prep._p, n, *args)
+        args = (batch._p, prep._p, n, *row, None, 0, None, 0, 0, None, 0, 0)
+    if _lib is None or _device() != batch._index:
+        _enqueue("moe_w4a8_latent_append", batch._index, *args)
+    elif status := _lib.moe_w4a8_latent_append(*args, _stream(batch._index)):
+        raise MoeError("moe_w4a8_latent_append", status)
     return q_rot_out
 
 
@@ -189,6 +209,10 @@ def moe_w4a8_latent_attention(batch: LatentBatch, q, out, lse=None, scale: float
     if workspace.get_device() != batch._index:
         raise ValueError(f"workspace is on {workspace.device}, the cache on {batch.device}")
     row = dc + batch.rot_dim
-    _call("moe_w4a8_latent_attention", batch._index, batch._p, n, *batch._rows(q, "q", (n, h, row)), *batch._rows(out, "out", (n, h, dc)), at,
-          row ** -0.5 if scale is None else scale, *_aligned(workspace))
+    args = (batch._p, n, *batch._rows3(q, "q", (n, h, row)), *batch._rows3(out, "out", (n, h, dc)), at, row ** -0.5 if scale is None else scale,
+            *_aligned(workspace))
+    if _lib is None or _device() != batch._index:
+        _enqueue("moe_w4a8_latent_attention", batch._index, *args)
+    elif status := _lib.moe_w4a8_latent_attention(*args, _stream(batch._index)):
+        raise MoeError("moe_w4a8_latent_attention", status)
     return out
