@@ -41,8 +41,9 @@ namespace moe {
 namespace {
 
 constexpr int kSlotKeys = 32;  // keys of a slot of the ring
-constexpr int kMinShare = 128; // keys of a CTA at least, where there are few
-constexpr int kExtra = 128;    // keys that a tile's beginning and end count for
+// Keys that a tile's beginning and end count for: 64 ragged sequences of 128 heads 128 us, with 128 keys 131, with 768 139; four
+// sequences' 48 rows and one tile of 131071 keys take the same with 128 to 768.
+constexpr int kExtra1 = 128, kExtra2 = 256;
 constexpr int kJoinWarps = 8;
 
 // ROWS rows of a CTA, CL CTAs that share a tile of keys, which come in units of KEYS.
@@ -144,11 +145,20 @@ __device__ __forceinline__ void commit_all(uint64_t* bar) {
                      "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
+// What is read once is the first to leave L2, where the pieces' sums have to stay.
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+    uint64_t first, normal;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(first));
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(normal));
+    return once ? first : normal;
+}
+
 // Eight rows of the cache into L2.
-__device__ __forceinline__ void prefetch_rows(const CUtensorMap* map, bool wide, int blocks, int row, int page) {
+__device__ __forceinline__ void prefetch_rows(const CUtensorMap* map, bool wide, int blocks, int row, int page, uint64_t policy) {
     const uint64_t m = reinterpret_cast<uint64_t>(map);
     if (wide) {
-        asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n" ::"l"(m), "r"(0), "r"(row), "r"(0), "r"(page) : "memory");
+        asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile.L2::cache_hint [%0, {%1, %2, %3, %4}], %5;\n" ::"l"(m), "r"(0), "r"(row), "r"(0), "r"(page),
+                     "l"(policy) : "memory");
         return;
     }
     for (int b = 0; b < blocks; ++b)
@@ -158,15 +168,17 @@ __device__ __forceinline__ void prefetch_rows(const CUtensorMap* map, bool wide,
 // Eight rows of the cache, all their 64-component blocks, [block][row] -> shared memory; counted on `bar`.  WIDE: a box
 // has all blocks (rows of whole blocks), else one box each.  BOTH: into both CTAs of a pair, counted on each one's barrier.
 template <bool BOTH>
-__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, bool wide, int blocks, int row, int page, uint32_t bar) {
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, bool wide, int blocks, int row, int page, uint32_t bar, uint64_t policy) {
     const uint64_t m = reinterpret_cast<uint64_t>(map);
     if (wide) {
         if constexpr (BOTH)
             asm volatile(
-                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, %4, %5}], [%6], "
-                "%7;\n" ::"r"(dst), "l"(m), "r"(0), "r"(row), "r"(0), "r"(page), "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3, %4, "
+                "%5}], [%6], %7, %8;\n" ::"r"(dst), "l"(m), "r"(0), "r"(row), "r"(0), "r"(page), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(policy) : "memory");
         else
-            tma_tile4d<1>(dst, map, 0, row, 0, page, bar);
+            asm volatile(
+                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], "
+                "%7;\n" ::"r"(dst), "l"(m), "r"(0), "r"(row), "r"(0), "r"(page), "r"(bar), "l"(policy) : "memory");
         return;
     }
     for (int b = 0; b < blocks; ++b) {
@@ -208,7 +220,7 @@ __device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int rank
 
 template <typename T, int ROWS, int CL, int KEYS>
 __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
-    attend_latent_kernel(const LatentArgs a, int wide, int q_rows, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
+    attend_latent_kernel(const __grid_constant__ LatentArgs a, int wide, int q_rows, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
     using C = LatCfg<ROWS, CL, KEYS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* empty = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [slots of the ring] MMA commit of each CTA: the slot is read
@@ -263,7 +275,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
     if (blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
     const int rank = CL == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CL;
     Cursor c;
-    deal_begin<C::kTile, KEYS>(a, reinterpret_cast<long long*>(smem + C::kOffRing), kMinShare / KEYS, kExtra / KEYS, me, gridDim.x / CL, c);  // (scratch: the ring)
+    deal_begin<C::kTile, KEYS>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 1, (CL == 2 ? kExtra2 : kExtra1) / KEYS, me, gridDim.x / CL, c);  // (scratch: the ring)
     if (tid == 0) *reinterpret_cast<Cursor*>(smem + C::kOffStart) = c;
     clear_stray_rows<T>(a);  // (kv.d is what the outputs have)
     tc_fence_before();
@@ -353,6 +365,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             int lo, hi;
             const int r0 = c.rt * C::kTile;
             key_range(kv, 0, c.s, r0, min(r0 + C::kTile, c.s.q_len * kv.group), lo, hi);
+            const uint64_t policy = l2_policy(c.s.q_len * kv.group <= C::kTile);
             for (int j = 0; j < c.take && ok; ++j) {
                 const int key0 = (c.first + c.off + j) * KEYS, key = key0 + 8 * lane;
                 const int p = div_by(max(key, 0), kv.by_page), row = key - p * kv.page;
@@ -381,8 +394,8 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                     __syncwarp();
                     if (lane / 4 == x) {          // outside the map: zeros
                         const int page = static_cast<unsigned>(id) < static_cast<unsigned>(kv.n_pages) ? id : kv.n_pages, y = seen ? row : 0;
-                        if (lane == cut) load_rows<false>(dst, &map, wide, blocks, y, page, smem_u32(cut_in));
-                        else if (CL == 1 || (lane & 1) == rank) load_rows<CL == 2>(dst, &map, wide, blocks, y, page, smem_u32(there));
+                        if (lane == cut) load_rows<false>(dst, &map, wide, blocks, y, page, smem_u32(cut_in), policy);
+                        else if (CL == 1 || (lane & 1) == rank) load_rows<CL == 2>(dst, &map, wide, blocks, y, page, smem_u32(there), policy);
                     }
                 }
                 __syncwarp();
@@ -404,6 +417,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             }
             deal_next<C::kTile, KEYS>(a, c);
         }
+        if (C::kPrefetch && lane == 0) *begun = 1u << 30;  // (past all units: nothing waits for more)
         // Nothing is on its way to this CTA's memory when it leaves: the ring's last units have landed and been read (or, after
         // a timeout, the limit has passed).
         const uint64_t end = global_ns() + kWaitNs;
@@ -465,15 +479,17 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             int lo, hi;
             const int r0 = c.rt * C::kTile;
             key_range(kv, 0, c.s, r0, min(r0 + C::kTile, c.s.q_len * kv.group), lo, hi);
+            const uint64_t policy = l2_policy(c.s.q_len * kv.group <= C::kTile);
             for (int j = 0; j < c.take; ++j, ++u) {
                 const int key = (c.first + c.off + j) * KEYS + 8 * lane;
                 const int p = div_by(max(key, 0), kv.by_page);
                 const bool mine = lane < KEYS / 8 && key < hi && p < kv.width && (CL == 1 || (lane & 1) == rank);
                 const int id = mine ? __ldg(kv.table + static_cast<int64_t>(c.b) * kv.width + p) : -1;
                 uint32_t now;
-                while ((now = *begun) + C::kAhead <= u && !*ctl.abort) __nanosleep(50);  // (ends: the loader's waits do)
+                // (not before the ring has gone round once: what it waits for comes first; ends, because the loader's waits do)
+                while (((now = *begun) + C::kAhead <= u || now <= C::kUnits) && !*ctl.abort) __nanosleep(50);
                 if (*ctl.abort) break;
-                if (now <= u && static_cast<unsigned>(id) < static_cast<unsigned>(kv.n_pages)) prefetch_rows(&map, wide, blocks, key - p * kv.page, id);
+                if (now <= u && static_cast<unsigned>(id) < static_cast<unsigned>(kv.n_pages)) prefetch_rows(&map, wide, blocks, key - p * kv.page, id, policy);
                 __syncwarp();
             }
             if (*ctl.abort) break;
@@ -641,30 +657,38 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             for (int x = half; x < parts; x += 2) {
                 const int e = 128 * x + 32 * w + lane;    // this thread's component
                 float* dst = a.part_o + part0 * (128 * parts) + e;
+                if (!whole) {
+                    // (rows past the tile's are written, too, and never read)
+                    constexpr int kR = ROWS < 32 ? ROWS : 32;
 #pragma unroll 1
-                for (int y = 0; y < rows; y += 16, dst += 16 * 128 * parts) {
+                    for (int y = 0; y < rows; y += kR) {
+                        uint32_t o[kR];
+                        if constexpr (kR == 32) tmem_ld32(tmem + lane_base + C::kOCol + ROWS * x + y, o);
+                        else tmem_ld16(tmem + lane_base + C::kOCol + ROWS * x + y, o);
+                        tmem_ld_wait();
+                        tmem_tie<kR>(o);
+#pragma unroll
+                        for (int r = 0; r < kR; ++r, dst += 128 * parts) *dst = __uint_as_float(o[r]);
+                    }
+                    continue;
+                }
+#pragma unroll 1
+                for (int y = 0; y < rows; y += 16) {
                     uint32_t o[16];
                     tmem_ld16(tmem + lane_base + C::kOCol + ROWS * x + y, o);
                     tmem_ld_wait();
                     tmem_tie<16>(o);
-                    if (whole) {
 #pragma unroll
-                        for (int r = 0; r < 16; r += 2) {
-                            // two rows: the even lane of a pair writes both lanes' components of the first, the odd lane of the second
-                            const float2 f = *reinterpret_cast<const float2*>(factor + y + r);
-                            const float f0 = __uint_as_float(o[r]) * f.x, f1 = __uint_as_float(o[r + 1]) * f.y;
-                            bad |= e < kv.d && ((f0 != f0 && y + r < rows) || (f1 != f1 && y + r + 1 < rows));
-                            const float got = __shfl_xor_sync(~0u, lane & 1 ? f0 : f1, 1);
-                            const int rr = y + r + (lane & 1);
-                            if (rr < rows && (e & ~1) < kv.d)
-                                *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row_at[rr] + (e & ~1)) =
-                                    lane & 1 ? Elem<T>::pack(got, f1) : Elem<T>::pack(f0, got);
-                        }
-                    } else {
-                        float* to = dst;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r, to += 128 * parts)  // (rows past the tile's are written, too, and never read)
-                            *to = __uint_as_float(o[r]);
+                    for (int r = 0; r < 16; r += 2) {
+                        // two rows: the even lane of a pair writes both lanes' components of the first, the odd lane of the second
+                        const float2 f = *reinterpret_cast<const float2*>(factor + y + r);
+                        const float f0 = __uint_as_float(o[r]) * f.x, f1 = __uint_as_float(o[r + 1]) * f.y;
+                        bad |= e < kv.d && ((f0 != f0 && y + r < rows) || (f1 != f1 && y + r + 1 < rows));
+                        const float got = __shfl_xor_sync(~0u, lane & 1 ? f0 : f1, 1);
+                        const int rr = y + r + (lane & 1);
+                        if (rr < rows && (e & ~1) < kv.d)
+                            *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row_at[rr] + (e & ~1)) =
+                                lane & 1 ? Elem<T>::pack(got, f1) : Elem<T>::pack(f0, got);
                     }
                 }
             }
@@ -686,121 +710,157 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
     }
 }
 
-// The join of the pieces of a cut tile.  Block (c, y) stands for the boundary before CTA c + 1; the rows of a tile that several
-// boundaries cut are dealt over their blocks.  A warp takes a row, all its components, its pieces' loads two at a time; where the
-// pieces are many, eight warps share those of 128 components of a row.  The sums' order is that of the pieces' CTAs, so two runs
-// give the same bits.
+// ---------------------------------------------------------------- the join
+// The pieces of a cut tile: CTAs c0 to c1 have one each.
+template <int ROWS>
+struct CutTile {
+    BoundaryRec rec;
+    int c0, c1, rows;
+    __device__ __forceinline__ CutTile(const LatentArgs& a, const BoundaryRec& r) : rec(r) {
+        c0 = static_cast<int>(div_line(r.begin, r.per));
+        c1 = static_cast<int>(div_line(r.begin + r.n - 1, r.per));
+        rows = min(r.q_len * a.kv.group - r.rt * ROWS, ROWS);
+    }
+    // Row r of CTA p's piece among the pieces' rows.
+    __device__ __forceinline__ int64_t at(int p, int r) const { return (2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1)) * ROWS + r; }
+};
+
+__device__ __forceinline__ void add_scaled(float4& to, const float4& x, float f) {
+    to.x += x.x * f;
+    to.y += x.y * f;
+    to.z += x.z * f;
+    to.w += x.w * f;
+}
+
+// Writes 128 components of a row from `col` on, a warp four a lane, and with component 0 the row's lse.
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kJoinWarps * 32, 3) latent_join_kernel(const LatentArgs a) {
-    wait_for_stream();
-    constexpr int kVec = kMaxLatent / 128;  // fours of components of a lane
-    __shared__ float4 part[kJoinWarps][32];
-    __shared__ float part_l[kJoinWarps];
-    const int cta = blockIdx.x + 1;
-    const BoundaryRec rec = a.recs[cta];
-    if (!rec.cut) return;
+__device__ __forceinline__ void join_finish(const LatentArgs& a, const CutTile<ROWS>& t, int r, const float4& o, int col, float m, float l) {
     const KvArgs& kv = a.kv;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int parts = (kv.d + 127) / 128;
-    const int c0 = static_cast<int>(div_line(rec.begin, rec.per)), c1 = static_cast<int>(div_line(rec.begin + rec.n - 1, rec.per));
-    const int r0 = rec.rt * ROWS, rows = min(rec.q_len * kv.group - r0, ROWS);
-    auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(p) + (p * rec.per >= rec.begin ? 0 : 1); };
-    const int step = c1 - c0, turn = cta - (c0 + 1);  // boundaries of the tile, and which of them this is
-    auto add = [](float4& to, const float4& x, float f) {
-        to.x += x.x * f;
-        to.y += x.y * f;
-        to.z += x.z * f;
-        to.w += x.w * f;
-    };
-    // Writes a row's components from `col` on, 128 at a time, and with component 0 its lse.
-    auto finish = [&](int r, const float4* acc, int n, int col, float mm, float ll) {
-        int i, head;
-        row_of(kv, r0 + r, i, head);
-        const int tok = rec.q0 + i;
-        bool bad = ll != ll;
-        for (int x = 0; x < n; ++x)  // (what lies behind the latent part may be anything)
-            bad |= col + 128 * x + 4 * lane < kv.d && (acc[x].x != acc[x].x || acc[x].y != acc[x].y || acc[x].z != acc[x].z || acc[x].w != acc[x].w);
-        if (__any_sync(~0u, bad)) {
-            latent_row<T>(a, rec.b, tok, head, rec.pos0 + i, col, col + 128 * n);
-            return;
-        }
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        T* dst = static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col + 4 * lane;
-        for (int x = 0; x < n; ++x)
-            if (col + 128 * x + 4 * lane < kv.d)
-                *reinterpret_cast<uint2*>(dst + 128 * x) = make_uint2(Elem<T>::pack(acc[x].x * inv, acc[x].y * inv), Elem<T>::pack(acc[x].z * inv, acc[x].w * inv));
-        if (lane == 0 && col == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * kLn2;
-    };
-    if (step < 8) {
-        for (int r = turn + step * (blockIdx.y * kJoinWarps + warp); r < rows; r += step * gridDim.y * kJoinWarps) {
-            float mm = kNegInf, ll = 0.f;
-            float4 acc[kVec];
-#pragma unroll
-            for (int x = 0; x < kVec; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p = c0; p <= c1; p += 2) {
-                const int64_t at0 = slot_of(p) * ROWS + r, at1 = slot_of(min(p + 1, c1)) * ROWS + r;
-                const bool two = p < c1;
-                float4 o0[kVec], o1[kVec];
-#pragma unroll
-                for (int x = 0; x < kVec; ++x) {
-                    o0[x] = o1[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (x < parts) o0[x] = reinterpret_cast<const float4*>(a.part_o + at0 * (128 * parts) + 128 * x)[lane];
-                    if (x < parts && two) o1[x] = reinterpret_cast<const float4*>(a.part_o + at1 * (128 * parts) + 128 * x)[lane];
-                }
-                const float2 v0 = a.part_ml[at0], v1 = two ? a.part_ml[at1] : make_float2(kNegInf, 0.f);
-                const float top = fmaxf(mm, fmaxf(v0.x, v1.x)), base = top == kNegInf ? 0.f : top;
-                const float f = exp2_fast(mm - base), f0 = exp2_fast(v0.x - base), f1 = exp2_fast(v1.x - base);
-                mm = top;
-                ll = ll * f + v0.y * f0 + v1.y * f1;
-#pragma unroll
-                for (int x = 0; x < kVec; ++x) {
-                    acc[x] = make_float4(acc[x].x * f, acc[x].y * f, acc[x].z * f, acc[x].w * f);
-                    add(acc[x], o0[x], f0);
-                    if (two) add(acc[x], o1[x], f1);
-                }
-            }
-            finish(r, acc, parts, 0, mm, ll);
-        }
+    const int lane = threadIdx.x & 31;
+    int i, head;
+    row_of(kv, t.rec.rt * ROWS + r, i, head);
+    const int tok = t.rec.q0 + i;
+    const bool in = col + 4 * lane < kv.d;  // (what lies behind the latent part may be anything)
+    if (__any_sync(~0u, l != l || (in && (o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w)))) {
+        latent_row<T>(a, t.rec.b, tok, head, t.rec.pos0 + i, col, col + 128);
         return;
     }
-    for (int k = blockIdx.y; turn + k * step < rows * parts; k += gridDim.y) {  // (every warp of the block has the same item)
-        const int item = turn + k * step, r = item / parts, col = item % parts * 128;
-        float mm = kNegInf, ll = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = c0 + lane; p <= c1; p += 32) mm = fmaxf(mm, a.part_ml[slot_of(p) * ROWS + r].x);
-        constexpr int kNext = 4;
-        for (int p0 = c0 + warp; p0 <= c1; p0 += kNext * kJoinWarps) {
-            float2 v[kNext];
-            float4 o[kNext];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (in)
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col + 4 * lane) =
+            make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
+    if (lane == 0 && col == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+}
+
+// A row by a warp, its pieces' loads two at a time.
+template <typename T, int ROWS>
+__device__ __forceinline__ void join_few(const LatentArgs& a, const CutTile<ROWS>& t, int r, int parts) {
+    constexpr int kVec = kMaxLatent / 128;  // fours of components of a lane
+    const int lane = threadIdx.x & 31;
+    float mm = kNegInf, ll = 0.f;
+    float4 acc[kVec];
 #pragma unroll
-            for (int y = 0; y < kNext; ++y) {
-                const int64_t at = slot_of(min(p0 + y * kJoinWarps, c1)) * ROWS + r;
-                v[y] = a.part_ml[at];
-                o[y] = reinterpret_cast<const float4*>(a.part_o + at * (128 * parts) + col)[lane];
-            }
-            if (p0 == c0 + warp) {
+    for (int x = 0; x < kVec; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = t.c0; p <= t.c1; p += 2) {
+        const bool two = p < t.c1;
+        const int64_t at0 = t.at(p, r), at1 = t.at(min(p + 1, t.c1), r);
+        float4 o0[kVec], o1[kVec];
 #pragma unroll
-                for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
-            }
-            const float base = mm == kNegInf ? 0.f : mm;
-#pragma unroll
-            for (int y = 0; y < kNext; ++y) {
-                if (p0 + y * kJoinWarps > c1) break;
-                const float f = exp2_fast(v[y].x - base);
-                ll += v[y].y * f;
-                add(acc, o[y], f);
-            }
+        for (int x = 0; x < kVec; ++x) {
+            o0[x] = o1[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < parts) o0[x] = reinterpret_cast<const float4*>(a.part_o + at0 * (128 * parts) + 128 * x)[lane];
+            if (x < parts && two) o1[x] = reinterpret_cast<const float4*>(a.part_o + at1 * (128 * parts) + 128 * x)[lane];
         }
-        __syncthreads();
-        part[warp][lane] = acc;
-        if (lane == 0) part_l[warp] = ll;
-        __syncthreads();
-        if (warp != 0) continue;
-        for (int w = 1; w < kJoinWarps; ++w) {
-            add(acc, part[w][lane], 1.f);
-            ll += part_l[w];
+        const float2 v0 = a.part_ml[at0], v1 = two ? a.part_ml[at1] : make_float2(kNegInf, 0.f);
+        const float top = fmaxf(mm, fmaxf(v0.x, v1.x)), base = top == kNegInf ? 0.f : top;
+        const float f = exp2_fast(mm - base), f0 = exp2_fast(v0.x - base), f1 = exp2_fast(v1.x - base);
+        mm = top;
+        ll = ll * f + v0.y * f0 + v1.y * f1;
+#pragma unroll
+        for (int x = 0; x < kVec; ++x) {
+            acc[x] = make_float4(acc[x].x * f, acc[x].y * f, acc[x].z * f, acc[x].w * f);
+            add_scaled(acc[x], o0[x], f0);
+            if (two) add_scaled(acc[x], o1[x], f1);
         }
-        finish(r, &acc, 1, col, mm, ll);
+    }
+#pragma unroll
+    for (int x = 0; x < kVec; ++x)
+        if (x < parts) join_finish<T, ROWS>(a, t, r, acc[x], 128 * x, mm, ll);
+}
+
+// 128 components of a row by the block, eight of the pieces' loads at a time in a warp.  part, part_ml: of the block.
+template <typename T, int ROWS>
+__device__ __forceinline__ void join_many(const LatentArgs& a, const CutTile<ROWS>& t, int r, int col, int parts, float4 (*part)[32], float2* part_ml) {
+    constexpr int kNext = 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float mm = kNegInf, ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = t.c0 + warp; p0 <= t.c1; p0 += kNext * kJoinWarps) {
+        float2 v[kNext];
+        float4 o[kNext];
+#pragma unroll
+        for (int y = 0; y < kNext; ++y) {
+            const int p = p0 + y * kJoinWarps;
+            v[y] = make_float2(kNegInf, 0.f);
+            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p > t.c1) continue;
+            v[y] = a.part_ml[t.at(p, r)];
+            o[y] = reinterpret_cast<const float4*>(a.part_o + t.at(p, r) * (128 * parts) + col)[lane];
+        }
+        float top = mm;
+#pragma unroll
+        for (int y = 0; y < kNext; ++y) top = fmaxf(top, v[y].x);
+        const float base = top == kNegInf ? 0.f : top, f = exp2_fast(mm - base);
+        mm = top;
+        ll *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+        for (int y = 0; y < kNext; ++y) {
+            const float g = exp2_fast(v[y].x - base);
+            ll += v[y].y * g;
+            if (p0 + y * kJoinWarps <= t.c1) add_scaled(acc, o[y], g);
+        }
+    }
+    __syncthreads();
+    if (lane == 0) part_ml[warp] = make_float2(mm, ll);
+    part[warp][lane] = acc;
+    __syncthreads();
+    if (warp != 0) return;
+    float top = kNegInf, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, part_ml[w].x);
+    const float base = top == kNegInf ? 0.f : top;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = exp2_fast(part_ml[w].x - base);
+        sum += part_ml[w].y * f;
+        add_scaled(o, part[w][lane], f);
+    }
+    join_finish<T, ROWS>(a, t, r, o, col, top, sum);
+}
+
+// The join of the pieces of the cut tiles.  Block (i, y) stands for the boundary before CTA i + 1; the items of a tile, eight rows, a
+// warp each, or where the pieces are many, 128 components of one row, are dealt over the blocks of the boundaries that cut it.  (One line of
+// all items for all blocks, found by sums over the boundaries, takes 2 us more.)  The sums' order goes by the pieces' CTAs alone, so two
+// runs give the same bits.
+constexpr int kManyPieces = 9;
+constexpr int kJoinTurns = 8;  // blocks of a boundary: 4 and 16 take 1 us more on four sequences' 48 rows, 64 sequences of 128 rows
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) latent_join_kernel(const __grid_constant__ LatentArgs a) {
+    wait_for_stream();
+    __shared__ float4 part[kJoinWarps][32];
+    __shared__ float2 part_ml[kJoinWarps];
+    const int warp = threadIdx.x >> 5, parts = (a.kv.d + 127) / 128;
+    const BoundaryRec rec = a.recs[blockIdx.x + 1];
+    if (!rec.cut) return;
+    const CutTile<ROWS> t(a, rec);
+    const int step = t.c1 - t.c0, first = blockIdx.x - t.c0 + step * blockIdx.y;
+    if (step + 1 >= kManyPieces) {
+        for (int k = first; k < t.rows * parts; k += step * kJoinTurns) join_many<T, ROWS>(a, t, k / parts, k % parts * 128, parts, part, part_ml);
+    } else {
+        for (int k = first; k * kJoinWarps < t.rows; k += step * kJoinTurns)
+            if (k * kJoinWarps + warp < t.rows) join_few<T, ROWS>(a, t, k * kJoinWarps + warp, parts);
     }
 }
 
@@ -850,8 +910,14 @@ int make_qmap(const LatentArgs& a, int dtype, CUtensorMap* map, cudaError_t* err
     return uniform ? 1 : 2;
 }
 
+// Up to so many positions a row tile stays with one CTA (pair): the pieces' way through memory and the second kernel cost more than
+// the keys' streaming by one.  Few tiles: one sequence of 16 heads, whole | split, 100 positions 9.6 | 10.5 us, 200 11.9 | 11.0.  Tiles
+// for half of the GPU and more: 64 sequences of 128 heads at 500 29 | 39 us, 32 26 | 27, 8 25 | 18; 32 of 16 heads (a fifth of
+// the GPU) 19.5 | 16.6.
+constexpr int64_t kWholeKeys = 128, kWholeKeysMany = 1024;
+
 template <typename T, int ROWS, int CL, int KEYS>
-cudaError_t launch_r(const LatentArgs& a, int dtype, int n_ctas, cudaStream_t st) {
+cudaError_t launch_r(LatentArgs a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
     using C = LatCfg<ROWS, CL, KEYS>;
     const bool wide = a.dk % 64 == 0;
     CUtensorMap map;
@@ -863,17 +929,19 @@ cudaError_t launch_r(const LatentArgs& a, int dtype, int n_ctas, cudaStream_t st
     e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS, CL, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int groups = n_ctas / CL;
+    const bool many = 2 * a.kv.n_seqs * ((rows + C::kTile - 1) / C::kTile) >= groups;
+    a.split = groups > 1 && a.max_keys > (many ? kWholeKeysMany : kWholeKeys);
     e = launch_in_stream(attend_latent_kernel<T, ROWS, CL, KEYS>, dim3(groups * CL), C::kThreads, C::kSmem, CL, st, a, wide ? 1 : 0, q_rows, map, qmap);
-    if (e != cudaSuccess || !a.split || groups < 2) return e;
-    return launch_in_stream(latent_join_kernel<T, C::kTile>, dim3(groups - 1, C::kTile / kJoinWarps), kJoinWarps * 32, 0, 1, st, a);
+    if (e != cudaSuccess || !a.split) return e;
+    return launch_in_stream(latent_join_kernel<T, C::kTile>, dim3(groups - 1, kJoinTurns), kJoinWarps * 32, 0, 1, st, a);
 }
 
 template <typename T>
 cudaError_t launch_t(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
-    if (rows <= 16) return launch_r<T, 16, 1, 32>(a, dtype, n_ctas, st);
-    if (rows <= 32) return launch_r<T, 32, 1, 32>(a, dtype, n_ctas, st);
-    if (rows <= 64 || n_ctas < 2) return launch_r<T, 64, 1, 32>(a, dtype, n_ctas, st);
-    return launch_r<T, 64, 2, 64>(a, dtype, n_ctas, st);
+    if (rows <= 16) return launch_r<T, 16, 1, 32>(a, dtype, rows, n_ctas, st);
+    if (rows <= 32) return launch_r<T, 32, 1, 32>(a, dtype, rows, n_ctas, st);
+    if (rows <= 64 || n_ctas < 2) return launch_r<T, 64, 1, 32>(a, dtype, rows, n_ctas, st);
+    return launch_r<T, 64, 2, 64>(a, dtype, rows, n_ctas, st);
 }
 
 }  // namespace

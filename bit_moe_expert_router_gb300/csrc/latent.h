@@ -9,7 +9,8 @@ namespace moe {
 // A latent batch goes as one with a single key/value head: kv.k is the cache, kv.d the latent part of its rows (what
 // the outputs have), kv.group = kv.hq the heads.
 struct LatentArgs : AttendArgs {
-    int dk;  // components of a row, and of a query
+    int dk;            // components of a row, and of a query
+    int64_t max_keys;  // of a sequence, by the caller's bound
 };
 
 struct LatentAppendArgs {
@@ -29,7 +30,7 @@ constexpr int kMaxLatent = 512, kMaxLatentRot = 64;
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int dtype, cudaStream_t st);
 
-// rows: of a sequence, at most.  The rows of a tile and the CTAs that share it go by them.
+// rows: of a sequence, by the caller's bound.  The rows of a tile, the CTAs that share it and whether it is cut go by the bounds.
 int latent_part_rows(int n_ctas);  // rows of all pieces, whatever the tile
 cudaError_t launch_latent(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st);
 

@@ -101,9 +101,6 @@ LatentLayout latent_layout(const moe_latent_batch_t* b) {
     return L;
 }
 
-// Up to this many positions a row tile stays with one CTA.
-constexpr int64_t kWholeKeys = 256;
-
 }  // namespace
 
 MOE_API int moe_w4a8_latent_append(const moe_latent_batch_t* batch, const moe_head_prep_t* prep, int64_t n_tokens, const void* latent,
@@ -180,7 +177,7 @@ MOE_API int moe_w4a8_latent_attention(const moe_latent_batch_t* batch, int64_t n
     a.recs = reinterpret_cast<moe::BoundaryRec*>(ws + L.recs);
     a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
     a.part_o = reinterpret_cast<float*>(ws + L.o);
-    a.split = std::min<int64_t>(batch->max_kv_len, a.kv.cap) > kWholeKeys;
+    a.max_keys = std::min<int64_t>(batch->max_kv_len, a.kv.cap);
     const int64_t rows = std::min(batch->max_q_len, n_tokens) * a.kv.group;
     return moe::cuda_status(moe::launch_latent(a, static_cast<int>(batch->dtype), rows, L.n_ctas, static_cast<cudaStream_t>(stream)),
                             "latent_attention");
