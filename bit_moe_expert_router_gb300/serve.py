@@ -5,7 +5,11 @@ projection, ``moe_w4a8_kv_append``, ``moe_w4a8_paged_attention``, the output pro
 and ``moe_w4a8_forward_bf16`` on the packed expert bank.  The four dense projections are torch matrix products; nothing
 in a step reads anything back to the host.
 
-    python -m bit_moe_expert_router_gb300.serve
+``LatentServingLayer`` is the same for layers that cache one latent vector per token for all heads and choose their
+experts by scores: ``moe_w4a8_latent_append``, ``moe_w4a8_latent_attention`` with the expansion of the latent vector
+absorbed into the queries and the output, ``moe_w4a8_route_scored`` and ``moe_w4a8_forward_bf16_routed``.
+
+    python -m bit_moe_expert_router_gb300.serve [latent]
 
 runs a synthetic layer on cuda:0 (seeded random weights): a prompt in two chunks beside a decoding request, then some
 decoding steps of both, and prints the time of each kind of step.
@@ -14,7 +18,7 @@ from __future__ import annotations
 
 import torch
 
-from . import attention, binding
+from . import attention, binding, latent
 
 
 def rms_norm(x, weight, eps=1e-6):
@@ -82,6 +86,88 @@ class ServingLayer:
         return (x.float() + moe).to(x.dtype)
 
 
+class LatentServingLayer:
+    """One layer of latent attention with its paged cache, for up to `seqs` sequences of up to `pages_per_seq` pages.
+
+    w: dict of torch CUDA tensors -- norm1, norm2 [H] and latent_norm [Dc] float32; wq [H, heads (Dn + R)] (a head's Dn components
+    without a position, then its R rotated ones), wkv [H, Dc + R] (the latent vector, then the key part), wk [heads, Dn, Dc] and wv
+    [heads, Dc, Dv] (the latent vector's expansion to a head's keys and values), wo [heads Dv, H], router [H, E] bf16; router_bias
+    [E] float32 or None; w13, s13, w2, s2: the expert bank (see the C header).  rule: how the experts are chosen.
+    """
+
+    def __init__(self, w, rule: binding.RouteRule, n_shared, group, seqs, pages_per_seq, page_size=64, base=10000.0):
+        self.w, self.rule, dev = w, rule, w["wq"].device
+        self.heads, self.dn, self.dc = w["wk"].shape
+        self.rot = w["wkv"].shape[1] - self.dc
+        self.n_shared, self.group = n_shared, group
+        self.scale = (self.dn + self.rot) ** -0.5  # of the heads before the absorption
+        i32 = dict(dtype=torch.int32, device=dev)
+        # a serving program's allocator hands out pages as sequences grow; here each sequence has its own
+        self.block_table = torch.arange(seqs * pages_per_seq, **i32).reshape(seqs, pages_per_seq)
+        self.q_start, self.kv_len = torch.zeros(seqs + 1, **i32), torch.zeros(seqs, **i32)
+        self.cache = torch.empty(seqs * pages_per_seq, page_size, self.dc + self.rot, dtype=torch.bfloat16, device=dev)
+        self.prep = attention.HeadPrep(attention.rope_table(pages_per_seq * page_size, self.rot, base, device=dev), interleaved=True,
+                                       k_weight=w["latent_norm"])
+        self.batch = latent.LatentBatch(self.cache, self.block_table, self.q_start, self.kv_len, n_heads=self.heads, latent_dim=self.dc, max_q_len=1)
+        self._attend_workspace, self._moe_workspaces = self.batch.alloc_workspace(), {}
+
+    def dims(self, tokens: int) -> binding.Dims:
+        w13, w2 = self.w["w13"], self.w["w2"]
+        return binding.Dims(tokens, w2.shape[1], w13.shape[1] // 2, w13.shape[0] - self.n_shared, self.n_shared, self.rule.top_k, self.group)
+
+    def moe_workspace(self, tokens: int):
+        """The experts' workspace of the next power of two of tokens, kept: a captured graph holds its address."""
+        size = 1 << (tokens - 1).bit_length()
+        if size not in self._moe_workspaces:
+            need = binding.moe_w4a8_forward_bf16_workspace_size(self.dims(size))
+            self._moe_workspaces[size] = binding.alloc_workspace(need, self.cache.device)
+        return self._moe_workspaces[size]
+
+    def forward(self, x, max_q_len: int):
+        """x [tokens, H] bf16, the new tokens of all sequences in order; q_start and kv_len hold the step's lengths."""
+        w, n, dev = self.w, x.shape[0], x.device
+        self.batch.max_q_len = max_q_len
+        y = rms_norm(x, w["norm1"])
+        q_nope, q_rot = (y @ w["wq"]).unflatten(1, (self.heads, self.dn + self.rot)).split([self.dn, self.rot], dim=2)
+        c, k_rot = (y @ w["wkv"]).split([self.dc, self.rot], dim=1)
+        # a head's query against the latent vectors themselves, its rotated part behind
+        q = torch.empty(n, self.heads, self.dc + self.rot, dtype=x.dtype, device=dev)
+        q[..., :self.dc] = torch.bmm(q_nope.transpose(0, 1), w["wk"]).transpose(0, 1)
+        latent.moe_w4a8_latent_append(self.batch, self.prep, c, k_rot, q_rot, q[..., self.dc:])
+        o = torch.empty(n, self.heads, self.dc, dtype=x.dtype, device=dev)
+        latent.moe_w4a8_latent_attention(self.batch, q, o, scale=self.scale, workspace=self._attend_workspace)
+        x = x + torch.bmm(o.transpose(0, 1), w["wv"]).transpose(0, 1).flatten(1) @ w["wo"]
+        y = rms_norm(x, w["norm2"])
+        ids = torch.empty(n, self.rule.top_k, dtype=torch.int32, device=dev)
+        weights = torch.empty(n, self.rule.top_k, dtype=torch.float32, device=dev)
+        binding.moe_w4a8_route_scored(y @ w["router"], self.rule, ids, weights, bias=w["router_bias"])
+        moe = torch.empty(n, x.shape[1], dtype=torch.float32, device=dev)
+        binding.moe_w4a8_forward_bf16_routed(y, ids, weights, w["w13"], w["s13"], w["w2"], w["s2"], self.dims(n), moe, self.moe_workspace(n))
+        return (x.float() + moe).to(x.dtype)
+
+
+def synthetic_latent_layer(workload, rule, heads, nope, latent_dim, rot_dim, v_dim, seqs, pages_per_seq, device="cuda:0", seed=0, **kw) -> LatentServingLayer:
+    """A layer of latent attention with the workload's expert bank and random dense weights."""
+    from . import synth
+    bank = synth.make_bank(workload)
+    g = torch.Generator(device=device)
+    g.manual_seed(seed)
+    h = workload.H
+
+    def dense(*shape, rows):
+        return (torch.randn(*shape, generator=g, device=device) * rows ** -0.5).bfloat16()
+
+    def norm(n):
+        return 1.0 + 0.1 * torch.randn(n, generator=g, device=device)
+
+    w = dict(norm1=norm(h), norm2=norm(h), latent_norm=norm(latent_dim), wq=dense(h, heads * (nope + rot_dim), rows=h),
+             wkv=dense(h, latent_dim + rot_dim, rows=h), wk=dense(heads, nope, latent_dim, rows=latent_dim), wv=dense(heads, latent_dim, v_dim, rows=latent_dim),
+             wo=dense(heads * v_dim, h, rows=heads * v_dim), router=dense(h, workload.E, rows=h),
+             router_bias=0.05 * torch.randn(workload.E, generator=g, device=device))
+    w.update({name: torch.from_numpy(getattr(bank, name)).to(device) for name in ("w13", "s13", "w2", "s2")})
+    return LatentServingLayer(w, rule, workload.S, workload.group, seqs, pages_per_seq, **kw)
+
+
 def synthetic_layer(workload, n_q_heads, n_kv_heads, head_dim, seqs, pages_per_seq, device="cuda:0", seed=0, **kw) -> ServingLayer:
     """A layer with the workload's expert bank and random dense weights."""
     from . import synth
@@ -102,10 +188,14 @@ def synthetic_layer(workload, n_q_heads, n_kv_heads, head_dim, seqs, pages_per_s
     return ServingLayer(w, n_q_heads, n_kv_heads, head_dim, workload.top_k, workload.S, workload.group, seqs, pages_per_seq, **kw)
 
 
-def main() -> None:
+def main(kind: str = "grouped") -> None:
     from . import synth
     w = synth.Workload("serve", T=4, H=2048, I=512, E=64, S=1, top_k=8, group=128)
-    layer = synthetic_layer(w, 16, 2, 256, seqs=2, pages_per_seq=64, rot_dim=64)
+    if kind == "latent":
+        rule = binding.RouteRule(w.E, w.top_k, "sigmoid", n_groups=8, topk_groups=4, group_top=2, scale=2.5)
+        layer = synthetic_latent_layer(w, rule, 16, 128, 512, 64, 128, seqs=2, pages_per_seq=64)
+    else:
+        layer = synthetic_layer(w, 16, 2, 256, seqs=2, pages_per_seq=64, rot_dim=64)
     g = torch.Generator(device="cuda:0")
     g.manual_seed(1)
     start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
@@ -126,4 +216,5 @@ def main() -> None:
 
 
 if __name__ == "__main__":
-    main()
+    import sys
+    main(*sys.argv[1:2])
