@@ -13,6 +13,8 @@
 // many query heads as their chunks fill the warp with (R = 64: 8 lanes a
 // head, 4 heads).  A lane has the same chunk of every head, so its cosines and
 // sines are loaded once.  Several rounds' loads are under way together.
+// 8192 tokens of 16 heads, 512 + 64: 13.3 us with inputs that L2 does not hold, 52 MB in and out, 3.9 TB/s (a copy of as many
+// bytes takes 18.6); of 128 heads 46.2 us, 287 MB, 6.2 TB/s.  Single tokens 2.5 us, the launch and the chain of lookups.
 #include <algorithm>
 
 #include "attention_common.cuh"
@@ -21,7 +23,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;  // 2048 tokens of 16 heads 3.7 us, with 128 threads 3.9, with 256 3.8; 64 tokens of 128 heads 2.5, 2.6, 2.8
 constexpr int kRounds = 4;  // rounds of heads whose loads are under way together
 
 // How a lane finds the partners of its chunk's components.
@@ -214,9 +216,12 @@ cudaError_t launch_m(const LatentAppendArgs& a, cudaStream_t st) {
     while ((1 << log2) < a.rot / 8) ++log2;
     const int heads = 32 >> log2, rounds = a.rot == 0 ? 0 : (a.kv.hq + heads - 1) / heads;
     // A warp for each round and one for the row while the GPU has warps to spare (latency), else a warp for a token's row and
-    // eight rounds.
-    const bool few = static_cast<int64_t>(a.kv.n_tokens) * (1 + rounds) <= 152 * 16;
-    const int per = few ? 1 : 2 * kRounds;
+    // four rounds, or eight once there are more of these than run at a time.  128 heads of 64, us with one | four | eight
+    // rounds: 64 tokens 2.6 | - | 3.5, 128 tokens 3.1 | 3.1 | 3.6, 256 4.5 | 3.5 | 3.8, 512 7.6 | 4.8 | 5.1, 2048 29.5 | 14.4 | 14.3,
+    // 8192 110.8 | 48.4 | 46.5 (sixteen: 46.5, but 4.6 of 256).
+    const int64_t tokens = a.kv.n_tokens;
+    const bool few = tokens * (1 + rounds) <= 152 * 16;
+    const int per = few ? 1 : tokens * ((rounds + kRounds - 1) / kRounds) <= 152 * 64 ? kRounds : 2 * kRounds;
     const int parts = std::max((rounds + per - 1) / per, few ? 0 : 1) + (few ? 1 : 0);
     const dim3 grid((a.kv.n_tokens + kThreads / 32 - 1) / (kThreads / 32), parts);
     return launch_in_stream(latent_append_kernel<T, TURN>, grid, kThreads, 0, 1, st, a, log2, per, few ? 1 : 0);
