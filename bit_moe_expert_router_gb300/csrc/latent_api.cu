@@ -46,7 +46,7 @@ int check_batch(const moe_latent_batch_t* b, int64_t n_tokens) {
     if (!b->cache || !aligned(b->cache, 16)) return MOE_ERR_INVALID_ARG;
     for (const int32_t* p : {b->block_table, b->q_start, b->kv_len})
         if (!p || !aligned(p, 4)) return MOE_ERR_INVALID_ARG;
-    if (n_tokens > kI32 / b->n_heads) return MOE_ERR_UNSUPPORTED;
+    if (n_tokens > (kI32 - 512) / b->n_heads) return MOE_ERR_UNSUPPORTED;  // (a last row tile's end stays in range)
     return MOE_OK;
 }
 

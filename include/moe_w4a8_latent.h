@@ -40,8 +40,8 @@
  * 8, a row stride below Dc + R, a scale that is not positive and finite, an
  * unknown dtype, a prep that does not fit (see below).  MOE_ERR_UNSUPPORTED:
  * Dc > 512, R > 64, a page size that is not a multiple of 8, n_heads > 1024,
- * B > 2048, n_heads tokens at or above 2^31 rows, strides of 2^39 elements and
- * more.
+ * B > 2048, more than 2^31 - 513 rows (tokens times heads), page and row strides
+ * of 2^39 elements and more.
  */
 #ifndef MOE_W4A8_LATENT_H
 #define MOE_W4A8_LATENT_H

@@ -279,6 +279,31 @@ def test_another_stream_and_a_graph():
             assert torch.equal(out, c.attend()[0])
 
 
+def test_one_workspace_for_calls_and_graphs_of_every_kind():
+    """What a call leaves in a workspace (pieces, their records) never reaches the next one, eager or replayed."""
+    from bit_moe_expert_router_gb300 import latent
+    cases = [Case(*LENGTHS[k], h, 512, 64, 16, seed=30) for k, h in (("mixed", 128), ("long", 16), ("one", 128), ("edges", 32), ("chunk", 48), ("empty", 16), ("long", 128))]
+    refs = [c.attend()[0] for c in cases]
+    ws, outs = cases[0].batch.alloc_workspace(), [torch.empty_like(r) for r in refs]
+    ws.fill_(255)
+
+    def attend(i):
+        latent.moe_w4a8_latent_attention(cases[i].batch, cases[i].q, outs[i], workspace=ws)
+    graphs = [torch.cuda.CUDAGraph() for _ in cases]
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            attend(i)
+    for turn in range(3):
+        for out in outs:
+            out.fill_(77.0)
+        for i in range(len(cases)):
+            j = (3 * i + turn) % len(cases)
+            graphs[j].replay() if (i + turn) % 2 else attend(j)
+        torch.cuda.synchronize()
+        for i, (out, ref) in enumerate(zip(outs, refs)):
+            assert torch.equal(out, ref), (turn, i)
+
+
 def test_two_calls_at_once():
     """Calls on two streams with a workspace each, over one cache."""
     from bit_moe_expert_router_gb300 import latent

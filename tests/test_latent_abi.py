@@ -17,8 +17,8 @@ def lib(cuda_lib):
 
 def _batch(**kw):
     from bit_moe_expert_router_gb300 import latent
-    f = dict(n_seqs=4, n_heads=8, latent_dim=128, rot_dim=64, page_size=16, n_pages=10, table_width=3, max_q_len=1, max_kv_len=48, dtype=0,
-             page_stride=16 * 192, row_stride=192, cache=FAKE, block_table=FAKE, q_start=FAKE, kv_len=FAKE)
+    f = dict(n_seqs=4, n_heads=8, latent_dim=128, rot_dim=64, page_size=24, n_pages=10, table_width=2, max_q_len=1, max_kv_len=48, dtype=0,
+             page_stride=24 * 192, row_stride=192, cache=FAKE, block_table=FAKE, q_start=FAKE, kv_len=FAKE)
     f.update(kw)
     return latent._LatentBatch(**f)
 
@@ -40,7 +40,7 @@ def _attend(lib, batch, n=4, q=FAKE, qs=(1536, 192), o=FAKE, os=(1024, 128), lse
 
 BAD_BATCH = [("n_seqs", 0, 1), ("n_heads", 0, 1), ("latent_dim", 0, 1), ("latent_dim", 100, 1), ("rot_dim", -8, 1), ("rot_dim", 60, 1), ("page_size", 0, 1),
              ("n_pages", 0, 1), ("table_width", 0, 1), ("max_q_len", 0, 1), ("max_kv_len", 0, 1), ("dtype", 2, 1), ("dtype", -1, 1),
-             ("page_stride", 3076, 1), ("page_stride", 0, 1), ("row_stride", -8, 1), ("row_stride", 184, 1), ("cache", None, 1), ("cache", FAKE + 8, 1),
+             ("page_stride", 4612, 1), ("page_stride", 0, 1), ("row_stride", -8, 1), ("row_stride", 184, 1), ("cache", None, 1), ("cache", FAKE + 8, 1),
              ("block_table", None, 1), ("q_start", FAKE + 2, 1), ("kv_len", None, 1), ("latent_dim", 520, 2), ("rot_dim", 72, 2), ("n_seqs", 2049, 2),
              ("n_heads", 1025, 2), ("page_size", 12, 2), ("page_size", 1 << 31, 2), ("n_pages", 1 << 31, 2), ("table_width", 1 << 31, 2),
              ("page_stride", 1 << 39, 2), ("row_stride", 1 << 39, 2)]
@@ -69,7 +69,7 @@ def test_bad_append_arguments_are_refused(lib, kw):
 
 @pytest.mark.parametrize("kw,status", [(dict(q=None), 1), (dict(q=FAKE + 8), 1), (dict(qs=(1536, 4)), 1), (dict(o=None), 1), (dict(os=(-8, 128)), 1), (dict(lse=FAKE + 2), 1),
                                        (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1), (dict(ws=None), 1),
-                                       (dict(ws=FAKE + 16), 1), (dict(n=-1), 1), (dict(nbytes=1 << 16), 3), (dict(n=1 << 29), 2)])
+                                       (dict(ws=FAKE + 16), 1), (dict(n=-1), 1), (dict(nbytes=1 << 16), 3), (dict(n=1 << 29), 2), (dict(n=(1 << 28) - 60), 2)])
 def test_bad_attend_arguments_are_refused(lib, kw, status):
     assert _attend(lib, _batch(), **kw) == status
 
