@@ -8,30 +8,37 @@
 //
 // Bound: HBM while the rows are few (a row of the cache, 2 (Dc + R) bytes, does 2 (2 Dc + R) flops per head: the ridge is at
 // about 130 heads), the tensor pipe beyond.  A CTA takes a tile of ROWS = 16, 32 or 64 (token, head) rows, token-major,
-// against tiles of 64 keys, which come by TMA straight from the pages and are read from shared memory by both
+// against units of 32 or 64 keys, which come by TMA straight from the pages and are read from shared memory by both
 // products, so a cache row is brought once:
-//   S = Q X^T       64 rows (of which ROWS count) x 64 keys, A = Q and B = X both along the components; fp32 in tensor
-//                   memory, two buffers, so that the next keys' S is computed during this one's softmax
+//   S = Q X^T       64 rows (of which ROWS count) x KEYS keys, A = Q and B = X both along the components; fp32 in tensor
+//                   memory, two buffers or more, so that the next keys' S is computed during this one's softmax
 //   O^T += X^T P^T  turned over: 128 components of the latent part x ROWS rows, four times, A = X along the keys' other
 //                   direction (no transposition is needed), B = P.  The accumulator takes 4 ROWS columns of tensor memory,
 //                   where O of 128 rows x 512 components alone would fill all of it.
-// A softmax thread has the matrix-fragment places of S (two rows, KEYS / 8 keys each), four lanes and two warps a row.  P goes to shared memory in
-// 16 bits.  The reference m is raised, and O rescaled, only when a row's maximum has grown by more than 2^8 over it.
+// A softmax thread has the matrix-fragment places of S (two rows, KEYS / 4 values), four lanes and two warps a row.  P goes to
+// shared memory in 16 bits.  The reference m is raised, and O rescaled, only when a row's maximum has grown by more than 2^8 over it.
 //
 // The keys come eight rows at a time with all their components, 9 KB that lie side by side in the cache, so that what DRAM opens
 // is read at once (boxes of 64 components x 64 rows stream at 3.3 TB/s, these at 5.6).  In shared memory such a group is
 // [block of 64 components][row], a swizzle atom each, so a product finds its next eight keys a group further, its next 64
-// components a KB further.  The ring has two units, free again in slots of 16 keys as O's products pass them.  From
+// components a KB further.  The ring has 128 keys (160 with few rows), free again in slots of 32 as O's products pass them.  From
 // 65 rows on two CTAs with 64 rows each share the units: each brings half of a unit into both (TMA multicast).
 // Pages that are not there and rows past the last visible one read zeros, and rows behind it inside a group are
-// cleared by hand.  Work is dealt in equal shares of 64-key units; the pieces of a cut tile go through the workspace and the
-// join.
+// cleared by hand.  Work is dealt in equal shares of units; the pieces of a cut tile go through the workspace and the join.
 //
 // Warps: 0 the products S and the tensor-memory allocation, 3 the products O, each issued by one lane, so that neither waits
-// for what the other needs; 1 the keys, 2 the queries, 4 to 11 softmax and output, a warp for half of
-// the keys of 16 rows, 12 what brings the keys to come into L2.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
+// for what the other needs (one warp that looked at both: 64 ragged sequences of 128 heads 224 us, at that state 170); 1 the
+// keys, 2 the queries, 4 to 11 softmax and output, a warp for half of the keys of 16 rows, 12 what brings the keys to come into
+// L2.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
 // its own copies in flight.  The softmax warps meet at a barrier once per tile, whatever became of their waits, and leave
 // together.
+//
+// Measured, bf16, 512 + 64 components, device time with the join: one sequence of 131071 positions, 32 heads 38.1 us (4.0 TB/s;
+// 22 by its bytes), 64 ragged ones up to 16384 of 16, 32, 64, 128 heads 65, 69, 84, 127 us (5.3, 5.0, 4.1, 2.8 TB/s; 51 to 52 by
+// their bytes), 509 tokens of 32 heads at 8000 positions beside eight single ones 363 us (0.79 PFLOP/s; 145 by its operations).  A
+// pair takes about 2800 cycles for 64 keys, of which the tensor pipe has work for 2130 (S 36 steps of 36, where 64 rows are
+// half of the pipe's width, O 16 of 52); the rest is the way from O's end through the empty slot and the copy to the next S,
+// for which the ring is too short.
 #include <algorithm>
 
 #include "latent_common.cuh"
@@ -40,7 +47,9 @@
 namespace moe {
 namespace {
 
-constexpr int kSlotKeys = 32;  // keys of a slot of the ring
+// Keys of a slot of the ring.  Slots that are free earlier against the pipe's stop at each commit: 64 ragged sequences of 128 heads
+// with 16 keys 136 us, with 32 127, with the unit's 64 132; a chunk of 509 tokens 400, 363, 371.
+constexpr int kSlotKeys = 32;
 // Keys that a tile's beginning and end count for: 64 ragged sequences of 128 heads 128 us, with 128 keys 131, with 768 139; four
 // sequences' 48 rows and one tile of 131071 keys take the same with 128 to 768.
 constexpr int kExtra1 = 128, kExtra2 = 256;
@@ -52,7 +61,7 @@ struct LatCfg {
     static constexpr int kTile = ROWS * CL;                      // rows of a tile
     static constexpr int kBlocks = (kMaxLatent + kMaxLatentRot) / 64;
     static constexpr int kSlots = KEYS / kSlotKeys;              // of a unit
-    static constexpr int kUnits = (ROWS == 64 ? 4 : 5) / kSlots; // of the ring
+    static constexpr int kUnits = (ROWS == 64 ? 128 : 160) / KEYS;  // of the ring
     static constexpr int kS = 128 / KEYS;                        // buffers of S: units that S may be ahead
     static constexpr int kPs = 64 / KEYS;                        // buffers of P, side by side in rows of 128 bytes
     static constexpr int kQBlock = ROWS * 128;                   // bytes: ROWS queries of 64 components
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                         for (int x = 0; x < parts; ++x)
                             mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, v + (x * 2048 >> 4), pd + ((p.slot * 64 + k * 32) >> 4), idesc16<T>(128, ROWS, false, true),
                                           j > 0 || k > 0);
-                        if (k & 1) commit_all<CL>(empty + in.slot * C::kSlots + k / 2);
+                        if ((16 * k + 16) % kSlotKeys == 0) commit_all<CL>(empty + in.slot * C::kSlots + 16 * k / kSlotKeys);
                     }
                     mma_commit<1>(o_done + p.slot);
                 }
@@ -392,7 +401,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (lane / 4 == x) {          // outside the map: zeros
+                    if (8 * lane / kSlotKeys == x) {  // outside the map: zeros
                         const int page = static_cast<unsigned>(id) < static_cast<unsigned>(kv.n_pages) ? id : kv.n_pages, y = seen ? row : 0;
                         if (lane == cut) load_rows<false>(dst, &map, wide, blocks, y, page, smem_u32(cut_in), policy);
                         else if (CL == 1 || (lane & 1) == rank) load_rows<CL == 2>(dst, &map, wide, blocks, y, page, smem_u32(there), policy);
@@ -936,6 +945,15 @@ cudaError_t launch_r(LatentArgs a, int dtype, int64_t rows, int n_ctas, cudaStre
     return launch_in_stream(latent_join_kernel<T, C::kTile>, dim3(groups - 1, kJoinTurns), kJoinWarps * 32, 0, 1, st, a);
 }
 
+// The fewest rows of a CTA that hold a token's (what is computed for rows that do not count costs time), pairs where one CTA
+// does not hold them, units of 64 keys for pairs (an S of 32 keys takes almost as long as one of 64, but a ring of more and
+// shorter units hides the keys' way better where that is what it waits for).  us, 64 ragged sequences | one of 131071:
+//   16 heads   ROWS 16 65.2 | 37.4, 32 66.7 | 37.9;  units of 64 69.6 | 40.1
+//   32 heads   ROWS 32 69.1 | 38.4, 64 73.2 | 40.7;  units of 64 73.4 | 41.4
+//   64 heads   units of 32 84.3 | 44.3, of 64 84.9 | 44.0
+//   128 heads  pairs, units of 64 127.8 | 65.2, of 32 131.9 | 67.6; one CTA, units of 32 141.0 | 65.9, of 64 143.5 | 66.4
+// and of a chunk of 509 tokens of 32 heads: pairs 363, with units of 32 439; one CTA 372, with units of 64 390.  Pairs whose CTAs
+// bring all keys for themselves, without multicast: 138 (128 heads) and 377 (the chunk).
 template <typename T>
 cudaError_t launch_t(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
     if (rows <= 16) return launch_r<T, 16, 1, 32>(a, dtype, rows, n_ctas, st);
