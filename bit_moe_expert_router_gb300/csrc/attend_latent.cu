@@ -33,9 +33,9 @@
 // its own copies in flight.  The softmax warps meet at a barrier once per tile, whatever became of their waits, and leave
 // together.
 //
-// Measured, bf16, 512 + 64 components, device time with the join: one sequence of 131071 positions, 32 heads 38.1 us (4.0 TB/s;
-// 22 by its bytes), 64 ragged ones up to 16384 of 16, 32, 64, 128 heads 65, 69, 84, 127 us (5.3, 5.0, 4.1, 2.8 TB/s; 51 to 52 by
-// their bytes), 509 tokens of 32 heads at 8000 positions beside eight single ones 363 us (0.79 PFLOP/s; 145 by its operations).  A
+// Measured, bf16, 512 + 64 components, device time with the join: one sequence of 131071 positions, 32 heads 36.8 us (4.1 TB/s;
+// 22 by its bytes), 64 ragged ones up to 16384 of 16, 32, 64, 128 heads 63, 67, 81, 124 us (5.5, 5.1, 4.3, 2.8 TB/s; 51 to 52 by
+// their bytes), 509 tokens of 32 heads at 8000 positions beside eight single ones 357 us (0.80 PFLOP/s; 145 by its operations).  A
 // pair takes about 2800 cycles for 64 keys, of which the tensor pipe has work for 2130 (S 36 steps of 36, where 64 rows are
 // half of the pipe's width, O 16 of 52); the rest is the way from O's end through the empty slot and the copy to the next S,
 // for which the ring is too short.
@@ -53,7 +53,7 @@ constexpr int kSlotKeys = 32;
 // Keys that a tile's beginning and end count for: 64 ragged sequences of 128 heads 128 us, with 128 keys 131, with 768 139; four
 // sequences' 48 rows and one tile of 131071 keys take the same with 128 to 768.
 constexpr int kExtra1 = 128, kExtra2 = 256;
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4;
 
 // ROWS rows of a CTA, CL CTAs that share a tile of keys, which come in units of KEYS.
 template <int ROWS, int CL, int KEYS>
@@ -849,14 +849,17 @@ __device__ __forceinline__ void join_many(const LatentArgs& a, const CutTile<ROW
     join_finish<T, ROWS>(a, t, r, o, col, top, sum);
 }
 
-// The join of the pieces of the cut tiles.  Block (i, y) stands for the boundary before CTA i + 1; the items of a tile, eight rows, a
+// The join of the pieces of the cut tiles.  Block (i, y) stands for the boundary before CTA i + 1; the items of a tile, four rows, a
 // warp each, or where the pieces are many, 128 components of one row, are dealt over the blocks of the boundaries that cut it.  (One line of
 // all items for all blocks, found by sums over the boundaries, takes 2 us more.)  The sums' order goes by the pieces' CTAs alone, so two
 // runs give the same bits.
+// us of the whole call, four sequences' 48 rows | 64 sequences of 128 heads | 131071 positions: 4 warps a block 22.4 | 124.1 | 36.8, 2 warps
+// 22.4 | 128.9 | 40.0, 8 warps 24.7 | 124.8 | 36.6, 8 warps at 80 registers (3 blocks an SM, spilled) 24.1 | 127.2 | 38.3; one row a block from 5
+// pieces on 22.4 | 136.0 | 36.8, from 17 on 22.4 | 124.4 | 36.8; 4 blocks a boundary 23.3 | 129.3 | 37.0, 16 22.8 | 123.9 | 36.9.
 constexpr int kManyPieces = 9;
-constexpr int kJoinTurns = 8;  // blocks of a boundary: 4 and 16 take 1 us more on four sequences' 48 rows, 64 sequences of 128 rows
+constexpr int kJoinTurns = 8;  // blocks of a boundary
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kJoinWarps * 32, 3) latent_join_kernel(const __grid_constant__ LatentArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) latent_join_kernel(const __grid_constant__ LatentArgs a) {
     wait_for_stream();
     __shared__ float4 part[kJoinWarps][32];
     __shared__ float2 part_ml[kJoinWarps];
@@ -948,6 +951,7 @@ cudaError_t launch_r(LatentArgs a, int dtype, int64_t rows, int n_ctas, cudaStre
 // The fewest rows of a CTA that hold a token's (what is computed for rows that do not count costs time), pairs where one CTA
 // does not hold them, units of 64 keys for pairs (an S of 32 keys takes almost as long as one of 64, but a ring of more and
 // shorter units hides the keys' way better where that is what it waits for).  us, 64 ragged sequences | one of 131071:
+// (with a join that took 1.5 to 5 us more than now)
 //   16 heads   ROWS 16 65.2 | 37.4, 32 66.7 | 37.9;  units of 64 69.6 | 40.1
 //   32 heads   ROWS 32 69.1 | 38.4, 64 73.2 | 40.7;  units of 64 73.4 | 41.4
 //   64 heads   units of 32 84.3 | 44.3, of 64 84.9 | 44.0
