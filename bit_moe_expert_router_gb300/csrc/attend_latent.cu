@@ -35,10 +35,11 @@
 //
 // Measured, bf16, 512 + 64 components, device time with the join: one sequence of 131071 positions, 32 heads 36.8 us (4.1 TB/s;
 // 22 by its bytes), 64 ragged ones up to 16384 of 16, 32, 64, 128 heads 63, 67, 81, 124 us (5.5, 5.1, 4.3, 2.8 TB/s; 51 to 52 by
-// their bytes), 509 tokens of 32 heads at 8000 positions beside eight single ones 357 us (0.80 PFLOP/s; 145 by its operations).  A
+// their bytes), 509 tokens of 32 heads at 8000 positions beside eight single ones 359 us (0.80 PFLOP/s; 145 by its operations).  A
 // pair takes about 2800 cycles for 64 keys, of which the tensor pipe has work for 2130 (S 36 steps of 36, where 64 rows are
-// half of the pipe's width, O 16 of 52); the rest is the way from O's end through the empty slot and the copy to the next S,
-// for which the ring is too short.
+// half of the pipe's width, O 16 of 52).  In a timeline of two units, 5600 cycles, the pipe waits three times: about 370 twice for
+// the next unit's copy, which begins when O has left its slot (the ring is too short to have it earlier), and 790 for P, which
+// has one place and follows the other unit's O.  Banks of shared memory are read in 15.6 of 64 places a cycle and written in 5.5.
 #include <algorithm>
 
 #include "latent_common.cuh"
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         *begun = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    __syncwarp();
     if (warp == 0) tmem_alloc<1>(tmem_holder, C::kCols);
     wait_for_stream();
     if (blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
@@ -297,7 +299,12 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
     const int parts = (kv.d + 127) / 128;        // of the latent part: 128 components each, the last may reach behind it
     const uint32_t group = blocks * 1024, unit = KEYS / 8 * group;  // bytes of eight rows, of a unit
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t phase) { return ok = __all_sync(~0u, ok && wait_bar(bar, phase, ctl)); };
+    // (the lanes leave the loop one by one; what follows may be an instruction of the whole warp, as the accesses to tensor memory are)
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+        ok = __all_sync(~0u, ok && wait_bar(bar, phase, ctl));
+        __syncwarp();
+        return ok;
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- S = Q X^T
@@ -672,6 +679,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
 #pragma unroll 1
                     for (int y = 0; y < rows; y += kR) {
                         uint32_t o[kR];
+                        __syncwarp();
                         if constexpr (kR == 32) tmem_ld32(tmem + lane_base + C::kOCol + ROWS * x + y, o);
                         else tmem_ld16(tmem + lane_base + C::kOCol + ROWS * x + y, o);
                         tmem_ld_wait();
@@ -684,6 +692,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
 #pragma unroll 1
                 for (int y = 0; y < rows; y += 16) {
                     uint32_t o[16];
+                    __syncwarp();                     // (the lanes store different rows)
                     tmem_ld16(tmem + lane_base + C::kOCol + ROWS * x + y, o);
                     tmem_ld_wait();
                     tmem_tie<16>(o);

@@ -156,6 +156,12 @@ def test_a_thousand_heads_and_a_prompt_of_many_tiles():
     Case([700], [900], 8, 256, 64, 32, "fp16", seed=5).check()
 
 
+@pytest.mark.parametrize("h", [16, 32, 64, 128])
+def test_a_long_context(h):
+    """One sequence that fills the GPU by its keys alone: a piece of many units for each CTA or pair, every tile cut."""
+    Case([1], [131071], h, 512, 64, 64, seed=31).check()
+
+
 @pytest.mark.parametrize("lengths", ["long", "chunk"])
 def test_sharp_and_flat_scores(lengths):
     """A scale that leaves one key, one that leaves them all, and scores that grow along the sequence (the reference
