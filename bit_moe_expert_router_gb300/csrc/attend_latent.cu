@@ -8,38 +8,34 @@
 //
 // Bound: HBM while the rows are few (a row of the cache, 2 (Dc + R) bytes, does 2 (2 Dc + R) flops per head: the ridge is at
 // about 130 heads), the tensor pipe beyond.  A CTA takes a tile of ROWS = 16, 32 or 64 (token, head) rows, token-major,
-// against units of 32 or 64 keys, which come by TMA straight from the pages and are read from shared memory by both
-// products, so a cache row is brought once:
-//   S = Q X^T       64 rows (of which ROWS count) x KEYS keys, A = Q and B = X both along the components; fp32 in tensor
-//                   memory, two buffers or more, so that the next keys' S is computed during this one's softmax
+// against units of 32 keys, which come by TMA straight from the pages and are read from shared memory by both
+// products, so a CTA brings a cache row once:
+//   S = Q X^T       64 rows (of which ROWS count) x 32 keys, A = Q and B = X both along the components; fp32 in tensor
+//                   memory, four buffers, so that S is computed ahead of the softmax
 //   O^T += X^T P^T  turned over: 128 components of the latent part x ROWS rows, four times, A = X along the keys' other
 //                   direction (no transposition is needed), B = P.  The accumulator takes 4 ROWS columns of tensor memory,
 //                   where O of 128 rows x 512 components alone would fill all of it.
-// A softmax thread has the matrix-fragment places of S (two rows, KEYS / 4 values), four lanes and two warps a row.  P goes to
+// A softmax thread has the matrix-fragment places of S (two rows, 8 values), four lanes and two warps a row.  P goes to
 // shared memory in 16 bits.  The reference m is raised, and O rescaled, only when a row's maximum has grown by more than 2^8 over it.
 //
 // The keys come eight rows at a time with all their components, 9 KB that lie side by side in the cache, so that what DRAM opens
 // is read at once (boxes of 64 components x 64 rows stream at 3.3 TB/s, these at 5.6).  In shared memory such a group is
 // [block of 64 components][row], a swizzle atom each, so a product finds its next eight keys a group further, its next 64
-// components a KB further.  The ring has 128 keys (160 with few rows), free again in slots of 32 as O's products pass them.  From
-// 65 rows on two CTAs with 64 rows each share the units: each brings half of a unit into both (TMA multicast).
+// components a KB further.  The ring has 128 keys (160 with few rows).
 // Pages that are not there and rows past the last visible one read zeros, and rows behind it inside a group are
 // cleared by hand.  Work is dealt in equal shares of units; the pieces of a cut tile go through the workspace and the join.
 //
 // Warps: 0 the products S and the tensor-memory allocation, 3 the products O, each issued by one lane, so that neither waits
-// for what the other needs (one warp that looked at both: 64 ragged sequences of 128 heads 224 us, at that state 170); 1 the
-// keys, 2 the queries, 4 to 11 softmax and output, a warp for half of the keys of 16 rows, 12 what brings the keys to come into
-// L2.  Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
+// for what the other needs; 1 the keys, 2 the queries, 4 to 11 softmax and output, a warp for half of the keys of 16 rows.
+// Every wait is bounded; a timeout sets the status word and every role leaves, having waited (again with a limit) for
 // its own copies in flight.  The softmax warps meet at a barrier once per tile, whatever became of their waits, and leave
 // together.
 //
-// Measured, bf16, 512 + 64 components, device time with the join: one sequence of 131071 positions, 32 heads 36.8 us (4.1 TB/s;
-// 22 by its bytes), 64 ragged ones up to 16384 of 16, 32, 64, 128 heads 63, 67, 81, 124 us (5.5, 5.1, 4.3, 2.8 TB/s; 51 to 52 by
-// their bytes), 509 tokens of 32 heads at 8000 positions beside eight single ones 359 us (0.80 PFLOP/s; 145 by its operations).  A
-// pair takes about 2800 cycles for 64 keys, of which the tensor pipe has work for 2130 (S 36 steps of 36, where 64 rows are
-// half of the pipe's width, O 16 of 52).  In a timeline of two units, 5600 cycles, the pipe waits three times: about 370 twice for
-// the next unit's copy, which begins when O has left its slot (the ring is too short to have it earlier), and 790 for P, which
-// has one place and follows the other unit's O.  Banks of shared memory are read in 15.6 of 64 places a cycle and written in 5.5.
+// Measured, bf16, 512 + 64 components, device time with the join: one sequence of 131071 positions, 32 heads 38.1 us (4.0 TB/s;
+// 22 by its bytes), 64 ragged ones up to 16384 of 16, 32, 64, 128 heads 65, 69, 84, 140 us (5.3, 5.0, 4.2, 2.5 TB/s; 51 to 52 by
+// their bytes, which two CTAs read from 65 heads on), 509 tokens of 32 heads at 8000 positions beside eight single ones 367 us
+// (0.78 PFLOP/s; 145 by its operations).  The tensor pipe: S takes 36 steps of about 30 cycles for 32 keys, as 64 rows are half of its
+// width, O 8 of 52.
 #include <algorithm>
 
 #include "latent_common.cuh"
@@ -48,30 +44,23 @@
 namespace moe {
 namespace {
 
-// Keys of a slot of the ring.  Slots that are free earlier against the pipe's stop at each commit: 64 ragged sequences of 128 heads
-// with 16 keys 136 us, with 32 127, with the unit's 64 132; a chunk of 509 tokens 400, 363, 371.
-constexpr int kSlotKeys = 32;
-// Keys that a tile's beginning and end count for: 64 ragged sequences of 128 heads 128 us, with 128 keys 131, with 768 139; four
-// sequences' 48 rows and one tile of 131071 keys take the same with 128 to 768.
-constexpr int kExtra1 = 128, kExtra2 = 256;
-constexpr int kJoinWarps = 4;
+constexpr int kKeys = 32;  // of a unit: what a wait of the products is for
+// Keys that a tile's beginning and end count for in the deal: four sequences' 48 rows and one tile of 131071 keys take the same with 128 to 768.
+constexpr int kExtra = 128;
+constexpr int kJoinWarps = 8;
 
-// ROWS rows of a CTA, CL CTAs that share a tile of keys, which come in units of KEYS.
-template <int ROWS, int CL, int KEYS>
+// ROWS rows of a CTA.
+template <int ROWS>
 struct LatCfg {
-    static constexpr int kTile = ROWS * CL;                      // rows of a tile
     static constexpr int kBlocks = (kMaxLatent + kMaxLatentRot) / 64;
-    static constexpr int kSlots = KEYS / kSlotKeys;              // of a unit
-    static constexpr int kUnits = (ROWS == 64 ? 128 : 160) / KEYS;  // of the ring
-    static constexpr int kS = 128 / KEYS;                        // buffers of S: units that S may be ahead
-    static constexpr int kPs = 64 / KEYS;                        // buffers of P, side by side in rows of 128 bytes
+    static constexpr int kUnits = ROWS == 64 ? 4 : 5;            // of the ring
+    static constexpr int kS = 4;                                 // buffers of S: units that S may be ahead
+    static constexpr int kPs = 2;                                // buffers of P, side by side in rows of 128 bytes
     static constexpr int kQBlock = ROWS * 128;                   // bytes: ROWS queries of 64 components
     static constexpr int kQ = kBlocks * kQBlock;
     static constexpr int kP = ROWS * 128;
-    static constexpr int kRing = kUnits * KEYS * kBlocks * 128;
-    static constexpr bool kPrefetch = CL == 2;
-    static constexpr int kThreads = kPrefetch ? 416 : 384;
-    static constexpr int kAhead = 256 / KEYS;                    // units between the copies and their prefetch into L2
+    static constexpr int kRing = kUnits * kKeys * kBlocks * 128;
+    static constexpr int kThreads = 384;
     static constexpr int kOCol = 0, kSCol = 4 * ROWS, kCols = 512;
     static constexpr int kOffQ = 0;
     // (S is of 64 rows of Q: where ROWS is less, the MMA reads what lies behind them, at most 6 KB behind Q's end, into
@@ -79,31 +68,22 @@ struct LatCfg {
     static constexpr int kOffP = kQ;
     static constexpr int kOffRing = kOffP + kP;
     static constexpr int kOffBars = kOffRing + kRing;
-    static constexpr int kBars = kUnits * (kSlots + 1) + 2 * kS + 2 * kPs + 6;
+    static constexpr int kBars = 2 * kUnits + 2 * kS + 2 * kPs + 6;
     static constexpr int kOffAt = (kOffBars + 8 * kBars + 15) & ~15;   // [ROWS] where an output row begins
     static constexpr int kOffFactor = kOffAt + 8 * ROWS;               // [ROWS] what O's rows are multiplied by
     static constexpr int kOffEx = kOffFactor + 4 * ROWS;               // [2][ROWS] what the halves of a row tell one another
     static constexpr int kOffMisc = kOffEx + 8 * ROWS;
     static constexpr int kOffStart = kOffMisc + 16;                    // the cursor at the share's beginning
     static constexpr int kSmem = kOffStart + sizeof(Cursor);
-    static_assert(kSCol + kS * KEYS <= kCols, "tensor-memory columns");
+    static_assert(kSCol + kS * kKeys <= kCols, "tensor-memory columns");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// 16 lanes x COLS columns of 32 bits, as the accumulator fragments of 16 x 8 matrices (no wait).
-template <int COLS>
+// 16 lanes x 16 columns of 32 bits, as the accumulator fragments of 16 x 8 matrices (no wait).
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* v) {
-    static_assert(COLS == 16 || COLS == 32, "of a warp");
-    if constexpr (COLS == 32)
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-              "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-            : "r"(taddr));
-    else
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                     : "r"(taddr));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
 }
 
 // Barrier 1 of the 256 softmax threads: plain, or with the OR of a predicate.
@@ -146,15 +126,6 @@ __device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// One arrival on `bar` of both CTAs of a pair when every MMA issued so far has finished (CL = 1: on the CTA's own).
-template <int CL>
-__device__ __forceinline__ void commit_all(uint64_t* bar) {
-    if constexpr (CL == 1) mma_commit<1>(bar);
-    else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(smem_u32(bar)),
-                     "h"(static_cast<uint16_t>(3)) : "memory");
-}
-
 // What is read once is the first to leave L2, where the pieces' sums have to stay.
 __device__ __forceinline__ uint64_t l2_policy(bool once) {
     uint64_t first, normal;
@@ -163,51 +134,24 @@ __device__ __forceinline__ uint64_t l2_policy(bool once) {
     return once ? first : normal;
 }
 
-// Eight rows of the cache into L2.
-__device__ __forceinline__ void prefetch_rows(const CUtensorMap* map, bool wide, int blocks, int row, int page, uint64_t policy) {
-    const uint64_t m = reinterpret_cast<uint64_t>(map);
-    if (wide) {
-        asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile.L2::cache_hint [%0, {%1, %2, %3, %4}], %5;\n" ::"l"(m), "r"(0), "r"(row), "r"(0), "r"(page),
-                     "l"(policy) : "memory");
-        return;
-    }
-    for (int b = 0; b < blocks; ++b)
-        asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n" ::"l"(m), "r"(64 * b), "r"(row), "r"(page) : "memory");
-}
-
 // Eight rows of the cache, all their 64-component blocks, [block][row] -> shared memory; counted on `bar`.  WIDE: a box
-// has all blocks (rows of whole blocks), else one box each.  BOTH: into both CTAs of a pair, counted on each one's barrier.
-template <bool BOTH>
+// has all blocks (rows of whole blocks), else one box each.
 __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, bool wide, int blocks, int row, int page, uint32_t bar, uint64_t policy) {
-    const uint64_t m = reinterpret_cast<uint64_t>(map);
     if (wide) {
-        if constexpr (BOTH)
-            asm volatile(
-                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3, %4, "
-                "%5}], [%6], %7, %8;\n" ::"r"(dst), "l"(m), "r"(0), "r"(row), "r"(0), "r"(page), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(policy) : "memory");
-        else
-            asm volatile(
-                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], "
-                "%7;\n" ::"r"(dst), "l"(m), "r"(0), "r"(row), "r"(0), "r"(page), "r"(bar), "l"(policy) : "memory");
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], "
+            "%7;\n" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(page), "r"(bar), "l"(policy) : "memory");
         return;
     }
-    for (int b = 0; b < blocks; ++b) {
-        if constexpr (BOTH)
-            asm volatile(
-                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], "
-                "%6;\n" ::"r"(dst + b * 1024), "l"(m), "r"(64 * b), "r"(row), "r"(page), "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
-        else
-            tma_tile3d<1>(dst + b * 1024, map, 64 * b, row, page, bar);
-    }
+    for (int b = 0; b < blocks; ++b) tma_tile3d<1>(dst + b * 1024, map, 64 * b, row, page, bar);
 }
 
 // The rows of the CTA's whole tiles that ended with a NaN, taken again one by one by the softmax warps.
-template <typename T, int ROWS, int CL, int KEYS>
-__device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int rank, int warp) {
-    constexpr int kTile = ROWS * CL;
+template <typename T, int ROWS>
+__device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int warp) {
     const int lane = threadIdx.x & 31;
     while (c.u < c.end) {
-        const int r0 = c.rt * kTile + ROWS * rank;
+        const int r0 = c.rt * ROWS;
         const int rows = c.whole() ? min(c.s.q_len * a.kv.group - r0, ROWS) : 0;
         for (int r = warp; r < rows; r += 8) {
             int tok, head;
@@ -224,17 +168,17 @@ __device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int rank
             }
             if (__any_sync(~0u, odd)) latent_row<T>(a, c.b, c.s.q0 + tok, head, c.s.pos0 + tok);
         }
-        deal_next<kTile, KEYS>(a, c);
+        deal_next<ROWS, kKeys>(a, c);
     }
 }
 
-template <typename T, int ROWS, int CL, int KEYS>
-__global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
     attend_latent_kernel(const __grid_constant__ LatentArgs a, int wide, int q_rows, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
-    using C = LatCfg<ROWS, CL, KEYS>;
+    using C = LatCfg<ROWS>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t* empty = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [slots of the ring] MMA commit of each CTA: the slot is read
-    uint64_t* full = empty + C::kUnits * C::kSlots;  // [units of the ring] the unit's bytes have landed
+    uint64_t* empty = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [units of the ring] MMA commit: the unit is read
+    uint64_t* full = empty + C::kUnits;      // [units of the ring] the unit's bytes have landed
     uint64_t* s_full = full + C::kUnits;     // [kS] MMA commit: S is there
     uint64_t* s_free = s_full + C::kS;       // [kS] the softmax warps: S is read
     uint64_t* p_full = s_free + C::kS;       // [kPs] the softmax warps: P is there, O rescaled
@@ -247,7 +191,6 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
     int* odd = abort_flag + 1;               // some row of a whole tile ended with a NaN
-    volatile uint32_t* begun = reinterpret_cast<uint32_t*>(odd + 1);  // units whose copies are begun
     int64_t* row_at = reinterpret_cast<int64_t*>(smem + C::kOffAt);
     float* factor = reinterpret_cast<float*>(smem + C::kOffFactor);
     float* ex = reinterpret_cast<float*>(smem + C::kOffEx);
@@ -260,8 +203,10 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < C::kUnits * C::kSlots; ++i) mbar_init(empty + i, CL);
-        for (int i = 0; i < C::kUnits; ++i) mbar_init(full + i, 1);
+        for (int i = 0; i < C::kUnits; ++i) {
+            mbar_init(empty + i, 1);
+            mbar_init(full + i, 1);
+        }
         for (int i = 0; i < C::kS; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(s_free + i, 8);
@@ -277,27 +222,24 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         mbar_init(done, 1);
         mbar_init(done + 1, 1);
         *abort_flag = *odd = 0;
-        *begun = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     __syncwarp();
     if (warp == 0) tmem_alloc<1>(tmem_holder, C::kCols);
     wait_for_stream();
     if (blockIdx.x == 0 && tid == 0) a.hdr->status = kDevOk;
-    const int rank = CL == 2 ? blockIdx.x & 1 : 0, me = blockIdx.x / CL;
     Cursor c;
-    deal_begin<C::kTile, KEYS>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 1, (CL == 2 ? kExtra2 : kExtra1) / KEYS, me, gridDim.x / CL, c);  // (scratch: the ring)
+    deal_begin<ROWS, kKeys>(a, reinterpret_cast<long long*>(smem + C::kOffRing), 1, kExtra / kKeys, blockIdx.x, gridDim.x, c);  // (scratch: the ring)
     if (tid == 0) *reinterpret_cast<Cursor*>(smem + C::kOffStart) = c;
     clear_stray_rows<T>(a);  // (kv.d is what the outputs have)
     tc_fence_before();
     fence_async_proxy();  // the scratch was written through the generic proxy, the ring is written by TMA
     __syncthreads();
-    if constexpr (CL == 2) cluster_sync();  // the peer's barriers are there
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(~0u, *tmem_holder, 0);
     const int blocks = (a.dk + 63) / 64;         // of a row of the cache, 64 components each
     const int parts = (kv.d + 127) / 128;        // of the latent part: 128 components each, the last may reach behind it
-    const uint32_t group = blocks * 1024, unit = KEYS / 8 * group;  // bytes of eight rows, of a unit
+    const uint32_t group = blocks * 1024, unit = kKeys / 8 * group;  // bytes of eight rows, of a unit
     bool ok = true;
     // (the lanes leave the loop one by one; what follows may be an instruction of the whole warp, as the accesses to tensor memory are)
     auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -320,11 +262,11 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 if (!wait(s_free + s.slot, s.phase ^ 1) || !wait(full + in.slot, in.phase)) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t s_col = tmem + C::kSCol + KEYS * s.slot;
+                    const uint32_t s_col = tmem + C::kSCol + kKeys * s.slot;
                     uint64_t q = qd, k = kd + ((in.slot * unit) >> 4);
                     for (int x = 0; x < blocks; ++x, q += C::kQBlock >> 4, k += 1024 >> 4) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f16_ss<1>(s_col, q + 2 * i, k + 2 * i, idesc16<T>(64, KEYS, false), x > 0 || i > 0);
+                        for (int i = 0; i < 4; ++i) mma_f16_ss<1>(s_col, q + 2 * i, k + 2 * i, idesc16<T>(64, kKeys, false), x > 0 || i > 0);
                     }
                     mma_commit<1>(s_full + s.slot);
                     if (j + 1 == n) mma_commit<1>(q_free);
@@ -334,7 +276,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 s.next();
             }
             ++items;
-            deal_next<C::kTile, KEYS>(a, c);
+            deal_next<ROWS, kKeys>(a, c);
         }
         if (leader) mma_commit<1>(done);
         __syncwarp();
@@ -354,12 +296,12 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 if (leader) {
                     uint64_t v = vd + ((in.slot * unit) >> 4);
 #pragma unroll
-                    for (int k = 0; k < KEYS / 16; ++k, v += 2 * group >> 4) {  // 16 keys, 128 components at a time
+                    for (int k = 0; k < kKeys / 16; ++k, v += 2 * group >> 4) {  // 16 keys, 128 components at a time
                         for (int x = 0; x < parts; ++x)
                             mma_f16_ss<1>(tmem + C::kOCol + ROWS * x, v + (x * 2048 >> 4), pd + ((p.slot * 64 + k * 32) >> 4), idesc16<T>(128, ROWS, false, true),
                                           j > 0 || k > 0);
-                        if ((16 * k + 16) % kSlotKeys == 0) commit_all<CL>(empty + in.slot * C::kSlots + 16 * k / kSlotKeys);
                     }
+                    mma_commit<1>(empty + in.slot);
                     mma_commit<1>(o_done + p.slot);
                 }
                 __syncwarp();
@@ -367,7 +309,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 p.next();
             }
             ++items;
-            deal_next<C::kTile, KEYS>(a, c);
+            deal_next<ROWS, kKeys>(a, c);
         }
         if (leader) mma_commit<1>(done + 1);
         __syncwarp();
@@ -379,27 +321,23 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         const uint32_t ring = smem_u32(smem + C::kOffRing);
         while (ok && c.u < c.end) {
             int lo, hi;
-            const int r0 = c.rt * C::kTile;
-            key_range(kv, 0, c.s, r0, min(r0 + C::kTile, c.s.q_len * kv.group), lo, hi);
-            const uint64_t policy = l2_policy(c.s.q_len * kv.group <= C::kTile);
+            const int r0 = c.rt * ROWS;
+            key_range(kv, 0, c.s, r0, min(r0 + ROWS, c.s.q_len * kv.group), lo, hi);
+            const uint64_t policy = l2_policy(c.s.q_len * kv.group <= ROWS);
             for (int j = 0; j < c.take && ok; ++j) {
-                const int key0 = (c.first + c.off + j) * KEYS, key = key0 + 8 * lane;
+                const int key0 = (c.first + c.off + j) * kKeys, key = key0 + 8 * lane;
                 const int p = div_by(max(key, 0), kv.by_page), row = key - p * kv.page;
-                const bool seen = lane < KEYS / 8 && key < hi && p < kv.width;
+                const bool seen = lane < kKeys / 8 && key < hi && p < kv.width;
                 // (looked at when the slot is free)
                 const int id = seen ? __ldg(kv.table + static_cast<int64_t>(c.b) * kv.width + p) : -1;
                 const int last = hi - key0;       // rows that some row of the tile sees
-                // eight rows of which some are seen: those behind are cleared before the products may read them; in a
-                // pair each CTA brings these for itself
-                const int cut = last > 0 && last < KEYS && last % 8 != 0 ? last / 8 : -1;
+                // eight rows of which some are seen: those behind are cleared before the products may read them
+                const int cut = last > 0 && last < kKeys && last % 8 != 0 ? last / 8 : -1;
                 uint64_t* there = full + in.slot;
                 const uint32_t dst = ring + in.slot * unit + lane * group;
                 ++uses;
-                if (C::kPrefetch && lane == 0) *begun = uses;
-#pragma unroll
-                for (int x = 0; x < C::kSlots; ++x) {
-                    if (!wait(empty + in.slot * C::kSlots + x, in.phase ^ 1)) break;
-                    if (x == 0 && lane == 0) {
+                if (wait(empty + in.slot, in.phase ^ 1)) {
+                    if (lane == 0) {
                         if (cut < 0) {
                             arrive_expect(there, unit);
                         } else {
@@ -408,19 +346,17 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (8 * lane / kSlotKeys == x) {  // outside the map: zeros
+                    if (lane < kKeys / 8) {       // outside the map: zeros
                         const int page = static_cast<unsigned>(id) < static_cast<unsigned>(kv.n_pages) ? id : kv.n_pages, y = seen ? row : 0;
-                        if (lane == cut) load_rows<false>(dst, &map, wide, blocks, y, page, smem_u32(cut_in), policy);
-                        else if (CL == 1 || (lane & 1) == rank) load_rows<CL == 2>(dst, &map, wide, blocks, y, page, smem_u32(there), policy);
+                        load_rows(dst, &map, wide, blocks, y, page, smem_u32(lane == cut ? cut_in : there), policy);
                     }
                 }
                 __syncwarp();
-                if (cut >= 0) {
-                    // (also when a slot was not to be had: the copy may be under way)
+                if (ok && cut >= 0) {
                     const bool got = __all_sync(~0u, wait_bar(cut_in, cuts & 1, ctl));
                     if (!got) drain_bar(cut_in, cuts & 1, global_ns() + kWaitNs);
                     ++cuts;
-                    ok = ok && got;
+                    ok = got;
                     if (!ok) break;
                     const int first = last % 8, per = (8 - first) * 8;
                     uint8_t* at = smem + C::kOffRing + in.slot * unit + cut * group + first * 128;
@@ -431,15 +367,14 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 }
                 in.next();
             }
-            deal_next<C::kTile, KEYS>(a, c);
+            deal_next<ROWS, kKeys>(a, c);
         }
-        if (C::kPrefetch && lane == 0) *begun = 1u << 30;  // (past all units: nothing waits for more)
         // Nothing is on its way to this CTA's memory when it leaves: the ring's last units have landed and been read (or, after
         // a timeout, the limit has passed).
         const uint64_t end = global_ns() + kWaitNs;
         for (uint32_t u = uses > C::kUnits ? uses - C::kUnits : 0; u < uses; ++u) {
             drain_bar(full + u % C::kUnits, u / C::kUnits & 1, end);
-            for (int x = 0; x < C::kSlots; ++x) drain_bar(empty + u % C::kUnits * C::kSlots + x, u / C::kUnits & 1, end);
+            drain_bar(empty + u % C::kUnits, u / C::kUnits & 1, end);
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------- the queries
@@ -447,7 +382,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
         while (ok && c.u < c.end) {
             if (!wait(q_free, (items & 1) ^ 1)) break;
             ++items;
-            const int r0 = c.rt * C::kTile + ROWS * rank, rows = min(c.s.q_len * kv.group - r0, ROWS);  // (a pair's second CTA may have none)
+            const int r0 = c.rt * ROWS, rows = min(c.s.q_len * kv.group - r0, ROWS);
             if (q_rows) {  // a box of ROWS rows for each block; rows past the sequence's are whatever follows
                 if (lane == 0) {
                     int tok, head;
@@ -457,7 +392,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                     for (int x = 0; x < blocks; ++x) tma_tile3d<1>(smem_u32(smem + C::kOffQ) + x * C::kQBlock, &qmap, 64 * x, y, z, own_bar(q_full));
                 }
                 __syncwarp();
-                deal_next<C::kTile, KEYS>(a, c);
+                deal_next<ROWS, kKeys>(a, c);
                 continue;
             }
             // where the rows begin: each lane finds its rows' places once, then passes them round
@@ -482,47 +417,24 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) arrive_own(q_full);
-            deal_next<C::kTile, KEYS>(a, c);
+            deal_next<ROWS, kKeys>(a, c);
         }
         if (items) {  // (its arrival, too, has come; after a timeout the queries may still be on their way)
             drain_bar(q_full, (items - 1) & 1, global_ns() + kWaitNs);
             drain_bar(q_free, (items - 1) & 1, global_ns() + kWaitNs);
         }
-    } else if (C::kPrefetch && warp == 12) {
-        // ---------------------------------------------------------------- the keys to come, into L2: the ring is too short for DRAM's way
-        uint32_t u = 0;
-        while (c.u < c.end) {
-            int lo, hi;
-            const int r0 = c.rt * C::kTile;
-            key_range(kv, 0, c.s, r0, min(r0 + C::kTile, c.s.q_len * kv.group), lo, hi);
-            const uint64_t policy = l2_policy(c.s.q_len * kv.group <= C::kTile);
-            for (int j = 0; j < c.take; ++j, ++u) {
-                const int key = (c.first + c.off + j) * KEYS + 8 * lane;
-                const int p = div_by(max(key, 0), kv.by_page);
-                const bool mine = lane < KEYS / 8 && key < hi && p < kv.width && (CL == 1 || (lane & 1) == rank);
-                const int id = mine ? __ldg(kv.table + static_cast<int64_t>(c.b) * kv.width + p) : -1;
-                uint32_t now;
-                // (not before the ring has gone round once: what it waits for comes first; ends, because the loader's waits do)
-                while (((now = *begun) + C::kAhead <= u || now <= C::kUnits) && !*ctl.abort) __nanosleep(50);
-                if (*ctl.abort) break;
-                if (now <= u && static_cast<unsigned>(id) < static_cast<unsigned>(kv.n_pages)) prefetch_rows(&map, wide, blocks, key - p * kv.page, id, policy);
-                __syncwarp();
-            }
-            if (*ctl.abort) break;
-            deal_next<C::kTile, KEYS>(a, c);
-        }
     } else {
         // ---------------------------------------------------------------- softmax and output
         const int w = warp & 3;                   // S: rows 16 w ..; O^T: components 32 w .. of each 128
-        const int half = warp / 4 - 1;            // S: keys KEYS / 2 half ..; O^T: every second 128 components
-        constexpr int kN = KEYS / 4;              // values of S of a thread
+        const int half = warp / 4 - 1;            // S: keys kKeys / 2 half ..; O^T: every second 128 components
+        constexpr int kN = kKeys / 4;              // values of S of a thread
         const uint32_t lane_base = static_cast<uint32_t>(32 * w) << 16;
         const float sc = a.scale * kLog2e;
         Place<C::kS> sb;
         Place<C::kPs> pb, before;                 // P's place, and that of the unit before
         while (ok && c.u < c.end) {
             const int n = c.take;
-            const int r0 = c.rt * C::kTile + ROWS * rank, rows = min(c.s.q_len * kv.group - r0, ROWS);  // (a pair's second CTA may have none)
+            const int r0 = c.rt * ROWS, rows = min(c.s.q_len * kv.group - r0, ROWS);
             const bool live = 16 * w < rows;
             int pos[2];                           // of this thread's rows: 16 w + lane / 4, and 8 on
 #pragma unroll
@@ -543,7 +455,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 bool grew = false;
                 if (ok && live) {
                     tc_fence_after();
-                    tmem_ld_frag<KEYS / 2>(tmem + lane_base + C::kSCol + KEYS * sb.slot + KEYS / 2 * half, v);
+                    tmem_ld_frag(tmem + lane_base + C::kSCol + kKeys * sb.slot + kKeys / 2 * half, v);
                     tmem_ld_wait();
                     tmem_tie<kN>(v);
                     tc_fence_before();
@@ -552,8 +464,8 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                 if (ok && lane == 0) arrive_own(s_free + sb.slot);
                 sb.next();
                 if (ok && live) {
-                    const int key0 = (c.first + c.off + j) * KEYS + KEYS / 2 * half;
-                    if (key0 + KEYS / 2 - 1 > all) {
+                    const int key0 = (c.first + c.off + j) * kKeys + kKeys / 2 * half;
+                    if (key0 + kKeys / 2 - 1 > all) {
 #pragma unroll
                         for (int i = 0; i < kN; ++i)
                             if (key0 + 8 * (i / 4) + 2 * (lane & 3) + (i & 1) > pos[i >> 1 & 1]) v[i] = __float_as_uint(kNegInf);
@@ -617,12 +529,12 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
                         const int r = 16 * w + lane / 4 + 8 * x;
                         uint8_t* at = smem + C::kOffP + r * 128 + (lane & 3) * 4;
 #pragma unroll
-                        for (int i = 0; i < KEYS / 16; ++i) {
+                        for (int i = 0; i < kKeys / 16; ++i) {
                             const float p0 = exp2_fast(fmaf(__uint_as_float(v[4 * i + 2 * x]), sc, -base));
                             const float p1 = exp2_fast(fmaf(__uint_as_float(v[4 * i + 2 * x + 1]), sc, -base));
                             l[x] += p0 + p1;
                             // the product's operand: 16 bits; the sum l is of the fp32 values
-                            *reinterpret_cast<uint32_t*>(at + (((4 * pb.slot + KEYS / 16 * half + i) ^ (r & 7)) << 4)) = Elem<T>::pack(p0, p1);
+                            *reinterpret_cast<uint32_t*>(at + (((4 * pb.slot + kKeys / 16 * half + i) ^ (r & 7)) << 4)) = Elem<T>::pack(p0, p1);
                         }
                     }
                     fence_async_proxy();
@@ -641,7 +553,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             // ------------------------------------------------------------ the tile's output
             tc_fence_after();
             const bool whole = c.whole();
-            const int64_t part0 = (2 * static_cast<int64_t>(me) + (c.u == c.begin ? 0 : 1)) * C::kTile + ROWS * rank;  // its first row among the pieces'
+            const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (c.u == c.begin ? 0 : 1)) * ROWS;  // its first row among the pieces'
             if (live) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -714,14 +626,13 @@ __global__ void __launch_bounds__(LatCfg<ROWS, CL, KEYS>::kThreads, 1)
             if (bad) *odd = 1;
             softmax_sync();                           // (`factor` and `row_at` are read)
             if (lane == 0) arrive_own(o_free);
-            deal_next<C::kTile, KEYS>(a, c);
+            deal_next<ROWS, kKeys>(a, c);
         }
-        if (ok && *odd) retake_rows<T, ROWS, CL, KEYS>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), rank, warp - 4);
+        if (ok && *odd) retake_rows<T, ROWS>(a, *reinterpret_cast<const Cursor*>(smem + C::kOffStart), warp - 4);
     }
 
     tc_fence_before();
     __syncthreads();
-    if constexpr (CL == 2) cluster_sync();  // nothing of the peer's comes any more
     if (warp == 0) {
         tc_fence_after();
         tmem_free<1>(tmem, C::kCols);
@@ -858,17 +769,14 @@ __device__ __forceinline__ void join_many(const LatentArgs& a, const CutTile<ROW
     join_finish<T, ROWS>(a, t, r, o, col, top, sum);
 }
 
-// The join of the pieces of the cut tiles.  Block (i, y) stands for the boundary before CTA i + 1; the items of a tile, four rows, a
+// The join of the pieces of the cut tiles.  Block (i, y) stands for the boundary before CTA i + 1; the items of a tile, eight rows, a
 // warp each, or where the pieces are many, 128 components of one row, are dealt over the blocks of the boundaries that cut it.  (One line of
 // all items for all blocks, found by sums over the boundaries, takes 2 us more.)  The sums' order goes by the pieces' CTAs alone, so two
 // runs give the same bits.
-// us of the whole call, four sequences' 48 rows | 64 sequences of 128 heads | 131071 positions: 4 warps a block 22.4 | 124.1 | 36.8, 2 warps
-// 22.4 | 128.9 | 40.0, 8 warps 24.7 | 124.8 | 36.6, 8 warps at 80 registers (3 blocks an SM, spilled) 24.1 | 127.2 | 38.3; one row a block from 5
-// pieces on 22.4 | 136.0 | 36.8, from 17 on 22.4 | 124.4 | 36.8; 4 blocks a boundary 23.3 | 129.3 | 37.0, 16 22.8 | 123.9 | 36.9.
 constexpr int kManyPieces = 9;
-constexpr int kJoinTurns = 8;  // blocks of a boundary
+constexpr int kJoinTurns = 8;  // blocks of a boundary: 4 and 16 take 1 us more on four sequences' 48 rows
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kJoinWarps * 32, 4) latent_join_kernel(const __grid_constant__ LatentArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) latent_join_kernel(const __grid_constant__ LatentArgs a) {
     wait_for_stream();
     __shared__ float4 part[kJoinWarps][32];
     __shared__ float2 part_ml[kJoinWarps];
@@ -931,15 +839,15 @@ int make_qmap(const LatentArgs& a, int dtype, CUtensorMap* map, cudaError_t* err
     return uniform ? 1 : 2;
 }
 
-// Up to so many positions a row tile stays with one CTA (pair): the pieces' way through memory and the second kernel cost more than
+// Up to so many positions a row tile stays with one CTA: the pieces' way through memory and the second kernel cost more than
 // the keys' streaming by one.  Few tiles: one sequence of 16 heads, whole | split, 100 positions 9.6 | 10.5 us, 200 11.9 | 11.0.  Tiles
-// for half of the GPU and more: 64 sequences of 128 heads at 500 29 | 39 us, 32 26 | 27, 8 25 | 18; 32 of 16 heads (a fifth of
-// the GPU) 19.5 | 16.6.
+// for half of the GPU and more: 64 sequences of 128 heads at 500 30.6 us, split 39; 32 of 16 heads (a fifth of the GPU) split
+// 16.3, whole 19.5.
 constexpr int64_t kWholeKeys = 128, kWholeKeysMany = 1024;
 
-template <typename T, int ROWS, int CL, int KEYS>
+template <typename T, int ROWS>
 cudaError_t launch_r(LatentArgs a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
-    using C = LatCfg<ROWS, CL, KEYS>;
+    using C = LatCfg<ROWS>;
     const bool wide = a.dk % 64 == 0;
     CUtensorMap map;
     if (cudaError_t e = make_map(a, dtype, wide, &map); e != cudaSuccess) return e;
@@ -947,32 +855,27 @@ cudaError_t launch_r(LatentArgs a, int dtype, int64_t rows, int n_ctas, cudaStre
     cudaError_t e = cudaSuccess;
     const int q_rows = make_qmap<ROWS>(a, dtype, &qmap, &e);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS, CL, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(attend_latent_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    const int groups = n_ctas / CL;
-    const bool many = 2 * a.kv.n_seqs * ((rows + C::kTile - 1) / C::kTile) >= groups;
-    a.split = groups > 1 && a.max_keys > (many ? kWholeKeysMany : kWholeKeys);
-    e = launch_in_stream(attend_latent_kernel<T, ROWS, CL, KEYS>, dim3(groups * CL), C::kThreads, C::kSmem, CL, st, a, wide ? 1 : 0, q_rows, map, qmap);
+    const bool many = 2 * a.kv.n_seqs * ((rows + ROWS - 1) / ROWS) >= n_ctas;
+    a.split = n_ctas > 1 && a.max_keys > (many ? kWholeKeysMany : kWholeKeys);
+    e = launch_in_stream(attend_latent_kernel<T, ROWS>, dim3(n_ctas), C::kThreads, C::kSmem, 1, st, a, wide ? 1 : 0, q_rows, map, qmap);
     if (e != cudaSuccess || !a.split) return e;
-    return launch_in_stream(latent_join_kernel<T, C::kTile>, dim3(groups - 1, kJoinTurns), kJoinWarps * 32, 0, 1, st, a);
+    return launch_in_stream(latent_join_kernel<T, ROWS>, dim3(n_ctas - 1, kJoinTurns), kJoinWarps * 32, 0, 1, st, a);
 }
 
-// The fewest rows of a CTA that hold a token's (what is computed for rows that do not count costs time), pairs where one CTA
-// does not hold them, units of 64 keys for pairs (an S of 32 keys takes almost as long as one of 64, but a ring of more and
-// shorter units hides the keys' way better where that is what it waits for).  us, 64 ragged sequences | one of 131071:
-// (with a join that took 1.5 to 5 us more than now)
-//   16 heads   ROWS 16 65.2 | 37.4, 32 66.7 | 37.9;  units of 64 69.6 | 40.1
-//   32 heads   ROWS 32 69.1 | 38.4, 64 73.2 | 40.7;  units of 64 73.4 | 41.4
-//   64 heads   units of 32 84.3 | 44.3, of 64 84.9 | 44.0
-//   128 heads  pairs, units of 64 127.8 | 65.2, of 32 131.9 | 67.6; one CTA, units of 32 141.0 | 65.9, of 64 143.5 | 66.4
-// and of a chunk of 509 tokens of 32 heads: pairs 363, with units of 32 439; one CTA 372, with units of 64 390.  Pairs whose CTAs
-// bring all keys for themselves, without multicast: 138 (128 heads) and 377 (the chunk).
+// The fewest rows of a CTA that hold a token's, up to 64 (what is computed for rows that do not count costs time; more rows leave no
+// room for the keys).  us, 64 ragged sequences | one of 131071:
+//   16 heads   ROWS 16 65.2 | 37.4, 32 66.7 | 37.9;  units of 64 keys 69.6 | 40.1
+//   32 heads   ROWS 32 69.1 | 38.4, 64 73.2 | 40.7;  units of 64 keys 73.4 | 41.4
+//   64 heads   units of 32 keys 84.3 | 44.3, of 64 84.9 | 44.0
+//   128 heads  units of 32 keys 141.0 | 65.9, of 64 143.5 | 66.4
+// and a chunk of 509 tokens of 32 heads: units of 32 keys 372, of 64 390.
 template <typename T>
 cudaError_t launch_t(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st) {
-    if (rows <= 16) return launch_r<T, 16, 1, 32>(a, dtype, rows, n_ctas, st);
-    if (rows <= 32) return launch_r<T, 32, 1, 32>(a, dtype, rows, n_ctas, st);
-    if (rows <= 64 || n_ctas < 2) return launch_r<T, 64, 1, 32>(a, dtype, rows, n_ctas, st);
-    return launch_r<T, 64, 2, 64>(a, dtype, rows, n_ctas, st);
+    if (rows <= 16) return launch_r<T, 16>(a, dtype, rows, n_ctas, st);
+    if (rows <= 32) return launch_r<T, 32>(a, dtype, rows, n_ctas, st);
+    return launch_r<T, 64>(a, dtype, rows, n_ctas, st);
 }
 
 }  // namespace
