@@ -33,7 +33,7 @@
 //
 // Measured, bf16, 512 + 64 components, device time with the join: one sequence of 131071 positions, 32 heads 38.1 us (4.0 TB/s;
 // 22 by its bytes), 64 ragged ones up to 16384 of 16, 32, 64, 128 heads 65, 69, 84, 140 us (5.3, 5.0, 4.2, 2.5 TB/s; 51 to 52 by
-// their bytes, which two CTAs read from 65 heads on), 509 tokens of 32 heads at 8000 positions beside eight single ones 367 us
+// their bytes; from 65 heads on two CTAs read the same keys, from DRAM 1.7 times), 509 tokens of 32 heads at 8000 positions beside eight single ones 367 us
 // (0.78 PFLOP/s; 145 by its operations).  The tensor pipe: S takes 36 steps of about 30 cycles for 32 keys, as 64 rows are half of its
 // width, O 8 of 52.
 #include <algorithm>
