@@ -20,11 +20,13 @@
 // without groups 9.7, without a bias 7.5.  64 tokens of 160 experts 3.2 us, 4 of 512 with 10 chosen 4.0: the launch and the
 // chain of a warp's steps.
 //
-// Errors.  2^x and the quotient are the fast ones: s is off by at most s (2e-6 + 1.2e-7 |x - c|), c the largest
-// logit for softmax and 0 for the sigmoid (two units in 2^22 of the exponential, the argument's rounding, the
-// sum's and the quotient's), which is below 2.2e-6 times the largest score whatever x is: s |x - c| is at most
-// 0.37 of it (of a sigmoid above one half, only 1 - s is off by that factor).  For the experts on the list s is
-// computed anew with expf and a correctly rounded quotient, off by 4e-7 s.
+// Errors, with u = 2^-24 and d = |x - c|, c the largest logit for softmax and 0 for the sigmoid.  A fast exponential is off by 2^-22 of
+// itself and, from the argument's three roundings, 1.4e-7 d.  The softmax's sum of them is off by the mean of that over its terms, in which d
+// is ln E at most (the entropy), and (J + 4) u for the additions: kSum.  A fast score is off by kFast times the largest score at
+// most, its own exponential, the quotient and the product counted (the part in d is largest at d = 0, as e^-d falls faster than d grows; a
+// sigmoid has no sum and stays below).  For the experts on the list s is computed anew with expf and a correctly rounded
+// quotient, off by 4e-7 s and, for softmax, by d u and kSum, as it has the same sum: that factor is the same for all experts
+// of a token, but does not cancel against a bias.  Below the smallest normal number fp32 is off by more than a part of s; 1e-37 covers that.
 #include <algorithm>
 
 #include "attention_common.cuh"
@@ -182,6 +184,8 @@ __device__ __forceinline__ void sort_down(uint32_t (&s)[MAXJ]) {
 template <int MAXJ>
 __global__ void __launch_bounds__(32 * kWarps, MAXJ <= 8 ? 8 : MAXJ == 16 ? 7 : 4) route_scored_kernel(const __grid_constant__ RouteScoredArgs a) {
     constexpr int kBits = MAXJ == 1 ? 0 : MAXJ == 2 ? 1 : MAXJ == 4 ? 2 : MAXJ == 8 ? 3 : MAXJ == 16 ? 4 : 5;
+    // the errors of the head of this file; ln E <= ln (32 MAXJ) = 3.47 + 0.694 kBits
+    constexpr float kSum = 2.4e-7f + 1.4e-7f * (3.5f + 0.7f * kBits) + (MAXJ + 4) * 6e-8f, kFast = kSum + 5.4e-7f;
     const int lane = threadIdx.x & 31, lanes = 1 << a.lanes_log2;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     wait_for_stream();
@@ -279,6 +283,9 @@ __global__ void __launch_bounds__(32 * kWarps, MAXJ <= 8 ? 8 : MAXJ == 16 ? 7 : 
         if (by_r) {
             const float in = key_number(__reduce_min_sync(~0u, kept ? g : ~0u)), out = key_number(__reduce_max_sync(~0u, kept ? 0u : g));
             const float size = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(fabsf(b1) + fabsf(b2))));
+            // two scores each: the sum's and the quotient's factor moves their difference by 2 (kSum + 2.4e-7) big at most, the rest four
+            // scores by 3e-7 big; size: the roundings of the additions
+            static_assert(2 * (kSum + 2.4e-7f) + 4 * 3e-7f < 1e-5f, "the border's width");
             const float near = 1e-5f * big + 5e-7f * size;
             if (!(in - out > near)) {
                 // The groups' values in fp64, of the experts that make them: the largest, and the largest of the others.  Where the next
@@ -362,15 +369,17 @@ __global__ void __launch_bounds__(32 * kWarps, MAXJ <= 8 ? 8 : MAXJ == 16 ? 7 : 
     if (a.bias) {
         // Each place against the next: what stands in the wrong order is close to its neighbour; what should be on the list and
         // is not has a key no better than the first one's behind it.
-        constexpr float kCut = MAXJ * 1.2e-7f;  // the keys' low bits
-        const float re = se + be, err = 4e-7f * se + 1.2e-7f * fabsf(re);
-        const float loose = 2.2e-6f * big + se * (2e-6f + 1.2e-7f * fabsf(xe - m)) + kCut * fabsf(re);
+        constexpr float kCut = (MAXJ + 1) * 1.2e-7f;  // the keys' low bits, and the sums with a bias
+        const float far = fminf(fabsf(xe - m), 128.f);  // (from 104 on s is zero)
+        const float re = se + be, err = se * (softmax ? 4e-7f + kSum + 6e-8f * far : 4e-7f) + 1.2e-7f * fabsf(re) + 1e-37f;
+        const float loose = kFast * big + se * (2e-6f + 1.2e-7f * far) + kCut * fabsf(re);
         float up = __shfl_down_sync(~0u, re + (lane == a.k ? loose : err), 1);
         const float next_x = __shfl_down_sync(~0u, xe, 1), next_b = __shfl_down_sync(~0u, be, 1);
         bool there = next_e >= 0;
         if (lane == 31) {
             there = rest != 0;
-            up = key_number((rest + 1) << kBits) + 2.2e-6f * big;
+            up = key_number((rest + 1) << kBits);
+            up += kFast * big + 1.2e-7f * fabsf(up);
         }
         const bool same = !last && next_x == xe && next_b == be && next_e > e;
         doubt |= lane < a.k && there && !same && !(re - err > up);
@@ -386,7 +395,8 @@ __global__ void __launch_bounds__(32 * kWarps, MAXJ <= 8 ? 8 : MAXJ == 16 ? 7 : 
         int n = 32;
         if (settled && a.k < 24) {
             const float low = __shfl_sync(~0u, a.bias ? se + be : xe, a.k - 1);
-            // (nothing with a key below it can be among the best)
+            // (nothing with a key below it can be among the best: two fast scores' errors and the difference of a fast and a listed one)
+            static_assert(2 * kFast + 1e-6f < 1e-5f, "the limit's width");
             const float limit = a.bias ? low - (1e-5f * big + 4.f * MAXJ * 1.2e-7f * fabsf(low)) : low;
             for (n = a.k + 1; n < 32; ++n) {  // the lanes' lists go on
                 const uint32_t own = s[0] >> kBits, best = __reduce_max_sync(~0u, own);
