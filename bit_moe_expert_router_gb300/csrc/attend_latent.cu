@@ -17,6 +17,8 @@
 //                   where O of 128 rows x 512 components alone would fill all of it.
 // A softmax thread has the matrix-fragment places of S (two rows, 8 values), four lanes and two warps a row.  P goes to
 // shared memory in 16 bits.  The reference m is raised, and O rescaled, only when a row's maximum has grown by more than 2^8 over it.
+// In fp16 the weights are 2^7 times as large (m is 7 less in base 2): at most 2^15, which the type holds, and what it rounds away
+// begins at 2^-32 of the largest one, not at 2^-25.
 //
 // The keys come eight rows at a time with all their components, 9 KB that lie side by side in the cache, so that what DRAM opens
 // is read at once (boxes of 64 components x 64 rows stream at 3.3 TB/s, these at 5.6).  In shared memory such a group is
@@ -48,6 +50,11 @@ constexpr int kKeys = 32;  // of a unit: what a wait of the products is for
 // Keys that a tile's beginning and end count for in the deal: four sequences' 48 rows and one tile of 131071 keys take the same with 128 to 768.
 constexpr int kExtra = 128;
 constexpr int kJoinWarps = 8;
+// What m is less than the row's reference, in base 2.
+template <typename T>
+constexpr float kLift = 0.f;
+template <>
+constexpr float kLift<__half> = 7.f;
 
 // ROWS rows of a CTA.
 template <int ROWS>
@@ -525,7 +532,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                 if (ok && live) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float base = m[x] == kNegInf ? 0.f : m[x] * sc;
+                        const float base = m[x] == kNegInf ? 0.f : m[x] * sc - kLift<T>;
                         const int r = 16 * w + lane / 4 + 8 * x;
                         uint8_t* at = smem + C::kOffP + r * 128 + (lane & 3) * 4;
 #pragma unroll
@@ -572,11 +579,11 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                     factor[r] = sum == 0.f ? 0.f : 1.f / sum;
                     if (sum != sum) *odd = 1;
                     if (!whole) {
-                        a.part_ml[part0 + r] = make_float2(m[x] == kNegInf ? kNegInf : m[x] * sc, sum);
+                        a.part_ml[part0 + r] = make_float2(m[x] == kNegInf ? kNegInf : m[x] * sc - kLift<T>, sum);
                     } else if (a.lse) {
                         int tok, head;
                         row_of(kv, r0 + r, tok, head);
-                        a.lse[static_cast<int64_t>(c.s.q0 + tok) * kv.hq + head] = sum == 0.f ? kNegInf : (m[x] * sc + log2f(sum)) * kLn2;
+                        a.lse[static_cast<int64_t>(c.s.q0 + tok) * kv.hq + head] = sum == 0.f ? kNegInf : (m[x] * sc - kLift<T> + log2f(sum)) * kLn2;
                     }
                 }
             }

@@ -22,7 +22,11 @@
  *
  * Rounding as in moe_w4a8_attention.h: fp32 between the inputs and the single
  * rounding of each output, except attend's weights, which are rounded to the
- * element type as operands of the matrix units.  The edge cases are the same:
+ * element type as operands of the matrix units (their sum is not).  In fp16 the
+ * weights are 2^7 exp(s - m), m at most the row's maximum and at most a factor of
+ * 2^8 behind it, so that what is rounded to a multiple of 2^-24 is a weight 2^-21
+ * below the largest, and what counts in the sum alone one 2^-32 below it.  The
+ * edge cases are the same:
  * rows that see nothing give out = 0 and lse = -inf, tokens of no sequence
  * too, append takes a token below position zero or past the table of cosines
  * as padding (q_rot_out = 0, nothing stored), rows past kv_len never reach a
