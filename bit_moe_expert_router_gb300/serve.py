@@ -140,7 +140,8 @@ class LatentServingLayer:
         y = rms_norm(x, w["norm2"])
         ids = torch.empty(n, self.rule.top_k, dtype=torch.int32, device=dev)
         weights = torch.empty(n, self.rule.top_k, dtype=torch.float32, device=dev)
-        binding.moe_w4a8_route_scored(y @ w["router"], self.rule, ids, weights, bias=w["router_bias"])
+        logits = torch.mm(y, w["router"], out_dtype=torch.float32)  # (rounded to 16 bits, close experts would change places)
+        binding.moe_w4a8_route_scored(logits, self.rule, ids, weights, bias=w["router_bias"])
         moe = torch.empty(n, x.shape[1], dtype=torch.float32, device=dev)
         binding.moe_w4a8_forward_bf16_routed(y, ids, weights, w["w13"], w["s13"], w["w2"], w["s2"], self.dims(n), moe, self.moe_workspace(n))
         return (x.float() + moe).to(x.dtype)
