@@ -668,24 +668,32 @@ __device__ __forceinline__ void add_scaled(float4& to, const float4& x, float f)
     to.w += x.w * f;
 }
 
+// Whether four components of a row from `col + 4 lane` on have a NaN (what lies behind the latent part may be anything).
+__device__ __forceinline__ bool odd_four(const LatentArgs& a, const float4& o, int col) {
+    return col + 4 * (threadIdx.x & 31) < a.kv.d && (o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w);
+}
+
 // Writes 128 components of a row from `col` on, a warp four a lane, and with component 0 the row's lse.
 template <typename T, int ROWS>
-__device__ __forceinline__ void join_finish(const LatentArgs& a, const CutTile<ROWS>& t, int r, const float4& o, int col, float m, float l) {
+__device__ __forceinline__ void join_store(const LatentArgs& a, const CutTile<ROWS>& t, int r, const float4& o, int col, float m, float l) {
     const KvArgs& kv = a.kv;
     const int lane = threadIdx.x & 31;
     int i, head;
     row_of(kv, t.rec.rt * ROWS + r, i, head);
     const int tok = t.rec.q0 + i;
-    const bool in = col + 4 * lane < kv.d;  // (what lies behind the latent part may be anything)
-    if (__any_sync(~0u, l != l || (in && (o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w)))) {
-        latent_row<T>(a, t.rec.b, tok, head, t.rec.pos0 + i, col, col + 128);
-        return;
-    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (in)
+    if (col + 4 * lane < kv.d)
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col + 4 * lane) =
             make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
     if (lane == 0 && col == 0 && a.lse) a.lse[static_cast<int64_t>(tok) * kv.hq + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+}
+
+// Components [col0, col1) of a row that has a NaN, taken again.
+template <typename T, int ROWS>
+__device__ __forceinline__ void join_retake(const LatentArgs& a, const CutTile<ROWS>& t, int r, int col0, int col1) {
+    int i, head;
+    row_of(a.kv, t.rec.rt * ROWS + r, i, head);
+    latent_row<T>(a, t.rec.b, t.rec.q0 + i, head, t.rec.pos0 + i, col0, col1);
 }
 
 // A row by a warp, its pieces' loads two at a time.
@@ -719,9 +727,16 @@ __device__ __forceinline__ void join_few(const LatentArgs& a, const CutTile<ROWS
             if (two) add_scaled(acc[x], o1[x], f1);
         }
     }
+    bool odd = ll != ll;
+#pragma unroll
+    for (int x = 0; x < kVec; ++x) odd |= x < parts && odd_four(a, acc[x], 128 * x);
+    if (__any_sync(~0u, odd)) {  // (once, however many of its components: it is a walk over all keys)
+        join_retake<T, ROWS>(a, t, r, 0, kMaxLatent);
+        return;
+    }
 #pragma unroll
     for (int x = 0; x < kVec; ++x)
-        if (x < parts) join_finish<T, ROWS>(a, t, r, acc[x], 128 * x, mm, ll);
+        if (x < parts) join_store<T, ROWS>(a, t, r, acc[x], 128 * x, mm, ll);
 }
 
 // 128 components of a row by the block, eight of the pieces' loads at a time in a warp.  part, part_ml: of the block.
@@ -773,7 +788,8 @@ __device__ __forceinline__ void join_many(const LatentArgs& a, const CutTile<ROW
         sum += part_ml[w].y * f;
         add_scaled(o, part[w][lane], f);
     }
-    join_finish<T, ROWS>(a, t, r, o, col, top, sum);
+    if (__any_sync(~0u, sum != sum || odd_four(a, o, col))) join_retake<T, ROWS>(a, t, r, col, col + 128);
+    else join_store<T, ROWS>(a, t, r, o, col, top, sum);
 }
 
 // The join of the pieces of the cut tiles.  Block (i, y) stands for the boundary before CTA i + 1; the items of a tile, eight rows, a

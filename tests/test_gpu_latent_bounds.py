@@ -82,3 +82,33 @@ def test_rows_that_see_an_infinity(h, q_len, kv_len):
                 assert (err <= d[:, 0] + (p + 65) * E + z[:, 0].abs() * 2.0 ** -22)[rows].all()
                 compared += int((ok & ~finite.all(-1)[:, None]).sum())
     assert compared > 0
+
+
+@pytest.mark.parametrize("h,dc", [(16, 512), (5, 384), (64, 512)])
+def test_a_row_of_few_pieces_is_taken_again_whole(h, dc):
+    """A row with a NaN in one component, its keys cut into fewer than nine pieces: all its components come from one walk over the
+    keys, which has weights of 32 bits, so the finite ones have no rounding of weights to bf16 in them.  (Few keys and scores close to one
+    another, so that the bound of what is left is below that rounding.)"""
+    n = 40
+    c = Case([1] * n, [200 + i for i in range(n)], h, dc, 64, 16, seed=53)
+    for i in range(n):
+        p = 60 + i
+        c.rows[i][p, 3] = math.inf
+        c.cache[c.where(i, [p])] = c.rows[i][p:p + 1]
+    scale, compared = 3e-4, 0
+    out, lse = c.attend(scale)
+    for i in range(n):
+        x, q, got = c.rows[i].double(), c.q[i].double(), out[i].double()
+        minus = q[:, 3] < 0  # the others' scores there are +inf
+        assert got[~minus].isnan().all() and got[minus][:, 3].isnan().all()
+        x[60 + i, 3] = 0.0
+        s = (q @ x.T * scale)
+        s[:, 60 + i] = -math.inf
+        w, v, p = torch.softmax(s, -1), x[:, :dc], c.kv_len[i]
+        ref, a = w @ v, w @ v.abs()
+        d = (c.d + 8) * E * (q.abs() @ x.abs().T * scale).amax(-1, keepdim=True)
+        tol = c.u * ref.abs() + (2 * d + (9 + 2 * p) * E) * a
+        keep = minus[:, None] & (torch.arange(dc, device=DEV) != 3)
+        assert ((got - ref).abs() <= tol)[keep].all()
+        compared += int(keep.sum())
+    assert compared > 0
