@@ -442,7 +442,7 @@ class RouteRule:
 def moe_w4a8_route_scored(router_logits, rule: RouteRule, topk_ids, topk_w, bias=None):
     """The experts of each token by their scores, and their weights (see the header).
 
-    router_logits [tokens, n_experts] float32, bfloat16 or float16, any token stride; bias [n_experts] float32, added to the
+    router_logits [tokens, n_experts] float32, bfloat16 or float16, any token stride from n_experts on; bias [n_experts] float32, added to the
     scores for the choice alone, or None; topk_ids [tokens, top_k] int32, topk_w [tokens, top_k] float32.
     """
     n, index, k = router_logits.shape[0], router_logits.get_device(), rule.top_k

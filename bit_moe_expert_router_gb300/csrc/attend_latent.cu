@@ -36,8 +36,9 @@
 // Measured, bf16, 512 + 64 components, device time with the join: one sequence of 131071 positions, 32 heads 38.1 us (4.0 TB/s;
 // 22 by its bytes), 64 ragged ones up to 16384 of 16, 32, 64, 128 heads 65, 69, 84, 140 us (5.3, 5.0, 4.2, 2.5 TB/s; 51 to 52 by
 // their bytes; from 65 heads on two CTAs read the same keys, from DRAM 1.7 times), 509 tokens of 32 heads at 8000 positions beside eight single ones 367 us
-// (0.78 PFLOP/s; 145 by its operations).  The tensor pipe: S takes 36 steps of about 30 cycles for 32 keys, as 64 rows are half of its
-// width, O 8 of 52.
+// (0.78 PFLOP/s; 145 by its operations).  The products fill the chunk's time: S takes 36 steps of about 30 cycles for 32 keys, O 8 of
+// 52.  Why these steps are longer than the pipe's rate says is not measured: half of its rows are idle in S, and both operands come from
+// shared memory anew in each step, 3 and 6 KB, which at 128 bytes a cycle are 24 and 48 cycles.
 #include <algorithm>
 
 #include "latent_common.cuh"
@@ -153,7 +154,7 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, 
     for (int b = 0; b < blocks; ++b) tma_tile3d<1>(dst + b * 1024, map, 64 * b, row, page, bar);
 }
 
-// The rows of the CTA's whole tiles that ended with a NaN, taken again one by one by the softmax warps.
+// The rows of the CTA's whole tiles that ended with a NaN, taken again one by one by the softmax warps (0.85 us a key and more).
 template <typename T, int ROWS>
 __device__ __noinline__ void retake_rows(const LatentArgs& a, Cursor c, int warp) {
     const int lane = threadIdx.x & 31;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(LatCfg<ROWS>::kThreads, 1)
                         }
                     }
                 }
-                // what P's place held before is read (with one place: the unit before's; with two, across pieces, it is known)
+                // what P's place held before is read (of a piece's first units it is known: the piece before ended with a wait for its last product)
                 if (j >= C::kPs) wait(o_done + pb.slot, pb.phase ^ 1);
                 if (ok && live) {
 #pragma unroll

@@ -30,7 +30,7 @@ constexpr int kMaxLatent = 512, kMaxLatentRot = 64;
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int dtype, cudaStream_t st);
 
-// rows: of a sequence, by the caller's bound.  The rows of a tile, the CTAs that share it and whether it is cut go by the bounds.
+// rows: of a sequence, by the caller's bound.  The rows of a tile and whether it is cut go by the bounds.
 int latent_part_rows(int n_ctas);  // rows of all pieces, whatever the tile
 cudaError_t launch_latent(const LatentArgs& a, int dtype, int64_t rows, int n_ctas, cudaStream_t st);
 

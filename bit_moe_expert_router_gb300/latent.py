@@ -195,7 +195,7 @@ def moe_w4a8_latent_attention(batch: LatentBatch, q, out, lse=None, scale: float
     """Causal attention of the batch's tokens over its cache of latent rows (which holds theirs already).
 
     q [tokens, heads, latent_dim + rot_dim], out [tokens, heads, latent_dim]; lse [tokens, heads] float32, the log-sum-exp of
-    each row's scaled scores, or None; scale defaults to (latent_dim + rot_dim)^-1/2, which is seldom what a model wants: its
+    each row's scaled scores, or None; out and lse must not overlap q or the cache; scale defaults to (latent_dim + rot_dim)^-1/2, which is seldom what a model wants: its
     scale goes by the size of the heads before the absorption.  workspace: batch.alloc_workspace().
     """
     n, h, dc = q.shape[0], batch.n_heads, batch.latent_dim

@@ -169,8 +169,9 @@ int moe_w4a8_route(const float* router_logits, const moe_dims_t* d,
  *           the topk_groups best groups are kept (equal values: the lower);
  *   ids  = the top_k best experts of the kept groups by r, descending (equal:
  *           the lower index); an expert whose logit is a NaN has a NaN for its
- *           score, stands behind all numbers and is left out of the others' sums;
- *   w    = s of those; with renormalise divided by their sum; times scale.
+ *           score, stands behind all numbers and is left out of the softmax's sum;
+ *   w    = s of those; with renormalise divided by their sum (a NaN for all of a
+ *           token's, if an expert with a NaN had to be chosen); times scale.
  *
  * The choice is that of exact arithmetic on the given logits and biases, where
  * fp64 tells the candidates apart; weights are fp32.  The results are what

@@ -26,12 +26,13 @@
  * weights are 2^7 exp(s - m), m at most the row's maximum and at most a factor of
  * 2^8 behind it, so that what is rounded to a multiple of 2^-24 is a weight 2^-21
  * below the largest, and what counts in the sum alone one 2^-32 below it.  The
- * edge cases are the same:
- * rows that see nothing give out = 0 and lse = -inf, tokens of no sequence
- * too, append takes a token below position zero or past the table of cosines
- * as padding (q_rot_out = 0, nothing stored), rows past kv_len never reach a
- * result, a NaN or an infinity at a position reaches the rows that see it and
- * no others, a bad page id is never dereferenced.
+ * edge cases are the same: rows that see nothing give out = 0 and lse = -inf,
+ * tokens of no sequence too, append takes a token below position zero or past
+ * the table of cosines as padding (q_rot_out = 0, nothing stored), rows past
+ * kv_len never reach a result, a NaN or an infinity at a position reaches the
+ * rows that see it and no others (a row that ends with a NaN is taken again key
+ * by key, about a microsecond each, at the end of the call), a bad page id is
+ * never dereferenced.
  *
  * Layout.  bf16 or fp16.  The cache is [pages][page_size][Dc + R] with any page
  * and row strides, a row contiguous.  Token arrays have any token and head
@@ -95,8 +96,10 @@ size_t moe_w4a8_latent_attention_workspace_size(const moe_latent_batch_t* batch)
 
 /*
  * attend.  q: [T][n_heads][Dc + R], out: [T][n_heads][Dc], with strides in
- * elements; lse: float [T][n_heads] contiguous, or null.  Two runs on the same
- * inputs give the same bits.  T = 0 enqueues nothing.
+ * elements; lse: float [T][n_heads] contiguous, or null.  out and lse must not
+ * overlap q or the cache (a row that is taken again reads its query at the end of
+ * the call).  Two runs on the same inputs give the same bits.  T = 0 enqueues
+ * nothing.
  */
 int moe_w4a8_latent_attention(const moe_latent_batch_t* batch, int64_t n_tokens,
                               const void* q, int64_t q_token_stride, int64_t q_head_stride,
