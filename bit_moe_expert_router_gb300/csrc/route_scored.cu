@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(32 * kWarps, MAXJ <= 8 ? 8 : MAXJ == 16 ? 7 : 
         float b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
         for (int i = 0; i < MAXJ; ++i) {
-            const float g = i < me.n ? (by_r ? r[i] : x[i]) : -INFINITY;
+            const float g = i < me.n ? fmaxf(by_r ? r[i] : x[i], -INFINITY) : -INFINITY;  // (of a NaN and b1 the smaller would be b1, twice)
             b2 = fmaxf(b2, fminf(b1, g));
             b1 = fmaxf(b1, g);
         }
