@@ -32,7 +32,8 @@
  * kv_len never reach a result, a NaN or an infinity at a position reaches the
  * rows that see it and no others (a row that ends with a NaN is taken again key
  * by key, about a microsecond each, at the end of the call), a bad page id is
- * never dereferenced.
+ * never dereferenced.  A row all of whose scores are -inf has weights of zero:
+ * lse = -inf, out = 0, a NaN in the components where it sees an infinity or a NaN.
  *
  * Layout.  bf16 or fp16.  The cache is [pages][page_size][Dc + R] with any page
  * and row strides, a row contiguous.  Token arrays have any token and head

@@ -112,3 +112,23 @@ def test_a_row_of_few_pieces_is_taken_again_whole(h, dc):
         assert ((got - ref).abs() <= tol)[keep].all()
         compared += int(keep.sum())
     assert compared > 0
+
+
+@pytest.mark.parametrize("h", [4, 40, 128])
+@pytest.mark.parametrize("kv_len", [1, 90, 3000])
+@pytest.mark.parametrize("part", [3, 540])
+def test_a_row_whose_scores_are_all_minus_infinity(h, kv_len, part):
+    """Every position it sees has an infinity against its query: weights of zero, so zeros, a NaN in a component that is infinite, and lse -inf."""
+    c = Case([1, 1], [kv_len, kv_len], h, 512, 64, 16, seed=54)
+    c.rows[0][:, part] = math.inf
+    c.cache[c.where(0)] = c.rows[0]
+    minus = c.q[0, :, part] < 0
+    out, lse = c.attend()
+    assert minus.any() or h == 4
+    assert (lse[0] == torch.where(minus, -math.inf, math.inf)).all()
+    other = torch.arange(512, device=DEV) != part
+    assert (out[0][minus][:, other] == 0).all() and out[0][~minus].isnan().all()
+    if part < 512:
+        assert out[0][minus][:, part].isnan().all()
+    ref, ref_lse, tol, ltol = c.reference()
+    assert ((out[1].double() - ref[1]).abs() <= tol[1]).all() and ((lse[1].double() - ref_lse[1]).abs() <= ltol[1]).all()
