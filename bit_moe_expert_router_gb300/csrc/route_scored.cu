@@ -16,7 +16,7 @@
 // holds J consecutive experts of one group (32 / groups lanes a group), so lane order is expert order.  It
 // sorts them once, by a network on 32-bit keys whose low bits are the expert's place in the lane; the k best
 // of the warp are then k rounds of a warp-wide maximum and one ballot, in which the winner moves its list up.
-// 8192 tokens of 256 experts, 8 of 4 groups of 8, sigmoid with a bias: 10.9 us, where the logits alone take 1.3 at HBM's rate;
+// 8192 tokens of 256 experts, 8 of 4 groups of 8, sigmoid with a bias: 11.4 us, where the logits alone take 1.3 at HBM's rate;
 // without groups 9.7, without a bias 7.5.  64 tokens of 160 experts 3.2 us, 4 of 512 with 10 chosen 4.0: the launch and the
 // chain of a warp's steps.
 //
